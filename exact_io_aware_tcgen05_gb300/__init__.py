@@ -26,6 +26,8 @@ __all__ = [
     "fa_fp8_quantize_qk_incoherent", "fa_bwd_set_dq_heads", "fa_fwd_set_heads", "fa_fwd_heads",
     "fa_bwd_dq_heads",
     "fa_fwd_fp8", "Fp8Operands", "quantize_fp8", "attention_forward_fp8",
+    "fa_kv8_plan", "fa_kv8_append", "fa_fwd_kv8", "fa_fwd_kv8_workspace_size", "FA_KV8_BLOCK",
+    "Kv8Cache", "kv8_cache", "kv8_plan", "kv8_append", "attention_forward_kv8",
     "fa_device_status",
     "fa_set_wait_limit_cycles", "fa_set_launch_events", "fa_last_error", "attention_forward", "attention_backward",
     "fa_debug_checks_enabled", "fa_debug_check_selftest",
@@ -40,6 +42,7 @@ STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3:
                 4: "FA_ERR_CUDA", 5: "FA_ERR_TIMEOUT"}
 
 FA_DTYPE_BF16, FA_DTYPE_F16 = 0, 1   # fa_dtype
+FA_KV8_BLOCK = 16                    # tokens of one scale block of the 8-bit cache
 FA_STATIC_WORKSPACE_BYTES = 16 * 1024 * 1024   # the array of fa_bwd_static_workspace
 FA_BWD_AUTO, FA_BWD_SPLIT, FA_BWD_FUSED = -1, 0, 1   # fa_bwd_path_kind
 
@@ -111,6 +114,15 @@ def load(path: str | None = None):
     lib.fa_fwd_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                _i, _i, _vp, _i, _f, _vp]
     lib.fa_fwd_fp8.restype = _i
+    lib.fa_kv8_plan.argtypes = [_vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp]
+    lib.fa_kv8_plan.restype = _i
+    lib.fa_kv8_append.argtypes = [_i, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp]
+    lib.fa_kv8_append.restype = _i
+    lib.fa_fwd_kv8_workspace_size.argtypes = [_i] * 6
+    lib.fa_fwd_kv8_workspace_size.restype = _sz
+    lib.fa_fwd_kv8.argtypes = [_i, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i,
+                               _i, _i, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]
+    lib.fa_fwd_kv8.restype = _i
     lib.fa_device_status.argtypes = [_vp]
     lib.fa_device_status.restype = _i
     lib.fa_set_wait_limit_cycles.argtypes = [_ll]
@@ -388,6 +400,47 @@ def fa_fwd_fp8(q8, q_scale, k8, k_scale, vt8, v_scale, nb, vt_tokens, o, lse, B,
     return st
 
 
+def fa_kv8_plan(lens, grow, B, table, width, ring, num_pages, page, state, lens_out, cu_out, slots,
+                T, state_out, stream=None, check: bool = True) -> int:
+    """Pages and slots of the requests' new tokens (see include/fa.h)."""
+    st = load().fa_kv8_plan(_ptr(lens), _ptr(grow), B, _ptr(table), width, _ptr(ring), num_pages,
+                            page, _ptr(state), _ptr(lens_out), _ptr(cu_out), _ptr(slots), T,
+                            _ptr(state_out), _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def fa_kv8_append(dtype, k, v, stride, k8, k_scale, v8, v_scale, num_pages, page, Hkv, d, slots, T,
+                  stream=None, check: bool = True) -> int:
+    """New keys and values into the 8-bit cache (see include/fa.h)."""
+    st = load().fa_kv8_append(int(dtype), _ptr(k), _ptr(v), int(stride), _ptr(k8), _ptr(k_scale),
+                              _ptr(v8), _ptr(v_scale), num_pages, page, Hkv, d, _ptr(slots), T,
+                              _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, total_tokens) -> int:
+    """Workspace bytes of fa_fwd_kv8 (total_tokens: T for a packed batch, 0 for a dense one)."""
+    return int(load().fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, int(total_tokens)))
+
+
+def fa_fwd_kv8(dtype, q, q_stride, k8, k_scale, v8, v_scale, num_pages, page, table, width, lens, o,
+               lse, B, Hq, Hkv, N, d, causal, window, cu_seqlens, total_tokens, scale, workspace,
+               workspace_bytes, stream=None, check: bool = True) -> int:
+    """Attention of new tokens over the paged 8-bit cache (see include/fa.h)."""
+    st = load().fa_fwd_kv8(int(dtype), _ptr(q), int(q_stride), _ptr(k8), _ptr(k_scale), _ptr(v8),
+                           _ptr(v_scale), num_pages, page, _ptr(table), width, _ptr(lens), _ptr(o),
+                           _ptr(lse), B, Hq, Hkv, N, d, int(bool(causal)), int(window),
+                           _ptr(cu_seqlens), int(total_tokens), float(scale), _ptr(workspace),
+                           int(workspace_bytes), _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
 def _geometry(q, k, cu_seqlens, max_seqlen):
     if cu_seqlens is None:
         B, N, Hq, d = q.shape
@@ -491,6 +544,202 @@ def attention_forward_fp8(ops: Fp8Operands, *, causal=False, window=0, scale=Non
     fa_fwd_fp8(q8, qs, k8, ks, vt8, vs, nb, vt_tokens, o, lse, B, Hq, Hkv, N, d, causal, window,
                cu_seqlens, T, scale, stream)
     return o, lse
+
+
+class Kv8Cache(tuple):
+    """(k8, k_scale, v8, v_scale), the paged 8-bit cache of include/fa.h: float8_e4m3fn codes
+    [num_pages, Hkv, page, d] and float32 scales [num_pages, Hkv, page / 16]."""
+    __slots__ = ()
+    _fields = ("k8", "k_scale", "v8", "v_scale")
+
+    def __getattr__(self, name):
+        try:
+            return self[self._fields.index(name)]
+        except ValueError:
+            raise AttributeError(name) from None
+
+
+def kv8_cache(num_pages, Hkv, d, *, page=64, device="cuda") -> Kv8Cache:
+    """A cache with no tokens in it (zero codes, scales of one)."""
+    import torch
+    codes = [torch.zeros((num_pages, Hkv, page, d), dtype=torch.uint8, device=device)
+             .view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones((num_pages, Hkv, page // FA_KV8_BLOCK), device=device) for _ in range(2)]
+    return Kv8Cache((codes[0], scales[0], codes[1], scales[1]))
+
+
+def _kv8_shape(cache):
+    """(num_pages, Hkv, page, d) of a cache whose four tensors fit together."""
+    import torch
+    k8, k_scale, v8, v_scale = cache
+    if k8.dtype != torch.float8_e4m3fn or v8.dtype != torch.float8_e4m3fn:
+        raise TypeError("the cache's codes must be float8_e4m3fn")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("the cache's scales must be float32")
+    if k8.dim() != 4 or v8.shape != k8.shape:
+        raise ValueError("k8 and v8 must both be [num_pages, Hkv, page, d]")
+    num_pages, Hkv, page, d = shape = k8.shape
+    if k_scale.shape != v_scale.shape or k_scale.shape != (num_pages, Hkv, page // FA_KV8_BLOCK):
+        raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page / 16]")
+    if not (k8.is_contiguous() and v8.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
+    _same_device(k8, k_scale, v8, v_scale)
+    return shape
+
+
+def _same_device(first, *others):
+    dev = first.device
+    if dev.type != "cuda" or any(x.device != dev for x in others):
+        raise ValueError("all tensors must be on one CUDA device")
+
+
+def _int32(name, x, *shape):
+    """A contiguous int32 tensor of the given shape (None: any size)."""
+    import torch
+    if x.dtype != torch.int32 or not x.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor")
+    if x.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(x.shape)}")
+
+
+def _rows(name, x, heads, d):
+    """Elements between the tokens of a [..., heads, d] tensor whose tokens are evenly spaced
+    (a slice of a wider projection's output, say)."""
+    lead = x.shape[:-2]
+    ok = x.shape[-2:] == (heads, d) and x.stride(-1) == 1 and (heads == 1 or x.stride(-2) == d)
+    stride = x.stride(-3) if lead[-1] > 1 else 0
+    if len(lead) == 2 and lead[0] > 1:
+        outer = x.stride(0)
+        ok = ok and outer % lead[1] == 0 and (lead[1] == 1 or outer == stride * lead[1])
+        stride = outer // lead[1]
+    if not ok:
+        raise ValueError(f"{name} must be [..., {heads}, {d}] with contiguous heads and evenly "
+                         "spaced tokens")
+    return stride or heads * d
+
+
+class _on:
+    """The device and stream of a call: the tensors' device becomes the current one and a
+    stream that was given the current stream, so that what the call allocates belongs to it."""
+    __slots__ = ("contexts",)
+
+    def __init__(self, device, stream):
+        import torch
+        self.contexts = []
+        if device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        import torch
+        for c in self.contexts:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+        return False
+
+
+def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
+    """(lens, cu_seqlens, slots, state) after the requests gain ``grow`` tokens each (below
+    zero: the request has ended and gives its pages back), for int32 CUDA tensors lens and
+    grow [B], table [B, width], ring [num_pages] and state [3] (first free page's place in
+    the ring, free pages, refused requests).  table and ring are updated in place; the
+    outputs are new tensors, slots of ``tokens`` elements (-1 for tokens that get no place)."""
+    import torch
+    _int32("lens", lens, None)
+    B = lens.shape[0]
+    _int32("grow", grow, B)
+    _int32("table", table, B, None)
+    _int32("ring", ring, None)
+    _int32("state", state, 3)
+    _same_device(lens, grow, table, ring, state)
+    tokens = int(tokens)
+    with _on(lens.device, stream) as s:
+        # one allocation, the parts 16-byte aligned
+        parts = [B, B + 1, max(tokens, 0), 3]
+        at = [0]
+        for n in parts:
+            at.append(at[-1] + (n + 3) // 4 * 4)
+        out = torch.empty(at[-1], dtype=torch.int32, device=lens.device)
+        lens_out, cu, slots, state_out = (out[a:a + n] for a, n in zip(at, parts))
+        fa_kv8_plan(lens, grow, B, table, table.shape[1], ring, ring.shape[0], page, state, lens_out,
+                    cu, slots, tokens, state_out, s)
+    return lens_out, cu, slots, state_out
+
+
+def kv8_append(cache: Kv8Cache, k, v, slots, *, stream=None) -> None:
+    """Writes the tokens k, v ([T, Hkv, d], both bf16 or both fp16, evenly spaced) into the
+    cache at ``slots`` (int32 [T], see kv8_plan), in 8 bits."""
+    num_pages, Hkv, page, d = _kv8_shape(cache)
+    dtype = _dtype_code(k, v)
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("k and v must both be [T, Hkv, d]")
+    T = k.shape[0]
+    stride = _rows("k", k, Hkv, d)
+    if _rows("v", v, Hkv, d) != stride:
+        raise ValueError("the tokens of k and v must be the same distance apart")
+    _int32("slots", slots, T)
+    _same_device(cache[0], k, v, slots)
+    with _on(k.device, stream) as s:
+        fa_kv8_append(dtype, k, v, stride, *cache, num_pages, page, Hkv, d, slots, T, s)
+
+
+def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, window=0, scale=None,
+                          cu_seqlens=None, max_seqlen=None, stream=None, out=None, lse=None,
+                          workspace=None):
+    """O, LSE of new tokens' attention over the paged 8-bit cache, which holds their own keys
+    and values already.  q: bf16 or fp16, dense [B, N, Hq, d] or packed [T, Hq, d] with
+    cu_seqlens (int32 [B + 1]) and max_seqlen; its tokens may lie apart (a slice of a wider
+    tensor).  table: int32 [B, width], lens: int32 [B], as kv8_plan keeps them.  Allocates
+    what of the outputs and the workspace (uint8, fa_fwd_kv8_workspace_size) is not given."""
+    import torch
+    num_pages, Hkv, page, d = _kv8_shape(cache)
+    dtype = _dtype_code(q)
+    packed = cu_seqlens is not None
+    _int32("lens", lens, None)
+    B = lens.shape[0]
+    _int32("table", table, B, None)
+    if q.dim() != (3 if packed else 4):
+        raise ValueError("q must be [B, N, Hq, d], or [T, Hq, d] with cu_seqlens")
+    Hq = q.shape[-2]
+    stride = _rows("q", q, Hq, d)
+    if packed:
+        if max_seqlen is None:
+            raise ValueError("packed batches need max_seqlen")
+        _int32("cu_seqlens", cu_seqlens, B + 1)
+        N, T = int(max_seqlen), q.shape[0]
+        _same_device(q, *cache, table, lens, cu_seqlens)
+    else:
+        if q.shape[0] != B:
+            raise ValueError(f"q has {q.shape[0]} requests, lens {B}")
+        N, T = q.shape[1], 0
+        _same_device(q, *cache, table, lens)
+    scale = d ** -0.5 if scale is None else scale
+    lse_shape = (Hq, T) if packed else (B, Hq, N)
+    with _on(q.device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of q's shape and type")
+        if lse is None:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous float32 {lse_shape}")
+        if workspace is None:
+            workspace = torch.empty(fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, T),
+                                    dtype=torch.uint8, device=q.device)
+        _same_device(q, out, lse, workspace)
+        fa_fwd_kv8(dtype, q, stride, *cache, num_pages, page, table, table.shape[1], lens, out, lse,
+                   B, Hq, Hkv, N, d, causal, window, cu_seqlens, T, scale, workspace,
+                   workspace.numel() * workspace.element_size(), s)
+    return out, lse
 
 
 _PATHS = {"auto": FA_BWD_AUTO, "split": FA_BWD_SPLIT, "fused": FA_BWD_FUSED}

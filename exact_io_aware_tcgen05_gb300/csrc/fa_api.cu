@@ -917,3 +917,180 @@ fa_status fa_debug_check_selftest(cudaStream_t stream) {
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------- paged 8-bit cache
+
+namespace fa {
+namespace {
+
+// Checks the cache's shape; *page_log2 is set for a valid page size.
+fa_status check_pages(const char* who, int num_pages, int page, int* page_log2) {
+    if (page != 16 && page != 32 && page != 64 && page != 128)
+        return fail(FA_ERR_UNSUPPORTED, "%s: page of %d tokens not in {16, 32, 64, 128}", who, page);
+    if (num_pages < 1) return fail(FA_ERR_INVALID_ARG, "%s: num_pages must be >= 1 (got %d)", who, num_pages);
+    if (static_cast<long long>(num_pages) * page > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "%s: num_pages * page = %lld is 2^31 or more", who,
+                    static_cast<long long>(num_pages) * page);
+    int l = 4;
+    while ((1 << l) < page) ++l;
+    *page_log2 = l;
+    return FA_OK;
+}
+
+fa_status check_table(const char* who, int B, int width, int page) {
+    if (B < 1 || width < 1)
+        return fail(FA_ERR_INVALID_ARG, "%s: B and width must be >= 1 (got %d, %d)", who, B, width);
+    if (B > kKv8MaxRequests)
+        return fail(FA_ERR_UNSUPPORTED, "%s: B = %d above %d", who, B, kKv8MaxRequests);
+    if (static_cast<long long>(width) * page > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "%s: table rows of %d pages hold 2^31 tokens or more", who, width);
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_kv8_plan(const int* lens, const int* grow, int B, int* table, int width, int* ring,
+                      int num_pages, int page, const int* state, int* lens_out, int* cu_out,
+                      int* slots, int T, int* state_out, cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    if (T < 0) return fail(FA_ERR_INVALID_ARG, "fa_kv8_plan: T must be >= 0 (got %d)", T);
+    if (!lens || !grow || !table || !ring || !state || !lens_out || !cu_out || (T > 0 && !slots) ||
+        !state_out)
+        return fail(FA_ERR_INVALID_ARG, "fa_kv8_plan: every pointer must be non-null");
+    for (const void* x : {static_cast<const void*>(lens), static_cast<const void*>(grow),
+                          static_cast<const void*>(table), static_cast<const void*>(ring),
+                          static_cast<const void*>(state), static_cast<const void*>(lens_out),
+                          static_cast<const void*>(cu_out), static_cast<const void*>(slots),
+                          static_cast<const void*>(state_out)})
+        if (!aligned4(x)) return fail(FA_ERR_INVALID_ARG, "fa_kv8_plan: arrays must be 4-byte aligned");
+    if (lens == lens_out || state == state_out)
+        return fail(FA_ERR_INVALID_ARG, "fa_kv8_plan: lens_out and state_out must not be lens and state");
+    Kv8PlanParams p;
+    fa_status st = check_pages("fa_kv8_plan", num_pages, page, &p.page_log2);
+    if (st == FA_OK) st = check_table("fa_kv8_plan", B, width, page);
+    if (st != FA_OK) return st;
+    p.lens = lens;
+    p.grow = grow;
+    p.table = table;
+    p.ring = ring;
+    p.state = state;
+    p.lens_out = lens_out;
+    p.cu_out = cu_out;
+    p.slots = slots;
+    p.state_out = state_out;
+    p.B = B;
+    p.width = width;
+    p.num_pages = num_pages;
+    p.T = T;
+    const cudaError_t e = launch_kv8_plan(p, sm_count(), stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_plan launch");
+}
+
+fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long stride, void* k8,
+                        float* k_scale, void* v8, float* v_scale, int num_pages, int page, int Hkv,
+                        int d, const int* slots, int T, cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    fa_status st = check_dtype(dtype, "fa_kv8_append");
+    if (st != FA_OK) return st;
+    if (T < 0 || Hkv < 1)
+        return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: T >= 0 and Hkv >= 1 needed (got %d, %d)", T, Hkv);
+    if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "fa_kv8_append: head dim %d not in {64, 128}", d);
+    Kv8AppendParams p;
+    if ((st = check_pages("fa_kv8_append", num_pages, page, &p.page_log2)) != FA_OK) return st;
+    if (!k8 || !v8 || !k_scale || !v_scale || (T > 0 && (!k || !v || !slots)))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: every pointer must be non-null");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || !aligned4(slots))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: k, v, k8 and v8 must be 16-byte aligned, the "
+                    "scales and slots 4-byte aligned");
+    if (stride % 8 != 0 || stride < static_cast<long long>(Hkv) * d)
+        return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: stride %lld must be a multiple of 8 and at "
+                    "least Hkv * d", stride);
+    if (T == 0) return FA_OK;
+    p.x[0] = k;
+    p.x[1] = v;
+    p.codes[0] = static_cast<uint8_t*>(k8);
+    p.codes[1] = static_cast<uint8_t*>(v8);
+    p.scales[0] = k_scale;
+    p.scales[1] = v_scale;
+    p.slots = slots;
+    p.stride = stride;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.num_slots = num_pages * page;
+    p.elem = static_cast<int>(dtype);
+    p.chunk = kKv8Block;
+    const cudaError_t e = launch_kv8_append(p, d, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append launch");
+}
+
+size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens) {
+    fa::Geometry g;
+    return fa::query_geometry(B, Hq, Hkv, N, d, 0, 0, total_tokens, &g) ? 256 : 0;
+}
+
+fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
+                     const float* k_scale, const void* v8, const float* v_scale, int num_pages,
+                     int page, const int* table, int width, const int* lens, void* o, float* lse,
+                     int B, int Hq, int Hkv, int N, int d, int causal, int window,
+                     const int* cu_seqlens, int total_tokens, float scale, void* workspace,
+                     size_t workspace_bytes, cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    const cudaEvent_t* ev = nullptr;
+    if (take_events(1, &ev) != FA_OK)
+        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: fa_set_launch_events needs >= 2 events");
+    fa_status st = check_dtype(dtype, "fa_fwd_kv8");
+    if (st != FA_OK) return st;
+    Geometry g;
+    st = check_common(B, Hq, Hkv, N, d, causal, window, cu_seqlens, total_tokens, scale, &g);
+    if (st != FA_OK) return st;
+    Kv8FwdParams p;
+    if ((st = check_pages("fa_fwd_kv8", num_pages, page, &p.page_log2)) != FA_OK) return st;
+    if ((st = check_table("fa_fwd_kv8", B, width, page)) != FA_OK) return st;
+    if (!q || !k8 || !k_scale || !v8 || !v_scale || !table || !lens || !o || !lse)
+        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: every pointer must be non-null");
+    if (!aligned16(q) || !aligned16(k8) || !aligned16(v8) || !aligned16(o) || !aligned16(lse) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(table) || !aligned4(lens))
+        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: q, k8, v8, o and lse must be 16-byte aligned, "
+                    "the scales, table and lens 4-byte aligned");
+    if (q_stride % 8 != 0 || q_stride < static_cast<long long>(Hq) * d)
+        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: q_stride %lld must be a multiple of 8 and at "
+                    "least Hq * d", q_stride);
+    const size_t need = fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, cu_seqlens ? total_tokens : 0);
+    if (!workspace || workspace_bytes < need)
+        return fail(FA_ERR_WORKSPACE, "fa_fwd_kv8: workspace of at least %zu bytes needed, got %zu%s",
+                    need, workspace_bytes, workspace ? "" : " (null)");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(FA_ERR_WORKSPACE, "fa_fwd_kv8: workspace must be 256-byte aligned");
+    if (g.tokens == 0) return FA_OK;
+    p.seq = g.seq;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.k8 = static_cast<const uint8_t*>(k8);
+    p.v8 = static_cast<const uint8_t*>(v8);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.table = table;
+    p.lens = lens;
+    p.o = o;
+    p.lse = lse;
+    p.width = width;
+    p.num_pages = num_pages;
+    p.scale_log2 = scale * kLog2e;
+    p.elem = static_cast<int>(dtype);
+    p.timeout_cycles = g_wait_limit.load();
+    p.status = status_word_ptr();
+    if (!p.status) return fail(FA_ERR_CUDA, "fa_fwd_kv8: cannot resolve the device status word");
+    cudaError_t e = record(ev, 0, stream);
+    if (e == cudaSuccess) e = launch_fwd_kv8(p, d, stream);
+    if (e == cudaSuccess) e = record(ev, 1, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_kv8 launch");
+}
+
+}  // extern "C"

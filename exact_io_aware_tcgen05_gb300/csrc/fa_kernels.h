@@ -115,6 +115,55 @@ struct Fp8QuantParams {
     uint32_t seed_lo, seed_hi;  // its seed, the Philox key
 };
 
+// The paged 8-bit cache (fa_kv8_* in fa.h).
+constexpr int kKv8Block = FA_KV8_BLOCK;   // tokens of one scale block
+constexpr int kKv8MaxRequests = 8192;
+
+struct Kv8PlanParams {
+    const int* lens;    // [B]
+    const int* grow;    // [B]
+    int* table;         // [B, width]
+    int* ring;          // [num_pages]
+    const int* state;   // head, count, refused
+    int* lens_out;
+    int* cu_out;        // [B + 1]
+    int* slots;         // [T]
+    int* state_out;
+    int B, width, num_pages, T;
+    int page_log2;
+};
+
+struct Kv8AppendParams {
+    const void* x[2];   // k, v: 16-bit [T, Hkv, d], tokens `stride` elements apart
+    uint8_t* codes[2];  // k8, v8
+    float* scales[2];
+    const int* slots;   // [T]
+    long long stride;
+    int T, Hkv, num_slots;
+    int page_log2;
+    int chunk;          // tokens of one warp: the blocks that start among them are its own
+    int elem;
+};
+
+struct Kv8FwdParams {
+    SeqInfo seq;        // the new tokens (queries); N: the most of a request
+    const void* q;
+    long long q_stride;
+    const uint8_t* k8;
+    const uint8_t* v8;
+    const float* k_scale;
+    const float* v_scale;
+    const int* table;   // [B, width]
+    const int* lens;    // [B]
+    void* o;
+    float* lse;
+    int width, num_pages, page_log2;
+    float scale_log2;
+    int elem;
+    long long timeout_cycles;
+    int* status;
+};
+
 // Launchers (defined in the kernel translation units).  They only enqueue on
 // `stream` and return the launch error.
 cudaError_t launch_fwd(const FwdParams& p, int d, cudaStream_t stream);
@@ -130,6 +179,9 @@ cudaError_t launch_bwd_dq_convert(const BwdParams& p, int d, cudaStream_t stream
 constexpr int kBoundSlots = 32;
 cudaError_t launch_fp8_quant_qk(const Fp8QuantParams& p, int d, int grid, cudaStream_t stream);
 cudaError_t launch_fp8_quant_v(const Fp8QuantParams& p, int d, int grid, cudaStream_t stream);
+cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stream);
+cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, cudaStream_t stream);
 
 int* device_status_word();  // library-owned device status word (fa_api.cu)
 

@@ -328,6 +328,92 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
                      const int* cu_seqlens, int total_tokens, float scale, cudaStream_t stream);
 
 /*
+ * Attention over a paged cache held in 8 bits: the serving form.  Three entry points
+ * make one step of a server: fa_kv8_plan gives the requests' new tokens their places,
+ * fa_kv8_append writes the new keys and values there, fa_fwd_kv8 attends to them.  All
+ * lengths, tables and counts live in device memory and nothing is read on the host, so
+ * a step can be captured into a graph and replayed as the requests grow.
+ *
+ * The cache.  `num_pages` pages of `page` tokens (16, 32, 64 or 128), the same for all
+ * key/value heads:
+ *   k8, v8            device, e4m3 [num_pages, Hkv, page, d]
+ *   k_scale, v_scale  device, fp32 [num_pages, Hkv, page / 16]: one per block of 16
+ *                     tokens and head, positive and finite; a value is code * scale.
+ *   table             device, int32 [B, width]: page k of request b holds its tokens
+ *                     k page .. k page + page - 1.  Entries past a request's tokens are
+ *                     not used and may hold anything, and so may the cache's bytes and
+ *                     scales there.
+ *   lens              device, int32 [B]: the tokens that each request holds (clamped to
+ *                     0 .. width page)
+ * A slot is a token's place in the cache, page id * page + offset in the page.
+ * Limits: num_pages * page < 2^31, B <= 8192 (FA_ERR_UNSUPPORTED beyond).
+ *
+ * fa_kv8_plan: request b gains grow[b] >= 0 tokens, or, where grow[b] < 0, it has ended.
+ * Free pages queue in a ring: ring[(head + i) mod num_pages], 0 <= i < count, with
+ * state = (head, count, requests refused).
+ *   lens, grow, state   device, read; state int32[3]
+ *   table, ring         device, read and written
+ *   lens_out            device, written: int32 [B], the new lengths
+ *   cu_out              device, written: int32 [B + 1], cu_seqlens of the new tokens (the
+ *                       sums of max(grow, 0))
+ *   slots               device, written: int32 [T], the slot of each new token of the
+ *                       packed batch, -1 for tokens that get none
+ *   state_out           device, written: int32[3]
+ * Pages are taken from the ring's front in the order of the requests and blocks, and an
+ * ended request's pages (its length becomes 0) go to its back in the same order; they
+ * can be taken from the next call on.  A request is refused, and keeps its length, where
+ * it would outgrow its table row, its tokens do not all lie in 0 .. T - 1, or the free
+ * pages do not reach: request b is served iff it needs no page or the pages needed by
+ * requests 0 .. b (those whose row and tokens fit) are no more than count.
+ * lens_out and state_out must not be lens and state: the call reads them throughout, and
+ * running it again on the same inputs gives the same outputs.
+ *
+ * fa_kv8_append: token t of k and v ([T, Hkv, d], bf16 or fp16, tokens `stride` elements
+ * apart, a multiple of 8) goes to slots[t]; a slot outside the cache (-1) leaves the token
+ * out.  The tokens of one block of 16 slots must be neighbours in the batch with
+ * consecutive slots, as fa_kv8_plan gives them.  For each block and head, with amax the
+ * largest finite magnitude among its new values and k >= -64 the least whole number with
+ * amax <= 448 2^k, the block's scale becomes 2^k where its first new token is the block's
+ * first, and max(old scale, 2^k) where the block held tokens before; those are then
+ * rounded again to the new scale, code = e4m3(code old / new).  A new code is
+ * e4m3(x / scale), to nearest, ties to even.  Scales are powers of two, so the
+ * divisions are exact, and so is the second rounding for codes that stay normal e4m3
+ * numbers.  Infinities and NaN become NaN codes.
+ *
+ * fa_fwd_kv8: O and LSE of the new tokens' attention over the cache.
+ *   q            device, read: bf16 or fp16; dense [B, N, Hq, d] or packed [T, Hq, d],
+ *                tokens `q_stride` elements apart (a multiple of 8, Hq d if contiguous)
+ *   o, lse       device, written: layouts and types of fa_fwd, contiguous
+ * Query i of the n of request b sits at position p = lens[b] - n + i.  Key j is visible
+ * iff j < lens[b], and with causal != 0 also j <= p and, if window > 0, p - j < window.
+ * (The new tokens' own keys are in the cache before the call.)  A row with no visible
+ * key gets O = 0 and LSE = -inf; rows of a packed batch behind cu_seqlens[B] are left as
+ * they were.  A table entry outside 0 .. num_pages - 1 hides its page's tokens.  A value
+ * in a place hidden from a row (NaN included) does not reach that row.
+ * N must be >= the most new tokens of a request.  The scores use the codes and q
+ * unrounded; the probabilities are rounded to 9 bits (bf16) or 11 bits (fp16).
+ *   workspace    device, >= fa_fwd_kv8_workspace_size(...) bytes, 256-byte aligned,
+ *                contents ignored; not to be shared by calls in flight together
+ *                (calls captured into graphs that replay at the same time among them)
+ * The size does not depend on lens.  The result does not depend on anything but the
+ * inputs, the geometry and the device's SM count.
+ */
+#define FA_KV8_BLOCK 16
+fa_status fa_kv8_plan(const int* lens, const int* grow, int B, int* table, int width, int* ring,
+                      int num_pages, int page, const int* state, int* lens_out, int* cu_out,
+                      int* slots, int T, int* state_out, cudaStream_t stream);
+fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long stride, void* k8,
+                        float* k_scale, void* v8, float* v_scale, int num_pages, int page, int Hkv,
+                        int d, const int* slots, int T, cudaStream_t stream);
+size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens);
+fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
+                     const float* k_scale, const void* v8, const float* v_scale, int num_pages,
+                     int page, const int* table, int width, const int* lens, void* o, float* lse,
+                     int B, int Hq, int Hkv, int N, int d, int causal, int window,
+                     const int* cu_seqlens, int total_tokens, float scale, void* workspace,
+                     size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Backward pass of fa_fwd for the loss gradient dO, recomputing S and P from
  * the saved logsumexp ("3. Recomputation in the Backward Pass"):
  *   D_i = dO_i . O_i,  P_ij = exp(S_ij - LSE_i),  dP_ij = dO_i . v_j,
