@@ -947,6 +947,50 @@ fa_status check_table(const char* who, int B, int width, int page) {
     return FA_OK;
 }
 
+// Rows of an item of the attention kernel.  A request's rows are its (new token, head of the
+// group) pairs, N * group at most; all of an item's rows take one pass over the keys.
+// Narrow items cost less per key tile, wide ones read the cache fewer times: the narrowest
+// that takes a request's rows in one item, and 64 for more rows than that.
+int kv8_columns(int N, int group) {
+    const long long rows = static_cast<long long>(N) * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+// Byte layout of fa_fwd_kv8's workspace, each part padded to 256 bytes.
+struct Kv8Workspace {
+    size_t stat, o, full;
+};
+Kv8Workspace kv8_workspace(int ctas, int columns, int d) {
+    auto pad = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    Kv8Workspace w;
+    const size_t rows = static_cast<size_t>(2) * ctas * columns;
+    w.stat = pad(ctas * sizeof(Kv8Join));
+    w.o = w.stat + pad(rows * sizeof(float2));
+    w.full = w.o + pad(rows * d * sizeof(float));
+    return w;
+}
+
+// [num_pages * Hkv, page, d] codes viewed as (d, page, num_pages * Hkv): the box is the page
+// of one head, rows of d bytes swizzled over d bytes.
+fa_status make_page_map(CUtensorMap* map, const void* base, int num_pages, int Hkv, int page, int d,
+                        const char* name) {
+    auto enc = encode_fn();
+    if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page),
+                          static_cast<cuuint64_t>(num_pages) * Hkv};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page) * d};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(page), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name,
+                    static_cast<int>(r));
+    return FA_OK;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -1031,7 +1075,8 @@ fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long 
 
 size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens) {
     fa::Geometry g;
-    return fa::query_geometry(B, Hq, Hkv, N, d, 0, 0, total_tokens, &g) ? 256 : 0;
+    if (!fa::query_geometry(B, Hq, Hkv, N, d, 0, 0, total_tokens, &g)) return 0;
+    return fa::kv8_workspace(fa::sm_count(), fa::kv8_columns(N, Hq / Hkv), d).full;
 }
 
 fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
@@ -1043,8 +1088,8 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     using namespace fa;
     t_last_error[0] = '\0';
     const cudaEvent_t* ev = nullptr;
-    if (take_events(1, &ev) != FA_OK)
-        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: fa_set_launch_events needs >= 2 events");
+    if (take_events(2, &ev) != FA_OK)
+        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: fa_set_launch_events needs >= 3 events");
     fa_status st = check_dtype(dtype, "fa_fwd_kv8");
     if (st != FA_OK) return st;
     Geometry g;
@@ -1062,7 +1107,13 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     if (q_stride % 8 != 0 || q_stride < static_cast<long long>(Hq) * d)
         return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: q_stride %lld must be a multiple of 8 and at "
                     "least Hq * d", q_stride);
-    const size_t need = fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, cu_seqlens ? total_tokens : 0);
+    if (static_cast<long long>(num_pages) * Hkv > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: num_pages * Hkv = %lld is 2^31 or more",
+                    static_cast<long long>(num_pages) * Hkv);
+    p.columns = kv8_columns(N, g.seq.group);
+    p.ctas = sm_count();
+    const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);
+    const size_t need = w.full;
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "fa_fwd_kv8: workspace of at least %zu bytes needed, got %zu%s",
                     need, workspace_bytes, workspace ? "" : " (null)");
@@ -1072,7 +1123,12 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     p.seq = g.seq;
     p.q = q;
     p.q_stride = q_stride;
-    p.k8 = static_cast<const uint8_t*>(k8);
+    if ((st = make_page_map(&p.tm_k, k8, num_pages, Hkv, page, d, "k8")) != FA_OK) return st;
+    if ((st = make_page_map(&p.tm_v, v8, num_pages, Hkv, page, d, "v8")) != FA_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.joins = reinterpret_cast<Kv8Join*>(ws);
+    p.part_stat = reinterpret_cast<float2*>(ws + w.stat);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
     p.v8 = static_cast<const uint8_t*>(v8);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
@@ -1087,9 +1143,7 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     p.timeout_cycles = g_wait_limit.load();
     p.status = status_word_ptr();
     if (!p.status) return fail(FA_ERR_CUDA, "fa_fwd_kv8: cannot resolve the device status word");
-    cudaError_t e = record(ev, 0, stream);
-    if (e == cudaSuccess) e = launch_fwd_kv8(p, d, stream);
-    if (e == cudaSuccess) e = record(ev, 1, stream);
+    const cudaError_t e = launch_fwd_kv8(p, d, ev, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_kv8 launch");
 }
 

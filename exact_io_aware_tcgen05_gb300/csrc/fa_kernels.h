@@ -145,11 +145,22 @@ struct Kv8AppendParams {
     int elem;
 };
 
+// What the attention kernel's CTA c leaves for the joining kernel where its range ends
+// inside an item: the item's first part is CTA c's second slot, the others are the first
+// slots of CTAs c + 1 .. last (0: the range ends between two items).
+struct Kv8Join {
+    int last;
+    int b, h;        // request, key/value head
+    int start, n;    // the request's first new token in the batch, and their count
+    int row0;        // the item's first row (rows are (token, head of the group) pairs)
+    long long total; // units of all CTAs' shares
+};
+
 struct Kv8FwdParams {
+    CUtensorMap tm_k, tm_v;   // codes as (d, page, num_pages * Hkv); the box is a page of one head
     SeqInfo seq;        // the new tokens (queries); N: the most of a request
     const void* q;
     long long q_stride;
-    const uint8_t* k8;
     const uint8_t* v8;
     const float* k_scale;
     const float* v_scale;
@@ -158,6 +169,12 @@ struct Kv8FwdParams {
     void* o;
     float* lse;
     int width, num_pages, page_log2;
+    int columns;        // rows of an item: 16, 32 or 64 (kv8_columns)
+    int ctas;
+    // workspace: [ctas] joins, [2 ctas, columns] (reference, sum), [2 ctas, columns, d] O
+    Kv8Join* joins;
+    float2* part_stat;
+    float* part_o;
     float scale_log2;
     int elem;
     long long timeout_cycles;
@@ -181,7 +198,8 @@ cudaError_t launch_fp8_quant_qk(const Fp8QuantParams& p, int d, int grid, cudaSt
 cudaError_t launch_fp8_quant_v(const Fp8QuantParams& p, int d, int grid, cudaStream_t stream);
 cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stream);
-cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, cudaStream_t stream);
+// launch_fwd_kv8 records ev[0..2] (if not null) around its two kernels.
+cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, cudaStream_t stream);
 
 int* device_status_word();  // library-owned device status word (fa_api.cu)
 

@@ -1,9 +1,49 @@
 // fa_kv8_fwd.cu -- attention of new tokens over the paged 8-bit cache (fa_fwd_kv8 in
-// include/fa.h).
+// include/fa.h) on sm_103a.
+//
+// A request's rows are its (new token, head of the group) pairs: they share a key/value
+// head and take one pass over its keys together, C = 16, 32 or 64 rows to an item.  With so
+// few rows the cache's bytes bound the pass (16 operations a byte at 8 rows and d = 128, too
+// many for the CUDA cores, few for the tensor cores), so nothing is done to a code but to
+// load it: TMA copies pages into shared memory and tcgen05 (kind::f8f6f4) multiplies them
+// as they are.  The products are transposed, keys and channels on the 128 rows of an MMA
+// tile, the few query rows on its columns:
+//   S^T [128 keys x C] = K [128 x d] Q^T         K as stored, K-major
+//   O^T [d x C]       += V^T [d x 128] P^T       V as stored, read MN-major
+// so that a tile costs 128 x C products, every lane of a softmax warp has a key of its own
+// (with its own scales, mask and page), and the running maxima are over lanes.
+//
+// Exactness.  The 8-bit products are exact and summed in fp32, but q and P have more bits
+// than a code, so each goes in as a sum of codes:
+//   q   each row times a power of two, so that its largest element is in (224, 448], as 2
+//       (bf16) or 3 (fp16) e4m3 pieces of 4 bits, each piece the rounding of what the ones
+//       before it left: exact down to 2^-18 of the row's largest element;
+//   P   as fp16 (11 bits), cut into e5m2 pieces of 3 bits (the high byte of an fp16 number
+//       is an e5m2 number): 3 pieces for bf16 outputs, the last one rounded (9 bits, one
+//       more than bf16 holds), 4 for fp16 (all 11).  e5m2 rather than e4m3 because long
+//       contexts need its range: weights are kept down to 2^-31 of the largest.
+// V's scale joins the exponent: with t_j = s_j + log2(v_scale_j) and M the running maximum
+// of t, the weights 2^(t_j - M) are at most 1 whatever the scales, and the sum of the
+// probabilities is that of 2^(t_j - M) / v_scale_j.
+//
+// Work split.  The key tiles of all items (request, key/value head, C rows) lie one behind
+// the other and every CTA, one per SM, takes an equal share of them (kItemCost more tiles
+// stand for an item's fixed cost), wherever items begin and end; a CTA's share begins and
+// ends inside at most two items, whose parts go to the workspace, and a second small
+// kernel, launched with this one (programmatic dependence), joins them.  All lengths are
+// read on the device, and the CTAs find their shares themselves.
+//
+// One CTA: 12 warps,
+//   warp 0       producer: pages by TMA, the tile's 16 scales by 4-byte asynchronous copies
+//   warp 1       tcgen05 issuer; owns the TMEM allocation
+//   warps 2, 3   the items' queries: scaled, cut into pieces, into shared memory
+//   warps 4..7, 8..11   two softmax groups: a lane has a key.  They take the tiles in turn,
+//                each with its own maxima, sums and O^T, put together at the end of a part.
 #include "fa_kernels.h"
 #include "fa_ptx.cuh"
 #include "fa_seq.cuh"
 
+#include <algorithm>
 #include <climits>
 
 namespace fa {
@@ -11,114 +51,1026 @@ namespace {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kKeys = 128;          // keys of a tile
+constexpr int kItemCost = 1;        // an item's fixed cost in tiles
+// Weights are at most 1 before this factor 2^15 (and 2^15 < 65504, fp16's largest).
+constexpr float kShift = 15.f;
+constexpr int kWindow = 128;        // requests whose lengths a CTA keeps in shared memory
+constexpr int kThreads = 384;
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(code));
-    return unpack2<kElemF16>(h).x;
+// --------------------------------------------------------------- work distribution
+
+struct Request {
+    int start, n;   // new tokens
+    int len;        // tokens in the cache, the new ones among them
+};
+
+__device__ __forceinline__ Request load_request(const Kv8FwdParams& p, int b) {
+    Request r;
+    seq_bounds(p.seq, b, r.start, r.n);
+    const long long room = static_cast<long long>(p.width) << p.page_log2;
+    r.len = static_cast<int>(min(max(static_cast<long long>(__ldg(p.lens + b)), 0LL), room));
+    return r;
 }
 
-// One warp per (new token, query head): lanes take keys for the scores, channels for the
-// sum over the values; the running maximum and sum of the online softmax are the warp's.
-template <int D, int E>
-__global__ void __launch_bounds__(128) fa_fwd_kv8_kernel(const Kv8FwdParams p) {
-    __shared__ float sq[4][D];
-    const SeqInfo& s = p.seq;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * 4 + warp;
-    const int h = static_cast<int>(item % s.Hq);
-    const long long t = item / s.Hq;
-    if (t >= s.total_tokens) return;
-    int b, first, n;
-    if (s.cu_seqlens) {
-        int lo = 0, hi = s.B;   // the first request that ends behind t
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s.cu_seqlens[mid + 1] > t) hi = mid;
-            else lo = mid + 1;
+// A request's items: `blocks` blocks of C rows for each key/value head, each with room for
+// `tiles` key tiles (the most that one of its blocks sees) and the fixed cost.
+struct Items {
+    int blocks;
+    int cost;   // units of an item
+};
+
+template <int C>
+__device__ __forceinline__ Items items_of(const Kv8FwdParams& p, const Request& r) {
+    Items it;
+    it.blocks = (r.n * p.seq.group + C - 1) / C;
+    int tiles = (r.len + kKeys - 1) / kKeys;
+    if (p.seq.window > 0) {
+        // a block's rows see window + (its tokens - 1) consecutive keys at most
+        const long long span = static_cast<long long>(p.seq.window) + (C - 1) / p.seq.group + 1;
+        tiles = static_cast<int>(min(static_cast<long long>(tiles), (span + kKeys - 2) / kKeys + 1));
+    }
+    it.cost = tiles + kItemCost;
+    return it;
+}
+
+// CTA c of G takes units [c total / G, (c + 1) total / G) of `total`.
+__device__ __forceinline__ long long share_begin(long long total, int c, int G) { return total * c / G; }
+__device__ __forceinline__ int share_of(long long total, long long unit, int G) {
+    return static_cast<int>(((unit + 1) * G - 1) / total);
+}
+
+// One CTA's part of an item.
+struct Part {
+    Request req;
+    int b, h, row0;     // request, key/value head, first row
+    int tile0, tiles;   // the part's key tiles (absolute), tiles may be 0: rows that see nothing
+    bool whole;         // all of the item's tiles
+    bool begins;        // the item's first tile is the part's
+    long long unit0;    // the item's first unit
+    int item_tiles;
+    int lo_key, hi_key; // the keys that any row of the item sees: [lo_key, hi_key]
+    int all_lo, all_hi; // the keys that every row sees
+};
+
+// Where a CTA's share begins, found by all its threads; and the requests from there on.
+struct Share {
+    long long begin, end, total;
+    long long offset;     // of `begin` within request b0's units
+    int b0;
+};
+
+// A walk over a CTA's parts; every role of the CTA walks for itself.
+template <int C>
+struct Walk {
+    const Kv8FwdParams& p;
+    const int3* window;   // (start, n, len) of requests b0 .. b0 + kWindow - 1, in shared memory
+    int b0, b;
+    long long at, left, unit;   // position within request b's units, units left, absolute unit
+    Request req;
+    Items it;
+
+    __device__ Walk(const Kv8FwdParams& p_, const Share& s, const int3* w)
+        : p(p_), window(w), b0(s.b0), b(s.b0), at(s.offset), left(s.end - s.begin), unit(s.begin) {
+        load();
+    }
+    __device__ void load() {
+        if (b >= p.seq.B) return;
+        if (b - b0 < kWindow) {
+            const int3 w = window[b - b0];
+            req.start = w.x;
+            req.n = w.y;
+            req.len = w.z;
+        } else {
+            req = load_request(p, b);
         }
-        if (lo == s.B) return;
-        b = lo;
-        first = s.cu_seqlens[b];
-        n = s.cu_seqlens[b + 1] - first;
+        it = items_of<C>(p, req);
+    }
+    __device__ bool next(Part& part) {
+        while (left > 0 && b < p.seq.B) {
+            const long long units = static_cast<long long>(it.blocks) * p.seq.Hkv * it.cost;
+            if (at >= units) {
+                ++b;
+                at = 0;
+                load();
+                continue;
+            }
+            const long long item = at / it.cost;
+            const int off = static_cast<int>(at - item * it.cost);
+            const int take = static_cast<int>(min(left, static_cast<long long>(it.cost - off)));
+            part.unit0 = unit - off;
+            at += take;
+            left -= take;
+            unit += take;
+            part.req = req;
+            part.b = b;
+            part.h = static_cast<int>(item / it.blocks);
+            part.row0 = static_cast<int>(item - static_cast<long long>(part.h) * it.blocks) * C;
+            // positions of the block's first and last token
+            const int G = p.seq.group;
+            const int first = req.len - req.n + part.row0 / G;
+            const int last = req.len - req.n + min((part.row0 + C - 1) / G, req.n - 1);
+            const bool win = p.seq.window > 0;
+            part.hi_key = p.seq.causal ? last : req.len - 1;
+            part.all_hi = p.seq.causal ? first : req.len - 1;
+            part.lo_key = win ? max(first - p.seq.window + 1, 0) : 0;
+            part.all_lo = win ? max(last - p.seq.window + 1, 0) : 0;
+            const int base = part.lo_key / kKeys;
+            part.item_tiles = part.hi_key >= part.lo_key ? part.hi_key / kKeys - base + 1 : 0;
+            const int t1 = min(off + take, part.item_tiles);
+            part.tile0 = base + off;
+            part.tiles = max(t1 - off, 0);
+            part.begins = off == 0;
+            part.whole = part.begins && t1 == part.item_tiles;
+            if (part.tiles > 0 || part.whole) return true;
+        }
+        return false;
+    }
+};
+
+// --------------------------------------------------------------------- configuration
+
+template <int D, int E, int C>
+struct Kv8Cfg {
+    static constexpr int kQ = E == kElemBf16 ? 2 : 3;    // pieces of q
+    static constexpr int kP = E == kElemBf16 ? 3 : 4;    // pieces of P
+    // With few columns an MMA costs the reading of its 128 rows, so the pieces of q and of P
+    // go side by side into one MMA of more columns and are added up when read; with 64
+    // columns (and no TMEM for more) they are added up by the tensor cores, one MMA each.
+    static constexpr bool kWide = C <= 32;
+    static constexpr int kSCols = kWide ? kQ * C : C;
+    static constexpr int kOCols = kWide ? kP * C : C;
+    static constexpr int kTmemUsed = 2 * (kSCols + kOCols);
+    static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    static_assert(kTmemUsed <= 512, "TMEM columns");
+    static constexpr int kSide = kKeys * D;              // K or V of a tile
+    static constexpr int kStageBytes = 2 * kSide;
+    static constexpr int kQBytes = kQ * C * D;           // one item's queries
+    static constexpr int kPBytes = kP * C * kKeys;       // one group's weights
+    static constexpr int kSwizzle = D == 128 ? 2 : 4;    // descriptor code of the D-byte swizzle
+    static constexpr int kGroup = 8 * D;                 // bytes of 8 rows
+};
+
+constexpr int kMaxStages = 12;
+
+template <int C>
+struct Kv8Smem {   // behind the tiles
+    float scales[kMaxStages][16];    // of the stage's tile: K's 8 blocks, V's 8 (V < 0: hidden)
+    float q_scale[2][C];
+    int row_pos[2][C];               // position of the row's token; INT_MIN: no row
+    float wmax[2][2][4][C];          // [group][tile parity][warp]
+    alignas(16) float ref[8][C];     // [softmax warp]
+    alignas(16) float fac[8][C];
+    float part_sum[2][4][C];         // [group][warp]
+    float2 stat[2][C];               // [group]: reference, sum
+    int3 window[kWindow];
+    Share share;
+    long long warp_sums[kThreads / 32];
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], pv_done[2];
+    uint64_t all_done;
+    uint32_t tmem;
+    int abort;
+    int poison[2];                   // NaN found among values that only some rows see
+};
+
+template <int D, int E, int C>
+constexpr int kv8_stages() {
+    using K = Kv8Cfg<D, E, C>;
+    const int left = 232448 - 1024 - 2 * K::kQBytes - 2 * K::kPBytes - static_cast<int>(sizeof(Kv8Smem<C>));
+    const int n = left / K::kStageBytes;
+    return n < kMaxStages ? n : kMaxStages;
+}
+
+template <int D, int E, int C>
+constexpr int kv8_smem_bytes() {
+    using K = Kv8Cfg<D, E, C>;
+    return 1024 + kv8_stages<D, E, C>() * K::kStageBytes + 2 * K::kQBytes + 2 * K::kPBytes +
+           static_cast<int>(sizeof(Kv8Smem<C>));
+}
+
+// named barriers (0 is __syncthreads)
+constexpr int kBarP = 1;      // + group: weights written; the group and the issuer
+constexpr int kBarMax = 3;    // + group: the warps' maxima written
+constexpr int kBarEnd = 5;    // both groups: a part's statistics written
+constexpr int kBarFree = 6;   // both groups: the accumulators have been read
+
+// The 16-byte unit u of row r in a tile of rows of D bytes, swizzled over D bytes.
+template <int D>
+__device__ __forceinline__ int unit_offset(int r, int u) {
+    return r * D + ((u ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 16 TMEM columns, several sets `stride` columns apart added up.
+template <int SETS>
+__device__ __forceinline__ void load_sum16(uint32_t addr, int stride, float (&v)[16]) {
+    uint32_t r[SETS][16];
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) tmem_ld16(addr + i * stride, r[i]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) reg_fence(r[i]);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        v[c] = __uint_as_float(r[0][c]);
+#pragma unroll
+        for (int i = 1; i < SETS; ++i) v[c] += __uint_as_float(r[i][c]);
+    }
+}
+
+// Sums of v[0 .. N) over the warp's lanes, by halving: lane l ends with the sums of column
+// l / 2 (N = 16, v[0]), l (N = 32, v[0]) or 2 l and 2 l + 1 (N = 64, v[0] and v[1]).
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
+    int width = N;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (width > 1) {
+            // the upper half of the lanes keeps the upper half of the columns
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i < width / 2) {
+                    const float give = up ? v[i] : v[i + width / 2];
+                    const float keep = up ? v[i + width / 2] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            }
+            width /= 2;
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+}
+
+// Exponent of the power of two that brings a row's largest magnitude into (224, 448].
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
+    const int e = static_cast<int>(amax_bits >> 23) - 127;
+    return max(e - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+}
+
+__device__ __forceinline__ float pow2f(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+
+// The e4m3 values that pack4_e4m3 gives for four floats, as floats.
+__device__ __forceinline__ void e4m3_floats(uint32_t w, float (&f)[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+    const float2 x = unpack2<kElemF16>(lo), y = unpack2<kElemF16>(hi);
+    f[0] = x.x;
+    f[1] = x.y;
+    f[2] = y.x;
+    f[3] = y.y;
+}
+
+// 8 TMEM columns, several sets added up.
+template <int SETS>
+__device__ __forceinline__ void load_sum8(uint32_t addr, int stride, float (&v)[8]) {
+    uint32_t r[SETS][8];
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[i][0]), "=r"(r[i][1]), "=r"(r[i][2]), "=r"(r[i][3]), "=r"(r[i][4]),
+                       "=r"(r[i][5]), "=r"(r[i][6]), "=r"(r[i][7])
+                     : "r"(addr + i * stride));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) reg_fence(r[i]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        v[c] = __uint_as_float(r[0][c]);
+#pragma unroll
+        for (int i = 1; i < SETS; ++i) v[c] += __uint_as_float(r[i][c]);
+    }
+}
+
+// Bytes of a word that are e4m3 NaN (0x7f or 0xff), as 0x80 in each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Finds this CTA's share: sums of the requests' units, by all threads.
+template <int C>
+__device__ __forceinline__ long long block_units(long long v, long long* warp_sums, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const long long x = warp_sums[w];
+        if (w < warp) before += x;
+        all += x;
+    }
+    *total = all;
+    return v + before;
+}
+
+template <int C>
+__device__ __forceinline__ long long units_of(const Kv8FwdParams& p, int b) {
+    if (b >= p.seq.B) return 0;
+    const Items it = items_of<C>(p, load_request(p, b));
+    return static_cast<long long>(it.blocks) * p.seq.Hkv * it.cost;
+}
+
+template <int C>
+__device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm) {
+    const int cta = blockIdx.x, G = gridDim.x, B = p.seq.B;
+    const long long first = units_of<C>(p, threadIdx.x);
+    long long sum = first;
+    for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units_of<C>(p, b);
+    long long total;
+    long long upto = block_units<C>(sum, sm.warp_sums, &total);
+    const long long begin = share_begin(total, cta, G);
+    if (threadIdx.x == 0) {
+        sm.share.begin = begin;
+        sm.share.end = share_begin(total, cta + 1, G);
+        sm.share.total = total;
+    }
+    auto look = [&](int b, long long mine, long long end) {
+        if (begin >= end - mine && begin < end) {
+            sm.share.b0 = b;
+            sm.share.offset = begin - (end - mine);
+        }
+    };
+    if (B <= kThreads) {
+        look(threadIdx.x, first, upto);
     } else {
-        b = static_cast<int>(t / s.N);
-        first = b * s.N;
-        n = s.N;
-    }
-    const int page = 1 << p.page_log2;
-    const int len = static_cast<int>(min(max(static_cast<long long>(p.lens[b]), 0LL),
-                                         static_cast<long long>(p.width) << p.page_log2));
-    const int pos = len - n + static_cast<int>(t - first);
-    const int hi = s.causal ? pos : len - 1;
-    const int lo = s.causal && s.window > 0 ? max(pos - s.window + 1, 0) : 0;
-    const int g = h / s.group;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.q_stride + h * D;
-    for (int c = lane; c < D; c += 32)
-        sq[warp][c] = E == kElemBf16 ? __uint_as_float(static_cast<uint32_t>(q[c]) << 16)
-                                     : unpack2<kElemF16>(q[c]).x;
-    __syncwarp();
-    float m = kNegInf, l = 0.f, o[D / 32];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
-    for (int j0 = lo / 32 * 32; j0 <= hi; j0 += 32) {
-        const int j = j0 + lane;
-        long long row = -1;
-        if (j >= lo && j <= hi) {
-            const int id = p.table[static_cast<long long>(b) * p.width + (j >> p.page_log2)];
-            if (id >= 0 && id < p.num_pages)
-                row = ((static_cast<long long>(id) * s.Hkv + g) << p.page_log2) + (j & (page - 1));
-        }
-        float x = kNegInf, vs = 0.f;
-        if (row >= 0) {
-            const uint8_t* k = p.k8 + row * D;
-            float dot = 0.f;
-            for (int c = 0; c < D; ++c) dot += sq[warp][c] * e4m3_value(k[c]);
-            x = dot * p.k_scale[row / kKv8Block] * p.scale_log2;
-            vs = p.v_scale[row / kKv8Block];
-        }
-        float top = m;
-#pragma unroll
-        for (int w = 0; w < 32; ++w) top = fmaxf(top, __shfl_sync(0xffffffffu, x, w));
-        const float ref = top == kNegInf ? 0.f : top;
-        const float w = exp2f(x - ref);
-        const float f = exp2f(m - ref);
-        m = top;
-        l *= f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) o[c] *= f;
-        for (int u = 0; u < 32; ++u) {
-            const long long r = __shfl_sync(0xffffffffu, row, u);
-            const float wu = __shfl_sync(0xffffffffu, w, u), su = __shfl_sync(0xffffffffu, vs, u);
-            if (r < 0) continue;
-            l += wu;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] += wu * su * e4m3_value(p.v8[r * D + lane + 32 * c]);
+        long long before = 0;
+        for (int b0 = 0; b0 < B; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            const long long mine = units_of<C>(p, b);
+            long long all;
+            upto = before + block_units<C>(mine, sm.warp_sums, &all);
+            look(b, mine, upto);
+            before += all;
         }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;   // (NaN divides on)
-    uint16_t* out = static_cast<uint16_t*>(p.o) + (t * s.Hq + h) * D;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-        out[lane + 32 * c] = static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
-    if (lane == 0) {
-        const long long at = s.cu_seqlens ? static_cast<long long>(h) * s.total_tokens + t
-                                          : (static_cast<long long>(b) * s.Hq + h) * s.N + (t - first);
-        p.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+    __syncthreads();
+}
+
+template <int D, int E, int C>
+__global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_constant__ Kv8FwdParams p) {
+    using K = Kv8Cfg<D, E, C>;
+    constexpr int kStages = kv8_stages<D, E, C>();
+    static_assert(kStages >= 3, "ring of key/value tiles");
+    // S^T: K e4m3 (K-major) times q's pieces e4m3 (K-major); O^T: V e4m3 (MN-major) times P's
+    // pieces e5m2 (MN-major; operand format code 1)
+    constexpr uint32_t kIdescS = idesc_f32acc(kKeys, K::kSCols, false, false, kElemFp8);
+    constexpr uint32_t kIdescO = idesc_f32acc(128, K::kOCols, true, true, kElemFp8) | (1u << 10);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sKV = smem;                                  // [stages][K, V]
+    uint8_t* sQ = smem + kStages * K::kStageBytes;        // [2][pieces][C][D]
+    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [2][pieces][C / 16][keys][16]
+    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + 2 * K::kPBytes);
+    volatile int* abort_flag = &sm.abort;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    grid_launch_dependents();
+
+    find_share<C>(p, sm);
+    if (sm.share.begin == sm.share.end) {
+        if (threadIdx.x == 0) p.joins[blockIdx.x].last = 0;
+        return;
     }
+    if (threadIdx.x < kWindow) {
+        const int b = sm.share.b0 + threadIdx.x;
+        Request r{0, 0, 0};
+        if (b < p.seq.B) r = load_request(p, b);
+        sm.window[threadIdx.x] = make_int3(r.start, r.n, r.len);
+    }
+    if (threadIdx.x == 0) {
+        sm.abort = 0;
+        sm.poison[0] = sm.poison[1] = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_addr(&sm.kv_full[i]), 33);   // 32 lanes and the bytes' announcement
+            mbar_init(smem_addr(&sm.kv_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sm.q_full[i]), 64);
+            mbar_init(smem_addr(&sm.q_empty[i]), 9);    // the last S^T of the part, 8 softmax warps
+            mbar_init(smem_addr(&sm.s_full[i]), 1);
+            mbar_init(smem_addr(&sm.pv_done[i]), 1);
+        }
+        mbar_init(smem_addr(&sm.all_done), 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&sm.tmem), K::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t colO = tmem + 2 * K::kSCols;
+
+    auto wait = [&](uint64_t* bar, int phase) {
+        return mbar_wait(smem_addr(bar), phase & 1, abort_flag, p.timeout_cycles, p.status);
+    };
+    Walk<C> walk(p, sm.share, sm.window);
+    Part part;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- producer
+        if (lane == 0) {
+            tma_prefetch_desc(&p.tm_k);
+            tma_prefetch_desc(&p.tm_v);
+        }
+        const int page = 1 << p.page_log2, per_tile = kKeys >> p.page_log2;
+        const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
+        const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
+        int c = 0;
+        bool ok = true;
+        while (ok && walk.next(part)) {
+            const int* row = p.table + static_cast<long long>(part.b) * p.width;
+            const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
+            const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
+            // the table's entries, 32 at a time, the next ones on their way
+            int base = part.tile0 * per_tile;
+            auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
+            int cur = part.tiles > 0 ? entry(base + lane) : -1;
+            int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
+            for (int i = 0; i < part.tiles; ++i, ++c) {
+                const int tile = part.tile0 + i;
+                const int st = c % kStages, use = c / kStages;
+                if (tile * per_tile >= base + 32) {
+                    base += 32;
+                    cur = nxt;
+                    nxt = entry(base + 32 + lane);
+                }
+                if (use > 0) {
+                    ok = __all_sync(0xffffffffu, wait(&sm.kv_empty[st], use - 1));
+                    if (!ok) break;
+                }
+                uint8_t* dst = sKV + st * K::kStageBytes;
+                const uint32_t full = smem_addr(&sm.kv_full[st]);
+                const int first = tile * per_tile - base;
+                // this lane's page of the tile
+                const int id = __shfl_sync(0xffffffffu, cur, (first + (lane & (per_tile - 1))) & 31);
+                const bool load = lane < per_tile && id >= 0 && id < p.num_pages;
+                const int pages = __popc(__ballot_sync(0xffffffffu, load));
+                if (lane == 0) mbar_arrive_expect_tx(full, pages * 2 * page * D);
+                __syncwarp();
+                if (load) {
+                    tma_load_3d(smem_addr(dst + lane * page * D), &p.tm_k, full, 0, 0,
+                                id * p.seq.Hkv + part.h);
+                    tma_load_3d(smem_addr(dst + K::kSide + lane * page * D), &p.tm_v, full, 0, 0,
+                                id * p.seq.Hkv + part.h);
+                }
+                // the scales of the tile's 8 blocks
+                const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
+                bool plain = true;
+                if (lane < 16) {
+                    float* to = &sm.scales[st][lane];
+                    if (sid >= 0 && sid < p.num_pages && tile * kKeys + side_blk * kKv8Block < lim) {
+                        const long long at =
+                            ((static_cast<long long>(sid) * p.seq.Hkv + part.h) << blocks_log2) +
+                            (side_blk & ((1 << blocks_log2) - 1));
+                        cp_async4(smem_addr(to), (lane < 8 ? p.k_scale : p.v_scale) + at);
+                        plain = false;
+                    } else {
+                        *to = lane < 8 ? 0.f : -1.f;   // hidden
+                    }
+                }
+                if (plain) mbar_arrive(full);
+                else cp_async_arrive(full);
+            }
+        }
+        // every copy lands before the CTA exits, whatever became of the other roles
+        for (int i = max(0, c - kStages); i < c; ++i)
+            mbar_wait_drain(smem_addr(&sm.kv_full[i % kStages]), (i / kStages) & 1, kDrainCycles);
+    } else if (warp == 1) {
+        // --------------------------------------------------------------- issuer
+        // After an abort it goes on issuing on stale data, so that every barrier's phases
+        // still complete.
+        int c = 0, np = 0;
+        const uint64_t kd0 = sdesc<K::kSwizzle>(smem_addr(sKV), 16, K::kGroup);
+        // V: 16 or 8 groups of 8 keys; the second half of the 128 rows of the product at
+        // d = 64 reads the next keys' channels and is not used
+        const uint64_t vd0 = sdesc<K::kSwizzle>(smem_addr(sKV + K::kSide), K::kGroup, K::kGroup);
+        const uint64_t qd0 = sdesc<K::kSwizzle>(smem_addr(sQ), 16, K::kGroup);
+        const uint64_t pd0 = sdesc<0>(smem_addr(sP), 128, kKeys * 16);
+        while (walk.next(part)) {
+            if (part.tiles == 0) {
+                // (its queries are laid out all the same)
+                if (lane == 0) {
+                    wait(&sm.q_full[np & 1], np >> 1);
+                    mma_commit(smem_addr(&sm.q_empty[np & 1]));
+                }
+                __syncwarp();
+                ++np;
+                continue;
+            }
+            auto issue_s = [&](int i) {   // lane 0
+                const int st = (c + i) % kStages, g = (c + i) & 1;
+                wait(&sm.kv_full[st], (c + i) / kStages);
+                tc_fence_after();
+                const uint64_t kd = kd0 + static_cast<uint64_t>((st * K::kStageBytes) >> 4);
+                const uint64_t qd = qd0 + static_cast<uint64_t>(((np & 1) * K::kQBytes) >> 4);
+#pragma unroll
+                for (int q = 0; q < (K::kWide ? 1 : K::kQ); ++q)
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_ss_f8(tmem + g * K::kSCols, kd + 2 * kk, qd + ((q * C * D) >> 4) + 2 * kk,
+                                  kIdescS, (q > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(smem_addr(&sm.s_full[g]));
+                if (i == part.tiles - 1) mma_commit(smem_addr(&sm.q_empty[np & 1]));
+            };
+            if (lane == 0) {
+                wait(&sm.q_full[np & 1], np >> 1);
+                issue_s(0);
+                if (part.tiles > 1) issue_s(1);
+            }
+            __syncwarp();
+            for (int i = 0; i < part.tiles; ++i) {
+                const int st = (c + i) % kStages, g = (c + i) & 1;
+                named_bar_sync(kBarP + g, 160);
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint64_t vd = vd0 + static_cast<uint64_t>((st * K::kStageBytes) >> 4);
+                    const uint64_t pd = pd0 + static_cast<uint64_t>((g * K::kPBytes) >> 4);
+#pragma unroll
+                    for (int q = 0; q < (K::kWide ? 1 : K::kP); ++q)
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 32; ++kk)
+                            mma_ss_f8(colO + g * K::kOCols, vd + ((kk * 32 * D) >> 4),
+                                      pd + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
+                                      (i >= 2 || q > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(smem_addr(&sm.pv_done[g]));
+                    mma_commit(smem_addr(&sm.kv_empty[st]));
+                    if (i + 2 < part.tiles) issue_s(i + 2);
+                }
+                __syncwarp();
+            }
+            c += part.tiles;
+            ++np;
+        }
+        if (lane == 0) {
+            mma_commit(smem_addr(&sm.all_done));
+            mbar_wait_drain(smem_addr(&sm.all_done), 0, kDrainCycles);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // -------------------------------------------------------------- queries
+        constexpr int kLanes = D / 8;         // threads of a row
+        constexpr int kRows = 64 / kLanes;    // rows at a time
+        const int t = threadIdx.x - 64, sub = t % kLanes;
+        int np = 0;
+        bool joined = false, ok = true;
+        while (walk.next(part)) {
+            if (t == 0 && part.begins && !part.whole) {
+                Kv8Join j;
+                j.last = share_of(sm.share.total, part.unit0 + part.item_tiles - 1, gridDim.x);
+                j.b = part.b;
+                j.h = part.h;
+                j.start = part.req.start;
+                j.n = part.req.n;
+                j.row0 = part.row0;
+                j.total = sm.share.total;
+                p.joins[blockIdx.x] = j;
+                joined = true;
+            }
+            const int buf = np & 1;
+            if (np >= 2) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty[buf], (np >> 1) - 1));
+            if (ok) {
+                uint8_t* dst = sQ + buf * K::kQBytes;
+                const int G = p.seq.group, rows = part.req.n * G;
+#pragma unroll 4
+                for (int n = t / kLanes; n < C; n += kRows) {
+                    const int r = part.row0 + n;
+                    const int tok = r / G, head = part.h * G + r % G;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (r < rows)
+                        w = __ldg(reinterpret_cast<const uint4*>(
+                            static_cast<const uint16_t*>(p.q) +
+                            static_cast<long long>(part.req.start + tok) * p.q_stride + head * D + sub * 8));
+                    float x[8];
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = unpack2<E>(u[j]);
+                        x[2 * j] = f.x;
+                        x[2 * j + 1] = f.y;
+                        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+                    }
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // an infinity or NaN makes the row NaN, through its scale
+                    const bool fine = top < 0x7f800000u;
+                    const int k = fine ? row_exponent(top) : 0;
+                    const float inv = fine ? pow2f(-k) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = fine ? x[j] * inv : 0.f;
+                    if (sub == 0) {
+                        sm.q_scale[buf][n] = fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
+                        sm.row_pos[buf][n] = r < rows ? part.req.len - part.req.n + tok : INT_MIN;
+                    }
+#pragma unroll
+                    for (int q = 0; q < K::kQ; ++q) {
+                        uint32_t codes[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            codes[j] = pack4_e4m3(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                            float f[4];
+                            e4m3_floats(codes[j], f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[4 * j + i] -= f[i];
+                        }
+                        *reinterpret_cast<uint2*>(dst + unit_offset<D>(q * C + n, sub >> 1) + (sub & 1) * 8) =
+                            make_uint2(codes[0], codes[1]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_addr(&sm.q_full[buf]));
+            ++np;
+        }
+        if (t == 0 && !joined) p.joins[blockIdx.x].last = 0;
+    } else {
+        // -------------------------------------------------------------- softmax
+        const int grp = (warp - 4) / 4, quad = warp % 4, key = quad * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_addr + grp * K::kSCols;
+        const uint32_t tO = colO + lane_addr + grp * K::kOCols;
+        uint8_t* myP = sP + grp * K::kPBytes + key * 16;
+        constexpr int kOwn = C == 64 ? 2 : 1;   // columns whose reference this lane keeps
+        const int G = p.seq.group;
+        int c = 0, np = 0, ns = 0, npv = 0;
+        bool ok = true;
+        while (walk.next(part)) {
+            const int buf = np & 1;
+            ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full[buf], np >> 1));
+            float l[C], ref[kOwn];
+#pragma unroll
+            for (int n = 0; n < C; ++n) l[n] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) ref[i] = kNegInf;
+            const int nrows = min(C, part.req.n * G - part.row0);
+            bool fresh = true;
+            for (int i = ((c & 1) != grp) ? 1 : 0; i < part.tiles; i += 2) {
+                const int st = (c + i) % kStages;
+                if (ok)
+                    ok = __all_sync(0xffffffffu, wait(&sm.kv_full[st], (c + i) / kStages) &&
+                                                     wait(&sm.s_full[grp], ns));
+                ++ns;
+                float t[C], inv_vs = 0.f;
+                if (ok) {
+                    tc_fence_after();
+                    const int kb = (part.tile0 + i) * kKeys, pos = kb + key;
+                    float ks = sm.scales[st][key / 16], vs = sm.scales[st][8 + key / 16];
+                    const bool hidden = vs < 0.f || pos < part.lo_key || pos > part.hi_key ||
+                                        pos >= part.req.len;
+                    const bool edge = kb < part.all_lo || kb + kKeys - 1 > part.all_hi;
+                    if (hidden) {
+                        ks = 0.f;
+                        vs = 1.f;
+                    }
+                    const uint32_t vb = __float_as_uint(vs);
+                    const float lvs = (vb & 0x7fffffu) == 0 && vb >= 0x00800000u
+                                          ? static_cast<float>(static_cast<int>(vb >> 23) - 127)
+                                          : log2f(vs);
+                    inv_vs = 1.f / vs;
+                    const float kc = ks * p.scale_log2;
+#pragma unroll
+                    for (int cc = 0; cc < C / 16; ++cc) {
+                        float v[16];
+                        load_sum16<K::kWide ? K::kQ : 1>(tS + cc * 16, C, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            t[cc * 16 + j] = fmaf(v[j], kc * sm.q_scale[buf][cc * 16 + j], lvs);
+                    }
+                    tc_fence_before();
+                    const bool some = !hidden && (pos < part.all_lo || pos > part.all_hi);
+                    if (edge || __any_sync(0xffffffffu, hidden)) {
+#pragma unroll
+                        for (int n = 0; n < C; ++n) {
+                            const int rp = sm.row_pos[buf][n];
+                            const bool see = !hidden && (!p.seq.causal ||
+                                                         (pos <= rp && (p.seq.window <= 0 || rp - pos < p.seq.window)));
+                            if (!see) t[n] = kNegInf;
+                        }
+                        // 0 * NaN is NaN: no row's product may meet a NaN that it does not see
+                        uint4* vrow = reinterpret_cast<uint4*>(sKV + st * K::kStageBytes + K::kSide + key * D);
+                        if (hidden) {
+#pragma unroll
+                            for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0, 0, 0, 0);
+                        } else if (some) {
+#pragma unroll
+                            for (int u = 0; u < D / 16; ++u) {
+                                uint4 w = vrow[u];
+                                const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), e = nan_bytes(w.z),
+                                               f = nan_bytes(w.w);
+                                if (a | b | e | f) {
+                                    // those channels become NaN at the part's end, for the rows that see them
+                                    w.x &= ~(a | (a - (a >> 7)));
+                                    w.y &= ~(b | (b - (b >> 7)));
+                                    w.z &= ~(e | (e - (e >> 7)));
+                                    w.w &= ~(f | (f - (f >> 7)));
+                                    vrow[u] = w;
+                                    sm.poison[buf] = 1;
+                                }
+                            }
+                        }
+                    }
+                    float mine[kOwn];
+#pragma unroll
+                    for (int i2 = 0; i2 < kOwn; ++i2) mine[i2] = kNegInf;
+#pragma unroll
+                    for (int n = 0; n < C; ++n) {
+                        const float m = warp_max(t[n]);
+                        if (lane == (n & 31)) mine[n / 32] = m;
+                    }
+#pragma unroll
+                    for (int i2 = 0; i2 < kOwn; ++i2)
+                        if (lane + 32 * i2 < C) sm.wmax[grp][ns & 1][quad][lane + 32 * i2] = mine[i2];
+                }
+                named_bar_sync(kBarMax + grp, 128);
+                if (ok) {
+                    // every warp of the group comes to the same references
+                    bool moved = false;
+#pragma unroll
+                    for (int i2 = 0; i2 < kOwn; ++i2) {
+                        const int n = lane + 32 * i2;
+                        if (n < C) {
+                            const auto& wm = sm.wmax[grp][ns & 1];
+                            const float m = fmaxf(fmaxf(wm[0][n], wm[1][n]), fmaxf(wm[2][n], wm[3][n]));
+                            float f = 1.f;
+                            if (m > ref[i2]) {
+                                f = ex2_approx(ref[i2] - m);
+                                ref[i2] = m;
+                                moved = true;
+                            }
+                            sm.fac[warp - 4][n] = f;
+                            sm.ref[warp - 4][n] = (ref[i2] == kNegInf ? 0.f : ref[i2]) - kShift;
+                        }
+                    }
+                    moved = __any_sync(0xffffffffu, moved);
+                    __syncwarp();
+                    // the group's last product has read its weights and left its sums
+                    if (npv > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done[grp], npv - 1));
+                    if (ok) {
+                        if (moved && !fresh) {
+                            tc_fence_after();
+#pragma unroll
+                            for (int n = 0; n < C; ++n) l[n] *= sm.fac[warp - 4][n];
+#pragma unroll
+                            for (int cc = 0; cc < K::kOCols / 16; ++cc) {
+                                uint32_t r[16];
+                                tmem_ld16(tO + cc * 16, r);
+                                tmem_ld_wait();
+                                reg_fence(r);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    r[j] = __float_as_uint(__uint_as_float(r[j]) *
+                                                           sm.fac[warp - 4][(cc * 16 + j) % C]);
+                                tmem_st16(tO + cc * 16, r);
+                            }
+                            tmem_st_wait();
+                        }
+#pragma unroll
+                        for (int cc = 0; cc < C / 16; ++cc) {
+                            uint32_t h[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int n = cc * 16 + 2 * j;
+                                const float w0 = ex2_approx(t[n] - sm.ref[warp - 4][n]);
+                                const float w1 = ex2_approx(t[n + 1] - sm.ref[warp - 4][n + 1]);
+                                l[n] = fmaf(w0, inv_vs, l[n]);
+                                l[n + 1] = fmaf(w1, inv_vs, l[n + 1]);
+                                h[j] = pack2<kElemF16>(w0, w1);
+                            }
+#pragma unroll
+                            for (int q = 0; q < K::kP; ++q) {
+                                // the last of 3 pieces is rounded, the others (and the fourth,
+                                // which is all that is left) are the leading bits
+                                if (q == 2 && K::kP == 3)
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) h[j] += 0x00800080u;
+                                uint4 w;
+                                w.x = __byte_perm(h[0], h[1], 0x7531);
+                                w.y = __byte_perm(h[2], h[3], 0x7531);
+                                w.z = __byte_perm(h[4], h[5], 0x7531);
+                                w.w = __byte_perm(h[6], h[7], 0x7531);
+                                *reinterpret_cast<uint4*>(myP + (q * (C / 16) + cc) * kKeys * 16) = w;
+                                if (q + 1 < K::kP)
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
+                            }
+                        }
+                        tc_fence_before();
+                        fence_proxy_async_smem();
+                    }
+                }
+                ++npv;
+                fresh = false;
+                named_bar_signal(kBarP + grp, 160, ok);
+            }
+            // ------------------------------------------------ the part's end
+            if (ok && !fresh) ok = __all_sync(0xffffffffu, wait(&sm.pv_done[grp], npv - 1));
+            tc_fence_after();
+            warp_sums(l, lane);
+            if (C == 16) {
+                if ((lane & 1) == 0) sm.part_sum[grp][quad][lane >> 1] = l[0];
+            } else if (C == 32) {
+                sm.part_sum[grp][quad][lane] = l[0];
+            } else {
+                sm.part_sum[grp][quad][2 * lane] = l[0];
+                sm.part_sum[grp][quad][2 * lane + 1] = l[1];
+            }
+            if (quad == 0) {
+#pragma unroll
+                for (int i2 = 0; i2 < kOwn; ++i2)
+                    if (lane + 32 * i2 < C) sm.stat[grp][lane + 32 * i2].x = ref[i2];
+            }
+            tc_fence_before();
+            named_bar_sync(kBarEnd, 256);
+            tc_fence_after();
+            const bool had0 = part.tiles > 1 || (part.tiles == 1 && (c & 1) == 0);
+            const bool had1 = part.tiles > 1 || (part.tiles == 1 && (c & 1) == 1);
+            const bool poison = sm.poison[buf] != 0;
+            if (ok) {
+#pragma unroll 1
+                for (int n0 = grp * (C / 2); n0 < grp * (C / 2) + C / 2 && n0 < nrows; n0 += 8) {
+                    float o0[8], o1[8];
+                    const uint32_t at = colO + lane_addr + n0;
+                    constexpr int kSets = K::kWide ? K::kP : 1;
+                    if (had0) load_sum8<kSets>(at, C, o0);
+                    if (had1) load_sum8<kSets>(at + K::kOCols, C, o1);
+                    uint32_t spoilt = 0;   // columns of these 8 that see a NaN in this channel
+                    if (poison && key < D) {
+                        const int first = part.tile0 * kKeys, past = first + part.tiles * kKeys;
+                        for (int j = max(first, part.lo_key); j < min(past, part.hi_key + 1); ++j) {
+                            if (j >= part.all_lo && j <= part.all_hi) {
+                                j = min(part.all_hi, past - 1);   // seen by all: the product has it
+                                continue;
+                            }
+                            const int id = __ldg(p.table + static_cast<long long>(part.b) * p.width +
+                                                 (j >> p.page_log2));
+                            if (id < 0 || id >= p.num_pages) continue;
+                            const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
+                                                (j & ((1 << p.page_log2) - 1));
+                            if ((__ldg(p.v8 + r * D + key) & 0x7f) != 0x7f) continue;
+                            for (int n = 0; n < 8; ++n) {
+                                const int rp = sm.row_pos[buf][n0 + n];
+                                if (j <= rp && (p.seq.window <= 0 || rp - j < p.seq.window)) spoilt |= 1u << n;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int n = n0 + j;
+                        const float r0 = sm.stat[0][n].x, r1 = sm.stat[1][n].x;
+                        const float m = fmaxf(r0, r1), mx = m == kNegInf ? 0.f : m;
+                        const float f0 = ex2_approx(r0 - mx), f1 = ex2_approx(r1 - mx);
+                        float sum = 0.f, o = 0.f;
+                        if (had0) {
+                            sum = f0 * ((sm.part_sum[0][0][n] + sm.part_sum[0][1][n]) +
+                                        (sm.part_sum[0][2][n] + sm.part_sum[0][3][n]));
+                            o = f0 * o0[j];
+                        }
+                        if (had1) {
+                            sum += f1 * ((sm.part_sum[1][0][n] + sm.part_sum[1][1][n]) +
+                                         (sm.part_sum[1][2][n] + sm.part_sum[1][3][n]));
+                            o = fmaf(f1, o1[j], o);
+                        }
+                        if ((spoilt >> j) & 1u) o = __uint_as_float(0x7fc00000u);
+                        if (n >= nrows) continue;
+                        if (part.whole) {
+                            const int r = part.row0 + n, tok = r / G, head = part.h * G + r % G;
+                            const long long row = part.req.start + tok;
+                            const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (NaN divides on)
+                            if (key < D && fa_index_ok(row, p.seq.total_tokens, p.status))
+                                static_cast<uint16_t*>(p.o)[(row * p.seq.Hq + head) * D + key] =
+                                    static_cast<uint16_t>(pack2<E>(o * inv, 0.f));
+                            if (key == 0 && fa_index_ok(row, p.seq.total_tokens, p.status))
+                                p.lse[row_stat_index(p.seq, part.b, head, part.req.start, tok)] =
+                                    sum != 0.f ? (mx - kShift + log2f(sum)) * kLn2 : kNegInf;
+                        } else {
+                            const long long at2 =
+                                (2LL * blockIdx.x + (part.begins ? 1 : 0)) * C + n;
+                            if (key < D) p.part_o[at2 * D + key] = o;
+                            if (key == 0) p.part_stat[at2] = make_float2(m, sum);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            named_bar_sync(kBarFree, 256);
+            if (threadIdx.x == 128) sm.poison[buf] = 0;
+            if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[buf]));
+            c += part.tiles;
+            ++np;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, K::kTmemCols);
+}
+
+// Joins the parts of the item that begins at the end of CTA c's share, c = blockIdx.x: a
+// warp per row, the parts in their order.
+template <int D, int E>
+__global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
+    grid_dependency_wait();
+    const int cta = blockIdx.x;
+    const Kv8Join j = p.joins[cta];
+    if (j.last <= cta) return;
+    const int C = p.columns, G = p.seq.group, lane = threadIdx.x & 31;
+    constexpr int kPer = D / 32;
+    for (int n = threadIdx.x >> 5; n < C && j.row0 + n < j.n * G; n += 8) {
+        float m = kNegInf, sum = 0.f, o[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] = 0.f;
+        for (int part = cta; part <= j.last; ++part) {
+            if (share_begin(j.total, part, gridDim.x) == share_begin(j.total, part + 1, gridDim.x))
+                continue;   // a CTA without a share
+            const long long at = (2LL * part + (part == cta ? 1 : 0)) * C + n;
+            const float2 st = p.part_stat[at];
+            float x[kPer];
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) x[c] = p.part_o[at * D + lane + 32 * c];
+            const float top = fmaxf(m, st.x), ref = top == kNegInf ? 0.f : top;
+            const float a = ex2_approx(m - ref), b = ex2_approx(st.x - ref);
+            sum = a * sum + b * st.y;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) o[c] = a * o[c] + b * x[c];
+            m = top;
+        }
+        const int r = j.row0 + n, tok = r / G, head = j.h * G + r % G;
+        const long long row = j.start + tok;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+            static_cast<uint16_t*>(p.o)[(row * p.seq.Hq + head) * D + lane + 32 * c] =
+                static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
+        if (lane == 0)
+            p.lse[row_stat_index(p.seq, j.b, head, j.start, tok)] =
+                sum != 0.f ? ((m == kNegInf ? 0.f : m) - kShift + log2f(sum)) * kLn2 : kNegInf;
+    }
+}
+
+template <int D, int E, int C>
+cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
+    constexpr int smem = kv8_smem_bytes<D, E, C>();
+    static_assert(smem <= 232448, "shared memory per CTA");
+    auto kern = fa_fwd_kv8_kernel<D, E, C>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.ctas, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, int E>
+cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
+    cudaError_t e = ev ? cudaEventRecord(ev[0], stream) : cudaSuccess;
+    if (e == cudaSuccess)
+        e = p.columns == 16   ? launch_attend<D, E, 16>(p, stream)
+            : p.columns == 32 ? launch_attend<D, E, 32>(p, stream)
+                              : launch_attend<D, E, 64>(p, stream);
+    if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fa_fwd_kv8_join_kernel<D, E>, p);
+    if (e == cudaSuccess && ev) e = cudaEventRecord(ev[2], stream);
+    return e;
 }
 
 }  // namespace
 
-cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, cudaStream_t stream) {
-    const long long grid = (static_cast<long long>(p.seq.total_tokens) * p.seq.Hq + 3) / 4;
-    if (grid > INT_MAX) return cudaErrorInvalidValue;
-    const unsigned g = static_cast<unsigned>(grid);
-    if (d == 128 && p.elem == kElemBf16Code) fa_fwd_kv8_kernel<128, kElemBf16><<<g, 128, 0, stream>>>(p);
-    else if (d == 128) fa_fwd_kv8_kernel<128, kElemF16><<<g, 128, 0, stream>>>(p);
-    else if (p.elem == kElemBf16Code) fa_fwd_kv8_kernel<64, kElemBf16><<<g, 128, 0, stream>>>(p);
-    else fa_fwd_kv8_kernel<64, kElemF16><<<g, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, cudaStream_t stream) {
+    if (d == 128)
+        return p.elem == kElemBf16Code ? launch_both<128, kElemBf16>(p, ev, stream)
+                                       : launch_both<128, kElemF16>(p, ev, stream);
+    return p.elem == kElemBf16Code ? launch_both<64, kElemBf16>(p, ev, stream)
+                                   : launch_both<64, kElemF16>(p, ev, stream);
 }
 
 }  // namespace fa

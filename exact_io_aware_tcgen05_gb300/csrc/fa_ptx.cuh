@@ -443,6 +443,16 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     return d;
 }
 
+// The same for other layouts: swizzle mode 4 is the 64-byte swizzle (64-byte rows; core
+// groups of 8 rows are 512 bytes), mode 0 none (16-byte rows, groups of 8 rows are 128
+// consecutive bytes; for an MN-major operand `lbo` = bytes between groups along K, `sbo` =
+// bytes between 16-byte blocks along M/N).
+template <int SWIZZLE_MODE>
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (sdesc_sw128(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) |
+           (static_cast<uint64_t>(SWIZZLE_MODE) << 61);
+}
+
 // Element type of the operands and outputs (accumulation is always fp32); the
 // codes of the C ABI's fa_dtype.
 constexpr int kElemBf16 = 0;
@@ -579,6 +589,24 @@ __device__ __forceinline__ void stage_acc_row(uint32_t t_acc, float mul, uint8_t
             *swizzled_unit(stage + (col / 64) * chunk_bytes, r, (col % 64) / 8) = w;
         }
     }
+}
+
+// ------------------------------------------------------- small helpers of kernels
+
+// Maximum over the warp's lanes, in every lane (NaN counts as absent; sm_100 and later).
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Asynchronous 4-byte copy global -> shared, and this thread's arrival on `bar` (counted in
+// its init) once all the copies it has issued have landed.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------ dropout
