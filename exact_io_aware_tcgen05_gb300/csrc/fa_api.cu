@@ -953,7 +953,7 @@ fa_status check_table(const char* who, int B, int width, int page) {
 // that takes a request's rows in one item, and 64 for more rows than that.
 int kv8_columns(int N, int group) {
     const long long rows = static_cast<long long>(N) * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 16 ? 16 : 32;
 }
 
 // Byte layout of fa_fwd_kv8's workspace, each part padded to 256 bytes.
@@ -1068,7 +1068,8 @@ fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long 
     p.Hkv = Hkv;
     p.num_slots = num_pages * page;
     p.elem = static_cast<int>(dtype);
-    p.chunk = kKv8Block;
+    // a warp a token while there are few, one for the blocks of 16 tokens beyond that
+    p.chunk = T <= 1024 ? 1 : kKv8Block;
     const cudaError_t e = launch_kv8_append(p, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append launch");
 }
@@ -1076,7 +1077,7 @@ fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long 
 size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens) {
     fa::Geometry g;
     if (!fa::query_geometry(B, Hq, Hkv, N, d, 0, 0, total_tokens, &g)) return 0;
-    return fa::kv8_workspace(fa::sm_count(), fa::kv8_columns(N, Hq / Hkv), d).full;
+    return fa::kv8_workspace(2 * fa::sm_count(), fa::kv8_columns(N, Hq / Hkv), d).full;
 }
 
 fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
@@ -1111,7 +1112,7 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
         return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: num_pages * Hkv = %lld is 2^31 or more",
                     static_cast<long long>(num_pages) * Hkv);
     p.columns = kv8_columns(N, g.seq.group);
-    p.ctas = sm_count();
+    p.ctas = 2 * sm_count();
     const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);
     const size_t need = w.full;
     if (!workspace || workspace_bytes < need)

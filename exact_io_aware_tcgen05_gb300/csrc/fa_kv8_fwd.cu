@@ -27,18 +27,20 @@
 // probabilities is that of 2^(t_j - M) / v_scale_j.
 //
 // Work split.  The key tiles of all items (request, key/value head, C rows) lie one behind
-// the other and every CTA, one per SM, takes an equal share of them (kItemCost more tiles
+// the other and every CTA, two per SM, takes an equal share of them (kItemCost more tiles
 // stand for an item's fixed cost), wherever items begin and end; a CTA's share begins and
 // ends inside at most two items, whose parts go to the workspace, and a second small
 // kernel, launched with this one (programmatic dependence), joins them.  All lengths are
 // read on the device, and the CTAs find their shares themselves.
 //
-// One CTA: 12 warps,
-//   warp 0       producer: pages by TMA, the tile's 16 scales by 4-byte asynchronous copies
-//   warp 1       tcgen05 issuer; owns the TMEM allocation
+// One CTA: 8 warps,
+//   warp 0       producer: pages by TMA, K and V in turn through one ring of slots, the
+//                tile's 16 scales by 4-byte asynchronous copies
+//   warp 1       tcgen05 issuer; owns the TMEM allocation.  S^T of the next tile is issued
+//                before the weights of this one are ready (two S^T buffers)
 //   warps 2, 3   the items' queries: scaled, cut into pieces, into shared memory
-//   warps 4..7, 8..11   two softmax groups: a lane has a key.  They take the tiles in turn,
-//                each with its own maxima, sums and O^T, put together at the end of a part.
+//   warps 4..7   softmax: a lane has a key
+// The second CTA of the SM works while this one waits at the ends of items.
 #include "fa_kernels.h"
 #include "fa_ptx.cuh"
 #include "fa_seq.cuh"
@@ -56,7 +58,7 @@ constexpr int kItemCost = 1;        // an item's fixed cost in tiles
 // Weights are at most 1 before this factor 2^15 (and 2^15 < 65504, fp16's largest).
 constexpr float kShift = 15.f;
 constexpr int kWindow = 128;        // requests whose lengths a CTA keeps in shared memory
-constexpr int kThreads = 384;
+constexpr int kThreads = 256;
 
 // --------------------------------------------------------------- work distribution
 
@@ -116,22 +118,22 @@ struct Part {
 // Where a CTA's share begins, found by all its threads; and the requests from there on.
 struct Share {
     long long begin, end, total;
-    long long offset;     // of `begin` within request b0's units
-    int b0;
+    int b0, h, blk, off;   // the request, head, block of rows and unit of that item it begins at
 };
 
 // A walk over a CTA's parts; every role of the CTA walks for itself.
 template <int C>
 struct Walk {
     const Kv8FwdParams& p;
-    const int3* window;   // (start, n, len) of requests b0 .. b0 + kWindow - 1, in shared memory
-    int b0, b;
-    long long at, left, unit;   // position within request b's units, units left, absolute unit
+    const int3* window;     // (start, n, len) of requests b0 .. b0 + kWindow - 1, in shared memory
+    int b0, b, h, blk, off; // request, head, block of rows, units of that item behind us
+    long long left, unit;   // units left, the next one's number
     Request req;
     Items it;
 
     __device__ Walk(const Kv8FwdParams& p_, const Share& s, const int3* w)
-        : p(p_), window(w), b0(s.b0), b(s.b0), at(s.offset), left(s.end - s.begin), unit(s.begin) {
+        : p(p_), window(w), b0(s.b0), b(s.b0), h(s.h), blk(s.blk), off(s.off),
+          left(s.end - s.begin), unit(s.begin) {
         load();
     }
     __device__ void load() {
@@ -148,24 +150,25 @@ struct Walk {
     }
     __device__ bool next(Part& part) {
         while (left > 0 && b < p.seq.B) {
-            const long long units = static_cast<long long>(it.blocks) * p.seq.Hkv * it.cost;
-            if (at >= units) {
-                ++b;
-                at = 0;
-                load();
+            if (off == it.cost) {
+                off = 0;
+                ++blk;
+            }
+            if (blk >= it.blocks) {
+                blk = 0;
+                if (it.blocks == 0 || ++h == p.seq.Hkv) {
+                    h = 0;
+                    ++b;
+                    load();
+                }
                 continue;
             }
-            const long long item = at / it.cost;
-            const int off = static_cast<int>(at - item * it.cost);
             const int take = static_cast<int>(min(left, static_cast<long long>(it.cost - off)));
             part.unit0 = unit - off;
-            at += take;
-            left -= take;
-            unit += take;
             part.req = req;
             part.b = b;
-            part.h = static_cast<int>(item / it.blocks);
-            part.row0 = static_cast<int>(item - static_cast<long long>(part.h) * it.blocks) * C;
+            part.h = h;
+            part.row0 = blk * C;
             // positions of the block's first and last token
             const int G = p.seq.group;
             const int first = req.len - req.n + part.row0 / G;
@@ -182,6 +185,9 @@ struct Walk {
             part.tiles = max(t1 - off, 0);
             part.begins = off == 0;
             part.whole = part.begins && t1 == part.item_tiles;
+            off += take;
+            left -= take;
+            unit += take;
             if (part.tiles > 0 || part.whole) return true;
         }
         return false;
@@ -195,66 +201,66 @@ struct Kv8Cfg {
     static constexpr int kQ = E == kElemBf16 ? 2 : 3;    // pieces of q
     static constexpr int kP = E == kElemBf16 ? 3 : 4;    // pieces of P
     // With few columns an MMA costs the reading of its 128 rows, so the pieces of q and of P
-    // go side by side into one MMA of more columns and are added up when read; with 64
-    // columns (and no TMEM for more) they are added up by the tensor cores, one MMA each.
-    static constexpr bool kWide = C <= 32;
-    static constexpr int kSCols = kWide ? kQ * C : C;
-    static constexpr int kOCols = kWide ? kP * C : C;
-    static constexpr int kTmemUsed = 2 * (kSCols + kOCols);
-    static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-    static_assert(kTmemUsed <= 512, "TMEM columns");
-    static constexpr int kSide = kKeys * D;              // K or V of a tile
-    static constexpr int kStageBytes = 2 * kSide;
+    // go side by side into one MMA of more columns and are added up when read.  (256 TMEM
+    // columns a CTA: where they do not hold P's pieces, the tensor cores add them up, an
+    // MMA each.)
+    static constexpr int kSCols = kQ * C;
+    static constexpr bool kWideO = 2 * kSCols + kP * C <= 256;
+    static constexpr int kOCols = kWideO ? kP * C : C;
+    static constexpr int kTmemCols = 2 * kSCols + kOCols <= 128 ? 128 : 256;
+    static_assert(2 * kSCols + kOCols <= 256, "TMEM columns, two CTAs per SM");
+    static constexpr int kSlotBytes = kKeys * D;         // K or V of a tile
     static constexpr int kQBytes = kQ * C * D;           // one item's queries
-    static constexpr int kPBytes = kP * C * kKeys;       // one group's weights
+    static constexpr int kPBytes = kP * C * kKeys;       // a tile's weights
     static constexpr int kSwizzle = D == 128 ? 2 : 4;    // descriptor code of the D-byte swizzle
     static constexpr int kGroup = 8 * D;                 // bytes of 8 rows
 };
 
-constexpr int kMaxStages = 12;
+constexpr int kMaxSlots = 12;
+constexpr int kScaleSlots = 16;   // tiles whose scales are kept: more than the ring is long
 
 template <int C>
 struct Kv8Smem {   // behind the tiles
-    float scales[kMaxStages][16];    // of the stage's tile: K's 8 blocks, V's 8 (V < 0: hidden)
+    float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
     float q_scale[2][C];
     int row_pos[2][C];               // position of the row's token; INT_MIN: no row
-    float wmax[2][2][4][C];          // [group][tile parity][warp]
-    alignas(16) float ref[8][C];     // [softmax warp]
-    alignas(16) float fac[8][C];
-    float part_sum[2][4][C];         // [group][warp]
-    float2 stat[2][C];               // [group]: reference, sum
+    long long out_at[2][C], lse_at[2][C];
+    float wmax[2][4][C];             // [tile parity][warp]
+    alignas(16) float ref[4][C];     // [warp]
+    alignas(16) float fac[4][C];
+    float part_sum[2][4][C];         // [part parity][warp]
     int3 window[kWindow];
     Share share;
     long long warp_sums[kThreads / 32];
-    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+    uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], pv_done[2];
+    uint64_t s_full[2], pv_done;
     uint64_t all_done;
     uint32_t tmem;
     int abort;
-    int poison[2];                   // NaN found among values that only some rows see
+    int poison;                      // NaN found among values that only some rows see
 };
 
+constexpr int kCtaSmem = 233472 / 2 - 1024;   // two CTAs per SM
+
 template <int D, int E, int C>
-constexpr int kv8_stages() {
+constexpr int kv8_slots() {
     using K = Kv8Cfg<D, E, C>;
-    const int left = 232448 - 1024 - 2 * K::kQBytes - 2 * K::kPBytes - static_cast<int>(sizeof(Kv8Smem<C>));
-    const int n = left / K::kStageBytes;
-    return n < kMaxStages ? n : kMaxStages;
+    const int left = kCtaSmem - 1024 - 2 * K::kQBytes - K::kPBytes - static_cast<int>(sizeof(Kv8Smem<C>));
+    const int n = left / K::kSlotBytes;
+    return n < kMaxSlots ? n : kMaxSlots;
 }
 
 template <int D, int E, int C>
 constexpr int kv8_smem_bytes() {
     using K = Kv8Cfg<D, E, C>;
-    return 1024 + kv8_stages<D, E, C>() * K::kStageBytes + 2 * K::kQBytes + 2 * K::kPBytes +
+    return 1024 + kv8_slots<D, E, C>() * K::kSlotBytes + 2 * K::kQBytes + K::kPBytes +
            static_cast<int>(sizeof(Kv8Smem<C>));
 }
 
 // named barriers (0 is __syncthreads)
-constexpr int kBarP = 1;      // + group: weights written; the group and the issuer
-constexpr int kBarMax = 3;    // + group: the warps' maxima written
-constexpr int kBarEnd = 5;    // both groups: a part's statistics written
-constexpr int kBarFree = 6;   // both groups: the accumulators have been read
+constexpr int kBarP = 1;      // weights written; the softmax warps and the issuer
+constexpr int kBarMax = 2;    // the softmax warps' maxima (or a part's sums) written
 
 // The 16-byte unit u of row r in a tile of rows of D bytes, swizzled over D bytes.
 template <int D>
@@ -403,8 +409,12 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm
     }
     auto look = [&](int b, long long mine, long long end) {
         if (begin >= end - mine && begin < end) {
+            const Items it = items_of<C>(p, load_request(p, b));
+            const long long at = begin - (end - mine), item = at / it.cost;
             sm.share.b0 = b;
-            sm.share.offset = begin - (end - mine);
+            sm.share.off = static_cast<int>(at - item * it.cost);
+            sm.share.h = static_cast<int>(item / it.blocks);
+            sm.share.blk = static_cast<int>(item % it.blocks);
         }
     };
     if (B <= kThreads) {
@@ -423,11 +433,36 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm
     __syncthreads();
 }
 
+// Which of the columns n0 .. n0 + 7 see a NaN code in this channel of a value that other
+// columns do not see, among the part's keys (a bit each).  Rare: the codes are read again.
+template <int D, int C>
+__device__ __noinline__ uint32_t find_nan(const Kv8FwdParams& p, const Part& part, const Kv8Smem<C>& sm,
+                                          int buf, int n0, int channel) {
+    uint32_t spoilt = 0;
+    const int first = part.tile0 * kKeys, past = first + part.tiles * kKeys;
+    for (int j = max(first, part.lo_key); j < min(past, part.hi_key + 1); ++j) {
+        if (j >= part.all_lo && j <= part.all_hi) {
+            j = part.all_hi;   // seen by all: the product has it
+            continue;
+        }
+        const int id = __ldg(p.table + static_cast<long long>(part.b) * p.width + (j >> p.page_log2));
+        if (id < 0 || id >= p.num_pages) continue;
+        const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
+                            (j & ((1 << p.page_log2) - 1));
+        if ((__ldg(p.v8 + r * D + channel) & 0x7f) != 0x7f) continue;
+        for (int n = 0; n < 8; ++n) {
+            const int rp = sm.row_pos[buf][n0 + n];
+            if (j <= rp && (p.seq.window <= 0 || rp - j < p.seq.window)) spoilt |= 1u << n;
+        }
+    }
+    return spoilt;
+}
+
 template <int D, int E, int C>
-__global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_constant__ Kv8FwdParams p) {
+__global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_constant__ Kv8FwdParams p) {
     using K = Kv8Cfg<D, E, C>;
-    constexpr int kStages = kv8_stages<D, E, C>();
-    static_assert(kStages >= 3, "ring of key/value tiles");
+    constexpr int kSlots = kv8_slots<D, E, C>();
+    static_assert(kSlots >= 4 && kSlots / 2 + 2 < kScaleSlots, "ring of key/value tiles");
     // S^T: K e4m3 (K-major) times q's pieces e4m3 (K-major); O^T: V e4m3 (MN-major) times P's
     // pieces e5m2 (MN-major; operand format code 1)
     constexpr uint32_t kIdescS = idesc_f32acc(kKeys, K::kSCols, false, false, kElemFp8);
@@ -436,15 +471,32 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* sKV = smem;                                  // [stages][K, V]
-    uint8_t* sQ = smem + kStages * K::kStageBytes;        // [2][pieces][C][D]
-    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [2][pieces][C / 16][keys][16]
-    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + 2 * K::kPBytes);
+    uint8_t* sKV = smem;                                  // [slots]
+    uint8_t* sQ = smem + kSlots * K::kSlotBytes;          // [2][pieces][C][D]
+    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [pieces][C / 16][keys][16]
+    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + K::kPBytes);
     volatile int* abort_flag = &sm.abort;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_launch_dependents();
 
+    if (threadIdx.x == 0) {
+        sm.abort = 0;
+        sm.poison = 0;
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_addr(&sm.kv_full[i]), 1);
+            mbar_init(smem_addr(&sm.kv_empty[i]), 1);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sm.q_full[i]), 64);
+            mbar_init(smem_addr(&sm.q_empty[i]), 5);    // the last S^T of the part, 4 softmax warps
+            mbar_init(smem_addr(&sm.s_full[i]), 1);
+        }
+        mbar_init(smem_addr(&sm.pv_done), 1);
+        mbar_init(smem_addr(&sm.all_done), 1);
+        fence_barrier_init();
+    }
     find_share<C>(p, sm);
     if (sm.share.begin == sm.share.end) {
         if (threadIdx.x == 0) p.joins[blockIdx.x].last = 0;
@@ -455,22 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
         Request r{0, 0, 0};
         if (b < p.seq.B) r = load_request(p, b);
         sm.window[threadIdx.x] = make_int3(r.start, r.n, r.len);
-    }
-    if (threadIdx.x == 0) {
-        sm.abort = 0;
-        sm.poison[0] = sm.poison[1] = 0;
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&sm.kv_full[i]), 33);   // 32 lanes and the bytes' announcement
-            mbar_init(smem_addr(&sm.kv_empty[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sm.q_full[i]), 64);
-            mbar_init(smem_addr(&sm.q_empty[i]), 9);    // the last S^T of the part, 8 softmax warps
-            mbar_init(smem_addr(&sm.s_full[i]), 1);
-            mbar_init(smem_addr(&sm.pv_done[i]), 1);
-        }
-        mbar_init(smem_addr(&sm.all_done), 1);
-        fence_barrier_init();
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(&sm.tmem), K::kTmemCols);
@@ -497,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
         const int page = 1 << p.page_log2, per_tile = kKeys >> p.page_log2;
         const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
         const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
-        int c = 0;
+        int c = 0, items = 0;                      // tiles, items of the ring
         bool ok = true;
         while (ok && walk.next(part)) {
             const int* row = p.table + static_cast<long long>(part.b) * p.width;
@@ -508,120 +544,135 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
             auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
             int cur = part.tiles > 0 ? entry(base + lane) : -1;
             int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
-            for (int i = 0; i < part.tiles; ++i, ++c) {
+            for (int i = 0; i < part.tiles && ok; ++i, ++c) {
                 const int tile = part.tile0 + i;
-                const int st = c % kStages, use = c / kStages;
                 if (tile * per_tile >= base + 32) {
                     base += 32;
                     cur = nxt;
                     nxt = entry(base + 32 + lane);
                 }
-                if (use > 0) {
-                    ok = __all_sync(0xffffffffu, wait(&sm.kv_empty[st], use - 1));
-                    if (!ok) break;
-                }
-                uint8_t* dst = sKV + st * K::kStageBytes;
-                const uint32_t full = smem_addr(&sm.kv_full[st]);
                 const int first = tile * per_tile - base;
                 // this lane's page of the tile
                 const int id = __shfl_sync(0xffffffffu, cur, (first + (lane & (per_tile - 1))) & 31);
                 const bool load = lane < per_tile && id >= 0 && id < p.num_pages;
-                const int pages = __popc(__ballot_sync(0xffffffffu, load));
-                if (lane == 0) mbar_arrive_expect_tx(full, pages * 2 * page * D);
-                __syncwarp();
-                if (load) {
-                    tma_load_3d(smem_addr(dst + lane * page * D), &p.tm_k, full, 0, 0,
-                                id * p.seq.Hkv + part.h);
-                    tma_load_3d(smem_addr(dst + K::kSide + lane * page * D), &p.tm_v, full, 0, 0,
-                                id * p.seq.Hkv + part.h);
-                }
-                // the scales of the tile's 8 blocks
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * page * D;
+                // the scales of the tile's 8 blocks (their slot's last tile is long done)
                 const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
-                bool plain = true;
-                if (lane < 16) {
-                    float* to = &sm.scales[st][lane];
-                    if (sid >= 0 && sid < p.num_pages && tile * kKeys + side_blk * kKv8Block < lim) {
-                        const long long at =
-                            ((static_cast<long long>(sid) * p.seq.Hkv + part.h) << blocks_log2) +
-                            (side_blk & ((1 << blocks_log2) - 1));
-                        cp_async4(smem_addr(to), (lane < 8 ? p.k_scale : p.v_scale) + at);
-                        plain = false;
-                    } else {
-                        *to = lane < 8 ? 0.f : -1.f;   // hidden
+                for (int side = 0; side < 2; ++side, ++items) {
+                    const int st = items % kSlots, use = items / kSlots;
+                    if (use > 0) {
+                        ok = __all_sync(0xffffffffu, wait(&sm.kv_empty[st], use - 1));
+                        if (!ok) break;
+                    }
+                    uint8_t* dst = sKV + st * K::kSlotBytes;
+                    const uint32_t full = smem_addr(&sm.kv_full[st]);
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    if (load)
+                        tma_load_3d(smem_addr(dst + lane * page * D), side ? &p.tm_v : &p.tm_k, full, 0, 0,
+                                    id * p.seq.Hkv + part.h);
+                    if (side == 0) {
+                        const uint32_t sbar = smem_addr(&sm.scales_full[c % kScaleSlots]);
+                        bool plain = true;
+                        if (lane < 16) {
+                            float* to = &sm.scales[c % kScaleSlots][lane];
+                            if (sid >= 0 && sid < p.num_pages && tile * kKeys + side_blk * kKv8Block < lim) {
+                                const long long at =
+                                    ((static_cast<long long>(sid) * p.seq.Hkv + part.h) << blocks_log2) +
+                                    (side_blk & ((1 << blocks_log2) - 1));
+                                cp_async4(smem_addr(to), (lane < 8 ? p.k_scale : p.v_scale) + at);
+                                plain = false;
+                            } else {
+                                *to = lane < 8 ? 0.f : -1.f;   // hidden
+                            }
+                        }
+                        if (plain) mbar_arrive(sbar);
+                        else cp_async_arrive(sbar);
                     }
                 }
-                if (plain) mbar_arrive(full);
-                else cp_async_arrive(full);
             }
         }
         // every copy lands before the CTA exits, whatever became of the other roles
-        for (int i = max(0, c - kStages); i < c; ++i)
-            mbar_wait_drain(smem_addr(&sm.kv_full[i % kStages]), (i / kStages) & 1, kDrainCycles);
+        for (int i = max(0, items - kSlots); i < items; ++i)
+            mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
+        for (int i = max(0, c - kScaleSlots); i < c; ++i)
+            mbar_wait_drain(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1, kDrainCycles);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
-        // After an abort it goes on issuing on stale data, so that every barrier's phases
-        // still complete.
-        int c = 0, np = 0;
-        const uint64_t kd0 = sdesc<K::kSwizzle>(smem_addr(sKV), 16, K::kGroup);
-        // V: 16 or 8 groups of 8 keys; the second half of the 128 rows of the product at
-        // d = 64 reads the next keys' channels and is not used
-        const uint64_t vd0 = sdesc<K::kSwizzle>(smem_addr(sKV + K::kSide), K::kGroup, K::kGroup);
+        // Walks the tiles of all parts one behind the other, one tile ahead with S^T.  After
+        // an abort it goes on issuing on stale data, so that every barrier's phases still
+        // complete.
+        const uint64_t kv0 = sdesc<K::kSwizzle>(smem_addr(sKV), 16, K::kGroup);
+        // V: the second half of the 128 rows of the product at d = 64 reads the next keys'
+        // channels and is not used
+        const uint64_t v0 = sdesc<K::kSwizzle>(smem_addr(sKV), K::kGroup, K::kGroup);
         const uint64_t qd0 = sdesc<K::kSwizzle>(smem_addr(sQ), 16, K::kGroup);
         const uint64_t pd0 = sdesc<0>(smem_addr(sP), 128, kKeys * 16);
-        while (walk.next(part)) {
-            if (part.tiles == 0) {
-                // (its queries are laid out all the same)
-                if (lane == 0) {
+        int np = -1, left = 0;   // the part of the next tile, its tiles from that one on
+        bool first = true;
+        auto advance = [&]() {   // to the next tile; false at the end
+            while (left == 0) {
+                if (!walk.next(part)) return false;
+                ++np;
+                left = part.tiles;
+                first = true;
+                if (left == 0 && lane == 0) {
+                    // (its queries are laid out all the same)
                     wait(&sm.q_full[np & 1], np >> 1);
                     mma_commit(smem_addr(&sm.q_empty[np & 1]));
                 }
-                __syncwarp();
-                ++np;
-                continue;
             }
-            auto issue_s = [&](int i) {   // lane 0
-                const int st = (c + i) % kStages, g = (c + i) & 1;
-                wait(&sm.kv_full[st], (c + i) / kStages);
-                tc_fence_after();
-                const uint64_t kd = kd0 + static_cast<uint64_t>((st * K::kStageBytes) >> 4);
-                const uint64_t qd = qd0 + static_cast<uint64_t>(((np & 1) * K::kQBytes) >> 4);
+            --left;
+            return true;
+        };
+        auto issue_s = [&](int T) {   // lane 0: S^T of the tile that advance() came to, number T
+            const int st = (2 * T) % kSlots;
+            if (first) wait(&sm.q_full[np & 1], np >> 1);
+            wait(&sm.kv_full[st], (2 * T) / kSlots);
+            tc_fence_after();
+            const uint64_t kd = kv0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
+            const uint64_t qd = qd0 + static_cast<uint64_t>(((np & 1) * K::kQBytes) >> 4);
 #pragma unroll
-                for (int q = 0; q < (K::kWide ? 1 : K::kQ); ++q)
-#pragma unroll
-                    for (int kk = 0; kk < D / 32; ++kk)
-                        mma_ss_f8(tmem + g * K::kSCols, kd + 2 * kk, qd + ((q * C * D) >> 4) + 2 * kk,
-                                  kIdescS, (q > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(smem_addr(&sm.s_full[g]));
-                if (i == part.tiles - 1) mma_commit(smem_addr(&sm.q_empty[np & 1]));
-            };
-            if (lane == 0) {
-                wait(&sm.q_full[np & 1], np >> 1);
-                issue_s(0);
-                if (part.tiles > 1) issue_s(1);
+            for (int kk = 0; kk < D / 32; ++kk)
+                mma_ss_f8(tmem + (T & 1) * K::kSCols, kd + 2 * kk, qd + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
+            mma_commit(smem_addr(&sm.s_full[T & 1]));
+            mma_commit(smem_addr(&sm.kv_empty[st]));
+            if (left == 0) mma_commit(smem_addr(&sm.q_empty[np & 1]));
+        };
+        int T = 0;
+        bool more = advance();
+        if (more && lane == 0) issue_s(0);
+        while (more) {
+            const bool fresh = first;   // tile T is its part's first
+            first = false;
+            more = advance();
+            // S^T of tile T + 1 first if its keys are there already
+            bool issued = false;
+            if (more && lane == 0 &&
+                mbar_try_wait(smem_addr(&sm.kv_full[(2 * T + 2) % kSlots]), ((2 * T + 2) / kSlots) & 1)) {
+                issue_s(T + 1);
+                issued = true;
             }
             __syncwarp();
-            for (int i = 0; i < part.tiles; ++i) {
-                const int st = (c + i) % kStages, g = (c + i) & 1;
-                named_bar_sync(kBarP + g, 160);
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint64_t vd = vd0 + static_cast<uint64_t>((st * K::kStageBytes) >> 4);
-                    const uint64_t pd = pd0 + static_cast<uint64_t>((g * K::kPBytes) >> 4);
+            named_bar_sync(kBarP, 160);
+            if (lane == 0) {
+                const int st = (2 * T + 1) % kSlots;
+                wait(&sm.kv_full[st], (2 * T + 1) / kSlots);
+                tc_fence_after();
+                const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
 #pragma unroll
-                    for (int q = 0; q < (K::kWide ? 1 : K::kP); ++q)
+                for (int q = 0; q < (K::kWideO ? 1 : K::kP); ++q)
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 32; ++kk)
-                            mma_ss_f8(colO + g * K::kOCols, vd + ((kk * 32 * D) >> 4),
-                                      pd + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
-                                      (i >= 2 || q > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(smem_addr(&sm.pv_done[g]));
-                    mma_commit(smem_addr(&sm.kv_empty[st]));
-                    if (i + 2 < part.tiles) issue_s(i + 2);
-                }
-                __syncwarp();
+                    for (int kk = 0; kk < kKeys / 32; ++kk)
+                        mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4),
+                                  pd0 + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
+                                  (!fresh || q > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(smem_addr(&sm.pv_done));
+                mma_commit(smem_addr(&sm.kv_empty[st]));
+                if (more && !issued) issue_s(T + 1);
             }
-            c += part.tiles;
-            ++np;
+            __syncwarp();
+            ++T;
         }
         if (lane == 0) {
             mma_commit(smem_addr(&sm.all_done));
@@ -657,11 +708,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
                 for (int n = t / kLanes; n < C; n += kRows) {
                     const int r = part.row0 + n;
                     const int tok = r / G, head = part.h * G + r % G;
+                    const long long token = part.req.start + tok;
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (r < rows)
                         w = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const uint16_t*>(p.q) +
-                            static_cast<long long>(part.req.start + tok) * p.q_stride + head * D + sub * 8));
+                            static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
                     float x[8];
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
                     uint32_t top = 0;
@@ -683,6 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
                     if (sub == 0) {
                         sm.q_scale[buf][n] = fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
                         sm.row_pos[buf][n] = r < rows ? part.req.len - part.req.n + tok : INT_MIN;
+                        sm.out_at[buf][n] = (token * p.seq.Hq + head) * D;
+                        sm.lse_at[buf][n] = row_stat_index(p.seq, part.b, head, part.req.start, tok);
                     }
 #pragma unroll
                     for (int q = 0; q < K::kQ; ++q) {
@@ -707,36 +760,29 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
         if (t == 0 && !joined) p.joins[blockIdx.x].last = 0;
     } else {
         // -------------------------------------------------------------- softmax
-        const int grp = (warp - 4) / 4, quad = warp % 4, key = quad * 32 + lane;
+        const int quad = warp - 4, key = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tS = tmem + lane_addr + grp * K::kSCols;
-        const uint32_t tO = colO + lane_addr + grp * K::kOCols;
-        uint8_t* myP = sP + grp * K::kPBytes + key * 16;
-        constexpr int kOwn = C == 64 ? 2 : 1;   // columns whose reference this lane keeps
-        const int G = p.seq.group;
-        int c = 0, np = 0, ns = 0, npv = 0;
+        const uint32_t tO = colO + lane_addr;
+        uint8_t* myP = sP + key * 16;
+        int T = 0, np = 0;
         bool ok = true;
         while (walk.next(part)) {
             const int buf = np & 1;
             ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full[buf], np >> 1));
-            float l[C], ref[kOwn];
+            float l[C], ref = kNegInf;   // lane n keeps column n's reference
 #pragma unroll
             for (int n = 0; n < C; ++n) l[n] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) ref[i] = kNegInf;
-            const int nrows = min(C, part.req.n * G - part.row0);
-            bool fresh = true;
-            for (int i = ((c & 1) != grp) ? 1 : 0; i < part.tiles; i += 2) {
-                const int st = (c + i) % kStages;
+            const int nrows = min(C, part.req.n * p.seq.group - part.row0);
+            for (int i = 0; i < part.tiles; ++i, ++T) {
+                const int sc = T % kScaleSlots;
                 if (ok)
-                    ok = __all_sync(0xffffffffu, wait(&sm.kv_full[st], (c + i) / kStages) &&
-                                                     wait(&sm.s_full[grp], ns));
-                ++ns;
+                    ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots) &&
+                                                     wait(&sm.s_full[T & 1], T >> 1));
                 float t[C], inv_vs = 0.f;
                 if (ok) {
                     tc_fence_after();
                     const int kb = (part.tile0 + i) * kKeys, pos = kb + key;
-                    float ks = sm.scales[st][key / 16], vs = sm.scales[st][8 + key / 16];
+                    float ks = sm.scales[sc][key / 16], vs = sm.scales[sc][8 + key / 16];
                     const bool hidden = vs < 0.f || pos < part.lo_key || pos > part.hi_key ||
                                         pos >= part.req.len;
                     const bool edge = kb < part.all_lo || kb + kKeys - 1 > part.all_hi;
@@ -753,14 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll
                     for (int cc = 0; cc < C / 16; ++cc) {
                         float v[16];
-                        load_sum16<K::kWide ? K::kQ : 1>(tS + cc * 16, C, v);
+                        load_sum16<K::kQ>(tmem + lane_addr + (T & 1) * K::kSCols + cc * 16, C, v);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             t[cc * 16 + j] = fmaf(v[j], kc * sm.q_scale[buf][cc * 16 + j], lvs);
                     }
                     tc_fence_before();
-                    const bool some = !hidden && (pos < part.all_lo || pos > part.all_hi);
                     if (edge || __any_sync(0xffffffffu, hidden)) {
+                        const bool some = !hidden && (pos < part.all_lo || pos > part.all_hi);
 #pragma unroll
                         for (int n = 0; n < C; ++n) {
                             const int rp = sm.row_pos[buf][n];
@@ -768,8 +814,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
                                                          (pos <= rp && (p.seq.window <= 0 || rp - pos < p.seq.window)));
                             if (!see) t[n] = kNegInf;
                         }
-                        // 0 * NaN is NaN: no row's product may meet a NaN that it does not see
-                        uint4* vrow = reinterpret_cast<uint4*>(sKV + st * K::kStageBytes + K::kSide + key * D);
+                        // 0 * NaN is NaN: no row's product may meet a NaN that it does not
+                        // see.  (The values have to be there to be looked at.)
+                        const int vi = 2 * T + 1;
+                        ok = __all_sync(0xffffffffu, wait(&sm.kv_full[vi % kSlots], vi / kSlots));
+                        uint4* vrow = reinterpret_cast<uint4*>(sKV + (vi % kSlots) * K::kSlotBytes + key * D);
                         if (hidden) {
 #pragma unroll
                             for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0, 0, 0, 0);
@@ -786,52 +835,48 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
                                     w.z &= ~(e | (e - (e >> 7)));
                                     w.w &= ~(f | (f - (f >> 7)));
                                     vrow[u] = w;
-                                    sm.poison[buf] = 1;
+                                    sm.poison = 1;
                                 }
                             }
                         }
                     }
-                    float mine[kOwn];
+                    float mine = kNegInf;
 #pragma unroll
-                    for (int i2 = 0; i2 < kOwn; ++i2) mine[i2] = kNegInf;
+                    for (int n4 = 0; n4 < C; n4 += 4)
+                        if (n4 < nrows) {
 #pragma unroll
-                    for (int n = 0; n < C; ++n) {
-                        const float m = warp_max(t[n]);
-                        if (lane == (n & 31)) mine[n / 32] = m;
-                    }
-#pragma unroll
-                    for (int i2 = 0; i2 < kOwn; ++i2)
-                        if (lane + 32 * i2 < C) sm.wmax[grp][ns & 1][quad][lane + 32 * i2] = mine[i2];
-                }
-                named_bar_sync(kBarMax + grp, 128);
-                if (ok) {
-                    // every warp of the group comes to the same references
-                    bool moved = false;
-#pragma unroll
-                    for (int i2 = 0; i2 < kOwn; ++i2) {
-                        const int n = lane + 32 * i2;
-                        if (n < C) {
-                            const auto& wm = sm.wmax[grp][ns & 1];
-                            const float m = fmaxf(fmaxf(wm[0][n], wm[1][n]), fmaxf(wm[2][n], wm[3][n]));
-                            float f = 1.f;
-                            if (m > ref[i2]) {
-                                f = ex2_approx(ref[i2] - m);
-                                ref[i2] = m;
-                                moved = true;
+                            for (int n = n4; n < n4 + 4; ++n) {
+                                const float m = warp_max(t[n]);
+                                if (lane == n) mine = m;
                             }
-                            sm.fac[warp - 4][n] = f;
-                            sm.ref[warp - 4][n] = (ref[i2] == kNegInf ? 0.f : ref[i2]) - kShift;
                         }
+                    if (lane < C) sm.wmax[T & 1][quad][lane] = mine;
+                }
+                named_bar_sync(kBarMax, 128);
+                if (ok) {
+                    // every warp comes to the same references
+                    bool moved = false;
+                    if (lane < C) {
+                        const auto& wm = sm.wmax[T & 1];
+                        const float m = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
+                        float f = 1.f;
+                        if (m > ref) {
+                            f = ex2_approx(ref - m);
+                            ref = m;
+                            moved = true;
+                        }
+                        sm.fac[quad][lane] = f;
+                        sm.ref[quad][lane] = (ref == kNegInf ? 0.f : ref) - kShift;
                     }
                     moved = __any_sync(0xffffffffu, moved);
                     __syncwarp();
-                    // the group's last product has read its weights and left its sums
-                    if (npv > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done[grp], npv - 1));
+                    // the last product has read its weights and left its sums
+                    if (T > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
                     if (ok) {
-                        if (moved && !fresh) {
+                        if (moved && i > 0) {
                             tc_fence_after();
 #pragma unroll
-                            for (int n = 0; n < C; ++n) l[n] *= sm.fac[warp - 4][n];
+                            for (int n = 0; n < C; ++n) l[n] *= sm.fac[quad][n];
 #pragma unroll
                             for (int cc = 0; cc < K::kOCols / 16; ++cc) {
                                 uint32_t r[16];
@@ -841,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
                                     r[j] = __float_as_uint(__uint_as_float(r[j]) *
-                                                           sm.fac[warp - 4][(cc * 16 + j) % C]);
+                                                           sm.fac[quad][(cc * 16 + j) % C]);
                                 tmem_st16(tO + cc * 16, r);
                             }
                             tmem_st_wait();
@@ -852,11 +897,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const int n = cc * 16 + 2 * j;
-                                const float w0 = ex2_approx(t[n] - sm.ref[warp - 4][n]);
-                                const float w1 = ex2_approx(t[n + 1] - sm.ref[warp - 4][n + 1]);
-                                l[n] = fmaf(w0, inv_vs, l[n]);
-                                l[n + 1] = fmaf(w1, inv_vs, l[n + 1]);
-                                h[j] = pack2<kElemF16>(w0, w1);
+                                h[j] = 0;
+                                if (n / 4 * 4 < nrows) {
+                                    const float w0 = ex2_approx(t[n] - sm.ref[quad][n]);
+                                    const float w1 = ex2_approx(t[n + 1] - sm.ref[quad][n + 1]);
+                                    l[n] = fmaf(w0, inv_vs, l[n]);
+                                    l[n + 1] = fmaf(w1, inv_vs, l[n + 1]);
+                                    h[j] = pack2<kElemF16>(w0, w1);
+                                }
                             }
 #pragma unroll
                             for (int q = 0; q < K::kP; ++q) {
@@ -880,104 +928,67 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kv8_kernel(const __grid_co
                         fence_proxy_async_smem();
                     }
                 }
-                ++npv;
-                fresh = false;
-                named_bar_signal(kBarP + grp, 160, ok);
+                named_bar_signal(kBarP, 160, ok);
             }
             // ------------------------------------------------ the part's end
-            if (ok && !fresh) ok = __all_sync(0xffffffffu, wait(&sm.pv_done[grp], npv - 1));
+            if (ok && part.tiles > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
             tc_fence_after();
             warp_sums(l, lane);
             if (C == 16) {
-                if ((lane & 1) == 0) sm.part_sum[grp][quad][lane >> 1] = l[0];
-            } else if (C == 32) {
-                sm.part_sum[grp][quad][lane] = l[0];
+                if ((lane & 1) == 0) sm.part_sum[buf][quad][lane >> 1] = l[0];
             } else {
-                sm.part_sum[grp][quad][2 * lane] = l[0];
-                sm.part_sum[grp][quad][2 * lane + 1] = l[1];
+                sm.part_sum[buf][quad][lane] = l[0];
             }
-            if (quad == 0) {
-#pragma unroll
-                for (int i2 = 0; i2 < kOwn; ++i2)
-                    if (lane + 32 * i2 < C) sm.stat[grp][lane + 32 * i2].x = ref[i2];
-            }
-            tc_fence_before();
-            named_bar_sync(kBarEnd, 256);
-            tc_fence_after();
-            const bool had0 = part.tiles > 1 || (part.tiles == 1 && (c & 1) == 0);
-            const bool had1 = part.tiles > 1 || (part.tiles == 1 && (c & 1) == 1);
-            const bool poison = sm.poison[buf] != 0;
+            named_bar_sync(kBarMax, 128);
+            const bool poison = sm.poison != 0;
             if (ok) {
-#pragma unroll 1
-                for (int n0 = grp * (C / 2); n0 < grp * (C / 2) + C / 2 && n0 < nrows; n0 += 8) {
-                    float o0[8], o1[8];
-                    const uint32_t at = colO + lane_addr + n0;
-                    constexpr int kSets = K::kWide ? K::kP : 1;
-                    if (had0) load_sum8<kSets>(at, C, o0);
-                    if (had1) load_sum8<kSets>(at + K::kOCols, C, o1);
-                    uint32_t spoilt = 0;   // columns of these 8 that see a NaN in this channel
-                    if (poison && key < D) {
-                        const int first = part.tile0 * kKeys, past = first + part.tiles * kKeys;
-                        for (int j = max(first, part.lo_key); j < min(past, part.hi_key + 1); ++j) {
-                            if (j >= part.all_lo && j <= part.all_hi) {
-                                j = min(part.all_hi, past - 1);   // seen by all: the product has it
-                                continue;
-                            }
-                            const int id = __ldg(p.table + static_cast<long long>(part.b) * p.width +
-                                                 (j >> p.page_log2));
-                            if (id < 0 || id >= p.num_pages) continue;
-                            const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
-                                                (j & ((1 << p.page_log2) - 1));
-                            if ((__ldg(p.v8 + r * D + key) & 0x7f) != 0x7f) continue;
-                            for (int n = 0; n < 8; ++n) {
-                                const int rp = sm.row_pos[buf][n0 + n];
-                                if (j <= rp && (p.seq.window <= 0 || rp - j < p.seq.window)) spoilt |= 1u << n;
-                            }
-                        }
+                // lane n: column n's sum, and what its accumulators are multiplied by
+                const long long slot = 2LL * blockIdx.x + (part.begins ? 1 : 0);
+                if (lane < C) {
+                    const float sum = (sm.part_sum[buf][0][lane] + sm.part_sum[buf][1][lane]) +
+                                      (sm.part_sum[buf][2][lane] + sm.part_sum[buf][3][lane]);
+                    sm.fac[quad][lane] = !part.whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;   // (NaN divides on)
+                    if (quad == 0 && lane < nrows) {
+                        if (!part.whole)
+                            p.part_stat[slot * C + lane] = make_float2(ref, sum);
+                        else if (fa_index_ok(sm.out_at[buf][lane], static_cast<long long>(p.seq.total_tokens) * p.seq.Hq * D, p.status))
+                            p.lse[sm.lse_at[buf][lane]] =
+                                sum != 0.f ? ((ref == kNegInf ? 0.f : ref) - kShift + log2f(sum)) * kLn2 : kNegInf;
                     }
+                }
+                __syncwarp();
+#pragma unroll 1
+                for (int n0 = 0; n0 < nrows; n0 += 8) {
+                    float o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = 0.f;
+                    if (part.tiles > 0) load_sum8<K::kWideO ? K::kP : 1>(tO + n0, C, o);
+                    uint32_t spoilt = 0;   // columns of these 8 that see a NaN in this channel
+                    if (poison && key < D) spoilt = find_nan<D, C>(p, part, sm, buf, n0, key);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int n = n0 + j;
-                        const float r0 = sm.stat[0][n].x, r1 = sm.stat[1][n].x;
-                        const float m = fmaxf(r0, r1), mx = m == kNegInf ? 0.f : m;
-                        const float f0 = ex2_approx(r0 - mx), f1 = ex2_approx(r1 - mx);
-                        float sum = 0.f, o = 0.f;
-                        if (had0) {
-                            sum = f0 * ((sm.part_sum[0][0][n] + sm.part_sum[0][1][n]) +
-                                        (sm.part_sum[0][2][n] + sm.part_sum[0][3][n]));
-                            o = f0 * o0[j];
-                        }
-                        if (had1) {
-                            sum += f1 * ((sm.part_sum[1][0][n] + sm.part_sum[1][1][n]) +
-                                         (sm.part_sum[1][2][n] + sm.part_sum[1][3][n]));
-                            o = fmaf(f1, o1[j], o);
-                        }
-                        if ((spoilt >> j) & 1u) o = __uint_as_float(0x7fc00000u);
-                        if (n >= nrows) continue;
+                        float x = o[j] * sm.fac[quad][n];
+                        if ((spoilt >> j) & 1u) x = __uint_as_float(0x7fc00000u);
+                        if (n >= nrows || key >= D) continue;
                         if (part.whole) {
-                            const int r = part.row0 + n, tok = r / G, head = part.h * G + r % G;
-                            const long long row = part.req.start + tok;
-                            const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (NaN divides on)
-                            if (key < D && fa_index_ok(row, p.seq.total_tokens, p.status))
-                                static_cast<uint16_t*>(p.o)[(row * p.seq.Hq + head) * D + key] =
-                                    static_cast<uint16_t>(pack2<E>(o * inv, 0.f));
-                            if (key == 0 && fa_index_ok(row, p.seq.total_tokens, p.status))
-                                p.lse[row_stat_index(p.seq, part.b, head, part.req.start, tok)] =
-                                    sum != 0.f ? (mx - kShift + log2f(sum)) * kLn2 : kNegInf;
+                            const long long at = sm.out_at[buf][n] + key;
+                            if (fa_index_ok(at, static_cast<long long>(p.seq.total_tokens) * p.seq.Hq * D, p.status))
+                                static_cast<uint16_t*>(p.o)[at] = static_cast<uint16_t>(pack2<E>(x, 0.f));
                         } else {
-                            const long long at2 =
-                                (2LL * blockIdx.x + (part.begins ? 1 : 0)) * C + n;
-                            if (key < D) p.part_o[at2 * D + key] = o;
-                            if (key == 0) p.part_stat[at2] = make_float2(m, sum);
+                            p.part_o[(slot * C + n) * D + key] = x;
                         }
                     }
                 }
             }
             tc_fence_before();
-            named_bar_sync(kBarFree, 256);
-            if (threadIdx.x == 128) sm.poison[buf] = 0;
+            if (poison) {   // (uniform) taken back once all have read it, before any sets it again
+                named_bar_sync(kBarMax, 128);
+                if (key == 0) sm.poison = 0;
+                named_bar_sync(kBarMax, 128);
+            }
+            __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[buf]));
-            c += part.tiles;
             ++np;
         }
     }
@@ -1032,7 +1043,7 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
 template <int D, int E, int C>
 cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
     constexpr int smem = kv8_smem_bytes<D, E, C>();
-    static_assert(smem <= 232448, "shared memory per CTA");
+    static_assert(smem <= kCtaSmem, "shared memory per CTA");
     auto kern = fa_fwd_kv8_kernel<D, E, C>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1044,9 +1055,7 @@ template <int D, int E>
 cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
     cudaError_t e = ev ? cudaEventRecord(ev[0], stream) : cudaSuccess;
     if (e == cudaSuccess)
-        e = p.columns == 16   ? launch_attend<D, E, 16>(p, stream)
-            : p.columns == 32 ? launch_attend<D, E, 32>(p, stream)
-                              : launch_attend<D, E, 64>(p, stream);
+        e = p.columns == 16 ? launch_attend<D, E, 16>(p, stream) : launch_attend<D, E, 32>(p, stream);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
