@@ -1111,6 +1111,7 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     if (static_cast<long long>(num_pages) * Hkv > INT_MAX)
         return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: num_pages * Hkv = %lld is 2^31 or more",
                     static_cast<long long>(num_pages) * Hkv);
+    p.group_inv = static_cast<uint32_t>(((1ull << 32) + g.seq.group - 1) / g.seq.group);
     p.columns = kv8_columns(N, g.seq.group);
     p.ctas = 2 * sm_count();
     const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);

@@ -21,10 +21,10 @@
 //   P   as fp16 (11 bits), cut into e5m2 pieces of 3 bits (the high byte of an fp16 number
 //       is an e5m2 number): 3 pieces for bf16 outputs, the last one rounded (9 bits, one
 //       more than bf16 holds), 4 for fp16 (all 11).  e5m2 rather than e4m3 because long
-//       contexts need its range: weights are kept down to 2^-31 of the largest.
+//       contexts need its range: weights are kept down to 2^-28 of the largest.
 // V's scale joins the exponent: with t_j = s_j + log2(v_scale_j) and M the running maximum
-// of t, the weights 2^(t_j - M) are at most 1 whatever the scales, and the sum of the
-// probabilities is that of 2^(t_j - M) / v_scale_j.
+// of t (or a little less, see kGrow), the weights 2^(t_j - M) are near 1 at most whatever the
+// scales, and the sum of the probabilities is that of 2^(t_j - M) / v_scale_j.
 //
 // Work split.  The key tiles of all items (request, key/value head, C rows) lie one behind
 // the other and every CTA, two per SM, takes an equal share of them (kItemCost more tiles
@@ -55,8 +55,12 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeys = 128;          // keys of a tile
 constexpr int kItemCost = 1;        // an item's fixed cost in tiles
-// Weights are at most 1 before this factor 2^15 (and 2^15 < 65504, fp16's largest).
-constexpr float kShift = 15.f;
+// Weights are kept times 2^12.  A column's reference M moves when a key exceeds it by more
+// than 2^3 (its weight then is above 2^15, near fp16's largest number, 65504), so that it
+// mostly does not: the maxima over the lanes and the accumulators' rescaling are rare.
+constexpr float kShift = 12.f;
+constexpr float kGrow = 3.f;
+constexpr float kNone = -1e30f;     // in place of a column's reference that has none yet
 constexpr int kWindow = 128;        // requests whose lengths a CTA keeps in shared memory
 constexpr int kThreads = 256;
 
@@ -96,8 +100,17 @@ __device__ __forceinline__ Items items_of(const Kv8FwdParams& p, const Request& 
     return it;
 }
 
+// 64-bit division that mostly is a 32-bit one.
+__device__ __forceinline__ long long divide(long long a, int b) {
+    if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // CTA c of G takes units [c total / G, (c + 1) total / G) of `total`.
-__device__ __forceinline__ long long share_begin(long long total, int c, int G) { return total * c / G; }
+__device__ __forceinline__ long long share_begin(long long total, int c, int G) {
+    const long long q = divide(total, G);
+    return q * c + divide((total - q * G) * c, G);
+}
 __device__ __forceinline__ int share_of(long long total, long long unit, int G) {
     return static_cast<int>(((unit + 1) * G - 1) / total);
 }
@@ -137,7 +150,7 @@ struct Walk {
         load();
     }
     __device__ void load() {
-        if (b >= p.seq.B) return;
+        if (b >= p.seq.B || left == 0) return;
         if (b - b0 < kWindow) {
             const int3 w = window[b - b0];
             req.start = w.x;
@@ -222,7 +235,7 @@ constexpr int kScaleSlots = 16;   // tiles whose scales are kept: more than the 
 template <int C>
 struct Kv8Smem {   // behind the tiles
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
-    float q_scale[2][C];
+    alignas(16) float q_scale[2][C];
     int row_pos[2][C];               // position of the row's token; INT_MIN: no row
     long long out_at[2][C], lse_at[2][C];
     float wmax[2][4][C];             // [tile parity][warp]
@@ -363,8 +376,14 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// a / b for 0 <= a < 2^16, with inv = ceil(2^32 / b): the product is within 2^-16 of a / b
+// from above.  (b = 1: inv would be 2^32.)
+__device__ __forceinline__ int small_div(int a, int b, uint32_t inv) {
+    if (b == 1) return a;
+    return a < 65536 ? static_cast<int>(__umulhi(static_cast<uint32_t>(a), inv)) : a / b;
+}
+
 // Finds this CTA's share: sums of the requests' units, by all threads.
-template <int C>
 __device__ __forceinline__ long long block_units(long long v, long long* warp_sums, long long* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -387,50 +406,60 @@ __device__ __forceinline__ long long block_units(long long v, long long* warp_su
 }
 
 template <int C>
-__device__ __forceinline__ long long units_of(const Kv8FwdParams& p, int b) {
-    if (b >= p.seq.B) return 0;
-    const Items it = items_of<C>(p, load_request(p, b));
-    return static_cast<long long>(it.blocks) * p.seq.Hkv * it.cost;
-}
-
-template <int C>
 __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm) {
     const int cta = blockIdx.x, G = gridDim.x, B = p.seq.B;
-    const long long first = units_of<C>(p, threadIdx.x);
+    long long begin = 0, before = 0, total = 0;
+    Request r{0, 0, 0};
+    auto units = [&](int b) -> long long {
+        if (b >= B) return 0;
+        r = load_request(p, b);
+        const Items it = items_of<C>(p, r);
+        return static_cast<long long>(it.blocks) * p.seq.Hkv * it.cost;
+    };
+    // request b's units end at `end`, `mine` of them: does the share begin there?
+    auto look = [&](int b, long long mine, long long end) {
+        if (begin >= end - mine && begin < end) {
+            const Items it = items_of<C>(p, r);
+            const long long at = begin - (end - mine), item = divide(at, it.cost);
+            const int h = static_cast<int>(divide(item, it.blocks));
+            sm.share.b0 = b;
+            sm.share.off = static_cast<int>(at - item * it.cost);
+            sm.share.h = h;
+            sm.share.blk = static_cast<int>(item - static_cast<long long>(h) * it.blocks);
+        }
+    };
+    const long long first = units(threadIdx.x);
     long long sum = first;
-    for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units_of<C>(p, b);
-    long long total;
-    long long upto = block_units<C>(sum, sm.warp_sums, &total);
-    const long long begin = share_begin(total, cta, G);
+    for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units(b);
+    const long long upto = block_units(sum, sm.warp_sums, &total);
+    begin = share_begin(total, cta, G);
     if (threadIdx.x == 0) {
         sm.share.begin = begin;
         sm.share.end = share_begin(total, cta + 1, G);
         sm.share.total = total;
     }
-    auto look = [&](int b, long long mine, long long end) {
-        if (begin >= end - mine && begin < end) {
-            const Items it = items_of<C>(p, load_request(p, b));
-            const long long at = begin - (end - mine), item = at / it.cost;
-            sm.share.b0 = b;
-            sm.share.off = static_cast<int>(at - item * it.cost);
-            sm.share.h = static_cast<int>(item / it.blocks);
-            sm.share.blk = static_cast<int>(item % it.blocks);
-        }
-    };
     if (B <= kThreads) {
         look(threadIdx.x, first, upto);
+        __syncthreads();
+        const int at = static_cast<int>(threadIdx.x) - sm.share.b0;
+        if (at >= 0 && at < kWindow) sm.window[at] = make_int3(r.start, r.n, r.len);
     } else {
-        long long before = 0;
         for (int b0 = 0; b0 < B; b0 += kThreads) {
             const int b = b0 + threadIdx.x;
-            const long long mine = units_of<C>(p, b);
+            const long long mine = units(b);
             long long all;
-            upto = before + block_units<C>(mine, sm.warp_sums, &all);
-            look(b, mine, upto);
+            const long long end = before + block_units(mine, sm.warp_sums, &all);
+            look(b, mine, end);
             before += all;
         }
+        __syncthreads();
+        const int b = sm.share.b0 + threadIdx.x;
+        if (threadIdx.x < kWindow && sm.share.begin < total) {
+            r = Request{0, 0, 0};
+            if (b < B) r = load_request(p, b);
+            sm.window[threadIdx.x] = make_int3(r.start, r.n, r.len);
+        }
     }
-    __syncthreads();
 }
 
 // Which of the columns n0 .. n0 + 7 see a NaN code in this channel of a value that other
@@ -497,21 +526,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         mbar_init(smem_addr(&sm.all_done), 1);
         fence_barrier_init();
     }
-    find_share<C>(p, sm);
-    if (sm.share.begin == sm.share.end) {
-        if (threadIdx.x == 0) p.joins[blockIdx.x].last = 0;
-        return;
-    }
-    if (threadIdx.x < kWindow) {
-        const int b = sm.share.b0 + threadIdx.x;
-        Request r{0, 0, 0};
-        if (b < p.seq.B) r = load_request(p, b);
-        sm.window[threadIdx.x] = make_int3(r.start, r.n, r.len);
-    }
     if (warp == 1) {
         tmem_alloc(smem_addr(&sm.tmem), K::kTmemCols);
         tmem_relinquish();
     }
+    // what the kernels before this one wrote is there from here on
+    grid_dependency_wait();
+    find_share<C>(p, sm);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -521,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     auto wait = [&](uint64_t* bar, int phase) {
         return mbar_wait(smem_addr(bar), phase & 1, abort_flag, p.timeout_cycles, p.status);
     };
+    // (a CTA without a share has no parts)
     Walk<C> walk(p, sm.share, sm.window);
     Part part;
 
@@ -704,10 +726,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             if (ok) {
                 uint8_t* dst = sQ + buf * K::kQBytes;
                 const int G = p.seq.group, rows = part.req.n * G;
-#pragma unroll 4
+                const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
+#pragma unroll
                 for (int n = t / kLanes; n < C; n += kRows) {
                     const int r = part.row0 + n;
-                    const int tok = r / G, head = part.h * G + r % G;
+                    const int more = small_div(rem0 + n, G, p.group_inv);
+                    const int tok = tok0 + more, head = part.h * G + rem0 + n - more * G;
                     const long long token = part.req.start + tok;
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (r < rows)
@@ -778,7 +802,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 if (ok)
                     ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots) &&
                                                      wait(&sm.s_full[T & 1], T >> 1));
-                float t[C], inv_vs = 0.f;
+                float v[C], kc = 0.f, lvs = 0.f, inv_vs = 0.f;
+                uint32_t seen = ~0u;   // a bit per column
+                bool fits = true;      // no weight exceeds its reference by more than kGrow
+                const float4* qs = reinterpret_cast<const float4*>(sm.q_scale[buf]);
+                const float4* rf = reinterpret_cast<const float4*>(sm.ref[quad]);
                 if (ok) {
                     tc_fence_after();
                     const int kb = (part.tile0 + i) * kKeys, pos = kb + key;
@@ -786,33 +814,33 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                     const bool hidden = vs < 0.f || pos < part.lo_key || pos > part.hi_key ||
                                         pos >= part.req.len;
                     const bool edge = kb < part.all_lo || kb + kKeys - 1 > part.all_hi;
+#pragma unroll
+                    for (int cc = 0; cc < C / 16; ++cc)
+                        load_sum16<K::kQ>(tmem + lane_addr + (T & 1) * K::kSCols + cc * 16, C,
+                                          *reinterpret_cast<float(*)[16]>(&v[cc * 16]));
+                    tc_fence_before();
                     if (hidden) {
                         ks = 0.f;
                         vs = 1.f;
                     }
                     const uint32_t vb = __float_as_uint(vs);
-                    const float lvs = (vb & 0x7fffffu) == 0 && vb >= 0x00800000u
-                                          ? static_cast<float>(static_cast<int>(vb >> 23) - 127)
-                                          : log2f(vs);
-                    inv_vs = 1.f / vs;
-                    const float kc = ks * p.scale_log2;
-#pragma unroll
-                    for (int cc = 0; cc < C / 16; ++cc) {
-                        float v[16];
-                        load_sum16<K::kQ>(tmem + lane_addr + (T & 1) * K::kSCols + cc * 16, C, v);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            t[cc * 16 + j] = fmaf(v[j], kc * sm.q_scale[buf][cc * 16 + j], lvs);
+                    lvs = static_cast<float>(static_cast<int>(vb >> 23) - 127);
+                    inv_vs = __uint_as_float((254u << 23) - vb);
+                    if ((vb & 0x7fffffu) != 0 || vb < 0x00800000u || vb > 0x7e000000u) {
+                        // not a power of two, or one without a normal inverse
+                        lvs = log2f(vs);
+                        inv_vs = 1.f / vs;
                     }
-                    tc_fence_before();
+                    kc = ks * p.scale_log2;
                     if (edge || __any_sync(0xffffffffu, hidden)) {
                         const bool some = !hidden && (pos < part.all_lo || pos > part.all_hi);
+                        seen = hidden ? 0u : ~0u;
+                        if (some) {
 #pragma unroll
-                        for (int n = 0; n < C; ++n) {
-                            const int rp = sm.row_pos[buf][n];
-                            const bool see = !hidden && (!p.seq.causal ||
-                                                         (pos <= rp && (p.seq.window <= 0 || rp - pos < p.seq.window)));
-                            if (!see) t[n] = kNegInf;
+                            for (int n = 0; n < C; ++n) {
+                                const int rp = sm.row_pos[buf][n];
+                                if (pos > rp || (p.seq.window > 0 && rp - pos >= p.seq.window)) seen &= ~(1u << n);
+                            }
                         }
                         // 0 * NaN is NaN: no row's product may meet a NaN that it does not
                         // see.  (The values have to be there to be looked at.)
@@ -823,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll
                             for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0, 0, 0, 0);
                         } else if (some) {
-#pragma unroll
+#pragma unroll 1
                             for (int u = 0; u < D / 16; ++u) {
                                 uint4 w = vrow[u];
                                 const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), e = nan_bytes(w.z),
@@ -840,93 +868,119 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                             }
                         }
                     }
-                    float mine = kNegInf;
+                    // e_n = t_n - M_n + kShift, in place of the products
+                    if (i > 0) {
+                        float top = kNegInf;
 #pragma unroll
-                    for (int n4 = 0; n4 < C; n4 += 4)
-                        if (n4 < nrows) {
+                        for (int n4 = 0; n4 < C; n4 += 4)
+                            if (n4 < nrows) {
+                                const float4 q4 = qs[n4 / 4], r4 = rf[n4 / 4];
+                                const float qq[4] = {q4.x, q4.y, q4.z, q4.w}, rr[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
-                            for (int n = n4; n < n4 + 4; ++n) {
-                                const float m = warp_max(t[n]);
-                                if (lane == n) mine = m;
+                                for (int j = 0; j < 4; ++j)
+                                    if ((seen >> (n4 + j)) & 1u)
+                                        top = fmaxf(top, fmaf(v[n4 + j], kc * qq[j], lvs - rr[j]));
                             }
-                        }
-                    if (lane < C) sm.wmax[T & 1][quad][lane] = mine;
-                }
-                named_bar_sync(kBarMax, 128);
-                if (ok) {
-                    // every warp comes to the same references
-                    bool moved = false;
-                    if (lane < C) {
-                        const auto& wm = sm.wmax[T & 1];
-                        const float m = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
-                        float f = 1.f;
-                        if (m > ref) {
-                            f = ex2_approx(ref - m);
-                            ref = m;
-                            moved = true;
-                        }
-                        sm.fac[quad][lane] = f;
-                        sm.ref[quad][lane] = (ref == kNegInf ? 0.f : ref) - kShift;
+                        fits = top <= kShift + kGrow;
+                    } else {
+                        fits = false;
                     }
-                    moved = __any_sync(0xffffffffu, moved);
-                    __syncwarp();
-                    // the last product has read its weights and left its sums
-                    if (T > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
+                }
+                if (!named_bar_all(kBarMax, 128, fits)) {
+                    // new references: the maxima over the tile's keys
+                    float mine = kNegInf;
                     if (ok) {
-                        if (moved && i > 0) {
+#pragma unroll
+                        for (int n4 = 0; n4 < C; n4 += 4)
+                            if (n4 < nrows) {
+#pragma unroll
+                                for (int n = n4; n < n4 + 4; ++n) {
+                                    const float m = warp_max((seen >> n) & 1u ? fmaf(v[n], kc * sm.q_scale[buf][n], lvs)
+                                                                              : kNegInf);
+                                    if (lane == n) mine = m;
+                                }
+                            }
+                        if (lane < C) sm.wmax[T & 1][quad][lane] = mine;
+                    }
+                    named_bar_sync(kBarMax, 128);
+                    if (ok) {
+                        // every warp comes to the same ones
+                        if (lane < C) {
+                            const auto& wm = sm.wmax[T & 1];
+                            const float m = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
+                            float f = 1.f;
+                            if (m > ref) {
+                                f = ex2_approx(ref - m);
+                                ref = m;
+                            }
+                            sm.fac[quad][lane] = f;
+                            sm.ref[quad][lane] = ref == kNegInf ? kNone : ref - kShift;
+                        }
+                        __syncwarp();
+                        if (i > 0) {
+                            ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
                             tc_fence_after();
 #pragma unroll
                             for (int n = 0; n < C; ++n) l[n] *= sm.fac[quad][n];
-#pragma unroll
-                            for (int cc = 0; cc < K::kOCols / 16; ++cc) {
+#pragma unroll 1
+                            for (int cc = 0; cc < K::kOCols; cc += 16) {
                                 uint32_t r[16];
-                                tmem_ld16(tO + cc * 16, r);
+                                tmem_ld16(tO + cc, r);
                                 tmem_ld_wait();
                                 reg_fence(r);
+                                const float* fc = &sm.fac[quad][cc % C];
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
-                                    r[j] = __float_as_uint(__uint_as_float(r[j]) *
-                                                           sm.fac[quad][(cc * 16 + j) % C]);
-                                tmem_st16(tO + cc * 16, r);
+                                    r[j] = __float_as_uint(__uint_as_float(r[j]) * fc[j]);
+                                tmem_st16(tO + cc, r);
                             }
                             tmem_st_wait();
                         }
-#pragma unroll
-                        for (int cc = 0; cc < C / 16; ++cc) {
-                            uint32_t h[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int n = cc * 16 + 2 * j;
-                                h[j] = 0;
-                                if (n / 4 * 4 < nrows) {
-                                    const float w0 = ex2_approx(t[n] - sm.ref[quad][n]);
-                                    const float w1 = ex2_approx(t[n + 1] - sm.ref[quad][n + 1]);
-                                    l[n] = fmaf(w0, inv_vs, l[n]);
-                                    l[n + 1] = fmaf(w1, inv_vs, l[n + 1]);
-                                    h[j] = pack2<kElemF16>(w0, w1);
-                                }
-                            }
-#pragma unroll
-                            for (int q = 0; q < K::kP; ++q) {
-                                // the last of 3 pieces is rounded, the others (and the fourth,
-                                // which is all that is left) are the leading bits
-                                if (q == 2 && K::kP == 3)
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) h[j] += 0x00800080u;
-                                uint4 w;
-                                w.x = __byte_perm(h[0], h[1], 0x7531);
-                                w.y = __byte_perm(h[2], h[3], 0x7531);
-                                w.z = __byte_perm(h[4], h[5], 0x7531);
-                                w.w = __byte_perm(h[6], h[7], 0x7531);
-                                *reinterpret_cast<uint4*>(myP + (q * (C / 16) + cc) * kKeys * 16) = w;
-                                if (q + 1 < K::kP)
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
-                            }
-                        }
-                        tc_fence_before();
-                        fence_proxy_async_smem();
                     }
+                }
+                // the last product has read its weights
+                if (ok && T > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
+                if (ok) {
+#pragma unroll
+                    for (int cc = 0; cc < C / 16; ++cc) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) h[j] = 0;
+#pragma unroll
+                        for (int n4 = cc * 16; n4 < cc * 16 + 16; n4 += 4)
+                            if (n4 < nrows) {
+                                const float4 q4 = qs[n4 / 4], r4 = rf[n4 / 4];
+                                const float qq[4] = {q4.x, q4.y, q4.z, q4.w}, rr[4] = {r4.x, r4.y, r4.z, r4.w};
+                                float w[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const float e = fmaf(v[n4 + j], kc * qq[j], lvs - rr[j]);
+                                    w[j] = ex2_approx((seen >> (n4 + j)) & 1u ? e : kNegInf);
+                                    l[n4 + j] = fmaf(w[j], inv_vs, l[n4 + j]);
+                                }
+                                h[n4 % 16 / 2] = pack2<kElemF16>(w[0], w[1]);
+                                h[n4 % 16 / 2 + 1] = pack2<kElemF16>(w[2], w[3]);
+                            }
+#pragma unroll
+                        for (int q = 0; q < K::kP; ++q) {
+                            // the last of 3 pieces is rounded, the others (and the fourth,
+                            // which is all that is left) are the leading bits
+                            if (q == 2 && K::kP == 3)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) h[j] += 0x00800080u;
+                            uint4 w;
+                            w.x = __byte_perm(h[0], h[1], 0x7531);
+                            w.y = __byte_perm(h[2], h[3], 0x7531);
+                            w.z = __byte_perm(h[4], h[5], 0x7531);
+                            w.w = __byte_perm(h[6], h[7], 0x7531);
+                            *reinterpret_cast<uint4*>(myP + (q * (C / 16) + cc) * kKeys * 16) = w;
+                            if (q + 1 < K::kP)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
+                        }
+                    }
+                    tc_fence_before();
+                    fence_proxy_async_smem();
                 }
                 named_bar_signal(kBarP, 160, ok);
             }
@@ -1002,6 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 // warp per row, the parts in their order.
 template <int D, int E>
 __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
+    grid_launch_dependents();
     grid_dependency_wait();
     const int cta = blockIdx.x;
     const Kv8Join j = p.joins[cta];
@@ -1040,6 +1095,23 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     }
 }
 
+// A launch that may begin while the kernel before it on the stream is ending (it waits for
+// that one's results itself).
+cudaError_t launch_dependent(void (*kern)(Kv8FwdParams), int grid, int threads, int smem,
+                             cudaStream_t stream, const Kv8FwdParams& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int D, int E, int C>
 cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
     constexpr int smem = kv8_smem_bytes<D, E, C>();
@@ -1047,8 +1119,7 @@ cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
     auto kern = fa_fwd_kv8_kernel<D, E, C>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<p.ctas, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kern, p.ctas, kThreads, smem, stream, p);
 }
 
 template <int D, int E>
@@ -1058,16 +1129,7 @@ cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream
         e = p.columns == 16 ? launch_attend<D, E, 16>(p, stream) : launch_attend<D, E, 32>(p, stream);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ctas);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fa_fwd_kv8_join_kernel<D, E>, p);
+    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, p.ctas, 256, 0, stream, p);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[2], stream);
     return e;
 }
