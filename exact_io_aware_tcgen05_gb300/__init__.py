@@ -14,6 +14,7 @@ the C ABI.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -455,11 +456,11 @@ def _geometry(q, k, cu_seqlens, max_seqlen):
 def _dtype_code(*tensors) -> int:
     """fa_dtype of torch tensors that must all be bf16, or all fp16."""
     import torch
-    codes = {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_F16}
+    first = tensors[0].dtype
+    if first in (torch.bfloat16, torch.float16) and all([t.dtype == first for t in tensors]):
+        return FA_DTYPE_BF16 if first == torch.bfloat16 else FA_DTYPE_F16
     kinds = {t.dtype for t in tensors}
-    if len(kinds) != 1 or next(iter(kinds)) not in codes:
-        raise TypeError(f"q, k, v (and o, dout) must all be bfloat16 or all float16, got {kinds}")
-    return codes[next(iter(kinds))]
+    raise TypeError(f"q, k, v (and o, dout) must all be bfloat16 or all float16, got {kinds}")
 
 
 def attention_forward(q, k, v, *, causal=False, window=0, scale=None, cu_seqlens=None,
@@ -568,82 +569,76 @@ def kv8_cache(num_pages, Hkv, d, *, page=64, device="cuda") -> Kv8Cache:
     return Kv8Cache((codes[0], scales[0], codes[1], scales[1]))
 
 
-def _kv8_shape(cache):
-    """(num_pages, Hkv, page, d) of a cache whose four tensors fit together."""
+def _kv8_shape(cache, device):
+    """The shape (num_pages, Hkv, page, d) of a cache whose four tensors fit together and are
+    on CUDA device number `device`."""
     import torch
     k8, k_scale, v8, v_scale = cache
+    shape, scales = k8.shape, k_scale.shape
     if k8.dtype != torch.float8_e4m3fn or v8.dtype != torch.float8_e4m3fn:
         raise TypeError("the cache's codes must be float8_e4m3fn")
     if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise TypeError("the cache's scales must be float32")
-    if k8.dim() != 4 or v8.shape != k8.shape:
+    if len(shape) != 4 or v8.shape != shape:
         raise ValueError("k8 and v8 must both be [num_pages, Hkv, page, d]")
-    num_pages, Hkv, page, d = shape = k8.shape
-    if k_scale.shape != v_scale.shape or k_scale.shape != (num_pages, Hkv, page // FA_KV8_BLOCK):
+    if v_scale.shape != scales or scales != (shape[0], shape[1], shape[2] // FA_KV8_BLOCK):
         raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page / 16]")
     if not (k8.is_contiguous() and v8.is_contiguous() and k_scale.is_contiguous()
             and v_scale.is_contiguous()):
         raise ValueError("the cache's tensors must be contiguous")
-    _same_device(k8, k_scale, v8, v_scale)
+    if not (k8.get_device() == k_scale.get_device() == v8.get_device() == v_scale.get_device() == device >= 0):
+        raise ValueError(_ONE_DEVICE)
     return shape
 
 
-def _same_device(first, *others):
-    dev = first.device
-    if dev.type != "cuda" or any(x.device != dev for x in others):
-        raise ValueError("all tensors must be on one CUDA device")
+_ONE_DEVICE = "all tensors must be on one CUDA device"
 
 
-def _int32(name, x, *shape):
-    """A contiguous int32 tensor of the given shape (None: any size)."""
+def _int32(name, x, shape, device):
+    """A contiguous int32 tensor of the given shape on CUDA device number `device`."""
     import torch
     if x.dtype != torch.int32 or not x.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor")
-    if x.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(x.shape)}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.get_device() != device or device < 0:
+        raise ValueError(_ONE_DEVICE)
 
 
 def _rows(name, x, heads, d):
     """Elements between the tokens of a [..., heads, d] tensor whose tokens are evenly spaced
     (a slice of a wider projection's output, say)."""
-    lead = x.shape[:-2]
-    ok = x.shape[-2:] == (heads, d) and x.stride(-1) == 1 and (heads == 1 or x.stride(-2) == d)
-    stride = x.stride(-3) if lead[-1] > 1 else 0
-    if len(lead) == 2 and lead[0] > 1:
-        outer = x.stride(0)
-        ok = ok and outer % lead[1] == 0 and (lead[1] == 1 or outer == stride * lead[1])
-        stride = outer // lead[1]
+    shape, strides = x.shape, x.stride()
+    stride = strides[-3] if shape[-3] > 1 else 0
+    ok = shape[-2] == heads and shape[-1] == d and strides[-1] == 1 and (heads == 1 or strides[-2] == d)
+    if len(shape) == 4 and shape[0] > 1:
+        n, outer = shape[1], strides[0]
+        ok = ok and outer % max(n, 1) == 0 and (n <= 1 or outer == stride * n)
+        stride = outer // max(n, 1)
     if not ok:
         raise ValueError(f"{name} must be [..., {heads}, {d}] with contiguous heads and evenly "
                          "spaced tokens")
     return stride or heads * d
 
 
-class _on:
-    """The device and stream of a call: the tensors' device becomes the current one and a
-    stream that was given the current stream, so that what the call allocates belongs to it."""
-    __slots__ = ("contexts",)
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream to run on `stream` (None: the
+    current one) of CUDA device number `device`."""
+    import torch
+    return stream is not None or device != torch.cuda.current_device()
 
-    def __init__(self, device, stream):
-        import torch
-        self.contexts = []
-        if device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-            self.contexts.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        import torch
-        for c in self.contexts:
-            c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-        return False
+def _there(call, device, stream, *args, **kwargs):
+    """`call` with CUDA device number `device`, and `stream` if given, as the current ones, so
+    that what the call allocates belongs to that stream."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
 
 
 def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
@@ -651,44 +646,61 @@ def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
     zero: the request has ended and gives its pages back), for int32 CUDA tensors lens and
     grow [B], table [B, width], ring [num_pages] and state [3] (first free page's place in
     the ring, free pages, refused requests).  table and ring are updated in place; the
-    outputs are new tensors, slots of ``tokens`` elements (-1 for tokens that get no place)."""
+    outputs are new tensors (parts of one), slots of ``tokens`` elements (-1 for tokens that
+    get no place)."""
+    dev = lens.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(kv8_plan, dev, stream, lens, grow, table, ring, state, page=page, tokens=tokens)
     import torch
-    _int32("lens", lens, None)
-    B = lens.shape[0]
-    _int32("grow", grow, B)
-    _int32("table", table, B, None)
-    _int32("ring", ring, None)
-    _int32("state", state, 3)
-    _same_device(lens, grow, table, ring, state)
+    if lens.dim() != 1 or table.dim() != 2 or ring.dim() != 1:
+        raise ValueError("lens must be [B], table [B, width], ring [num_pages]")
+    B, width = lens.shape[0], table.shape[1]
     tokens = int(tokens)
-    with _on(lens.device, stream) as s:
-        # one allocation, the parts 16-byte aligned
-        parts = [B, B + 1, max(tokens, 0), 3]
-        at = [0]
-        for n in parts:
-            at.append(at[-1] + (n + 3) // 4 * 4)
-        out = torch.empty(at[-1], dtype=torch.int32, device=lens.device)
-        lens_out, cu, slots, state_out = (out[a:a + n] for a, n in zip(at, parts))
-        fa_kv8_plan(lens, grow, B, table, table.shape[1], ring, ring.shape[0], page, state, lens_out,
-                    cu, slots, tokens, state_out, s)
+    if tokens < 0:
+        raise ValueError(f"tokens must be >= 0, got {tokens}")
+    _int32("lens", lens, (B,), dev)
+    _int32("grow", grow, (B,), dev)
+    _int32("table", table, (B, width), dev)
+    _int32("ring", ring, ring.shape, dev)
+    _int32("state", state, (3,), dev)
+    lens_out, cu, slots, state_out = torch.split_with_sizes(
+        lens.new_empty(2 * B + tokens + 4), (B, B + 1, tokens, 3))
+    at = lens_out.data_ptr()
+    _check(load().fa_kv8_plan(lens.data_ptr(), grow.data_ptr(), B, table.data_ptr(), width,
+                              ring.data_ptr(), ring.shape[0], page, state.data_ptr(), at, at + 4 * B,
+                              at + 8 * B + 4, tokens, at + 8 * B + 4 + 4 * tokens,
+                              torch._C._cuda_getCurrentRawStream(dev)))
     return lens_out, cu, slots, state_out
 
 
 def kv8_append(cache: Kv8Cache, k, v, slots, *, stream=None) -> None:
     """Writes the tokens k, v ([T, Hkv, d], both bf16 or both fp16, evenly spaced) into the
     cache at ``slots`` (int32 [T], see kv8_plan), in 8 bits."""
-    num_pages, Hkv, page, d = _kv8_shape(cache)
-    dtype = _dtype_code(k, v)
-    if k.dim() != 3 or k.shape != v.shape:
+    dev = k.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(kv8_append, dev, stream, cache, k, v, slots)
+    import torch
+    num_pages, Hkv, page, d = _kv8_shape(cache, dev)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must both be [T, Hkv, d]")
-    T = k.shape[0]
     stride = _rows("k", k, Hkv, d)
     if _rows("v", v, Hkv, d) != stride:
         raise ValueError("the tokens of k and v must be the same distance apart")
-    _int32("slots", slots, T)
-    _same_device(cache[0], k, v, slots)
-    with _on(k.device, stream) as s:
-        fa_kv8_append(dtype, k, v, stride, *cache, num_pages, page, Hkv, d, slots, T, s)
+    _int32("slots", slots, shape[:1], dev)
+    if v.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    k8, k_scale, v8, v_scale = cache
+    _check(load().fa_kv8_append(_dtype_code(k, v), k.data_ptr(), v.data_ptr(), stride, k8.data_ptr(),
+                                k_scale.data_ptr(), v8.data_ptr(), v_scale.data_ptr(), num_pages, page,
+                                Hkv, d, slots.data_ptr(), shape[0],
+                                torch._C._cuda_getCurrentRawStream(dev)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv8_workspace(device, B, Hq, Hkv, N, d, total_tokens):
+    """fa_fwd_kv8_workspace_size on CUDA device number `device`, the current one."""
+    return fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, total_tokens)
 
 
 def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, window=0, scale=None,
@@ -699,46 +711,56 @@ def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, windo
     cu_seqlens (int32 [B + 1]) and max_seqlen; its tokens may lie apart (a slice of a wider
     tensor).  table: int32 [B, width], lens: int32 [B], as kv8_plan keeps them.  Allocates
     what of the outputs and the workspace (uint8, fa_fwd_kv8_workspace_size) is not given."""
+    dev = q.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(attention_forward_kv8, dev, stream, q, cache, table, lens, causal=causal,
+                      window=window, scale=scale, cu_seqlens=cu_seqlens, max_seqlen=max_seqlen, out=out,
+                      lse=lse, workspace=workspace)
     import torch
-    num_pages, Hkv, page, d = _kv8_shape(cache)
     dtype = _dtype_code(q)
     packed = cu_seqlens is not None
-    _int32("lens", lens, None)
-    B = lens.shape[0]
-    _int32("table", table, B, None)
-    if q.dim() != (3 if packed else 4):
+    shape = q.shape
+    if len(shape) != (3 if packed else 4):
         raise ValueError("q must be [B, N, Hq, d], or [T, Hq, d] with cu_seqlens")
-    Hq = q.shape[-2]
+    if lens.dim() != 1 or table.dim() != 2:
+        raise ValueError("lens must be [B], table [B, width]")
+    Hq, d = shape[-2], shape[-1]
     stride = _rows("q", q, Hq, d)
+    B, width = lens.shape[0], table.shape[1]
+    _int32("lens", lens, (B,), dev)
+    _int32("table", table, (B, width), dev)
+    num_pages, Hkv, page, dk = _kv8_shape(cache, dev)
+    if dk != d:
+        raise ValueError(f"the cache's head dimension is {dk}, q's {d}")
     if packed:
         if max_seqlen is None:
             raise ValueError("packed batches need max_seqlen")
-        _int32("cu_seqlens", cu_seqlens, B + 1)
-        N, T = int(max_seqlen), q.shape[0]
-        _same_device(q, *cache, table, lens, cu_seqlens)
+        _int32("cu_seqlens", cu_seqlens, (B + 1,), dev)
+        N, T, lse_shape = int(max_seqlen), shape[0], (Hq, shape[0])
     else:
-        if q.shape[0] != B:
-            raise ValueError(f"q has {q.shape[0]} requests, lens {B}")
-        N, T = q.shape[1], 0
-        _same_device(q, *cache, table, lens)
-    scale = d ** -0.5 if scale is None else scale
-    lse_shape = (Hq, T) if packed else (B, Hq, N)
-    with _on(q.device, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-            raise ValueError("out must be contiguous, of q's shape and type")
-        if lse is None:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-        elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous float32 {lse_shape}")
-        if workspace is None:
-            workspace = torch.empty(fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, T),
-                                    dtype=torch.uint8, device=q.device)
-        _same_device(q, out, lse, workspace)
-        fa_fwd_kv8(dtype, q, stride, *cache, num_pages, page, table, table.shape[1], lens, out, lse,
-                   B, Hq, Hkv, N, d, causal, window, cu_seqlens, T, scale, workspace,
-                   workspace.numel() * workspace.element_size(), s)
+        if shape[0] != B:
+            raise ValueError(f"q has {shape[0]} requests, lens {B}")
+        N, T, lse_shape = shape[1], 0, (B, Hq, shape[1])
+    if out is None:
+        out = q.new_empty(shape)
+    elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError("out must be contiguous, of q's shape, type and device")
+    if lse is None:
+        lse = q.new_empty(lse_shape, dtype=torch.float32)
+    elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError(f"lse must be contiguous float32 {lse_shape} on q's device")
+    if workspace is None:
+        workspace = lens.new_empty(_kv8_workspace(dev, B, Hq, Hkv, N, d, T), dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on q's device")
+    k8, k_scale, v8, v_scale = cache
+    _check(load().fa_fwd_kv8(
+        dtype, q.data_ptr(), stride, k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(),
+        v_scale.data_ptr(), num_pages, page, table.data_ptr(), width, lens.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), B, Hq, Hkv, N, d, 1 if causal else 0, window,
+        cu_seqlens.data_ptr() if packed else None, T, d ** -0.5 if scale is None else scale,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        torch._C._cuda_getCurrentRawStream(dev)))
     return out, lse
 
 

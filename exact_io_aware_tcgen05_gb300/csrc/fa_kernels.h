@@ -153,7 +153,7 @@ struct Kv8Join {
     int b, h;        // request, key/value head
     int start, n;    // the request's first new token in the batch, and their count
     int row0;        // the item's first row (rows are (token, head of the group) pairs)
-    long long total; // units of all CTAs' shares
+    int pad[2];
 };
 
 struct Kv8FwdParams {

@@ -106,13 +106,18 @@ __device__ __forceinline__ long long divide(long long a, int b) {
     return a / b;
 }
 
-// CTA c of G takes units [c total / G, (c + 1) total / G) of `total`.
+// CTA c of the first G takes units [c total / G, (c + 1) total / G) of `total`; G is the
+// number of CTAs, or of units where there are fewer, so that no share among them is empty.
+__device__ __forceinline__ int sharers(long long total, int ctas) {
+    return static_cast<int>(min(total, static_cast<long long>(ctas)));
+}
 __device__ __forceinline__ long long share_begin(long long total, int c, int G) {
     const long long q = divide(total, G);
     return q * c + divide((total - q * G) * c, G);
 }
 __device__ __forceinline__ int share_of(long long total, long long unit, int G) {
-    return static_cast<int>(((unit + 1) * G - 1) / total);
+    const long long a = (unit + 1) * G - 1;
+    return (total >> 31) == 0 ? static_cast<int>(divide(a, static_cast<int>(total))) : static_cast<int>(a / total);
 }
 
 // One CTA's part of an item.
@@ -134,7 +139,7 @@ struct Share {
     int b0, h, blk, off;   // the request, head, block of rows and unit of that item it begins at
 };
 
-// A walk over a CTA's parts; every role of the CTA walks for itself.
+// A walk over a CTA's parts (the producer's; it hands them to the other roles).
 template <int C>
 struct Walk {
     const Kv8FwdParams& p;
@@ -230,6 +235,7 @@ struct Kv8Cfg {
 };
 
 constexpr int kMaxSlots = 12;
+constexpr int kParts = 4;         // parts the producer may be ahead
 constexpr int kScaleSlots = 16;   // tiles whose scales are kept: more than the ring is long
 
 template <int C>
@@ -244,8 +250,10 @@ struct Kv8Smem {   // behind the tiles
     float part_sum[2][4][C];         // [part parity][warp]
     int3 window[kWindow];
     Share share;
+    Part parts[kParts];
     long long warp_sums[kThreads / 32];
     uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
+    uint64_t part_full[kParts], part_empty[kParts];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], pv_done;
     uint64_t all_done;
@@ -407,7 +415,7 @@ __device__ __forceinline__ long long block_units(long long v, long long* warp_su
 
 template <int C>
 __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm) {
-    const int cta = blockIdx.x, G = gridDim.x, B = p.seq.B;
+    const int cta = blockIdx.x, B = p.seq.B;
     long long begin = 0, before = 0, total = 0;
     Request r{0, 0, 0};
     auto units = [&](int b) -> long long {
@@ -432,10 +440,11 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm
     long long sum = first;
     for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units(b);
     const long long upto = block_units(sum, sm.warp_sums, &total);
-    begin = share_begin(total, cta, G);
+    const int G = sharers(total, gridDim.x);
+    begin = cta < G ? share_begin(total, cta, G) : total;
     if (threadIdx.x == 0) {
         sm.share.begin = begin;
-        sm.share.end = share_begin(total, cta + 1, G);
+        sm.share.end = cta < G ? share_begin(total, cta + 1, G) : total;
         sm.share.total = total;
     }
     if (B <= kThreads) {
@@ -517,6 +526,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             mbar_init(smem_addr(&sm.kv_empty[i]), 1);
         }
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(smem_addr(&sm.part_full[i]), 1);
+            mbar_init(smem_addr(&sm.part_empty[i]), 5);   // the issuer, 4 softmax warps
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sm.q_full[i]), 64);
             mbar_init(smem_addr(&sm.q_empty[i]), 5);    // the last S^T of the part, 4 softmax warps
@@ -542,8 +555,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     auto wait = [&](uint64_t* bar, int phase) {
         return mbar_wait(smem_addr(bar), phase & 1, abort_flag, p.timeout_cycles, p.status);
     };
-    // (a CTA without a share has no parts)
-    Walk<C> walk(p, sm.share, sm.window);
+    // Part number np, in registers; false behind the last.  After an abort too every role
+    // goes through all the parts (their named barriers pair up), so these waits ignore it.
+    auto take = [&](int np, Part& part) {
+        mbar_wait_drain(smem_addr(&sm.part_full[np % kParts]), (np / kParts) & 1, kDrainCycles);
+        part = sm.parts[np % kParts];
+        return part.tiles >= 0;
+    };
     Part part;
 
     if (warp == 0) {
@@ -556,8 +574,31 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
         const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
         int c = 0, items = 0;                      // tiles, items of the ring
-        bool ok = true;
-        while (ok && walk.next(part)) {
+        bool ok = true, joined = false;
+        Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
+        for (int np = 0;; ++np) {
+            if (np >= kParts)
+                mbar_wait_drain(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1, kDrainCycles);
+            const bool more = walk.next(part);
+            if (lane == 0) {
+                if (!more) part.tiles = -1;
+                sm.parts[np % kParts] = part;
+                mbar_arrive(smem_addr(&sm.part_full[np % kParts]));
+                if (more && part.begins && !part.whole) {
+                    Kv8Join j;
+                    j.last = share_of(sm.share.total, part.unit0 + part.item_tiles - 1,
+                                      sharers(sm.share.total, gridDim.x));
+                    j.b = part.b;
+                    j.h = part.h;
+                    j.start = part.req.start;
+                    j.n = part.req.n;
+                    j.row0 = part.row0;
+                    p.joins[blockIdx.x] = j;
+                    joined = true;
+                }
+            }
+            __syncwarp();
+            if (!more) break;
             const int* row = p.table + static_cast<long long>(part.b) * p.width;
             const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
             const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
@@ -614,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 }
             }
         }
+        if (lane == 0 && !joined) p.joins[blockIdx.x].last = 0;
         // every copy lands before the CTA exits, whatever became of the other roles
         for (int i = max(0, items - kSlots); i < items; ++i)
             mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
@@ -634,10 +676,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         bool first = true;
         auto advance = [&]() {   // to the next tile; false at the end
             while (left == 0) {
-                if (!walk.next(part)) return false;
+                if (!take(np + 1, part)) return false;
                 ++np;
                 left = part.tiles;
                 first = true;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
                 if (left == 0 && lane == 0) {
                     // (its queries are laid out all the same)
                     wait(&sm.q_full[np & 1], np >> 1);
@@ -706,21 +750,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         constexpr int kLanes = D / 8;         // threads of a row
         constexpr int kRows = 64 / kLanes;    // rows at a time
         const int t = threadIdx.x - 64, sub = t % kLanes;
-        int np = 0;
-        bool joined = false, ok = true;
-        while (walk.next(part)) {
-            if (t == 0 && part.begins && !part.whole) {
-                Kv8Join j;
-                j.last = share_of(sm.share.total, part.unit0 + part.item_tiles - 1, gridDim.x);
-                j.b = part.b;
-                j.h = part.h;
-                j.start = part.req.start;
-                j.n = part.req.n;
-                j.row0 = part.row0;
-                j.total = sm.share.total;
-                p.joins[blockIdx.x] = j;
-                joined = true;
-            }
+        bool ok = true;
+        for (int np = 0; take(np, part); ++np) {
             const int buf = np & 1;
             if (np >= 2) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty[buf], (np >> 1) - 1));
             if (ok) {
@@ -779,18 +810,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&sm.q_full[buf]));
-            ++np;
         }
-        if (t == 0 && !joined) p.joins[blockIdx.x].last = 0;
     } else {
         // -------------------------------------------------------------- softmax
         const int quad = warp - 4, key = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tO = colO + lane_addr;
         uint8_t* myP = sP + key * 16;
-        int T = 0, np = 0;
+        int T = 0;
         bool ok = true;
-        while (walk.next(part)) {
+        for (int np = 0; take(np, part); ++np) {
             const int buf = np & 1;
             ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full[buf], np >> 1));
             float l[C], ref = kNegInf;   // lane n keeps column n's reference
@@ -1042,8 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 named_bar_sync(kBarMax, 128);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[buf]));
-            ++np;
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&sm.q_empty[buf]));
+                mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
+            }
         }
     }
     tc_fence_before();
@@ -1053,7 +1084,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 }
 
 // Joins the parts of the item that begins at the end of CTA c's share, c = blockIdx.x: a
-// warp per row, the parts in their order.
+// warp per row.  Its lanes take 32 parts' references and sums at a time, then the warp adds
+// those parts' accumulators up in their order.
 template <int D, int E>
 __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
     grid_launch_dependents();
@@ -1063,23 +1095,32 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     if (j.last <= cta) return;
     const int C = p.columns, G = p.seq.group, lane = threadIdx.x & 31;
     constexpr int kPer = D / 32;
+    // the parts: this CTA's second slot, the first slots of the ones behind it
+    const int parts = j.last - cta + 1;
     for (int n = threadIdx.x >> 5; n < C && j.row0 + n < j.n * G; n += 8) {
+        auto row_of = [&](int part) { return (2LL * (cta + part) + (part == 0 ? 1 : 0)) * C + n; };
         float m = kNegInf, sum = 0.f, o[kPer];
 #pragma unroll
         for (int c = 0; c < kPer; ++c) o[c] = 0.f;
-        for (int part = cta; part <= j.last; ++part) {
-            if (share_begin(j.total, part, gridDim.x) == share_begin(j.total, part + 1, gridDim.x))
-                continue;   // a CTA without a share
-            const long long at = (2LL * part + (part == cta ? 1 : 0)) * C + n;
-            const float2 st = p.part_stat[at];
-            float x[kPer];
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            float2 st = make_float2(kNegInf, 0.f);
+            if (p0 + lane < parts) st = p.part_stat[row_of(p0 + lane)];
+            const float top = fmaxf(m, warp_max(st.x)), ref = top == kNegInf ? 0.f : top;
+            const float old = ex2_approx(m - ref), mine = ex2_approx(st.x - ref);
+            float s = mine * st.y;
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) x[c] = p.part_o[at * D + lane + 32 * c];
-            const float top = fmaxf(m, st.x), ref = top == kNegInf ? 0.f : top;
-            const float a = ex2_approx(m - ref), b = ex2_approx(st.x - ref);
-            sum = a * sum + b * st.y;
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            sum = old * sum + s;
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) o[c] = a * o[c] + b * x[c];
+            for (int c = 0; c < kPer; ++c) o[c] *= old;
+            const int here = min(32, parts - p0);
+#pragma unroll 4
+            for (int q = 0; q < here; ++q) {
+                const float f = __shfl_sync(0xffffffffu, mine, q);
+                const float* x = p.part_o + row_of(p0 + q) * D + lane;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, x[32 * c], o[c]);
+            }
             m = top;
         }
         const int r = j.row0 + n, tok = r / G, head = j.h * G + r % G;
