@@ -953,7 +953,7 @@ fa_status check_table(const char* who, int B, int width, int page) {
 // that takes a request's rows in one item, and 64 for more rows than that.
 int kv8_columns(int N, int group) {
     const long long rows = static_cast<long long>(N) * group;
-    return rows <= 16 ? 16 : 32;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 
 // Byte layout of fa_fwd_kv8's workspace, each part padded to 256 bytes.

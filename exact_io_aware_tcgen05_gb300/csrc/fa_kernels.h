@@ -170,7 +170,7 @@ struct Kv8FwdParams {
     float* lse;
     int width, num_pages, page_log2;
     uint32_t group_inv; // ceil(2^32 / group)
-    int columns;        // rows of an item: 16, 32 or 64 (kv8_columns)
+    int columns;        // rows of an item (kv8_columns)
     int ctas;
     // workspace: [ctas] joins, [2 ctas, columns] (reference, sum), [2 ctas, columns, d] O
     Kv8Join* joins;

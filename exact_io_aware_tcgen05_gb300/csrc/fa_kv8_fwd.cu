@@ -2,7 +2,7 @@
 // include/fa.h) on sm_103a.
 //
 // A request's rows are its (new token, head of the group) pairs: they share a key/value
-// head and take one pass over its keys together, C = 16, 32 or 64 rows to an item.  With so
+// head and take one pass over its keys together, C = 8, 16 or 32 rows to an item.  With so
 // few rows the cache's bytes bound the pass (16 operations a byte at 8 rows and d = 128, too
 // many for the CUDA cores, few for the tensor cores), so nothing is done to a code but to
 // load it: TMA copies pages into shared memory and tcgen05 (kind::f8f6f4) multiplies them
@@ -54,14 +54,14 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeys = 128;          // keys of a tile
-constexpr int kItemCost = 1;        // an item's fixed cost in tiles
+constexpr int kItemCost = 2;        // an item's fixed cost in tiles
 // Weights are kept times 2^12.  A column's reference M moves when a key exceeds it by more
 // than 2^3 (its weight then is above 2^15, near fp16's largest number, 65504), so that it
 // mostly does not: the maxima over the lanes and the accumulators' rescaling are rare.
 constexpr float kShift = 12.f;
 constexpr float kGrow = 3.f;
 constexpr float kNone = -1e30f;     // in place of a column's reference that has none yet
-constexpr int kWindow = 128;        // requests whose lengths a CTA keeps in shared memory
+constexpr int kWindow = 64;         // requests whose lengths a CTA keeps in shared memory
 constexpr int kThreads = 256;
 
 // --------------------------------------------------------------- work distribution
@@ -100,10 +100,12 @@ __device__ __forceinline__ Items items_of(const Kv8FwdParams& p, const Request& 
     return it;
 }
 
+__device__ __noinline__ long long divide_long(long long a, long long b) { return a / b; }
+
 // 64-bit division that mostly is a 32-bit one.
-__device__ __forceinline__ long long divide(long long a, int b) {
-    if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return divide_long(a, b);
 }
 
 // CTA c of the first G takes units [c total / G, (c + 1) total / G) of `total`; G is the
@@ -116,8 +118,7 @@ __device__ __forceinline__ long long share_begin(long long total, int c, int G) 
     return q * c + divide((total - q * G) * c, G);
 }
 __device__ __forceinline__ int share_of(long long total, long long unit, int G) {
-    const long long a = (unit + 1) * G - 1;
-    return (total >> 31) == 0 ? static_cast<int>(divide(a, static_cast<int>(total))) : static_cast<int>(a / total);
+    return static_cast<int>(divide((unit + 1) * G - 1, total));
 }
 
 // One CTA's part of an item.
@@ -167,6 +168,7 @@ struct Walk {
         it = items_of<C>(p, req);
     }
     __device__ bool next(Part& part) {
+#pragma unroll 1
         while (left > 0 && b < p.seq.B) {
             if (off == it.cost) {
                 off = 0;
@@ -219,17 +221,21 @@ struct Kv8Cfg {
     static constexpr int kQ = E == kElemBf16 ? 2 : 3;    // pieces of q
     static constexpr int kP = E == kElemBf16 ? 3 : 4;    // pieces of P
     // With few columns an MMA costs the reading of its 128 rows, so the pieces of q and of P
-    // go side by side into one MMA of more columns and are added up when read.  (256 TMEM
-    // columns a CTA: where they do not hold P's pieces, the tensor cores add them up, an
-    // MMA each.)
-    static constexpr int kSCols = kQ * C;
-    static constexpr bool kWideO = 2 * kSCols + kP * C <= 256;
-    static constexpr int kOCols = kWideO ? kP * C : C;
-    static constexpr int kTmemCols = 2 * kSCols + kOCols <= 128 ? 128 : 256;
-    static_assert(2 * kSCols + kOCols <= 256, "TMEM columns, two CTAs per SM");
+    // go side by side into one MMA of more columns (a multiple of 16, the rest zeros) and
+    // are added up when read.  (256 TMEM columns a CTA: where they do not hold P's pieces,
+    // the tensor cores add them up, an MMA each.)
+    static constexpr int kSCols = (kQ * C + 15) / 16 * 16;
+    static constexpr int kPCols = (kP * C + 15) / 16 * 16;
+    static constexpr bool kWideO = 2 * kSCols + kPCols <= 256;
+    static constexpr int kOCols = kWideO ? kPCols : C;
+    static constexpr int kTmemUsed = 2 * kSCols + kOCols;
+    static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : 256;
+    static_assert(kTmemUsed <= 256, "TMEM columns, two CTAs per SM");
     static constexpr int kSlotBytes = kKeys * D;         // K or V of a tile
-    static constexpr int kQBytes = kQ * C * D;           // one item's queries
-    static constexpr int kPBytes = kP * C * kKeys;       // a tile's weights
+    static constexpr int kQBytes = kSCols * D;           // one item's queries
+    static constexpr int kPBytes = kPCols * kKeys;       // a tile's weights
+    // two tiles' weights, unless they leave the ring fewer than 4 slots
+    static constexpr int kPBufs = D == 64 || kQBytes + kPBytes <= 20480 ? 2 : 1;
     static constexpr int kSwizzle = D == 128 ? 2 : 4;    // descriptor code of the D-byte swizzle
     static constexpr int kGroup = 8 * D;                 // bytes of 8 rows
 };
@@ -267,7 +273,7 @@ constexpr int kCtaSmem = 233472 / 2 - 1024;   // two CTAs per SM
 template <int D, int E, int C>
 constexpr int kv8_slots() {
     using K = Kv8Cfg<D, E, C>;
-    const int left = kCtaSmem - 1024 - 2 * K::kQBytes - K::kPBytes - static_cast<int>(sizeof(Kv8Smem<C>));
+    const int left = kCtaSmem - 1024 - 2 * K::kQBytes - K::kPBufs * K::kPBytes - static_cast<int>(sizeof(Kv8Smem<C>));
     const int n = left / K::kSlotBytes;
     return n < kMaxSlots ? n : kMaxSlots;
 }
@@ -275,12 +281,12 @@ constexpr int kv8_slots() {
 template <int D, int E, int C>
 constexpr int kv8_smem_bytes() {
     using K = Kv8Cfg<D, E, C>;
-    return 1024 + kv8_slots<D, E, C>() * K::kSlotBytes + 2 * K::kQBytes + K::kPBytes +
+    return 1024 + kv8_slots<D, E, C>() * K::kSlotBytes + 2 * K::kQBytes + K::kPBufs * K::kPBytes +
            static_cast<int>(sizeof(Kv8Smem<C>));
 }
 
 // named barriers (0 is __syncthreads)
-constexpr int kBarP = 1;      // weights written; the softmax warps and the issuer
+constexpr int kBarP = 1;      // weights written, or not fitting; the softmax warps and the issuer
 constexpr int kBarMax = 2;    // the softmax warps' maxima (or a part's sums) written
 
 // The 16-byte unit u of row r in a tile of rows of D bytes, swizzled over D bytes.
@@ -295,25 +301,8 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// 16 TMEM columns, several sets `stride` columns apart added up.
-template <int SETS>
-__device__ __forceinline__ void load_sum16(uint32_t addr, int stride, float (&v)[16]) {
-    uint32_t r[SETS][16];
-#pragma unroll
-    for (int i = 0; i < SETS; ++i) tmem_ld16(addr + i * stride, r[i]);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < SETS; ++i) reg_fence(r[i]);
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        v[c] = __uint_as_float(r[0][c]);
-#pragma unroll
-        for (int i = 1; i < SETS; ++i) v[c] += __uint_as_float(r[i][c]);
-    }
-}
-
-// Sums of v[0 .. N) over the warp's lanes, by halving: lane l ends with the sums of column
-// l / 2 (N = 16, v[0]), l (N = 32, v[0]) or 2 l and 2 l + 1 (N = 64, v[0] and v[1]).
+// Sums of v[0 .. N) over the warp's lanes, by halving: lane l ends with the sum of column
+// l / (32 / N) in v[0].
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
     int width = N;
@@ -379,6 +368,34 @@ __device__ __forceinline__ void load_sum8(uint32_t addr, int stride, float (&v)[
     }
 }
 
+// A key's weights into its rows of the P operand, cut into KP e5m2 pieces: an fp16 number's
+// high byte is its leading 3 bits as e5m2, and what is left is an fp16 number again.  The
+// last of 3 pieces is rounded; the fourth is all that is left.  The pieces' columns lie one
+// behind the other in blocks of 16 (kKeys * 16 bytes each), zeros behind the last.
+template <int KP, int C>
+__device__ __forceinline__ void store_weights(uint8_t* at, const float (&w)[C]) {
+    uint32_t h[C / 2], words[(KP * C + 15) / 16 * 4];
+#pragma unroll
+    for (int j = 0; j < C / 2; ++j) h[j] = pack2<kElemF16>(w[2 * j], w[2 * j + 1]);
+#pragma unroll
+    for (int j = KP * C / 4; j < (KP * C + 15) / 16 * 4; ++j) words[j] = 0;
+#pragma unroll
+    for (int q = 0; q < KP; ++q) {
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j)
+            if (KP == 3 && q == 2) h[j] += 0x00800080u;
+#pragma unroll
+        for (int j = 0; j < C / 4; ++j) words[q * (C / 4) + j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j)
+            if (q + 1 < KP) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
+    }
+#pragma unroll
+    for (int b = 0; b < (KP * C + 15) / 16; ++b)
+        *reinterpret_cast<uint4*>(at + b * kKeys * 16) =
+            make_uint4(words[4 * b], words[4 * b + 1], words[4 * b + 2], words[4 * b + 3]);
+}
+
 // Bytes of a word that are e4m3 NaN (0x7f or 0xff), as 0x80 in each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
@@ -438,6 +455,7 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm
     };
     const long long first = units(threadIdx.x);
     long long sum = first;
+#pragma unroll 1
     for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units(b);
     const long long upto = block_units(sum, sm.warp_sums, &total);
     const int G = sharers(total, gridDim.x);
@@ -453,6 +471,7 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm
         const int at = static_cast<int>(threadIdx.x) - sm.share.b0;
         if (at >= 0 && at < kWindow) sm.window[at] = make_int3(r.start, r.n, r.len);
     } else {
+#pragma unroll 1
         for (int b0 = 0; b0 < B; b0 += kThreads) {
             const int b = b0 + threadIdx.x;
             const long long mine = units(b);
@@ -469,6 +488,13 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm
             sm.window[threadIdx.x] = make_int3(r.start, r.n, r.len);
         }
     }
+}
+
+// The part of a wait that is not over at once, out of line: the kernel's roles wait in many
+// places, and its instructions have to be fetched.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, long long limit,
+                                     int* status) {
+    return mbar_wait(bar, parity, abort, limit, status);
 }
 
 // Which of the columns n0 .. n0 + 7 see a NaN code in this channel of a value that other
@@ -510,21 +536,21 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sKV = smem;                                  // [slots]
-    uint8_t* sQ = smem + kSlots * K::kSlotBytes;          // [2][pieces][C][D]
-    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [pieces][C / 16][keys][16]
-    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + K::kPBytes);
-    volatile int* abort_flag = &sm.abort;
-
+    uint8_t* sQ = smem + kSlots * K::kSlotBytes;          // [2][pieces and rows][D]
+    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [kPBufs][blocks of 16 columns][keys][16]
+    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + K::kPBufs * K::kPBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_launch_dependents();
 
     if (threadIdx.x == 0) {
         sm.abort = 0;
         sm.poison = 0;
+#pragma unroll 1
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_addr(&sm.kv_full[i]), 1);
             mbar_init(smem_addr(&sm.kv_empty[i]), 1);
         }
+#pragma unroll 1
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
         for (int i = 0; i < kParts; ++i) {
             mbar_init(smem_addr(&sm.part_full[i]), 1);
@@ -543,6 +569,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         tmem_alloc(smem_addr(&sm.tmem), K::kTmemCols);
         tmem_relinquish();
     }
+    if constexpr (K::kSCols > K::kQ * C) {   // the columns behind the pieces
+        constexpr int kPad = (K::kSCols - K::kQ * C) * D / 16;
+        for (int i = threadIdx.x; i < 2 * kPad; i += kThreads)
+            *reinterpret_cast<uint4*>(sQ + i / kPad * K::kQBytes + K::kQ * C * D + i % kPad * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
     // what the kernels before this one wrote is there from here on
     grid_dependency_wait();
     find_share<C>(p, sm);
@@ -553,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     const uint32_t colO = tmem + 2 * K::kSCols;
 
     auto wait = [&](uint64_t* bar, int phase) {
-        return mbar_wait(smem_addr(bar), phase & 1, abort_flag, p.timeout_cycles, p.status);
+        return mbar_try_wait(smem_addr(bar), phase & 1) ||
+               wait_on(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
     };
     // Part number np, in registers; false behind the last.  After an abort too every role
     // goes through all the parts (their named barriers pair up), so these waits ignore it.
@@ -576,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         int c = 0, items = 0;                      // tiles, items of the ring
         bool ok = true, joined = false;
         Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
+#pragma unroll 1
         for (int np = 0;; ++np) {
             if (np >= kParts)
                 mbar_wait_drain(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1, kDrainCycles);
@@ -607,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
             int cur = part.tiles > 0 ? entry(base + lane) : -1;
             int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
+#pragma unroll 1
             for (int i = 0; i < part.tiles && ok; ++i, ++c) {
                 const int tile = part.tile0 + i;
                 if (tile * per_tile >= base + 32) {
@@ -621,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * page * D;
                 // the scales of the tile's 8 blocks (their slot's last tile is long done)
                 const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
+#pragma unroll 1
                 for (int side = 0; side < 2; ++side, ++items) {
                     const int st = items % kSlots, use = items / kSlots;
                     if (use > 0) {
@@ -657,8 +694,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         }
         if (lane == 0 && !joined) p.joins[blockIdx.x].last = 0;
         // every copy lands before the CTA exits, whatever became of the other roles
+#pragma unroll 1
         for (int i = max(0, items - kSlots); i < items; ++i)
             mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
+#pragma unroll 1
         for (int i = max(0, c - kScaleSlots); i < c; ++i)
             mbar_wait_drain(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1, kDrainCycles);
     } else if (warp == 1) {
@@ -675,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         int np = -1, left = 0;   // the part of the next tile, its tiles from that one on
         bool first = true;
         auto advance = [&]() {   // to the next tile; false at the end
+#pragma unroll 1
             while (left == 0) {
                 if (!take(np + 1, part)) return false;
                 ++np;
@@ -708,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         int T = 0;
         bool more = advance();
         if (more && lane == 0) issue_s(0);
+#pragma unroll 1
         while (more) {
             const bool fresh = first;   // tile T is its part's first
             first = false;
@@ -720,18 +761,20 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 issued = true;
             }
             __syncwarp();
-            named_bar_sync(kBarP, 160);
+#pragma unroll 1
+            while (!named_bar_all(kBarP, 160, true)) {}   // until the weights fit
             if (lane == 0) {
                 const int st = (2 * T + 1) % kSlots;
                 wait(&sm.kv_full[st], (2 * T + 1) / kSlots);
                 tc_fence_after();
                 const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
+                const uint64_t pd = pd0 + static_cast<uint64_t>((T % K::kPBufs * K::kPBytes) >> 4);
 #pragma unroll
                 for (int q = 0; q < (K::kWideO ? 1 : K::kP); ++q)
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 32; ++kk)
                         mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4),
-                                  pd0 + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
+                                  pd + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
                                   (!fresh || q > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(smem_addr(&sm.pv_done));
                 mma_commit(smem_addr(&sm.kv_empty[st]));
@@ -751,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         constexpr int kRows = 64 / kLanes;    // rows at a time
         const int t = threadIdx.x - 64, sub = t % kLanes;
         bool ok = true;
+#pragma unroll 1
         for (int np = 0; take(np, part); ++np) {
             const int buf = np & 1;
             if (np >= 2) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty[buf], (np >> 1) - 1));
@@ -816,9 +860,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         const int quad = warp - 4, key = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tO = colO + lane_addr;
-        uint8_t* myP = sP + key * 16;
         int T = 0;
         bool ok = true;
+#pragma unroll 1
         for (int np = 0; take(np, part); ++np) {
             const int buf = np & 1;
             ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full[buf], np >> 1));
@@ -826,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll
             for (int n = 0; n < C; ++n) l[n] = 0.f;
             const int nrows = min(C, part.req.n * p.seq.group - part.row0);
+#pragma unroll 1
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
                 if (ok)
@@ -833,7 +878,6 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                                                      wait(&sm.s_full[T & 1], T >> 1));
                 float v[C], kc = 0.f, lvs = 0.f, inv_vs = 0.f;
                 uint32_t seen = ~0u;   // a bit per column
-                bool fits = true;      // no weight exceeds its reference by more than kGrow
                 const float4* qs = reinterpret_cast<const float4*>(sm.q_scale[buf]);
                 const float4* rf = reinterpret_cast<const float4*>(sm.ref[quad]);
                 if (ok) {
@@ -844,9 +888,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                                         pos >= part.req.len;
                     const bool edge = kb < part.all_lo || kb + kKeys - 1 > part.all_hi;
 #pragma unroll
-                    for (int cc = 0; cc < C / 16; ++cc)
-                        load_sum16<K::kQ>(tmem + lane_addr + (T & 1) * K::kSCols + cc * 16, C,
-                                          *reinterpret_cast<float(*)[16]>(&v[cc * 16]));
+                    for (int cc = 0; cc < C; cc += 8)
+                        if (cc < nrows)
+                            load_sum8<K::kQ>(tmem + lane_addr + (T & 1) * K::kSCols + cc, C,
+                                             *reinterpret_cast<float(*)[8]>(&v[cc]));
                     tc_fence_before();
                     if (hidden) {
                         ks = 0.f;
@@ -897,8 +942,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                             }
                         }
                     }
-                    // e_n = t_n - M_n + kShift, in place of the products
-                    if (i > 0) {
+                }
+                // The weights 2^(t - M + kShift); at the part's first tile, and where one is
+                // too large, new references come first.  The fence and the barrier hand
+                // them to the issuer.
+                float w[C];
+                bool fits = i > 0;
+#pragma unroll 1
+                for (int attempt = 0;; ++attempt) {
+                    if (ok && (attempt > 0 || i > 0)) {
                         float top = kNegInf;
 #pragma unroll
                         for (int n4 = 0; n4 < C; n4 += 4)
@@ -906,17 +958,26 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                                 const float4 q4 = qs[n4 / 4], r4 = rf[n4 / 4];
                                 const float qq[4] = {q4.x, q4.y, q4.z, q4.w}, rr[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    if ((seen >> (n4 + j)) & 1u)
-                                        top = fmaxf(top, fmaf(v[n4 + j], kc * qq[j], lvs - rr[j]));
+                                for (int j = 0; j < 4; ++j) {
+                                    float e = fmaf(v[n4 + j], kc * qq[j], lvs - rr[j]);
+                                    if (!((seen >> (n4 + j)) & 1u)) e = kNegInf;
+                                    top = fmaxf(top, e);
+                                    w[n4 + j] = ex2_approx(e);
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) w[n4 + j] = 0.f;
                             }
-                        fits = top <= kShift + kGrow;
-                    } else {
-                        fits = false;
+                        fits = attempt > 0 || top <= kShift + kGrow;
+                        // Two buffers: tile T - 2's product was complete before this tile's
+                        // S^T was.  One: the last tile's has to be.
+                        if (K::kPBufs == 1 && T > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
+                        store_weights<K::kP, C>(sP + T % K::kPBufs * K::kPBytes + key * 16, w);
+                        tc_fence_before();
+                        fence_proxy_async_smem();
                     }
-                }
-                if (!named_bar_all(kBarMax, 128, fits)) {
-                    // new references: the maxima over the tile's keys
+                    if (named_bar_all(kBarP, 160, !ok || fits)) break;
+                    // the maxima over the tile's keys
                     float mine = kNegInf;
                     if (ok) {
 #pragma unroll
@@ -933,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                     }
                     named_bar_sync(kBarMax, 128);
                     if (ok) {
-                        // every warp comes to the same ones
+                        // every warp comes to the same references
                         if (lane < C) {
                             const auto& wm = sm.wmax[T & 1];
                             const float m = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
@@ -960,68 +1021,24 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                                 const float* fc = &sm.fac[quad][cc % C];
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
-                                    r[j] = __float_as_uint(__uint_as_float(r[j]) * fc[j]);
+                                    r[j] = __float_as_uint(__uint_as_float(r[j]) * fc[C < 16 ? j % C : j]);
                                 tmem_st16(tO + cc, r);
                             }
                             tmem_st_wait();
                         }
                     }
                 }
-                // the last product has read its weights
-                if (ok && T > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
                 if (ok) {
 #pragma unroll
-                    for (int cc = 0; cc < C / 16; ++cc) {
-                        uint32_t h[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) h[j] = 0;
-#pragma unroll
-                        for (int n4 = cc * 16; n4 < cc * 16 + 16; n4 += 4)
-                            if (n4 < nrows) {
-                                const float4 q4 = qs[n4 / 4], r4 = rf[n4 / 4];
-                                const float qq[4] = {q4.x, q4.y, q4.z, q4.w}, rr[4] = {r4.x, r4.y, r4.z, r4.w};
-                                float w[4];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float e = fmaf(v[n4 + j], kc * qq[j], lvs - rr[j]);
-                                    w[j] = ex2_approx((seen >> (n4 + j)) & 1u ? e : kNegInf);
-                                    l[n4 + j] = fmaf(w[j], inv_vs, l[n4 + j]);
-                                }
-                                h[n4 % 16 / 2] = pack2<kElemF16>(w[0], w[1]);
-                                h[n4 % 16 / 2 + 1] = pack2<kElemF16>(w[2], w[3]);
-                            }
-#pragma unroll
-                        for (int q = 0; q < K::kP; ++q) {
-                            // the last of 3 pieces is rounded, the others (and the fourth,
-                            // which is all that is left) are the leading bits
-                            if (q == 2 && K::kP == 3)
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) h[j] += 0x00800080u;
-                            uint4 w;
-                            w.x = __byte_perm(h[0], h[1], 0x7531);
-                            w.y = __byte_perm(h[2], h[3], 0x7531);
-                            w.z = __byte_perm(h[4], h[5], 0x7531);
-                            w.w = __byte_perm(h[6], h[7], 0x7531);
-                            *reinterpret_cast<uint4*>(myP + (q * (C / 16) + cc) * kKeys * 16) = w;
-                            if (q + 1 < K::kP)
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
-                        }
-                    }
-                    tc_fence_before();
-                    fence_proxy_async_smem();
+                    for (int n = 0; n < C; ++n) l[n] = fmaf(w[n], inv_vs, l[n]);
                 }
-                named_bar_signal(kBarP, 160, ok);
             }
             // ------------------------------------------------ the part's end
             if (ok && part.tiles > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
             tc_fence_after();
             warp_sums(l, lane);
-            if (C == 16) {
-                if ((lane & 1) == 0) sm.part_sum[buf][quad][lane >> 1] = l[0];
-            } else {
-                sm.part_sum[buf][quad][lane] = l[0];
-            }
+            constexpr int kSame = 32 / C;   // lanes that hold the same column's sum
+            if (lane % kSame == 0) sm.part_sum[buf][quad][lane / kSame] = l[0];
             named_bar_sync(kBarMax, 128);
             const bool poison = sm.poison != 0;
             if (ok) {
@@ -1167,7 +1184,9 @@ template <int D, int E>
 cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
     cudaError_t e = ev ? cudaEventRecord(ev[0], stream) : cudaSuccess;
     if (e == cudaSuccess)
-        e = p.columns == 16 ? launch_attend<D, E, 16>(p, stream) : launch_attend<D, E, 32>(p, stream);
+        e = p.columns == 8    ? launch_attend<D, E, 8>(p, stream)
+            : p.columns == 16 ? launch_attend<D, E, 16>(p, stream)
+                              : launch_attend<D, E, 32>(p, stream);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
     if (e != cudaSuccess) return e;
     e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, p.ctas, 256, 0, stream, p);
