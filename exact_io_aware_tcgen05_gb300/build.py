@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 # touching memory out of range
 DEBUG_LIB_PATH = os.path.join(HERE, "libfa_gb300_debug.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_fused.cu", "fa_fp8.cu", "fa_static_ws.cu",
-           "fa_kv8_cache.cu", "fa_kv8_fwd.cu"]
+           "fa_kv8_cache.cu", "fa_kv8_fwd.cu", "fa_kv8_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", CSRC, "-I", INCLUDE]

@@ -947,13 +947,13 @@ fa_status check_table(const char* who, int B, int width, int page) {
     return FA_OK;
 }
 
-// Rows of an item of the attention kernel.  A request's rows are its (new token, head of the
+// Rows of an item of the attention kernels.  A request's rows are its (new token, head of the
 // group) pairs, N * group at most; all of an item's rows take one pass over the keys.
-// Narrow items cost less per key tile, wide ones read the cache fewer times: the narrowest
-// that takes a request's rows in one item, and 64 for more rows than that.
+// Narrow items (fa_kv8_fwd.cu) cost less per key tile: 8 or 16 where that takes a request's
+// rows in one item, and items of 128 rows (fa_kv8_rows.cu) for more rows than that.
 int kv8_columns(int N, int group) {
     const long long rows = static_cast<long long>(N) * group;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
 }
 
 // Byte layout of fa_fwd_kv8's workspace, each part padded to 256 bytes.
@@ -1112,6 +1112,8 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
         return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: num_pages * Hkv = %lld is 2^31 or more",
                     static_cast<long long>(num_pages) * Hkv);
     p.group_inv = static_cast<uint32_t>(((1ull << 32) + g.seq.group - 1) / g.seq.group);
+    if (static_cast<long long>(g.tokens) * g.seq.group > INT_MAX - 128)
+        return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: problem too large for one launch");
     p.columns = kv8_columns(N, g.seq.group);
     p.ctas = 2 * sm_count();
     const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);

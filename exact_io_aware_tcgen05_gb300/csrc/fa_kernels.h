@@ -199,6 +199,7 @@ cudaError_t launch_fp8_quant_qk(const Fp8QuantParams& p, int d, int grid, cudaSt
 cudaError_t launch_fp8_quant_v(const Fp8QuantParams& p, int d, int grid, cudaStream_t stream);
 cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stream);
+cudaError_t launch_fwd_kv8_rows(const Kv8FwdParams& p, int d, cudaStream_t stream);
 // launch_fwd_kv8 records ev[0..2] (if not null) around its two kernels.
 cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, cudaStream_t stream);
 

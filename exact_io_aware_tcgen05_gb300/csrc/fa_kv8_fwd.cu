@@ -41,178 +41,14 @@
 //   warps 2, 3   the items' queries: scaled, cut into pieces, into shared memory
 //   warps 4..7   softmax: a lane has a key
 // The second CTA of the SM works while this one waits at the ends of items.
-#include "fa_kernels.h"
-#include "fa_ptx.cuh"
-#include "fa_seq.cuh"
+#include "fa_kv8_work.cuh"
 
 #include <algorithm>
-#include <climits>
 
 namespace fa {
 namespace {
 
-constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kKeys = 128;          // keys of a tile
-constexpr int kItemCost = 2;        // an item's fixed cost in tiles
-// Weights are kept times 2^12.  A column's reference M moves when a key exceeds it by more
-// than 2^3 (its weight then is above 2^15, near fp16's largest number, 65504), so that it
-// mostly does not: the maxima over the lanes and the accumulators' rescaling are rare.
-constexpr float kShift = 12.f;
-constexpr float kGrow = 3.f;
-constexpr float kNone = -1e30f;     // in place of a column's reference that has none yet
-constexpr int kWindow = 64;         // requests whose lengths a CTA keeps in shared memory
-constexpr int kThreads = 256;
-
-// --------------------------------------------------------------- work distribution
-
-struct Request {
-    int start, n;   // new tokens
-    int len;        // tokens in the cache, the new ones among them
-};
-
-__device__ __forceinline__ Request load_request(const Kv8FwdParams& p, int b) {
-    Request r;
-    seq_bounds(p.seq, b, r.start, r.n);
-    const long long room = static_cast<long long>(p.width) << p.page_log2;
-    r.len = static_cast<int>(min(max(static_cast<long long>(__ldg(p.lens + b)), 0LL), room));
-    return r;
-}
-
-// A request's items: `blocks` blocks of C rows for each key/value head, each with room for
-// `tiles` key tiles (the most that one of its blocks sees) and the fixed cost.
-struct Items {
-    int blocks;
-    int cost;   // units of an item
-};
-
-template <int C>
-__device__ __forceinline__ Items items_of(const Kv8FwdParams& p, const Request& r) {
-    Items it;
-    it.blocks = (r.n * p.seq.group + C - 1) / C;
-    int tiles = (r.len + kKeys - 1) / kKeys;
-    if (p.seq.window > 0) {
-        // a block's rows see window + (its tokens - 1) consecutive keys at most
-        const long long span = static_cast<long long>(p.seq.window) + (C - 1) / p.seq.group + 1;
-        tiles = static_cast<int>(min(static_cast<long long>(tiles), (span + kKeys - 2) / kKeys + 1));
-    }
-    it.cost = tiles + kItemCost;
-    return it;
-}
-
-__device__ __noinline__ long long divide_long(long long a, long long b) { return a / b; }
-
-// 64-bit division that mostly is a 32-bit one.
-__device__ __forceinline__ long long divide(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return divide_long(a, b);
-}
-
-// CTA c of the first G takes units [c total / G, (c + 1) total / G) of `total`; G is the
-// number of CTAs, or of units where there are fewer, so that no share among them is empty.
-__device__ __forceinline__ int sharers(long long total, int ctas) {
-    return static_cast<int>(min(total, static_cast<long long>(ctas)));
-}
-__device__ __forceinline__ long long share_begin(long long total, int c, int G) {
-    const long long q = divide(total, G);
-    return q * c + divide((total - q * G) * c, G);
-}
-__device__ __forceinline__ int share_of(long long total, long long unit, int G) {
-    return static_cast<int>(divide((unit + 1) * G - 1, total));
-}
-
-// One CTA's part of an item.
-struct Part {
-    Request req;
-    int b, h, row0;     // request, key/value head, first row
-    int tile0, tiles;   // the part's key tiles (absolute), tiles may be 0: rows that see nothing
-    bool whole;         // all of the item's tiles
-    bool begins;        // the item's first tile is the part's
-    long long unit0;    // the item's first unit
-    int item_tiles;
-    int lo_key, hi_key; // the keys that any row of the item sees: [lo_key, hi_key]
-    int all_lo, all_hi; // the keys that every row sees
-};
-
-// Where a CTA's share begins, found by all its threads; and the requests from there on.
-struct Share {
-    long long begin, end, total;
-    int b0, h, blk, off;   // the request, head, block of rows and unit of that item it begins at
-};
-
-// A walk over a CTA's parts (the producer's; it hands them to the other roles).
-template <int C>
-struct Walk {
-    const Kv8FwdParams& p;
-    const int3* window;     // (start, n, len) of requests b0 .. b0 + kWindow - 1, in shared memory
-    int b0, b, h, blk, off; // request, head, block of rows, units of that item behind us
-    long long left, unit;   // units left, the next one's number
-    Request req;
-    Items it;
-
-    __device__ Walk(const Kv8FwdParams& p_, const Share& s, const int3* w)
-        : p(p_), window(w), b0(s.b0), b(s.b0), h(s.h), blk(s.blk), off(s.off),
-          left(s.end - s.begin), unit(s.begin) {
-        load();
-    }
-    __device__ void load() {
-        if (b >= p.seq.B || left == 0) return;
-        if (b - b0 < kWindow) {
-            const int3 w = window[b - b0];
-            req.start = w.x;
-            req.n = w.y;
-            req.len = w.z;
-        } else {
-            req = load_request(p, b);
-        }
-        it = items_of<C>(p, req);
-    }
-    __device__ bool next(Part& part) {
-#pragma unroll 1
-        while (left > 0 && b < p.seq.B) {
-            if (off == it.cost) {
-                off = 0;
-                ++blk;
-            }
-            if (blk >= it.blocks) {
-                blk = 0;
-                if (it.blocks == 0 || ++h == p.seq.Hkv) {
-                    h = 0;
-                    ++b;
-                    load();
-                }
-                continue;
-            }
-            const int take = static_cast<int>(min(left, static_cast<long long>(it.cost - off)));
-            part.unit0 = unit - off;
-            part.req = req;
-            part.b = b;
-            part.h = h;
-            part.row0 = blk * C;
-            // positions of the block's first and last token
-            const int G = p.seq.group;
-            const int first = req.len - req.n + part.row0 / G;
-            const int last = req.len - req.n + min((part.row0 + C - 1) / G, req.n - 1);
-            const bool win = p.seq.window > 0;
-            part.hi_key = p.seq.causal ? last : req.len - 1;
-            part.all_hi = p.seq.causal ? first : req.len - 1;
-            part.lo_key = win ? max(first - p.seq.window + 1, 0) : 0;
-            part.all_lo = win ? max(last - p.seq.window + 1, 0) : 0;
-            const int base = part.lo_key / kKeys;
-            part.item_tiles = part.hi_key >= part.lo_key ? part.hi_key / kKeys - base + 1 : 0;
-            const int t1 = min(off + take, part.item_tiles);
-            part.tile0 = base + off;
-            part.tiles = max(t1 - off, 0);
-            part.begins = off == 0;
-            part.whole = part.begins && t1 == part.item_tiles;
-            off += take;
-            left -= take;
-            unit += take;
-            if (part.tiles > 0 || part.whole) return true;
-        }
-        return false;
-    }
-};
+using namespace kv8;
 
 // --------------------------------------------------------------------- configuration
 
@@ -240,12 +76,9 @@ struct Kv8Cfg {
     static constexpr int kGroup = 8 * D;                 // bytes of 8 rows
 };
 
-constexpr int kMaxSlots = 12;
-constexpr int kParts = 4;         // parts the producer may be ahead
-constexpr int kScaleSlots = 16;   // tiles whose scales are kept: more than the ring is long
-
 template <int C>
 struct Kv8Smem {   // behind the tiles
+    static constexpr bool kOutOfLine = true;
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
     alignas(16) float q_scale[2][C];
     int row_pos[2][C];               // position of the row's token; INT_MIN: no row
@@ -268,8 +101,6 @@ struct Kv8Smem {   // behind the tiles
     int poison;                      // NaN found among values that only some rows see
 };
 
-constexpr int kCtaSmem = 233472 / 2 - 1024;   // two CTAs per SM
-
 template <int D, int E, int C>
 constexpr int kv8_slots() {
     using K = Kv8Cfg<D, E, C>;
@@ -288,18 +119,6 @@ constexpr int kv8_smem_bytes() {
 // named barriers (0 is __syncthreads)
 constexpr int kBarP = 1;      // weights written, or not fitting; the softmax warps and the issuer
 constexpr int kBarMax = 2;    // the softmax warps' maxima (or a part's sums) written
-
-// The 16-byte unit u of row r in a tile of rows of D bytes, swizzled over D bytes.
-template <int D>
-__device__ __forceinline__ int unit_offset(int r, int u) {
-    return r * D + ((u ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
-}
-
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 
 // Sums of v[0 .. N) over the warp's lanes, by halving: lane l ends with the sum of column
 // l / (32 / N) in v[0].
@@ -324,27 +143,6 @@ __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
         }
     }
-}
-
-// Exponent of the power of two that brings a row's largest magnitude into (224, 448].
-__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
-    const int e = static_cast<int>(amax_bits >> 23) - 127;
-    return max(e - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-}
-
-__device__ __forceinline__ float pow2f(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
-
-// The e4m3 values that pack4_e4m3 gives for four floats, as floats.
-__device__ __forceinline__ void e4m3_floats(uint32_t w, float (&f)[4]) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-    const float2 x = unpack2<kElemF16>(lo), y = unpack2<kElemF16>(hi);
-    f[0] = x.x;
-    f[1] = x.y;
-    f[2] = y.x;
-    f[3] = y.y;
 }
 
 // 8 TMEM columns, several sets added up.
@@ -394,107 +192,6 @@ __device__ __forceinline__ void store_weights(uint8_t* at, const float (&w)[C]) 
     for (int b = 0; b < (KP * C + 15) / 16; ++b)
         *reinterpret_cast<uint4*>(at + b * kKeys * 16) =
             make_uint4(words[4 * b], words[4 * b + 1], words[4 * b + 2], words[4 * b + 3]);
-}
-
-// Bytes of a word that are e4m3 NaN (0x7f or 0xff), as 0x80 in each.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
-// a / b for 0 <= a < 2^16, with inv = ceil(2^32 / b): the product is within 2^-16 of a / b
-// from above.  (b = 1: inv would be 2^32.)
-__device__ __forceinline__ int small_div(int a, int b, uint32_t inv) {
-    if (b == 1) return a;
-    return a < 65536 ? static_cast<int>(__umulhi(static_cast<uint32_t>(a), inv)) : a / b;
-}
-
-// Finds this CTA's share: sums of the requests' units, by all threads.
-__device__ __forceinline__ long long block_units(long long v, long long* warp_sums, long long* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const long long x = warp_sums[w];
-        if (w < warp) before += x;
-        all += x;
-    }
-    *total = all;
-    return v + before;
-}
-
-template <int C>
-__device__ __forceinline__ void find_share(const Kv8FwdParams& p, Kv8Smem<C>& sm) {
-    const int cta = blockIdx.x, B = p.seq.B;
-    long long begin = 0, before = 0, total = 0;
-    Request r{0, 0, 0};
-    auto units = [&](int b) -> long long {
-        if (b >= B) return 0;
-        r = load_request(p, b);
-        const Items it = items_of<C>(p, r);
-        return static_cast<long long>(it.blocks) * p.seq.Hkv * it.cost;
-    };
-    // request b's units end at `end`, `mine` of them: does the share begin there?
-    auto look = [&](int b, long long mine, long long end) {
-        if (begin >= end - mine && begin < end) {
-            const Items it = items_of<C>(p, r);
-            const long long at = begin - (end - mine), item = divide(at, it.cost);
-            const int h = static_cast<int>(divide(item, it.blocks));
-            sm.share.b0 = b;
-            sm.share.off = static_cast<int>(at - item * it.cost);
-            sm.share.h = h;
-            sm.share.blk = static_cast<int>(item - static_cast<long long>(h) * it.blocks);
-        }
-    };
-    const long long first = units(threadIdx.x);
-    long long sum = first;
-#pragma unroll 1
-    for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units(b);
-    const long long upto = block_units(sum, sm.warp_sums, &total);
-    const int G = sharers(total, gridDim.x);
-    begin = cta < G ? share_begin(total, cta, G) : total;
-    if (threadIdx.x == 0) {
-        sm.share.begin = begin;
-        sm.share.end = cta < G ? share_begin(total, cta + 1, G) : total;
-        sm.share.total = total;
-    }
-    if (B <= kThreads) {
-        look(threadIdx.x, first, upto);
-        __syncthreads();
-        const int at = static_cast<int>(threadIdx.x) - sm.share.b0;
-        if (at >= 0 && at < kWindow) sm.window[at] = make_int3(r.start, r.n, r.len);
-    } else {
-#pragma unroll 1
-        for (int b0 = 0; b0 < B; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            const long long mine = units(b);
-            long long all;
-            const long long end = before + block_units(mine, sm.warp_sums, &all);
-            look(b, mine, end);
-            before += all;
-        }
-        __syncthreads();
-        const int b = sm.share.b0 + threadIdx.x;
-        if (threadIdx.x < kWindow && sm.share.begin < total) {
-            r = Request{0, 0, 0};
-            if (b < B) r = load_request(p, b);
-            sm.window[threadIdx.x] = make_int3(r.start, r.n, r.len);
-        }
-    }
-}
-
-// The part of a wait that is not over at once, out of line: the kernel's roles wait in many
-// places, and its instructions have to be fetched.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, long long limit,
-                                     int* status) {
-    return mbar_wait(bar, parity, abort, limit, status);
 }
 
 // Which of the columns n0 .. n0 + 7 see a NaN code in this channel of a value that other
@@ -585,121 +282,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     const uint32_t tmem = sm.tmem;
     const uint32_t colO = tmem + 2 * K::kSCols;
 
-    auto wait = [&](uint64_t* bar, int phase) {
-        return mbar_try_wait(smem_addr(bar), phase & 1) ||
-               wait_on(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
-    };
-    // Part number np, in registers; false behind the last.  After an abort too every role
-    // goes through all the parts (their named barriers pair up), so these waits ignore it.
-    auto take = [&](int np, Part& part) {
-        mbar_wait_drain(smem_addr(&sm.part_full[np % kParts]), (np / kParts) & 1, kDrainCycles);
-        part = sm.parts[np % kParts];
-        return part.tiles >= 0;
-    };
+    auto wait = [&](uint64_t* bar, int phase) { return wait_for(p, sm, bar, phase); };
+    auto take = [&](int np, Part& part) { return take_part(sm, np, part); };
     Part part;
 
     if (warp == 0) {
-        // ------------------------------------------------------------- producer
-        if (lane == 0) {
-            tma_prefetch_desc(&p.tm_k);
-            tma_prefetch_desc(&p.tm_v);
-        }
-        const int page = 1 << p.page_log2, per_tile = kKeys >> p.page_log2;
-        const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
-        const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
-        int c = 0, items = 0;                      // tiles, items of the ring
-        bool ok = true, joined = false;
-        Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
-#pragma unroll 1
-        for (int np = 0;; ++np) {
-            if (np >= kParts)
-                mbar_wait_drain(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1, kDrainCycles);
-            const bool more = walk.next(part);
-            if (lane == 0) {
-                if (!more) part.tiles = -1;
-                sm.parts[np % kParts] = part;
-                mbar_arrive(smem_addr(&sm.part_full[np % kParts]));
-                if (more && part.begins && !part.whole) {
-                    Kv8Join j;
-                    j.last = share_of(sm.share.total, part.unit0 + part.item_tiles - 1,
-                                      sharers(sm.share.total, gridDim.x));
-                    j.b = part.b;
-                    j.h = part.h;
-                    j.start = part.req.start;
-                    j.n = part.req.n;
-                    j.row0 = part.row0;
-                    p.joins[blockIdx.x] = j;
-                    joined = true;
-                }
-            }
-            __syncwarp();
-            if (!more) break;
-            const int* row = p.table + static_cast<long long>(part.b) * p.width;
-            const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
-            const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
-            // the table's entries, 32 at a time, the next ones on their way
-            int base = part.tile0 * per_tile;
-            auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
-            int cur = part.tiles > 0 ? entry(base + lane) : -1;
-            int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
-#pragma unroll 1
-            for (int i = 0; i < part.tiles && ok; ++i, ++c) {
-                const int tile = part.tile0 + i;
-                if (tile * per_tile >= base + 32) {
-                    base += 32;
-                    cur = nxt;
-                    nxt = entry(base + 32 + lane);
-                }
-                const int first = tile * per_tile - base;
-                // this lane's page of the tile
-                const int id = __shfl_sync(0xffffffffu, cur, (first + (lane & (per_tile - 1))) & 31);
-                const bool load = lane < per_tile && id >= 0 && id < p.num_pages;
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * page * D;
-                // the scales of the tile's 8 blocks (their slot's last tile is long done)
-                const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
-#pragma unroll 1
-                for (int side = 0; side < 2; ++side, ++items) {
-                    const int st = items % kSlots, use = items / kSlots;
-                    if (use > 0) {
-                        ok = __all_sync(0xffffffffu, wait(&sm.kv_empty[st], use - 1));
-                        if (!ok) break;
-                    }
-                    uint8_t* dst = sKV + st * K::kSlotBytes;
-                    const uint32_t full = smem_addr(&sm.kv_full[st]);
-                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                    __syncwarp();
-                    if (load)
-                        tma_load_3d(smem_addr(dst + lane * page * D), side ? &p.tm_v : &p.tm_k, full, 0, 0,
-                                    id * p.seq.Hkv + part.h);
-                    if (side == 0) {
-                        const uint32_t sbar = smem_addr(&sm.scales_full[c % kScaleSlots]);
-                        bool plain = true;
-                        if (lane < 16) {
-                            float* to = &sm.scales[c % kScaleSlots][lane];
-                            if (sid >= 0 && sid < p.num_pages && tile * kKeys + side_blk * kKv8Block < lim) {
-                                const long long at =
-                                    ((static_cast<long long>(sid) * p.seq.Hkv + part.h) << blocks_log2) +
-                                    (side_blk & ((1 << blocks_log2) - 1));
-                                cp_async4(smem_addr(to), (lane < 8 ? p.k_scale : p.v_scale) + at);
-                                plain = false;
-                            } else {
-                                *to = lane < 8 ? 0.f : -1.f;   // hidden
-                            }
-                        }
-                        if (plain) mbar_arrive(sbar);
-                        else cp_async_arrive(sbar);
-                    }
-                }
-            }
-        }
-        if (lane == 0 && !joined) p.joins[blockIdx.x].last = 0;
-        // every copy lands before the CTA exits, whatever became of the other roles
-#pragma unroll 1
-        for (int i = max(0, items - kSlots); i < items; ++i)
-            mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
-#pragma unroll 1
-        for (int i = max(0, c - kScaleSlots); i < c; ++i)
-            mbar_wait_drain(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1, kDrainCycles);
+        produce<D, C, kSlots>(p, sm, sKV);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
         // Walks the tiles of all parts one behind the other, one tile ahead with S^T.  After
@@ -1153,23 +741,6 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     }
 }
 
-// A launch that may begin while the kernel before it on the stream is ending (it waits for
-// that one's results itself).
-cudaError_t launch_dependent(void (*kern)(Kv8FwdParams), int grid, int threads, int smem,
-                             cudaStream_t stream, const Kv8FwdParams& p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 template <int D, int E, int C>
 cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
     constexpr int smem = kv8_smem_bytes<D, E, C>();
@@ -1186,7 +757,7 @@ cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream
     if (e == cudaSuccess)
         e = p.columns == 8    ? launch_attend<D, E, 8>(p, stream)
             : p.columns == 16 ? launch_attend<D, E, 16>(p, stream)
-                              : launch_attend<D, E, 32>(p, stream);
+                              : launch_fwd_kv8_rows(p, D, stream);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
     if (e != cudaSuccess) return e;
     e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, p.ctas, 256, 0, stream, p);
