@@ -11,16 +11,16 @@
 //
 // Bound by the tensor cores and the exponentials together: a 128 x 128 tile at d = 128
 // takes 2 x 4 + 3 x 4 MMAs of 128 x 128 x 32 for bf16 (Q in 2 pieces, P in 3), 1280 cycles
-// at the 8-bit rate, and 16384 exponentials, 1024 cycles at 16 a cycle.  A CTA's steps depend
-// on one another (P takes the place of S in TMEM); the second CTA of the SM fills the gaps,
-// each using the tensor cores while the other is in its softmax.
+// at the 8-bit rate, and 16384 exponentials, 1024 cycles at 16 a cycle.  So that neither
+// waits for the other, a tile goes in two halves of 64 keys, each with its own S columns,
+// which its P takes over: while the softmax is on one half, the tensor cores multiply the
+// other one's P and the next tile's keys; and two CTAs share the SM.
 //
-// One CTA (256 threads, two per SM, half the TMEM each: S and P 128 columns, O d):
+// One CTA (256 threads, two per SM, half the TMEM each: S and P 2 x 64 columns, O d):
 //   warp 0       producer (fa_kv8_work.cuh)
 //   warp 1       tcgen05 issuer; owns the TMEM allocation
-//   warp 2       the tiles' scales, made ready for the exponents
-//   warps 4..7   a row per thread: the row's queries scaled and cut into pieces, softmax,
-//                the output.  They take the registers that the others give up.
+//   warps 2, 3   the items' queries: scaled, cut into pieces, into shared memory
+//   warps 4..7   softmax and output, a row per thread
 #include "fa_kv8_work.cuh"
 
 namespace fa {
@@ -37,25 +37,22 @@ struct RowsCfg {
     static constexpr int kSlotBytes = kKeys * D;
     static constexpr int kQPiece = kRows * D;
     static constexpr int kQBytes = kQ * kQPiece;
+    static constexpr int kQBufs = D == 64 ? 2 : 1;       // (at d = 128 the ring needs the room)
     static constexpr int kSwizzle = D == 128 ? 2 : 4;
     static constexpr int kGroup = 8 * D;
 };
 
 struct RowsSmem {   // behind the tiles
-    static constexpr bool kOutOfLine = false;
+    static constexpr bool kOutOfLine = true;
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
-    // the same, ready: K's scale and log2 of V's; 1 / V's (-1: hidden); whether any is hidden
-    float2 ready[kScaleSlots][8];
-    float inv_vs[kScaleSlots][8];
-    int absent[kScaleSlots];
+    float q_scale[2][kRows];
     int3 window[kWindow];
     Share share;
     Part parts[kParts];
     long long warp_sums[kThreads / 32];
     uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
-    uint64_t ready_full[kScaleSlots];
     uint64_t part_full[kParts], part_empty[kParts];
-    uint64_t q_full, s_full, o_full, all_done;
+    uint64_t q_full[2], q_empty[2], s_full[2], o_half[2], all_done;
     uint32_t tmem;
     int abort;
     int poison;                      // NaN found among values that only some rows see
@@ -64,28 +61,23 @@ struct RowsSmem {   // behind the tiles
 template <int D, int E>
 constexpr int rows_slots() {
     using K = RowsCfg<D, E>;
-    const int n = (kCtaSmem - 1024 - K::kQBytes - static_cast<int>(sizeof(RowsSmem))) / K::kSlotBytes;
+    const int n = (kCtaSmem - 1024 - K::kQBufs * K::kQBytes - static_cast<int>(sizeof(RowsSmem))) / K::kSlotBytes;
     return n < 8 ? n : 8;
 }
 
 template <int D, int E>
 constexpr int rows_smem_bytes() {
     using K = RowsCfg<D, E>;
-    return 1024 + rows_slots<D, E>() * K::kSlotBytes + K::kQBytes + static_cast<int>(sizeof(RowsSmem));
+    return 1024 + rows_slots<D, E>() * K::kSlotBytes + K::kQBufs * K::kQBytes + static_cast<int>(sizeof(RowsSmem));
 }
 
-// Registers: 256 threads at 128; the first warpgroup gives up what the softmax warps take.
-constexpr int kRegsCtl = 72;
-constexpr int kRegsSoftmax = 184;
-static_assert(128 * kRegsCtl + 128 * kRegsSoftmax <= kThreads * 128, "register split");
-
-constexpr int kBarP = 1;     // weights written; the softmax warps and the issuer
-constexpr int kBarRows = 2;  // the softmax warps among themselves
+constexpr int kBarP = 1;     // + half: weights written; the softmax warps and the issuer
+constexpr int kBarRows = 3;  // the softmax warps among themselves
 
 // The channels (a bit each) in which a row sees a NaN code among the part's values that
 // not every row sees.  Rare: the codes are read again.
 template <int D>
-__device__ __forceinline__ void row_nan(const Kv8FwdParams& p, const Part& part, int lo, int hi, uint32_t (&mask)[D / 32]) {
+__device__ __noinline__ void row_nan(const Kv8FwdParams& p, const Part& part, int lo, int hi, uint32_t (&mask)[D / 32]) {
     const int first = part.tile0 * kKeys, past = first + part.tiles * kKeys;
     for (int j = max(first, lo); j < min(past, hi + 1); ++j) {
         if (j >= part.all_lo && j <= part.all_hi) {
@@ -109,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     using K = RowsCfg<D, E>;
     constexpr int kSlots = rows_slots<D, E>();
     static_assert(kSlots >= 3 && kSlots / 2 + 2 < kScaleSlots, "ring of key/value tiles");
-    constexpr uint32_t kIdescS = idesc_f32acc(kRows, kKeys, false, false, kElemFp8);
+    constexpr uint32_t kIdescS = idesc_f32acc(kRows, kKeys / 2, false, false, kElemFp8);
     // P's pieces are e5m2 (operand format code 1), V e4m3, MN-major
     constexpr uint32_t kIdescO = idesc_f32acc(kRows, D, false, true, kElemFp8) | (1u << 7);
 
@@ -117,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sKV = smem;                               // [slots]
-    uint8_t* sQ = smem + kSlots * K::kSlotBytes;       // [pieces][rows][D]
-    RowsSmem& sm = *reinterpret_cast<RowsSmem*>(sQ + K::kQBytes);
+    uint8_t* sQ = smem + kSlots * K::kSlotBytes;       // [kQBufs][pieces][rows][D]
+    RowsSmem& sm = *reinterpret_cast<RowsSmem*>(sQ + K::kQBufs * K::kQBytes);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_launch_dependents();
@@ -132,17 +124,17 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             mbar_init(smem_addr(&sm.kv_empty[i]), 1);
         }
 #pragma unroll 1
-        for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(smem_addr(&sm.scales_full[i]), 32);
-            mbar_init(smem_addr(&sm.ready_full[i]), 1);
-        }
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
         for (int i = 0; i < kParts; ++i) {
             mbar_init(smem_addr(&sm.part_full[i]), 1);
-            mbar_init(smem_addr(&sm.part_empty[i]), 6);   // the issuer, the scales' warp, 4 softmax warps
+            mbar_init(smem_addr(&sm.part_empty[i]), 7);   // every warp but the producer
         }
-        mbar_init(smem_addr(&sm.q_full), 128);
-        mbar_init(smem_addr(&sm.s_full), 1);
-        mbar_init(smem_addr(&sm.o_full), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sm.q_full[i]), 64);
+            mbar_init(smem_addr(&sm.q_empty[i]), 5);      // the last S of the part, 4 softmax warps
+            mbar_init(smem_addr(&sm.s_full[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sm.o_half[i]), 1);
         mbar_init(smem_addr(&sm.all_done), 1);
         fence_barrier_init();
     }
@@ -156,118 +148,182 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;   // S and P: 128 columns, then O
+    const uint32_t tmem = sm.tmem;   // S and P of a tile's halves, 64 columns each, then O
 
     auto wait = [&](uint64_t* bar, int phase) { return wait_for(p, sm, bar, phase); };
     Part part;
 
     if (warp == 0) {
-        regs_lower<kRegsCtl>();
         produce<D, kRows, kSlots>(p, sm, sKV);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
-        // After an abort it goes on issuing on stale data, so that every barrier's phases
-        // still complete.
-        regs_lower<kRegsCtl>();
+        // Walks the tiles of all parts one behind the other; S of a tile's half is issued
+        // behind the last tile's product of that half, whose P it overwrites.  After an
+        // abort it goes on issuing on stale data, so that every barrier's phases still
+        // complete.
         const uint64_t k0 = sdesc<K::kSwizzle>(smem_addr(sKV), 16, K::kGroup);
         const uint64_t v0 = sdesc<K::kSwizzle>(smem_addr(sKV), K::kGroup, K::kGroup);
         const uint64_t q0 = sdesc<K::kSwizzle>(smem_addr(sQ), 16, K::kGroup);
-        int T = 0, nq = 0;   // tiles, parts with tiles
-        auto issue_s = [&](int tile) {   // lane 0
-            const int st = (2 * tile) % kSlots;
-            wait(&sm.kv_full[st], (2 * tile) / kSlots);
-            tc_fence_after();
-            const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
+        int np = -1, nq = -1, left = 0;   // the next tile's part, its number among those with tiles
+        bool first = true;                // the next tile is its part's first
+        auto advance = [&]() {            // to the next tile; false at the end
+#pragma unroll 1
+            while (left == 0) {
+                if (!take_part(sm, np + 1, part)) return false;
+                ++np;
+                left = part.tiles;
+                first = true;
+                if (left > 0) ++nq;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
+            }
+            --left;
+            return true;
+        };
+        auto issue_s = [&](int T, int half) {   // lane 0: half of S of the tile advance() came to
+            const int st = (2 * T) % kSlots, qb = nq % K::kQBufs;
+            if (half == 0) {
+                if (first) wait(&sm.q_full[qb], nq / K::kQBufs);
+                wait(&sm.kv_full[st], (2 * T) / kSlots);
+                tc_fence_after();
+            }
+            const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes + half * 64 * D) >> 4);
+            const uint64_t qd = q0 + static_cast<uint64_t>((qb * K::kQBytes) >> 4);
 #pragma unroll
             for (int q = 0; q < K::kQ; ++q)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
-                    mma_ss_f8(tmem, q0 + ((q * K::kQPiece) >> 4) + 2 * kk, kd + 2 * kk, kIdescS,
+                    mma_ss_f8(tmem + 64 * half, qd + ((q * K::kQPiece) >> 4) + 2 * kk, kd + 2 * kk, kIdescS,
                               (q > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(smem_addr(&sm.s_full));
-            mma_commit(smem_addr(&sm.kv_empty[st]));
+            mma_commit(smem_addr(&sm.s_full[half]));
+            if (half == 1) {
+                mma_commit(smem_addr(&sm.kv_empty[st]));
+                if (left == 0) mma_commit(smem_addr(&sm.q_empty[qb]));
+            }
         };
+        auto issue_o = [&](int T, int half, bool fresh) {   // lane 0: O += P V of tile T's half
+            const int st = (2 * T + 1) % kSlots;
+            if (half == 0) wait(&sm.kv_full[st], (2 * T + 1) / kSlots);
+            tc_fence_after();
+            const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes + half * 64 * D) >> 4);
+#pragma unroll
+            for (int q = 0; q < K::kP; ++q)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    mma_ts_f8(tmem + 128, tmem + 64 * half + 16 * q + 8 * kk, vd + ((kk * 32 * D) >> 4), kIdescO,
+                              (!fresh || half > 0 || q > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(smem_addr(&sm.o_half[half]));
+            if (half == 1) mma_commit(smem_addr(&sm.kv_empty[st]));
+        };
+        int T = 0;
+        bool more = advance();
+        if (more && lane == 0) {
+            issue_s(0, 0);
+            issue_s(0, 1);
+        }
 #pragma unroll 1
-        for (int np = 0; take_part(sm, np, part); ++np) {
+        while (more) {
+            const bool fresh = first;   // tile T is its part's first
+            first = false;
+            more = advance();
             __syncwarp();
+            named_bar_sync(kBarP, 160);
+            bool ahead = false;
             if (lane == 0) {
-                mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
-                if (part.tiles > 0) {
-                    wait(&sm.q_full, nq);
-                    issue_s(T);
-                }
+                issue_o(T, 0, fresh);
+                // S of the next tile, unless its keys or its part's queries are still on the way
+                ahead = more && mbar_try_wait(smem_addr(&sm.kv_full[(2 * T + 2) % kSlots]), ((2 * T + 2) / kSlots) & 1) &&
+                        (!first || mbar_try_wait(smem_addr(&sm.q_full[nq % K::kQBufs]), (nq / K::kQBufs) & 1));
+                if (ahead) issue_s(T + 1, 0);
             }
-            if (part.tiles > 0) ++nq;
             __syncwarp();
-#pragma unroll 1
-            for (int i = 0; i < part.tiles; ++i, ++T) {
-                named_bar_sync(kBarP, 160);
-                if (lane == 0) {
-                    const int st = (2 * T + 1) % kSlots;
-                    wait(&sm.kv_full[st], (2 * T + 1) / kSlots);
-                    tc_fence_after();
-                    const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
-#pragma unroll
-                    for (int q = 0; q < K::kP; ++q)
-#pragma unroll
-                        for (int kk = 0; kk < kKeys / 32; ++kk)
-                            mma_ts_f8(tmem + 128, tmem + 32 * q + 8 * kk, vd + ((kk * 32 * D) >> 4), kIdescO,
-                                      (i > 0 || q > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(smem_addr(&sm.kv_empty[st]));
-                    // S of the next tile overwrites P behind this product
-                    if (i + 1 < part.tiles) issue_s(T + 1);
-                    else mma_commit(smem_addr(&sm.o_full));
-                }
-                __syncwarp();
+            named_bar_sync(kBarP + 1, 160);
+            if (lane == 0) {
+                issue_o(T, 1, fresh);
+                if (more && !ahead) issue_s(T + 1, 0);
+                if (more) issue_s(T + 1, 1);
             }
+            __syncwarp();
+            ++T;
         }
         if (lane == 0) {
             mma_commit(smem_addr(&sm.all_done));
             mbar_wait_drain(smem_addr(&sm.all_done), 0, kDrainCycles);
         }
         __syncwarp();
-    } else if (warp == 2) {
-        // --------------------------------------------------------------- scales
-        regs_lower<kRegsCtl>();
-        int T = 0;
+    } else if (warp < 4) {
+        // -------------------------------------------------------------- queries
+        constexpr int kLanes = D / 8;         // threads of a row
+        constexpr int kPass = 64 / kLanes;    // rows at a time
+        const int t = threadIdx.x - 64, sub = t % kLanes;
+        int nq = 0;
+        bool ok = true;
 #pragma unroll 1
         for (int np = 0; take_part(sm, np, part); ++np) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
-#pragma unroll 1
-            for (int i = 0; i < part.tiles; ++i, ++T) {
-                const int sc = T % kScaleSlots;
-                wait(&sm.scales_full[sc], T / kScaleSlots);
-                const int b = lane & 7;
-                const float ks = sm.scales[sc][b], vs = sm.scales[sc][8 + b];
-                const bool gone = vs < 0.f;
-                const uint32_t vb = __float_as_uint(vs);
-                float lvs = static_cast<float>(static_cast<int>(vb >> 23) - 127);
-                float inv = __uint_as_float((254u << 23) - vb);
-                if ((vb & 0x7fffffu) != 0 || vb < 0x00800000u || vb > 0x7e000000u) {
-                    // not a power of two, or one without a normal inverse
-                    lvs = log2f(vs);
-                    inv = 1.f / vs;
+            if (part.tiles == 0) continue;
+            const int buf = nq % K::kQBufs;
+            if (nq >= K::kQBufs)
+                ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty[buf], nq / K::kQBufs - 1));
+            if (ok) {
+                uint8_t* dst = sQ + buf * K::kQBytes;
+                const int G = p.seq.group, rows = part.req.n * G;
+                const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
+#pragma unroll 4
+                for (int n = t / kLanes; n < kRows; n += kPass) {
+                    const int more = small_div(rem0 + n, G, p.group_inv);
+                    const int head = part.h * G + rem0 + n - more * G;
+                    const long long token = part.req.start + tok0 + more;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (part.row0 + n < rows)
+                        w = __ldg(reinterpret_cast<const uint4*>(
+                            static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
+                    float x[8];
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = unpack2<E>(u[j]);
+                        x[2 * j] = f.x;
+                        x[2 * j + 1] = f.y;
+                        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+                    }
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // an infinity or NaN makes the row NaN, through its scale
+                    const bool fine = top < 0x7f800000u;
+                    const int k = fine ? row_exponent(top) : 0;
+                    const float inv = fine ? pow2f(-k) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = fine ? x[j] * inv : 0.f;
+                    if (sub == 0) sm.q_scale[buf][n] = fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
+#pragma unroll
+                    for (int q = 0; q < K::kQ; ++q) {
+                        uint32_t codes[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            codes[j] = pack4_e4m3(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                            float f[4];
+                            e4m3_floats(codes[j], f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[4 * j + i] -= f[i];
+                        }
+                        *reinterpret_cast<uint2*>(dst + q * K::kQPiece + unit_offset<D>(n, sub >> 1) +
+                                                  (sub & 1) * 8) = make_uint2(codes[0], codes[1]);
+                    }
                 }
-                const bool any = __any_sync(0xffffffffu, gone);
-                if (lane < 8) {
-                    sm.ready[sc][b] = gone ? make_float2(0.f, 0.f) : make_float2(ks, lvs);
-                    sm.inv_vs[sc][b] = gone ? -1.f : inv;
-                }
-                if (lane == 0) sm.absent[sc] = any ? 1 : 0;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sm.ready_full[sc]));
             }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_addr(&sm.q_full[buf]));
+            ++nq;
         }
-    } else if (warp == 3) {
-        regs_lower<kRegsCtl>();   // idle; its warpgroup gives registers away
     } else {
         // -------------------------------------------------------------- softmax
-        regs_raise<kRegsSoftmax>();
         const int quad = warp - 4, row = quad * 32 + lane;   // TMEM lane; in V's tiles, the key
-        const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16), tO = tS + 128;
+        const uint32_t tS0 = tmem + (static_cast<uint32_t>(quad * 32) << 16), tO = tS0 + 128;
         const int G = p.seq.group;
-        int T = 0, no = 0;   // tiles, parts with tiles
+        int T = 0, nq = 0;   // tiles, parts with tiles
         bool ok = true;
 #pragma unroll 1
         for (int np = 0; take_part(sm, np, part); ++np) {
@@ -281,199 +337,182 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             const int lo = p.seq.window > 0 ? max(pos_row - p.seq.window + 1, 0) : 0;
             float rowc = 0.f;   // the row's scale, and the exponent's
             if (part.tiles > 0) {
-                // the row's queries (the last part's products with the last ones are complete)
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                                  token * p.q_stride + head * D);
-                uint4 w[D / 8];
-#pragma unroll
-                for (int u = 0; u < D / 8; ++u) w[u] = real ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-                uint32_t top = 0;
-#pragma unroll
-                for (int u = 0; u < D / 8; ++u) {
-                    const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack2<E>(x[j]);
-                        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-                    }
-                }
-                // an infinity or NaN makes the row NaN, through its scale
-                const bool fine = top < 0x7f800000u;
-                const int k = fine ? row_exponent(top) : 0;
-                const float inv = fine ? pow2f(-k) : 0.f;
-                rowc = (fine ? pow2f(k) : __uint_as_float(0x7fc00000u)) * p.scale_log2;
-#pragma unroll
-                for (int u = 0; u < D / 16; ++u) {   // 16 elements, 16 bytes of each piece
-                    float x[16];
-                    const uint32_t y[8] = {w[2 * u].x, w[2 * u].y, w[2 * u].z, w[2 * u].w,
-                                           w[2 * u + 1].x, w[2 * u + 1].y, w[2 * u + 1].z, w[2 * u + 1].w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = unpack2<E>(y[j]);
-                        x[2 * j] = fine ? f.x * inv : 0.f;
-                        x[2 * j + 1] = fine ? f.y * inv : 0.f;
-                    }
-#pragma unroll
-                    for (int q = 0; q < K::kQ; ++q) {
-                        uint32_t codes[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            codes[j] = pack4_e4m3(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                            float f[4];
-                            e4m3_floats(codes[j], f);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[4 * j + i] -= f[i];
-                        }
-                        *reinterpret_cast<uint4*>(sQ + q * K::kQPiece + unit_offset<D>(row, u)) =
-                            make_uint4(codes[0], codes[1], codes[2], codes[3]);
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_addr(&sm.q_full));
+                const int buf = nq % K::kQBufs;
+                ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full[buf], nq / K::kQBufs));
+                rowc = sm.q_scale[buf][row] * p.scale_log2;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[buf]));
             }
             float l = 0.f, ref = kNone;   // the exponents' offset: M - kShift
 #pragma unroll 1
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
-                if (ok)
-                    ok = __all_sync(0xffffffffu, wait(&sm.ready_full[sc], T / kScaleSlots) && wait(&sm.s_full, T));
-                if (ok) {
-                    tc_fence_after();
-                    float s[kKeys];
+                const int kt = (part.tile0 + i) * kKeys;
+                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots));
+                const bool absent =   // a block on a page that the cache does not have, or not needed
+                    __any_sync(0xffffffffu, sm.scales[sc][8 + (lane & 7)] < 0.f);
+                const bool edge = absent || kt < part.all_lo || kt + kKeys - 1 > part.all_hi;
+                if (ok && edge) {
+                    // 0 * NaN is NaN: no row's product may meet a NaN that it does not see.
+                    // (The values have to be there to be looked at.)  This thread looks after
+                    // key kt + row.
+                    const int vi = 2 * T + 1, pos = kt + row;
+                    ok = __all_sync(0xffffffffu, wait(&sm.kv_full[vi % kSlots], vi / kSlots));
+                    uint4* vrow = reinterpret_cast<uint4*>(sKV + (vi % kSlots) * K::kSlotBytes + row * D);
+                    const bool hidden = sm.scales[sc][8 + row / 16] < 0.f || pos < part.lo_key ||
+                                        pos > part.hi_key || pos >= part.req.len;
+                    if (hidden) {
 #pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c)
-                        tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
-                    tmem_ld_wait();
-                    reg_fence(*reinterpret_cast<uint32_t(*)[kKeys]>(&s[0]));
-                    const int kb = (part.tile0 + i) * kKeys;
-                    // exponents t - M + kShift in place of the products (M = 0 of a row that has
-                    // no reference yet)
-                    const bool none = ref == kNone;
-                    const float base = none ? 0.f : ref;
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        const float2 kv = sm.ready[sc][b];
-                        const float kc = kv.x * rowc, off = kv.y - base;
-                        const uint64_t c2 = f2_pack(kc, kc), o2 = f2_pack(off, off);
-#pragma unroll
-                        for (int c = 16 * b; c < 16 * b + 16; c += 2) {
-                            const float2 e = f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), c2, o2));
-                            s[c] = e.x;
-                            s[c + 1] = e.y;
+                        for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0, 0, 0, 0);
+                    } else if (pos < part.all_lo || pos > part.all_hi) {
+#pragma unroll 1
+                        for (int u = 0; u < D / 16; ++u) {
+                            uint4 w = vrow[u];
+                            const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), e = nan_bytes(w.z),
+                                           f = nan_bytes(w.w);
+                            if (a | b | e | f) {
+                                // those channels become NaN at the part's end, for the rows that see them
+                                w.x &= ~(a | (a - (a >> 7)));
+                                w.y &= ~(b | (b - (b >> 7)));
+                                w.z &= ~(e | (e - (e >> 7)));
+                                w.w &= ~(f | (f - (f >> 7)));
+                                vrow[u] = w;
+                                sm.poison = 1;
+                            }
                         }
                     }
-                    if (sm.absent[sc] || kb < part.all_lo || kb + kKeys - 1 > part.all_hi) {
-                        const int clo = lo - kb, chi = min(hi, part.req.len - 1) - kb;
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const bool gone = sm.inv_vs[sc][b] < 0.f;
-#pragma unroll
-                            for (int c = 16 * b; c < 16 * b + 16; ++c)
-                                if (c < clo || c > chi || gone) s[c] = kNegInf;
-                        }
-                        // 0 * NaN is NaN: no row's product may meet a NaN that it does not
-                        // see.  (The values have to be there to be looked at.)  This thread
-                        // looks after key kb + row.
-                        const int vi = 2 * T + 1, pos = kb + row;
-                        ok = __all_sync(0xffffffffu, wait(&sm.kv_full[vi % kSlots], vi / kSlots));
-                        uint4* vrow = reinterpret_cast<uint4*>(sKV + (vi % kSlots) * K::kSlotBytes + row * D);
-                        const bool hidden = sm.inv_vs[sc][row / 16] < 0.f || pos < part.lo_key ||
-                                            pos > part.hi_key || pos >= part.req.len;
-                        if (hidden) {
-#pragma unroll
-                            for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0, 0, 0, 0);
-                        } else if (pos < part.all_lo || pos > part.all_hi) {
+                    fence_proxy_async_smem();
+                }
 #pragma unroll 1
-                            for (int u = 0; u < D / 16; ++u) {
-                                uint4 w = vrow[u];
-                                const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), e = nan_bytes(w.z),
-                                               f = nan_bytes(w.w);
-                                if (a | b | e | f) {
-                                    // those channels become NaN at the part's end, for the rows that see them
-                                    w.x &= ~(a | (a - (a >> 7)));
-                                    w.y &= ~(b | (b - (b >> 7)));
-                                    w.z &= ~(e | (e - (e >> 7)));
-                                    w.w &= ~(f | (f - (f >> 7)));
-                                    vrow[u] = w;
-                                    sm.poison = 1;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t tS = tS0 + 64 * half;
+                    const int kb = kt + 64 * half;
+                    if (ok) ok = __all_sync(0xffffffffu, wait(&sm.s_full[half], T));
+                    if (ok) {
+                        tc_fence_after();
+                        float s[64];
+                        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                        // the scales of the half's 4 blocks
+                        const bool none = ref == kNone;
+                        const float base = none ? 0.f : ref;
+                        float kc[4], off[4], inv_vs[4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float vs = sm.scales[sc][8 + 4 * half + b];
+                            const uint32_t vb = __float_as_uint(vs);
+                            float lvs = static_cast<float>(static_cast<int>(vb >> 23) - 127);
+                            inv_vs[b] = __uint_as_float((254u << 23) - vb);
+                            if ((vb & 0x7fffffu) != 0 || vb < 0x00800000u || vb > 0x7e000000u) {
+                                // not a power of two, or one without a normal inverse
+                                const float v = vs < 0.f ? 1.f : vs;
+                                lvs = log2f(v);
+                                inv_vs[b] = 1.f / v;
+                            }
+                            kc[b] = sm.scales[sc][4 * half + b] * rowc;
+                            off[b] = lvs - base;
+                        }
+                        tmem_ld_wait();
+                        reg_fence(*reinterpret_cast<uint32_t(*)[64]>(&s[0]));
+                        // exponents t - M + kShift in place of the products (M = 0 of a row that
+                        // has no reference yet)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint64_t c2 = f2_pack(kc[b], kc[b]), o2 = f2_pack(off[b], off[b]);
+#pragma unroll
+                            for (int c = 16 * b; c < 16 * b + 16; c += 2) {
+                                const float2 e = f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), c2, o2));
+                                s[c] = e.x;
+                                s[c + 1] = e.y;
+                            }
+                        }
+                        if (absent || kb < part.all_lo || kb + 63 > part.all_hi) {
+                            const int clo = lo - kb, chi = min(hi, part.req.len - 1) - kb;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const bool gone = sm.scales[sc][8 + 4 * half + b] < 0.f;
+#pragma unroll
+                                for (int c = 16 * b; c < 16 * b + 16; ++c)
+                                    if (c < clo || c > chi || gone) s[c] = kNegInf;
+                            }
+                        }
+                        float top4[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top4[j] = s[j];
+#pragma unroll
+                        for (int c = 4; c + 8 <= 64; c += 8)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) top4[j] = fmax3(top4[j], s[c + 2 * j], s[c + 2 * j + 1]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top4[j] = fmaxf(top4[j], s[60 + j]);
+                        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                        const bool moves = none ? top > kNegInf : top > kShift + kGrow;
+                        if (__any_sync(0xffffffffu, moves)) {
+                            // the row's reference moves up to its largest key
+                            const float by = moves ? kShift - top : 0.f;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) s[c] += by;
+                            const float f = none ? 1.f : ex2_approx(by);
+                            l *= f;
+                            if (moves) ref = base - by;
+                            if (i > 0 || half > 0) {
+                                // The last tile's product of this half was complete before this S;
+                                // that of the half before this one is waited for.
+                                ok = __all_sync(0xffffffffu, wait(&sm.o_half[half ^ 1], half == 0 ? T - 1 : T));
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t x[16];
+                                    tmem_ld16(tO + c, x);
+                                    tmem_ld_wait();
+                                    reg_fence(x);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                                    tmem_st16(tO + c, x);
                                 }
                             }
                         }
-                        fence_proxy_async_smem();
-                    }
-                    float top4[4];
+                        // weights, their sum, and their pieces (32 keys are 8 columns of a piece)
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) top4[i4] = fmax3(s[3 * i4], s[3 * i4 + 1], s[3 * i4 + 2]);
+                        for (int c0 = 0; c0 < 64; c0 += 32) {
+                            uint32_t h[16];
 #pragma unroll
-                    for (int c = 12; c < kKeys - 4; c += 8)
+                            for (int b = 0; b < 2; ++b) {
+                                uint64_t sum2 = 0;
 #pragma unroll
-                        for (int i4 = 0; i4 < 4; ++i4) top4[i4] = fmax3(top4[i4], s[c + 2 * i4], s[c + 2 * i4 + 1]);
+                                for (int j = 0; j < 8; ++j) {
+                                    const int c = c0 + 16 * b + 2 * j;
+                                    const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]);
+                                    sum2 = j == 0 ? f2_pack(w0, w1) : f2_add(sum2, f2_pack(w0, w1));
+                                    h[8 * b + j] = pack2<kElemF16>(w0, w1);
+                                }
+                                const float2 sum = f2_unpack(sum2);
+                                l = fmaf(sum.x + sum.y, inv_vs[c0 / 16 + b], l);
+                            }
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) top4[i4] = fmaxf(top4[i4], s[kKeys - 4 + i4]);
-                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    const bool moves = none ? top > kNegInf : top > kShift + kGrow;
-                    if (__any_sync(0xffffffffu, moves)) {
-                        // the row's reference moves up to its largest key
-                        const float by = moves ? kShift - top : 0.f;
+                            for (int q = 0; q < K::kP; ++q) {
+                                uint32_t words[8];
 #pragma unroll
-                        for (int c = 0; c < kKeys; ++c) s[c] += by;
-                        const float f = none ? 1.f : ex2_approx(by);
-                        l *= f;
-                        if (moves) ref = base - by;
-                        if (i > 0) {
-                            // (the last tile's product was complete before this tile's S)
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t x[16];
-                                tmem_ld16(tO + c, x);
-                                tmem_ld_wait();
-                                reg_fence(x);
+                                for (int j = 0; j < 16; ++j)
+                                    if (K::kP == 3 && q == 2) h[j] += 0x00800080u;
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                                tmem_st16(tO + c, x);
+                                for (int j = 0; j < 8; ++j) words[j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (q + 1 < K::kP) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
+                                tmem_st8(tS + 16 * q + c0 / 4, words);
                             }
                         }
+                        tmem_st_wait();
+                        tc_fence_before();
                     }
-                    // weights, their sum, and their pieces (32 keys are 8 columns of a piece)
-#pragma unroll
-                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        uint32_t h[16];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            uint64_t sum2 = 0;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int c = c0 + 16 * b + 2 * j;
-                                const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]);
-                                sum2 = j == 0 ? f2_pack(w0, w1) : f2_add(sum2, f2_pack(w0, w1));
-                                h[8 * b + j] = pack2<kElemF16>(w0, w1);
-                            }
-                            const float2 sum = f2_unpack(sum2);
-                            l = fmaf(sum.x + sum.y, sm.inv_vs[sc][c0 / 16 + b], l);
-                        }
-#pragma unroll
-                        for (int q = 0; q < K::kP; ++q) {
-                            uint32_t words[8];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (K::kP == 3 && q == 2) h[j] += 0x00800080u;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) words[j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (q + 1 < K::kP) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
-                            tmem_st8(tS + 32 * q + c0 / 4, words);
-                        }
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
+                    named_bar_signal(kBarP + half, 160, ok);
                 }
-                named_bar_signal(kBarP, 160, ok);
             }
             // ------------------------------------------------ the part's end
             if (part.tiles > 0) {
-                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.o_full, no));
-                ++no;
+                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.o_half[1], T - 1));
+                ++nq;
             }
             tc_fence_after();
             bool poison = false;
