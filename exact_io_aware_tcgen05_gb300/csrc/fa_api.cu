@@ -971,15 +971,15 @@ Kv8Workspace kv8_workspace(int ctas, int columns, int d) {
 }
 
 // [num_pages * Hkv, page, d] codes viewed as (d, page, num_pages * Hkv): the box is the page
-// of one head, rows of d bytes swizzled over d bytes.
+// of one head, or box_rows rows of it, rows of d bytes swizzled over d bytes.
 fa_status make_page_map(CUtensorMap* map, const void* base, int num_pages, int Hkv, int page, int d,
-                        const char* name) {
+                        int box_rows, const char* name) {
     auto enc = encode_fn();
     if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page),
                           static_cast<cuuint64_t>(num_pages) * Hkv};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page) * d};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(page), 1};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows), 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1127,8 +1127,10 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     p.seq = g.seq;
     p.q = q;
     p.q_stride = q_stride;
-    if ((st = make_page_map(&p.tm_k, k8, num_pages, Hkv, page, d, "k8")) != FA_OK) return st;
-    if ((st = make_page_map(&p.tm_v, v8, num_pages, Hkv, page, d, "v8")) != FA_OK) return st;
+    // the kernel for items of 128 rows copies 64 keys at a time
+    const int box = p.columns == 128 && page > 64 ? 64 : page;
+    if ((st = make_page_map(&p.tm_k, k8, num_pages, Hkv, page, d, box, "k8")) != FA_OK) return st;
+    if ((st = make_page_map(&p.tm_v, v8, num_pages, Hkv, page, d, box, "v8")) != FA_OK) return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.joins = reinterpret_cast<Kv8Join*>(ws);
     p.part_stat = reinterpret_cast<float2*>(ws + w.stat);

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     Part part;
 
     if (warp == 0) {
-        produce<D, C, kSlots>(p, sm, sKV);
+        produce<D, C, kKeys, kSlots>(p, sm, sKV);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
         // Walks the tiles of all parts one behind the other, one tile ahead with S^T.  After
@@ -390,54 +390,30 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 uint8_t* dst = sQ + buf * K::kQBytes;
                 const int G = p.seq.group, rows = part.req.n * G;
                 const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
+                constexpr int kPasses = C / kRows;
+                uint4 w[kPasses];
 #pragma unroll
-                for (int n = t / kLanes; n < C; n += kRows) {
-                    const int r = part.row0 + n;
+                for (int i = 0; i < kPasses; ++i) {
+                    const int n = t / kLanes + i * kRows;
                     const int more = small_div(rem0 + n, G, p.group_inv);
-                    const int tok = tok0 + more, head = part.h * G + rem0 + n - more * G;
-                    const long long token = part.req.start + tok;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        w = __ldg(reinterpret_cast<const uint4*>(
+                    const long long token = part.req.start + tok0 + more;
+                    const int head = part.h * G + rem0 + n - more * G;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (part.row0 + n < rows)
+                        w[i] = __ldg(reinterpret_cast<const uint4*>(
                             static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
-                    float x[8];
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack2<E>(u[j]);
-                        x[2 * j] = f.x;
-                        x[2 * j + 1] = f.y;
-                        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-                    }
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // an infinity or NaN makes the row NaN, through its scale
-                    const bool fine = top < 0x7f800000u;
-                    const int k = fine ? row_exponent(top) : 0;
-                    const float inv = fine ? pow2f(-k) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = fine ? x[j] * inv : 0.f;
                     if (sub == 0) {
-                        sm.q_scale[buf][n] = fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
-                        sm.row_pos[buf][n] = r < rows ? part.req.len - part.req.n + tok : INT_MIN;
+                        sm.row_pos[buf][n] = part.row0 + n < rows ? part.req.len - part.req.n + tok0 + more : INT_MIN;
                         sm.out_at[buf][n] = (token * p.seq.Hq + head) * D;
-                        sm.lse_at[buf][n] = row_stat_index(p.seq, part.b, head, part.req.start, tok);
+                        sm.lse_at[buf][n] = row_stat_index(p.seq, part.b, head, part.req.start, tok0 + more);
                     }
+                }
 #pragma unroll
-                    for (int q = 0; q < K::kQ; ++q) {
-                        uint32_t codes[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            codes[j] = pack4_e4m3(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                            float f[4];
-                            e4m3_floats(codes[j], f);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[4 * j + i] -= f[i];
-                        }
-                        *reinterpret_cast<uint2*>(dst + unit_offset<D>(q * C + n, sub >> 1) + (sub & 1) * 8) =
-                            make_uint2(codes[0], codes[1]);
-                    }
+                for (int i = 0; i < kPasses; ++i) {
+                    const int n = t / kLanes + i * kRows;
+                    const float scale = cut_queries<D, E, K::kQ>(
+                        w[i], dst + unit_offset<D>(n, sub >> 1) + (sub & 1) * 8, C * D);
+                    if (sub == 0) sm.q_scale[buf][n] = scale;
                 }
             }
             fence_proxy_async_smem();

@@ -4,22 +4,26 @@
 // With 128 rows the products fill the tensor cores' tiles the usual way round, rows on the
 // 128 TMEM lanes, keys on the columns:
 //   S [128 x 128 keys] = Q K^T     Q's pieces from shared memory, K as stored, K-major
-//   O [128 x d]       += P V       P's pieces from TMEM, V as stored, read MN-major
-// (kind::f8f6f4).  The number formats, the pieces and V's scale in the exponent are those
-// of fa_kv8_fwd.cu; a key's scales are the same for the 16 columns of its block, and a
-// softmax thread has a row, so no maximum crosses lanes.
+//   O [128 x d]       += P V       P (fp16) from TMEM, V as fp16, read MN-major
+// The first is kind::f8f6f4 with Q in pieces (fa_kv8_fwd.cu has the number formats) and K
+// untouched.  For the second, each value's code is widened to fp16 (exact) once for all 128
+// rows, by two warps, which costs far less than cutting 128 x 128 weights into 8-bit pieces,
+// and one fp16 product takes two thirds of the time of three 8-bit ones.  The weights are
+// rounded to fp16's 11 bits.  V's scale is in the exponent as in fa_kv8_fwd.cu; a key's scales
+// are the same for the 16 columns of its block, and a softmax thread has a row, so no
+// maximum crosses lanes.
 //
-// Bound by the tensor cores and the exponentials together: a 128 x 128 tile at d = 128
-// takes 2 x 4 + 3 x 4 MMAs of 128 x 128 x 32 for bf16 (Q in 2 pieces, P in 3), 1280 cycles
-// at the 8-bit rate, and 16384 exponentials, 1024 cycles at 16 a cycle.  So that neither
-// waits for the other, a tile goes in two halves of 64 keys, each with its own S columns,
-// which its P takes over: while the softmax is on one half, the tensor cores multiply the
-// other one's P and the next tile's keys; and two CTAs share the SM.
+// Bound by the tensor cores and the exponentials together: a 128 x 128 tile at d = 128 takes
+// 1024 cycles of MMAs for bf16 (2 x 4 of 128 x 128 x 32 8-bit, 8 of 128 x 128 x 16), and 16384
+// exponentials, 1024 cycles at 16 a cycle.  So that neither waits for the other, a tile goes
+// in two halves of 64 keys, each with its own S columns, which its P takes over: while the
+// softmax is on one half, the tensor cores multiply the other one's P and the next tile's
+// keys; and two CTAs share the SM.
 //
 // One CTA (256 threads, two per SM, half the TMEM each: S and P 2 x 64 columns, O d):
 //   warp 0       producer (fa_kv8_work.cuh)
 //   warp 1       tcgen05 issuer; owns the TMEM allocation
-//   warps 2, 3   the items' queries: scaled, cut into pieces, into shared memory
+//   warps 2, 3   an item's queries, scaled and cut into pieces; then the tiles' values to fp16
 //   warps 4..7   softmax and output, a row per thread
 #include "fa_kv8_work.cuh"
 
@@ -30,14 +34,18 @@ using namespace kv8;
 
 constexpr int kRows = 128;
 
+constexpr int kHalf = 64;   // keys of a half tile
+
 template <int D, int E>
 struct RowsCfg {
     static constexpr int kQ = E == kElemBf16 ? 2 : 3;    // pieces of q
-    static constexpr int kP = E == kElemBf16 ? 3 : 4;    // pieces of P
-    static constexpr int kSlotBytes = kKeys * D;
+    static constexpr int kSlotBytes = kHalf * D;
     static constexpr int kQPiece = kRows * D;
     static constexpr int kQBytes = kQ * kQPiece;
-    static constexpr int kQBufs = D == 64 ? 2 : 1;       // (at d = 128 the ring needs the room)
+    static constexpr int kV16Bytes = kHalf * D * 2;      // [d / 64][keys][64], swizzled over 128 bytes
+    static constexpr int kV16Chunk = kHalf * 128;
+    // the halves' values, each in its place, unless the queries leave no room for both
+    static constexpr int kV16Bufs = kQBytes > 32768 ? 1 : 2;
     static constexpr int kSwizzle = D == 128 ? 2 : 4;
     static constexpr int kGroup = 8 * D;
 };
@@ -45,39 +53,52 @@ struct RowsCfg {
 struct RowsSmem {   // behind the tiles
     static constexpr bool kOutOfLine = true;
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
-    float q_scale[2][kRows];
+    float q_scale[kRows];
     int3 window[kWindow];
     Share share;
     Part parts[kParts];
     long long warp_sums[kThreads / 32];
     uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
     uint64_t part_full[kParts], part_empty[kParts];
-    uint64_t q_full[2], q_empty[2], s_full[2], o_half[2], all_done;
+    uint64_t q_full, q_empty, s_full[2], v_full[2], o_half[2], all_done;
     uint32_t tmem;
     int abort;
-    int poison;                      // NaN found among values that only some rows see
+    int poison[2];                   // [part parity] NaN found among values that only some rows see
 };
 
 template <int D, int E>
-constexpr int rows_slots() {
+constexpr int rows_fixed_bytes() {
     using K = RowsCfg<D, E>;
-    const int n = (kCtaSmem - 1024 - K::kQBufs * K::kQBytes - static_cast<int>(sizeof(RowsSmem))) / K::kSlotBytes;
-    return n < 8 ? n : 8;
+    return 1024 + K::kQBytes + K::kV16Bufs * K::kV16Bytes + static_cast<int>(sizeof(RowsSmem));
+}
+
+template <int D, int E>
+constexpr int rows_slots() {
+    const int n = (kCtaSmem - rows_fixed_bytes<D, E>()) / RowsCfg<D, E>::kSlotBytes;
+    return n < kMaxSlots ? n : kMaxSlots;
 }
 
 template <int D, int E>
 constexpr int rows_smem_bytes() {
-    using K = RowsCfg<D, E>;
-    return 1024 + rows_slots<D, E>() * K::kSlotBytes + K::kQBufs * K::kQBytes + static_cast<int>(sizeof(RowsSmem));
+    return rows_fixed_bytes<D, E>() + rows_slots<D, E>() * RowsCfg<D, E>::kSlotBytes;
 }
 
 constexpr int kBarP = 1;     // + half: weights written; the softmax warps and the issuer
 constexpr int kBarRows = 3;  // the softmax warps among themselves
+constexpr int kBarConv = 4;  // warps 2 and 3 among themselves
 
-// The channels (a bit each) in which a row sees a NaN code among the part's values that
-// not every row sees.  Rare: the codes are read again.
+// Four e4m3 codes to fp16 (exact; NaN stays NaN).
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// NaN for the channels in which a row sees a NaN code among the part's values that not every
+// row sees.  Rare: the codes are read again.
 template <int D>
-__device__ __noinline__ void row_nan(const Kv8FwdParams& p, const Part& part, int lo, int hi, uint32_t (&mask)[D / 32]) {
+__device__ __noinline__ void spoil_row(const Kv8FwdParams& p, const Part& part, int lo, int hi, uint16_t* out,
+                                       float* partial) {
     const int first = part.tile0 * kKeys, past = first + part.tiles * kKeys;
     for (int j = max(first, lo); j < min(past, hi + 1); ++j) {
         if (j >= part.all_lo && j <= part.all_hi) {
@@ -88,11 +109,11 @@ __device__ __noinline__ void row_nan(const Kv8FwdParams& p, const Part& part, in
         if (id < 0 || id >= p.num_pages) continue;
         const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
                             (j & ((1 << p.page_log2) - 1));
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w)
-#pragma unroll 1
-            for (int c = 0; c < 32; ++c)
-                if ((__ldg(p.v8 + r * D + 32 * w + c) & 0x7f) == 0x7f) mask[w] |= 1u << c;
+        for (int c = 0; c < D; ++c) {
+            if ((__ldg(p.v8 + r * D + c) & 0x7f) != 0x7f) continue;
+            if (out) out[c] = 0x7fff;   // a NaN of either type
+            else partial[c] = __uint_as_float(0x7fc00000u);
+        }
     }
 }
 
@@ -100,24 +121,24 @@ template <int D, int E>
 __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __grid_constant__ Kv8FwdParams p) {
     using K = RowsCfg<D, E>;
     constexpr int kSlots = rows_slots<D, E>();
-    static_assert(kSlots >= 3 && kSlots / 2 + 2 < kScaleSlots, "ring of key/value tiles");
-    constexpr uint32_t kIdescS = idesc_f32acc(kRows, kKeys / 2, false, false, kElemFp8);
-    // P's pieces are e5m2 (operand format code 1), V e4m3, MN-major
-    constexpr uint32_t kIdescO = idesc_f32acc(kRows, D, false, true, kElemFp8) | (1u << 7);
+    static_assert(kSlots >= 4 && kSlots / 4 + 2 < kScaleSlots, "ring of key/value tiles");
+    constexpr uint32_t kIdescS = idesc_f32acc(kRows, kHalf, false, false, kElemFp8);
+    constexpr uint32_t kIdescO = idesc_f32acc(kRows, D, false, true, kElemF16);
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sKV = smem;                               // [slots]
-    uint8_t* sQ = smem + kSlots * K::kSlotBytes;       // [kQBufs][pieces][rows][D]
-    RowsSmem& sm = *reinterpret_cast<RowsSmem*>(sQ + K::kQBufs * K::kQBytes);
+    uint8_t* sQ = smem + kSlots * K::kSlotBytes;       // [pieces][rows][D]
+    uint8_t* sV = sQ + K::kQBytes;                     // [kV16Bufs]
+    RowsSmem& sm = *reinterpret_cast<RowsSmem*>(sV + K::kV16Bufs * K::kV16Bytes);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_launch_dependents();
 
     if (threadIdx.x == 0) {
         sm.abort = 0;
-        sm.poison = 0;
+        sm.poison[0] = sm.poison[1] = 0;
 #pragma unroll 1
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_addr(&sm.kv_full[i]), 1);
@@ -129,12 +150,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             mbar_init(smem_addr(&sm.part_full[i]), 1);
             mbar_init(smem_addr(&sm.part_empty[i]), 7);   // every warp but the producer
         }
+        mbar_init(smem_addr(&sm.q_full), 64);
+        mbar_init(smem_addr(&sm.q_empty), 5);             // the last S of the part, 4 softmax warps
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sm.q_full[i]), 64);
-            mbar_init(smem_addr(&sm.q_empty[i]), 5);      // the last S of the part, 4 softmax warps
             mbar_init(smem_addr(&sm.s_full[i]), 1);
+            mbar_init(smem_addr(&sm.v_full[i]), 64);
+            mbar_init(smem_addr(&sm.o_half[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sm.o_half[i]), 1);
         mbar_init(smem_addr(&sm.all_done), 1);
         fence_barrier_init();
     }
@@ -154,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     Part part;
 
     if (warp == 0) {
-        produce<D, kRows, kSlots>(p, sm, sKV);
+        produce<D, kRows, kHalf, kSlots>(p, sm, sKV);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
         // Walks the tiles of all parts one behind the other; S of a tile's half is issued
@@ -162,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         // abort it goes on issuing on stale data, so that every barrier's phases still
         // complete.
         const uint64_t k0 = sdesc<K::kSwizzle>(smem_addr(sKV), 16, K::kGroup);
-        const uint64_t v0 = sdesc<K::kSwizzle>(smem_addr(sKV), K::kGroup, K::kGroup);
+        const uint64_t v0 = sdesc_sw128(smem_addr(sV), K::kV16Chunk, 1024);
         const uint64_t q0 = sdesc<K::kSwizzle>(smem_addr(sQ), 16, K::kGroup);
         int np = -1, nq = -1, left = 0;   // the next tile's part, its number among those with tiles
         bool first = true;                // the next tile is its part's first
@@ -181,70 +203,56 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             return true;
         };
         auto issue_s = [&](int T, int half) {   // lane 0: half of S of the tile advance() came to
-            const int st = (2 * T) % kSlots, qb = nq % K::kQBufs;
-            if (half == 0) {
-                if (first) wait(&sm.q_full[qb], nq / K::kQBufs);
-                wait(&sm.kv_full[st], (2 * T) / kSlots);
-                tc_fence_after();
-            }
-            const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes + half * 64 * D) >> 4);
-            const uint64_t qd = q0 + static_cast<uint64_t>((qb * K::kQBytes) >> 4);
+            const int it = 4 * T + half, st = it % kSlots;
+            if (half == 0 && first) wait(&sm.q_full, nq);
+            wait(&sm.kv_full[st], it / kSlots);
+            tc_fence_after();
+            const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
 #pragma unroll
             for (int q = 0; q < K::kQ; ++q)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
-                    mma_ss_f8(tmem + 64 * half, qd + ((q * K::kQPiece) >> 4) + 2 * kk, kd + 2 * kk, kIdescS,
+                    mma_ss_f8(tmem + kHalf * half, q0 + ((q * K::kQPiece) >> 4) + 2 * kk, kd + 2 * kk, kIdescS,
                               (q > 0 || kk > 0) ? 1u : 0u);
             mma_commit(smem_addr(&sm.s_full[half]));
-            if (half == 1) {
-                mma_commit(smem_addr(&sm.kv_empty[st]));
-                if (left == 0) mma_commit(smem_addr(&sm.q_empty[qb]));
-            }
+            mma_commit(smem_addr(&sm.kv_empty[st]));
+            if (half == 1 && left == 0) mma_commit(smem_addr(&sm.q_empty));
         };
         auto issue_o = [&](int T, int half, bool fresh) {   // lane 0: O += P V of tile T's half
-            const int st = (2 * T + 1) % kSlots;
-            if (half == 0) wait(&sm.kv_full[st], (2 * T + 1) / kSlots);
+            wait(&sm.v_full[half], T);
             tc_fence_after();
-            const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes + half * 64 * D) >> 4);
+            const uint64_t vd = v0 + static_cast<uint64_t>((half % K::kV16Bufs * K::kV16Bytes) >> 4);
 #pragma unroll
-            for (int q = 0; q < K::kP; ++q)
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                    mma_ts_f8(tmem + 128, tmem + 64 * half + 16 * q + 8 * kk, vd + ((kk * 32 * D) >> 4), kIdescO,
-                              (!fresh || half > 0 || q > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+                mma_ts(tmem + 128, tmem + kHalf * half + 8 * kk, vd + ((kk * 2048) >> 4), kIdescO,
+                       (!fresh || half > 0 || kk > 0) ? 1u : 0u);
             mma_commit(smem_addr(&sm.o_half[half]));
-            if (half == 1) mma_commit(smem_addr(&sm.kv_empty[st]));
         };
-        int T = 0;
-        bool more = advance();
-        if (more && lane == 0) {
-            issue_s(0, 0);
-            issue_s(0, 1);
-        }
+        // Step (T, half): the product of tile T's half (none for T = -1), then S of tile T + 1's.
+        bool more = advance(), fresh = true, ahead = false;
 #pragma unroll 1
-        while (more) {
-            const bool fresh = first;   // tile T is its part's first
+        for (int T = -1;; ++T) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (T >= 0) named_bar_sync(kBarP + half, 160);
+                if (lane == 0) {
+                    if (T >= 0) issue_o(T, half, fresh);
+                    // In the first half S of the next tile goes ahead unless its keys or its
+                    // part's queries are still on the way; what is left follows in the second.
+                    const int it = 4 * T + 4;
+                    if (half == 0)
+                        ahead = more && mbar_try_wait(smem_addr(&sm.kv_full[it % kSlots]), (it / kSlots) & 1) &&
+                                (!first || mbar_try_wait(smem_addr(&sm.q_full), nq & 1));
+#pragma unroll 1
+                    for (int h = half == 1 && !ahead ? 0 : half; more && h <= half && (half == 1 || ahead); ++h)
+                        issue_s(T + 1, h);
+                }
+                __syncwarp();
+            }
+            if (!more) break;
+            fresh = first;   // tile T + 1 is its part's first
             first = false;
             more = advance();
-            __syncwarp();
-            named_bar_sync(kBarP, 160);
-            bool ahead = false;
-            if (lane == 0) {
-                issue_o(T, 0, fresh);
-                // S of the next tile, unless its keys or its part's queries are still on the way
-                ahead = more && mbar_try_wait(smem_addr(&sm.kv_full[(2 * T + 2) % kSlots]), ((2 * T + 2) / kSlots) & 1) &&
-                        (!first || mbar_try_wait(smem_addr(&sm.q_full[nq % K::kQBufs]), (nq / K::kQBufs) & 1));
-                if (ahead) issue_s(T + 1, 0);
-            }
-            __syncwarp();
-            named_bar_sync(kBarP + 1, 160);
-            if (lane == 0) {
-                issue_o(T, 1, fresh);
-                if (more && !ahead) issue_s(T + 1, 0);
-                if (more) issue_s(T + 1, 1);
-            }
-            __syncwarp();
-            ++T;
         }
         if (lane == 0) {
             mma_commit(smem_addr(&sm.all_done));
@@ -252,75 +260,125 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         }
         __syncwarp();
     } else if (warp < 4) {
-        // -------------------------------------------------------------- queries
-        constexpr int kLanes = D / 8;         // threads of a row
+        // ----------------------------------------------------- queries and values
+        constexpr int kLanes = D / 8;         // threads of a row of queries
         constexpr int kPass = 64 / kLanes;    // rows at a time
+        constexpr int kBatch = 4;             // passes whose loads are in flight together
         const int t = threadIdx.x - 64, sub = t % kLanes;
-        int nq = 0;
+        int nq = 0, T = 0;
         bool ok = true;
 #pragma unroll 1
         for (int np = 0; take_part(sm, np, part); ++np) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
             if (part.tiles == 0) continue;
-            const int buf = nq % K::kQBufs;
-            if (nq >= K::kQBufs)
-                ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty[buf], nq / K::kQBufs - 1));
-            if (ok) {
-                uint8_t* dst = sQ + buf * K::kQBytes;
-                const int G = p.seq.group, rows = part.req.n * G;
-                const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
-#pragma unroll 4
-                for (int n = t / kLanes; n < kRows; n += kPass) {
+            const int G = p.seq.group, rows = part.req.n * G;
+            const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
+            // a batch of rows' loads is in flight while the one before it is cut into pieces
+            uint4 w[2][kBatch];
+            auto load = [&](uint4 (&x)[kBatch], int n0) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int n = n0 + i * kPass;
                     const int more = small_div(rem0 + n, G, p.group_inv);
                     const int head = part.h * G + rem0 + n - more * G;
                     const long long token = part.req.start + tok0 + more;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (part.row0 + n < rows)
-                        w = __ldg(reinterpret_cast<const uint4*>(
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (n < kRows && part.row0 + n < rows)
+                        x[i] = __ldg(reinterpret_cast<const uint4*>(
                             static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
-                    float x[8];
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t top = 0;
+                }
+            };
+            load(w[0], t / kLanes);
+            // the last part's products with its queries
+            if (nq > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, nq - 1));
+#pragma unroll 1
+            for (int n0 = t / kLanes; n0 < kRows; n0 += kBatch * kPass) {
+                load(w[1], n0 + kBatch * kPass);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack2<E>(u[j]);
-                        x[2 * j] = f.x;
-                        x[2 * j + 1] = f.y;
-                        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-                    }
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // an infinity or NaN makes the row NaN, through its scale
-                    const bool fine = top < 0x7f800000u;
-                    const int k = fine ? row_exponent(top) : 0;
-                    const float inv = fine ? pow2f(-k) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = fine ? x[j] * inv : 0.f;
-                    if (sub == 0) sm.q_scale[buf][n] = fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
-#pragma unroll
-                    for (int q = 0; q < K::kQ; ++q) {
-                        uint32_t codes[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            codes[j] = pack4_e4m3(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                            float f[4];
-                            e4m3_floats(codes[j], f);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[4 * j + i] -= f[i];
-                        }
-                        *reinterpret_cast<uint2*>(dst + q * K::kQPiece + unit_offset<D>(n, sub >> 1) +
-                                                  (sub & 1) * 8) = make_uint2(codes[0], codes[1]);
-                    }
+                for (int i = 0; i < kBatch; ++i) {
+                    const int n = n0 + i * kPass;
+                    const float scale = cut_queries<D, E, K::kQ>(
+                        w[0][i], sQ + unit_offset<D>(n, sub >> 1) + (sub & 1) * 8, K::kQPiece);
+                    if (sub == 0) sm.q_scale[n] = scale;
+                    w[0][i] = w[1][i];
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(smem_addr(&sm.q_full[buf]));
+            mbar_arrive(smem_addr(&sm.q_full));
             ++nq;
+            // Values: a unit of 16 codes becomes two of 8 fp16 numbers.  A key's D / 16 units
+            // are D / 16 threads', so that a warp reads whole rows.
+            constexpr int kPer = D / 16;
+            const int vu = t % kPer;
+#pragma unroll 1
+            for (int i = 0; i < part.tiles; ++i, ++T) {
+                const int sc = T % kScaleSlots;
+                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots));
+                const int kt = (part.tile0 + i) * kKeys;
+                const bool edge = __any_sync(0xffffffffu, sm.scales[sc][8 + (lane & 7)] < 0.f) ||
+                                  kt < part.all_lo || kt + kKeys - 1 > part.all_hi;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int it = 4 * T + 2 + half, st = it % kSlots;
+                    if (ok) ok = __all_sync(0xffffffffu, wait(&sm.kv_full[st], it / kSlots));
+                    // the place's last values have been multiplied
+                    const int o = K::kV16Bufs == 2 ? half : half ^ 1, use = K::kV16Bufs == 2 || half == 0 ? T - 1 : T;
+                    if (ok && use >= 0) ok = __all_sync(0xffffffffu, wait(&sm.o_half[o], use));
+                    if (ok) {
+                        uint8_t* src = sKV + st * K::kSlotBytes;
+                        uint8_t* dst = sV + half % K::kV16Bufs * K::kV16Bytes + vu / 4 * K::kV16Chunk;
+                        if (edge) {
+                            // 0 * NaN is NaN: no row's product may meet a NaN that it does not see.
+                            // Values that no row sees count as zeros (their place may hold
+                            // anything); where some rows see a NaN and others do not, it counts as
+                            // zero too, and its channel becomes NaN at the part's end for the rows
+                            // that see it.
+#pragma unroll 1
+                            for (int key = t / kPer; key < kHalf; key += 64 / kPer) {
+                                uint4* at = reinterpret_cast<uint4*>(src + unit_offset<D>(key, vu));
+                                const int pos = kt + half * kHalf + key;
+                                const bool hidden = sm.scales[sc][8 + half * 4 + key / 16] < 0.f ||
+                                                    pos < part.lo_key || pos > part.hi_key || pos >= part.req.len;
+                                if (hidden) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else if (pos < part.all_lo || pos > part.all_hi) {
+                                    uint4 w = *at;
+                                    const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), e = nan_bytes(w.z),
+                                                   f = nan_bytes(w.w);
+                                    if (a | b | e | f) {
+                                        w.x &= ~(a | (a - (a >> 7)));
+                                        w.y &= ~(b | (b - (b >> 7)));
+                                        w.z &= ~(e | (e - (e >> 7)));
+                                        w.w &= ~(f | (f - (f >> 7)));
+                                        *at = w;
+                                        sm.poison[(nq - 1) & 1] = 1;
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll 4
+                        for (int key = t / kPer; key < kHalf; key += 64 / kPer) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(src + unit_offset<D>(key, vu));
+                            uint4 x, y;
+                            widen4(w.x, x.x, x.y);
+                            widen4(w.y, x.z, x.w);
+                            widen4(w.z, y.x, y.y);
+                            widen4(w.w, y.z, y.w);
+                            *swizzled_unit(dst, key, vu % 4 * 2) = x;
+                            *swizzled_unit(dst, key, vu % 4 * 2 + 1) = y;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_addr(&sm.v_full[half]));
+                    named_bar_sync(kBarConv, 64);   // both warps have read the slot
+                    if (t == 0) mbar_arrive(smem_addr(&sm.kv_empty[st]));
+                }
+            }
         }
     } else {
         // -------------------------------------------------------------- softmax
-        const int quad = warp - 4, row = quad * 32 + lane;   // TMEM lane; in V's tiles, the key
+        const int quad = warp - 4, row = quad * 32 + lane;   // TMEM lane
         const uint32_t tS0 = tmem + (static_cast<uint32_t>(quad * 32) << 16), tO = tS0 + 128;
         const int G = p.seq.group;
         int T = 0, nq = 0;   // tiles, parts with tiles
@@ -337,11 +395,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             const int lo = p.seq.window > 0 ? max(pos_row - p.seq.window + 1, 0) : 0;
             float rowc = 0.f;   // the row's scale, and the exponent's
             if (part.tiles > 0) {
-                const int buf = nq % K::kQBufs;
-                ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full[buf], nq / K::kQBufs));
-                rowc = sm.q_scale[buf][row] * p.scale_log2;
+                ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full, nq));
+                rowc = sm.q_scale[row] * p.scale_log2;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty[buf]));
+                if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty));
             }
             float l = 0.f, ref = kNone;   // the exponents' offset: M - kShift
 #pragma unroll 1
@@ -351,42 +408,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                 if (ok) ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots));
                 const bool absent =   // a block on a page that the cache does not have, or not needed
                     __any_sync(0xffffffffu, sm.scales[sc][8 + (lane & 7)] < 0.f);
-                const bool edge = absent || kt < part.all_lo || kt + kKeys - 1 > part.all_hi;
-                if (ok && edge) {
-                    // 0 * NaN is NaN: no row's product may meet a NaN that it does not see.
-                    // (The values have to be there to be looked at.)  This thread looks after
-                    // key kt + row.
-                    const int vi = 2 * T + 1, pos = kt + row;
-                    ok = __all_sync(0xffffffffu, wait(&sm.kv_full[vi % kSlots], vi / kSlots));
-                    uint4* vrow = reinterpret_cast<uint4*>(sKV + (vi % kSlots) * K::kSlotBytes + row * D);
-                    const bool hidden = sm.scales[sc][8 + row / 16] < 0.f || pos < part.lo_key ||
-                                        pos > part.hi_key || pos >= part.req.len;
-                    if (hidden) {
-#pragma unroll
-                        for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0, 0, 0, 0);
-                    } else if (pos < part.all_lo || pos > part.all_hi) {
-#pragma unroll 1
-                        for (int u = 0; u < D / 16; ++u) {
-                            uint4 w = vrow[u];
-                            const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), e = nan_bytes(w.z),
-                                           f = nan_bytes(w.w);
-                            if (a | b | e | f) {
-                                // those channels become NaN at the part's end, for the rows that see them
-                                w.x &= ~(a | (a - (a >> 7)));
-                                w.y &= ~(b | (b - (b >> 7)));
-                                w.z &= ~(e | (e - (e >> 7)));
-                                w.w &= ~(f | (f - (f >> 7)));
-                                vrow[u] = w;
-                                sm.poison = 1;
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                }
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    const uint32_t tS = tS0 + 64 * half;
-                    const int kb = kt + 64 * half;
+                    const uint32_t tS = tS0 + kHalf * half;
+                    const int kb = kt + kHalf * half;
                     if (ok) ok = __all_sync(0xffffffffu, wait(&sm.s_full[half], T));
                     if (ok) {
                         tc_fence_after();
@@ -472,37 +497,23 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                 }
                             }
                         }
-                        // weights, their sum, and their pieces (32 keys are 8 columns of a piece)
+                        // weights and their sum
+                        uint32_t h[32];
 #pragma unroll
-                        for (int c0 = 0; c0 < 64; c0 += 32) {
-                            uint32_t h[16];
+                        for (int b = 0; b < 4; ++b) {
+                            uint64_t sum2[2];
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                uint64_t sum2 = 0;
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int c = c0 + 16 * b + 2 * j;
-                                    const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]);
-                                    sum2 = j == 0 ? f2_pack(w0, w1) : f2_add(sum2, f2_pack(w0, w1));
-                                    h[8 * b + j] = pack2<kElemF16>(w0, w1);
-                                }
-                                const float2 sum = f2_unpack(sum2);
-                                l = fmaf(sum.x + sum.y, inv_vs[c0 / 16 + b], l);
+                            for (int j = 0; j < 8; ++j) {
+                                const int c = 16 * b + 2 * j;
+                                const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]);
+                                const uint64_t w2 = f2_pack(w0, w1);
+                                sum2[j & 1] = j < 2 ? w2 : f2_add(sum2[j & 1], w2);
+                                h[8 * b + j] = pack2<kElemF16>(w0, w1);
                             }
-#pragma unroll
-                            for (int q = 0; q < K::kP; ++q) {
-                                uint32_t words[8];
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (K::kP == 3 && q == 2) h[j] += 0x00800080u;
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) words[j] = __byte_perm(h[2 * j], h[2 * j + 1], 0x7531);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (q + 1 < K::kP) h[j] = sub_f16x2(h[j], h[j] & 0xff00ff00u);
-                                tmem_st8(tS + 16 * q + c0 / 4, words);
-                            }
+                            const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
+                            l = fmaf(sum.x + sum.y, inv_vs[b], l);
                         }
+                        tmem_st32(tS, h);
                         tmem_st_wait();
                         tc_fence_before();
                     }
@@ -520,51 +531,46 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                    (part.tile0 + part.tiles) * kKeys - 1 > part.all_hi)) {
                 // (parts with no such edge set no poison)
                 named_bar_sync(kBarRows, 128);
-                poison = sm.poison != 0;
+                poison = sm.poison[(nq - 1) & 1] != 0;
                 named_bar_sync(kBarRows, 128);
-                if (row == 0) sm.poison = 0;
+                if (row == 0) sm.poison[(nq - 1) & 1] = 0;
             }
             if (ok) {
-                uint32_t nan[D / 32] = {};
-                if (poison && real) row_nan<D>(p, part, lo, hi, nan);
                 const bool whole = part.whole;
                 const float mul = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;   // (NaN divides on)
                 const long long slot = (2LL * blockIdx.x + (part.begins ? 1 : 0)) * kRows + row;
                 const bool in = real && fa_index_ok(token, p.seq.total_tokens, p.status);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+                uint16_t* out = static_cast<uint16_t*>(p.o) + (token * p.seq.Hq + head) * D;
+                float* partial = p.part_o + slot * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
                     uint32_t x[32];
                     if (part.tiles > 0) {
-                        tmem_ld32(tO + c * 32, x);
+                        tmem_ld32(tO + c, x);
                         tmem_ld_wait();
                         reg_fence(x);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) x[j] = 0;
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        x[j] = __float_as_uint(__uint_as_float(x[j]) * mul);
-                        if ((nan[c] >> j) & 1u) x[j] = 0x7fc00000u;
-                    }
                     if (in && whole) {
-                        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
-                                                              (token * p.seq.Hq + head) * D + c * 32);
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             uint32_t y[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                y[j] = pack2<E>(__uint_as_float(x[8 * u + 2 * j]), __uint_as_float(x[8 * u + 2 * j + 1]));
-                            out[u] = make_uint4(y[0], y[1], y[2], y[3]);
+                                y[j] = pack2<E>(__uint_as_float(x[8 * u + 2 * j]) * mul,
+                                                __uint_as_float(x[8 * u + 2 * j + 1]) * mul);
+                            *reinterpret_cast<uint4*>(out + c + 8 * u) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     } else if (in) {
-                        uint4* out = reinterpret_cast<uint4*>(p.part_o + slot * D + c * 32);
 #pragma unroll
                         for (int u = 0; u < 8; ++u)
-                            out[u] = make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+                            *reinterpret_cast<uint4*>(partial + c + 4 * u) =
+                                make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
                     }
                 }
+                if (poison && in) spoil_row<D>(p, part, lo, hi, whole ? out : nullptr, whole ? nullptr : partial);
                 const float m = ref == kNone ? 0.f : ref + kShift;
                 if (in && whole)
                     p.lse[row_stat_index(p.seq, part.b, head, part.req.start, tok)] =

@@ -48,7 +48,7 @@ struct Request {
     int len;        // tokens in the cache, the new ones among them
 };
 
-__device__ __forceinline__ Request load_request(const Kv8FwdParams& p, int b) {
+static __device__ __noinline__ Request load_request(const Kv8FwdParams& p, int b) {
     Request r;
     seq_bounds(p.seq, b, r.start, r.n);
     const long long room = static_cast<long long>(p.width) << p.page_log2;
@@ -65,13 +65,15 @@ struct Items {
     int blocks, pairs, cost;
 };
 
+// (Out of line, like the division: the kernels' many roles make much code, and what does not
+// fit the SM's instruction cache has to be fetched again and again.)
 template <int C>
-__device__ __forceinline__ Items items_of(const Kv8FwdParams& p, const Request& r) {
+static __device__ __noinline__ Items items_of(const Kv8FwdParams& p, int n, int len) {
     Items it;
     const int G = p.seq.group;
-    it.blocks = (r.n * G + C - 1) / C;
+    it.blocks = (n * G + C - 1) / C;
     it.pairs = (it.blocks + 1) / 2;
-    int most = (r.len + kKeys - 1) / kKeys;   // tiles of a block
+    int most = (len + kKeys - 1) / kKeys;   // tiles of a block
     if (p.seq.window > 0) {
         // a block's rows see window + (its tokens - 1) consecutive keys at most
         const long long span = static_cast<long long>(p.seq.window) + (C - 1) / G + 1;
@@ -84,17 +86,19 @@ __device__ __forceinline__ Items items_of(const Kv8FwdParams& p, const Request& 
     int both = 2 * most;
     if (p.seq.causal) {
         // blocks i and blocks - 1 - i end at positions that add up to this or less
-        const long long ends = 2LL * (r.len - r.n) + (it.blocks + 1) * static_cast<long long>(C) / G;
+        const long long ends = 2LL * (len - n) + (it.blocks + 1) * static_cast<long long>(C) / G;
         both = static_cast<int>(min(static_cast<long long>(both), max(ends / kKeys + 2, static_cast<long long>(most))));
     }
     it.cost = both + 2 * kItemCost<C>;
     return it;
 }
 
+static __device__ __noinline__ long long divide_long(long long a, long long b) { return a / b; }
+
 // 64-bit division that mostly is a 32-bit one.
 __device__ __forceinline__ long long divide(long long a, long long b) {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
+    return divide_long(a, b);
 }
 
 // CTA c of the first G takes units [c total / G, (c + 1) total / G) of `total`; G is the
@@ -154,10 +158,10 @@ struct Walk {
         } else {
             req = load_request(p, b);
         }
-        it = items_of<C>(p, req);
+        it = items_of<C>(p, req.n, req.len);
     }
     // The keys that the rows of block `blk` see.
-    __device__ void see(int blk, Part& part) const {
+    __device__ __noinline__ void see(int blk, Part& part) const {
         const int G = p.seq.group;
         part.row0 = blk * C;
         const int first = req.len - req.n + part.row0 / G;   // positions of its first and last token
@@ -235,17 +239,53 @@ __device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
 
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
-// The e4m3 values that pack4_e4m3 gives for four floats, as floats.
-__device__ __forceinline__ void e4m3_floats(uint32_t w, float (&f)[4]) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-    const float2 x = unpack2<kElemF16>(lo), y = unpack2<kElemF16>(hi);
-    f[0] = x.x;
-    f[1] = x.y;
-    f[2] = y.x;
-    f[3] = y.y;
+// Eight consecutive elements of a row of queries (D / 8 neighbouring lanes have the row, all
+// of them take part), cut into KQ e4m3 pieces for `dst` (pieces `piece` bytes apart): the row
+// times the power of two that brings its largest element into (224, 448], as fp16 numbers
+// (exact: 8 or 11 bits), each piece the rounding of what the ones before it leave.  Returns
+// the row's scale; an infinity or NaN makes it NaN, and with it the row.
+template <int D, int E, int KQ>
+__device__ __forceinline__ float cut_queries(uint4 w, uint8_t* dst, int piece) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t top = 0;   // magnitudes, as the integers of two 16-bit numbers
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __vmaxu2(top, u[j] & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t amax = __float_as_uint(unpack2<E>(top).x);
+    const bool fine = amax < 0x7f800000u;
+    const int k = fine ? row_exponent(amax) : 0;
+    const float inv = pow2f(-k);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<E>(u[j]);
+        h[j] = pack2<kElemF16>(f.x * inv, f.y * inv);
+    }
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+        uint32_t c[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            asm("{\n\t.reg .b16 lo, hi;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\t"
+                "mov.b32 %0, {lo, hi};\n\t}"
+                : "=r"(c[j]) : "r"(h[2 * j]), "r"(h[2 * j + 1]));
+        *reinterpret_cast<uint2*>(dst + q * piece) = make_uint2(c[0], c[1]);
+        if (q + 1 < KQ) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t lo, hi;
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+                    : "=r"(lo), "=r"(hi) : "r"(c[j]));
+                h[2 * j] = sub_f16x2(h[2 * j], lo);
+                h[2 * j + 1] = sub_f16x2(h[2 * j + 1], hi);
+            }
+        }
+    }
+    return fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
 }
 
 // Bytes of a word that are e4m3 NaN (0x7f or 0xff), as 0x80 in each.
@@ -291,13 +331,13 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Smem& sm) {
     auto units = [&](int b) -> long long {
         if (b >= B) return 0;
         r = load_request(p, b);
-        const Items it = items_of<C>(p, r);
+        const Items it = items_of<C>(p, r.n, r.len);
         return static_cast<long long>(it.pairs) * p.seq.Hkv * it.cost;
     };
     // request b's units end at `end`, `mine` of them: does the share begin there?
     auto look = [&](int b, long long mine, long long end) {
         if (begin >= end - mine && begin < end) {
-            const Items it = items_of<C>(p, r);
+            const Items it = items_of<C>(p, r.n, r.len);
             const long long at = begin - (end - mine), item = divide(at, it.cost);
             const int h = static_cast<int>(divide(item, it.pairs));
             sm.share.b0 = b;
@@ -369,113 +409,116 @@ __device__ __forceinline__ bool take_part(Smem& sm, int np, Part& part) {
 }
 
 // The producer warp: walks the CTA's share, hands its parts out, and for each part's tiles
-// copies K and V in turn into the ring of slots (pages by TMA, rows of d bytes swizzled over
-// d bytes) and the tile's 16 scales (K's, then V's; -1 for V's where a block's tokens are
-// hidden: behind the last key that is seen, or on a page that the cache does not have).
-template <int D, int C, int kSlots, class Smem>
+// copies K and V in units of U keys (K's units, then V's) through the ring of slots (pages by
+// TMA, rows of d bytes swizzled over d bytes), and with the first of them the tile's 16
+// scales (K's, then V's; -1 for V's where a block's tokens are hidden: behind the last key
+// that is seen, or on a page that the cache does not have).
+template <int D, int C, int U, int kSlots, class Smem>
 __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t* sKV) {
+    constexpr int kUnits = kKeys / U;          // of a side
     const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
+    const int page = 1 << p.page_log2, per_tile = kKeys >> p.page_log2;
+    const int box = min(page, U), boxes = U / box;   // keys of a copy, copies of a unit
+    const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
+    const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
+    int c = 0, items = 0;                      // tiles, units of the ring
+    bool ok = true, joined = false;
     Part part;
-            if (lane == 0) {
-                tma_prefetch_desc(&p.tm_k);
-                tma_prefetch_desc(&p.tm_v);
+    Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
+#pragma unroll 1
+    for (int np = 0;; ++np) {
+        if (np >= kParts)
+            mbar_wait_drain(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1, kDrainCycles);
+        const bool more = walk.next(part);
+        if (lane == 0) {
+            if (!more) part.tiles = -1;
+            sm.parts[np % kParts] = part;
+            mbar_arrive(smem_addr(&sm.part_full[np % kParts]));
+            if (more && part.begins && !part.whole) {
+                Kv8Join j;
+                j.last = share_of(sm.share.total, part.unit0 + part.item_tiles - 1,
+                                  sharers(sm.share.total, gridDim.x));
+                j.b = part.b;
+                j.h = part.h;
+                j.start = part.req.start;
+                j.n = part.req.n;
+                j.row0 = part.row0;
+                p.joins[blockIdx.x] = j;
+                joined = true;
             }
-            const int page = 1 << p.page_log2, per_tile = kKeys >> p.page_log2;
-            const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
-            const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
-            int c = 0, items = 0;                      // tiles, items of the ring
-            bool ok = true, joined = false;
-            Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
-    #pragma unroll 1
-            for (int np = 0;; ++np) {
-                if (np >= kParts)
-                    mbar_wait_drain(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1, kDrainCycles);
-                const bool more = walk.next(part);
-                if (lane == 0) {
-                    if (!more) part.tiles = -1;
-                    sm.parts[np % kParts] = part;
-                    mbar_arrive(smem_addr(&sm.part_full[np % kParts]));
-                    if (more && part.begins && !part.whole) {
-                        Kv8Join j;
-                        j.last = share_of(sm.share.total, part.unit0 + part.item_tiles - 1,
-                                          sharers(sm.share.total, gridDim.x));
-                        j.b = part.b;
-                        j.h = part.h;
-                        j.start = part.req.start;
-                        j.n = part.req.n;
-                        j.row0 = part.row0;
-                        p.joins[blockIdx.x] = j;
-                        joined = true;
-                    }
+        }
+        __syncwarp();
+        if (!more) break;
+        const int* row = p.table + static_cast<long long>(part.b) * p.width;
+        const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
+        const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
+        // the table's entries, 32 at a time, the next ones on their way
+        int base = part.tile0 * per_tile;
+        auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
+        int cur = part.tiles > 0 ? entry(base + lane) : -1;
+        int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
+#pragma unroll 1
+        for (int i = 0; i < part.tiles && ok; ++i, ++c) {
+            const int tile = part.tile0 + i;
+            if (tile * per_tile >= base + 32) {
+                base += 32;
+                cur = nxt;
+                nxt = entry(base + 32 + lane);
+            }
+            const int first = tile * per_tile - base;
+            // the scales of the tile's 8 blocks (their slot's last tile is long done)
+            const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
+#pragma unroll 1
+            for (int unit = 0; unit < 2 * kUnits; ++unit, ++items) {
+                // this lane's copy: keys from `key` of the tile on
+                const int key = (unit % kUnits) * U + (lane & (boxes - 1)) * box;
+                const int id = __shfl_sync(0xffffffffu, cur, (first + (key >> p.page_log2)) & 31);
+                const bool load = lane < boxes && id >= 0 && id < p.num_pages && tile * kKeys + key < lim;
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * D;
+                const int st = items % kSlots, use = items / kSlots;
+                if (use > 0) {
+                    ok = __all_sync(0xffffffffu, wait_for(p, sm, &sm.kv_empty[st], use - 1));
+                    if (!ok) break;
                 }
+                const uint32_t full = smem_addr(&sm.kv_full[st]);
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
-                if (!more) break;
-                const int* row = p.table + static_cast<long long>(part.b) * p.width;
-                const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
-                const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
-                // the table's entries, 32 at a time, the next ones on their way
-                int base = part.tile0 * per_tile;
-                auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
-                int cur = part.tiles > 0 ? entry(base + lane) : -1;
-                int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
-    #pragma unroll 1
-                for (int i = 0; i < part.tiles && ok; ++i, ++c) {
-                    const int tile = part.tile0 + i;
-                    if (tile * per_tile >= base + 32) {
-                        base += 32;
-                        cur = nxt;
-                        nxt = entry(base + 32 + lane);
-                    }
-                    const int first = tile * per_tile - base;
-                    // this lane's page of the tile
-                    const int id = __shfl_sync(0xffffffffu, cur, (first + (lane & (per_tile - 1))) & 31);
-                    const bool load = lane < per_tile && id >= 0 && id < p.num_pages;
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * page * D;
-                    // the scales of the tile's 8 blocks (their slot's last tile is long done)
-                    const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
-    #pragma unroll 1
-                    for (int side = 0; side < 2; ++side, ++items) {
-                        const int st = items % kSlots, use = items / kSlots;
-                        if (use > 0) {
-                            ok = __all_sync(0xffffffffu, wait_for(p, sm, &sm.kv_empty[st], use - 1));
-                            if (!ok) break;
-                        }
-                        uint8_t* dst = sKV + st * kKeys * D;
-                        const uint32_t full = smem_addr(&sm.kv_full[st]);
-                        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                        __syncwarp();
-                        if (load)
-                            tma_load_3d(smem_addr(dst + lane * page * D), side ? &p.tm_v : &p.tm_k, full, 0, 0,
-                                        id * p.seq.Hkv + part.h);
-                        if (side == 0) {
-                            const uint32_t sbar = smem_addr(&sm.scales_full[c % kScaleSlots]);
-                            bool plain = true;
-                            if (lane < 16) {
-                                float* to = &sm.scales[c % kScaleSlots][lane];
-                                if (sid >= 0 && sid < p.num_pages && tile * kKeys + side_blk * kKv8Block < lim) {
-                                    const long long at =
-                                        ((static_cast<long long>(sid) * p.seq.Hkv + part.h) << blocks_log2) +
-                                        (side_blk & ((1 << blocks_log2) - 1));
-                                    cp_async4(smem_addr(to), (lane < 8 ? p.k_scale : p.v_scale) + at);
-                                    plain = false;
-                                } else {
-                                    *to = lane < 8 ? 0.f : -1.f;   // hidden
-                                }
-                            }
-                            if (plain) mbar_arrive(sbar);
-                            else cp_async_arrive(sbar);
+                if (load)
+                    tma_load_3d(smem_addr(sKV + st * U * D + lane * box * D), unit < kUnits ? &p.tm_k : &p.tm_v,
+                                full, 0, key & (page - 1), id * p.seq.Hkv + part.h);
+                if (unit == 0) {
+                    const uint32_t sbar = smem_addr(&sm.scales_full[c % kScaleSlots]);
+                    bool plain = true;
+                    if (lane < 16) {
+                        float* to = &sm.scales[c % kScaleSlots][lane];
+                        if (sid >= 0 && sid < p.num_pages && tile * kKeys + side_blk * kKv8Block < lim) {
+                            const long long at =
+                                ((static_cast<long long>(sid) * p.seq.Hkv + part.h) << blocks_log2) +
+                                (side_blk & ((1 << blocks_log2) - 1));
+                            cp_async4(smem_addr(to), (lane < 8 ? p.k_scale : p.v_scale) + at);
+                            plain = false;
+                        } else {
+                            *to = lane < 8 ? 0.f : -1.f;   // hidden
                         }
                     }
+                    if (plain) mbar_arrive(sbar);
+                    else cp_async_arrive(sbar);
                 }
             }
-            if (lane == 0 && !joined) p.joins[blockIdx.x].last = 0;
-            // every copy lands before the CTA exits, whatever became of the other roles
-    #pragma unroll 1
-            for (int i = max(0, items - kSlots); i < items; ++i)
-                mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
-    #pragma unroll 1
-            for (int i = max(0, c - kScaleSlots); i < c; ++i)
-                mbar_wait_drain(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1, kDrainCycles);
+        }
+    }
+    if (lane == 0 && !joined) p.joins[blockIdx.x].last = 0;
+    // every copy lands before the CTA exits, whatever became of the other roles
+#pragma unroll 1
+    for (int i = max(0, items - kSlots); i < items; ++i)
+        mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
+#pragma unroll 1
+    for (int i = max(0, c - kScaleSlots); i < c; ++i)
+        mbar_wait_drain(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1, kDrainCycles);
 }
 
 // A launch that may begin while the kernel before it on the stream is ending (it waits for
