@@ -33,6 +33,11 @@ namespace {
 using namespace kv8;
 
 constexpr int kRows = 128;
+// The weights are fp16 numbers here, times 2^9: a row's reference moves when a key exceeds it
+// by more than 2^6 (fp16's largest number is near 2^16), which hardly happens once a row has
+// seen some keys, and weights down to 2^-23 of it keep all 11 bits.
+constexpr float kRowsShift = 9.f;
+constexpr float kRowsGrow = 6.f;
 
 constexpr int kHalf = 64;   // keys of a half tile
 
@@ -53,12 +58,16 @@ struct RowsCfg {
 struct RowsSmem {   // behind the tiles
     static constexpr bool kOutOfLine = true;
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
+    // the same, ready for the exponents: K's scale, log2 of V's, 1 / V's (-1: hidden)
+    float4 ready[kScaleSlots][8];
+    int absent[kScaleSlots];         // whether a block is hidden
     float q_scale[kRows];
     int3 window[kWindow];
     Share share;
     Part parts[kParts];
     long long warp_sums[kThreads / 32];
     uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
+    uint64_t ready_full[kScaleSlots];
     uint64_t part_full[kParts], part_empty[kParts];
     uint64_t q_full, q_empty, s_full[2], v_full[2], o_half[2], all_done;
     uint32_t tmem;
@@ -145,7 +154,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             mbar_init(smem_addr(&sm.kv_empty[i]), 1);
         }
 #pragma unroll 1
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(smem_addr(&sm.scales_full[i]), 32);
+            mbar_init(smem_addr(&sm.ready_full[i]), 1);
+        }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(smem_addr(&sm.part_full[i]), 1);
             mbar_init(smem_addr(&sm.part_empty[i]), 7);   // every warp but the producer
@@ -315,9 +327,24 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
                 if (ok) ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots));
+                const float ks = sm.scales[sc][lane & 7], vs = sm.scales[sc][8 + (lane & 7)];
+                const bool gone = vs < 0.f, absent = __any_sync(0xffffffffu, gone);
+                if (warp == 2) {
+                    const uint32_t vb = __float_as_uint(vs);
+                    float lvs = static_cast<float>(static_cast<int>(vb >> 23) - 127);
+                    float inv = __uint_as_float((254u << 23) - vb);
+                    if ((vb & 0x7fffffu) != 0 || vb < 0x00800000u || vb > 0x7e000000u) {
+                        // not a power of two, or one without a normal inverse
+                        lvs = log2f(vs);
+                        inv = 1.f / vs;
+                    }
+                    if (lane < 8) sm.ready[sc][lane] = gone ? make_float4(0.f, 0.f, -1.f, 0.f) : make_float4(ks, lvs, inv, 0.f);
+                    if (lane == 0) sm.absent[sc] = absent ? 1 : 0;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sm.ready_full[sc]));
+                }
                 const int kt = (part.tile0 + i) * kKeys;
-                const bool edge = __any_sync(0xffffffffu, sm.scales[sc][8 + (lane & 7)] < 0.f) ||
-                                  kt < part.all_lo || kt + kKeys - 1 > part.all_hi;
+                const bool edge = absent || kt < part.all_lo || kt + kKeys - 1 > part.all_hi;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const int it = 4 * T + 2 + half, st = it % kSlots;
@@ -405,78 +432,85 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
                 const int kt = (part.tile0 + i) * kKeys;
-                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots));
-                const bool absent =   // a block on a page that the cache does not have, or not needed
-                    __any_sync(0xffffffffu, sm.scales[sc][8 + (lane & 7)] < 0.f);
+                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.ready_full[sc], T / kScaleSlots));
+                const bool absent = sm.absent[sc] != 0;   // a block on a page that the cache does not have, or behind the last key
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const uint32_t tS = tS0 + kHalf * half;
                     const int kb = kt + kHalf * half;
+                    const float4* ready = &sm.ready[sc][4 * half];
+                    const bool edge = absent || kb < part.all_lo || kb + kHalf - 1 > part.all_hi;
                     if (ok) ok = __all_sync(0xffffffffu, wait(&sm.s_full[half], T));
                     if (ok) {
                         tc_fence_after();
-                        float s[64];
-                        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                        // the scales of the half's 4 blocks
-                        const bool none = ref == kNone;
-                        const float base = none ? 0.f : ref;
-                        float kc[4], off[4], inv_vs[4];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const float vs = sm.scales[sc][8 + 4 * half + b];
-                            const uint32_t vb = __float_as_uint(vs);
-                            float lvs = static_cast<float>(static_cast<int>(vb >> 23) - 127);
-                            inv_vs[b] = __uint_as_float((254u << 23) - vb);
-                            if ((vb & 0x7fffffu) != 0 || vb < 0x00800000u || vb > 0x7e000000u) {
-                                // not a power of two, or one without a normal inverse
-                                const float v = vs < 0.f ? 1.f : vs;
-                                lvs = log2f(v);
-                                inv_vs[b] = 1.f / v;
-                            }
-                            kc[b] = sm.scales[sc][4 * half + b] * rowc;
-                            off[b] = lvs - base;
-                        }
-                        tmem_ld_wait();
-                        reg_fence(*reinterpret_cast<uint32_t(*)[64]>(&s[0]));
-                        // exponents t - M + kShift in place of the products (M = 0 of a row that
-                        // has no reference yet)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint64_t c2 = f2_pack(kc[b], kc[b]), o2 = f2_pack(off[b], off[b]);
-#pragma unroll
-                            for (int c = 16 * b; c < 16 * b + 16; c += 2) {
-                                const float2 e = f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), c2, o2));
-                                s[c] = e.x;
-                                s[c + 1] = e.y;
-                            }
-                        }
-                        if (absent || kb < part.all_lo || kb + 63 > part.all_hi) {
+                        if (edge) {
+                            // hidden keys' products become -inf
                             const int clo = lo - kb, chi = min(hi, part.req.len - 1) - kb;
+#pragma unroll 1
+                            for (int c0 = 0; c0 < kHalf; c0 += 16) {
+                                const bool gone = ready[c0 / 16].z < 0.f;
+                                uint32_t x[16];
+                                tmem_ld16(tS + c0, x);
+                                tmem_ld_wait();
+                                reg_fence(x);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (c0 + j < clo || c0 + j > chi || gone) x[j] = 0xff800000u;
+                                tmem_st16(tS + c0, x);
+                            }
+                            tmem_st_wait();
+                        }
+                        uint32_t h[32];
+                        float sum[4];
+                        // Weights 2^(t - M + kRowsShift) (M = 0 of a row that has no reference yet).  They
+                        // are computed before it is known that no row's reference has to move, so
+                        // that the exponentials do not wait for the maxima; where one has, they
+                        // are computed again from the products.
+#pragma unroll 1
+                        for (bool again = false;; again = true) {
+                            const bool none = ref == kNone;
+                            const float base = none ? 0.f : ref;
+                            float s[64];
+                            tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                            tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                            tmem_ld_wait();
+                            reg_fence(*reinterpret_cast<uint32_t(*)[64]>(&s[0]));
 #pragma unroll
                             for (int b = 0; b < 4; ++b) {
-                                const bool gone = sm.scales[sc][8 + 4 * half + b] < 0.f;
+                                const float4 rd = ready[b];
+                                const float off = rd.y - base;
+                                float kc = rd.x * rowc;
+                                if (kc < 1e-30f) kc = 1e-30f;   // (0 * -inf is NaN; no product is that large)
+                                const uint64_t c2 = f2_pack(kc, kc), o2 = f2_pack(off, off);
 #pragma unroll
-                                for (int c = 16 * b; c < 16 * b + 16; ++c)
-                                    if (c < clo || c > chi || gone) s[c] = kNegInf;
+                                for (int c = 16 * b; c < 16 * b + 16; c += 2) {
+                                    const float2 e = f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), c2, o2));
+                                    s[c] = e.x;
+                                    s[c + 1] = e.y;
+                                }
                             }
-                        }
-                        float top4[4];
+                            float top4[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) top4[j] = s[j];
+                            for (int b = 0; b < 4; ++b) {
+                                uint64_t sum2[2];
+                                top4[b] = s[16 * b];
 #pragma unroll
-                        for (int c = 4; c + 8 <= 64; c += 8)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) top4[j] = fmax3(top4[j], s[c + 2 * j], s[c + 2 * j + 1]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) top4[j] = fmaxf(top4[j], s[60 + j]);
-                        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                        const bool moves = none ? top > kNegInf : top > kShift + kGrow;
-                        if (__any_sync(0xffffffffu, moves)) {
+                                for (int j = 0; j < 8; ++j) {
+                                    const int c = 16 * b + 2 * j;
+                                    const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]);
+                                    top4[b] = fmax3(top4[b], s[c], s[c + 1]);
+                                    const uint64_t w2 = f2_pack(w0, w1);
+                                    sum2[j & 1] = j < 2 ? w2 : f2_add(sum2[j & 1], w2);
+                                    h[8 * b + j] = pack2<kElemF16>(w0, w1);
+                                }
+                                const float2 both = f2_unpack(f2_add(sum2[0], sum2[1]));
+                                sum[b] = both.x + both.y;
+                            }
+                            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                            const bool moves = none ? top > kNegInf : top > kRowsShift + kRowsGrow;
+                            if (again || !__any_sync(0xffffffffu, moves)) break;
                             // the row's reference moves up to its largest key
-                            const float by = moves ? kShift - top : 0.f;
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) s[c] += by;
+                            const float by = moves ? kRowsShift - top : 0.f;
                             const float f = none ? 1.f : ex2_approx(by);
                             l *= f;
                             if (moves) ref = base - by;
@@ -497,22 +531,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                 }
                             }
                         }
-                        // weights and their sum
-                        uint32_t h[32];
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            uint64_t sum2[2];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int c = 16 * b + 2 * j;
-                                const float w0 = ex2_approx(s[c]), w1 = ex2_approx(s[c + 1]);
-                                const uint64_t w2 = f2_pack(w0, w1);
-                                sum2[j & 1] = j < 2 ? w2 : f2_add(sum2[j & 1], w2);
-                                h[8 * b + j] = pack2<kElemF16>(w0, w1);
-                            }
-                            const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
-                            l = fmaf(sum.x + sum.y, inv_vs[b], l);
-                        }
+                        for (int b = 0; b < 4; ++b) l = fmaf(sum[b], ready[b].z, l);
                         tmem_st32(tS, h);
                         tmem_st_wait();
                         tc_fence_before();
