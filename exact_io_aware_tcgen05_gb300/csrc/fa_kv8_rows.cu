@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         // ----------------------------------------------------- queries and values
         constexpr int kLanes = D / 8;         // threads of a row of queries
         constexpr int kPass = 64 / kLanes;    // rows at a time
-        constexpr int kBatch = 4;             // passes whose loads are in flight together
+        constexpr int kAhead = 4;
         const int t = threadIdx.x - 64, sub = t % kLanes;
         int nq = 0, T = 0;
         bool ok = true;
@@ -286,35 +286,31 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             if (part.tiles == 0) continue;
             const int G = p.seq.group, rows = part.req.n * G;
             const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
-            // a batch of rows' loads is in flight while the one before it is cut into pieces
-            uint4 w[2][kBatch];
-            auto load = [&](uint4 (&x)[kBatch], int n0) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int n = n0 + i * kPass;
-                    const int more = small_div(rem0 + n, G, p.group_inv);
-                    const int head = part.h * G + rem0 + n - more * G;
-                    const long long token = part.req.start + tok0 + more;
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (n < kRows && part.row0 + n < rows)
-                        x[i] = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
-                }
+            // (rows' loads are kAhead passes ahead of the cutting into pieces)
+            auto load = [&](int n) {
+                const int more = small_div(rem0 + n, G, p.group_inv);
+                const int head = part.h * G + rem0 + n - more * G;
+                const long long token = part.req.start + tok0 + more;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (n < kRows && part.row0 + n < rows)
+                    x = __ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
+                return x;
             };
-            load(w[0], t / kLanes);
+            uint4 w[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) w[i] = load(t / kLanes + i * kPass);
             // the last part's products with its queries
             if (nq > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, nq - 1));
 #pragma unroll 1
-            for (int n0 = t / kLanes; n0 < kRows; n0 += kBatch * kPass) {
-                load(w[1], n0 + kBatch * kPass);
+            for (int n = t / kLanes; n < kRows; n += kPass) {
+                const uint4 x = w[0];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int n = n0 + i * kPass;
-                    const float scale = cut_queries<D, E, K::kQ>(
-                        w[0][i], sQ + unit_offset<D>(n, sub >> 1) + (sub & 1) * 8, K::kQPiece);
-                    if (sub == 0) sm.q_scale[n] = scale;
-                    w[0][i] = w[1][i];
-                }
+                for (int i = 0; i + 1 < kAhead; ++i) w[i] = w[i + 1];
+                w[kAhead - 1] = load(n + kAhead * kPass);
+                const float scale = cut_queries<D, E, K::kQ>(
+                    x, sQ + unit_offset<D>(n, sub >> 1) + (sub & 1) * 8, K::kQPiece);
+                if (sub == 0) sm.q_scale[n] = scale;
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&sm.q_full));
@@ -384,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                 }
                             }
                         }
-#pragma unroll 4
+#pragma unroll 2
                         for (int key = t / kPer; key < kHalf; key += 64 / kPer) {
                             const uint4 w = *reinterpret_cast<const uint4*>(src + unit_offset<D>(key, vu));
                             uint4 x, y;

@@ -161,7 +161,7 @@ struct Walk {
         it = items_of<C>(p, req.n, req.len);
     }
     // The keys that the rows of block `blk` see.
-    __device__ __noinline__ void see(int blk, Part& part) const {
+    __device__ __forceinline__ void see(int blk, Part& part) const {
         const int G = p.seq.group;
         part.row0 = blk * C;
         const int first = req.len - req.n + part.row0 / G;   // positions of its first and last token
@@ -174,7 +174,7 @@ struct Walk {
         part.tile0 = part.lo_key / kKeys;
         part.item_tiles = part.hi_key >= part.lo_key ? part.hi_key / kKeys - part.tile0 + 1 : 0;
     }
-    __device__ bool next(Part& part) {
+    __device__ __forceinline__ bool next(Part& part) {
 #pragma unroll 1
         while (left > 0 && b < p.seq.B) {
             if (off >= it.cost) {
@@ -383,11 +383,29 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Smem& sm) {
     }
 }
 
-// The part of a wait that is not over at once, out of line: the kernel's roles wait in many
-// places, and its instructions have to be fetched.
+// The part of a wait that is not over at once, out of line: the kernels' roles wait in many
+// places.  The hardware suspends the thread for up to 20 us at a time, so that waiting warps
+// take no issue slots from the others; gives up as mbar_wait does.
 static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, long long limit,
-                                     int* status) {
-    return mbar_wait(bar, parity, abort, limit, status);
+                                            int* status) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > limit) {
+            *abort = 1;
+            atomicExch(status, kDevTimeout);
+            return false;
+        }
+    }
 }
 
 template <class Smem>
@@ -399,11 +417,16 @@ __device__ __forceinline__ bool wait_for(const Kv8FwdParams& p, Smem& sm, uint64
         return mbar_wait(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
 }
 
+// mbar_wait_drain, out of line.
+static __device__ __noinline__ void drain_on(uint32_t bar, uint32_t parity) {
+    mbar_wait_drain(bar, parity, kDrainCycles);
+}
+
 // Part number np, in registers; false behind the last.  After an abort too every role goes
 // through all the parts (their named barriers pair up), so these waits ignore it.
 template <class Smem>
 __device__ __forceinline__ bool take_part(Smem& sm, int np, Part& part) {
-    mbar_wait_drain(smem_addr(&sm.part_full[np % kParts]), (np / kParts) & 1, kDrainCycles);
+    drain_on(smem_addr(&sm.part_full[np % kParts]), (np / kParts) & 1);
     part = sm.parts[np % kParts];
     return part.tiles >= 0;
 }
@@ -432,7 +455,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
 #pragma unroll 1
     for (int np = 0;; ++np) {
         if (np >= kParts)
-            mbar_wait_drain(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1, kDrainCycles);
+            drain_on(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1);
         const bool more = walk.next(part);
         if (lane == 0) {
             if (!more) part.tiles = -1;
@@ -515,10 +538,10 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
     // every copy lands before the CTA exits, whatever became of the other roles
 #pragma unroll 1
     for (int i = max(0, items - kSlots); i < items; ++i)
-        mbar_wait_drain(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1, kDrainCycles);
+        drain_on(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1);
 #pragma unroll 1
     for (int i = max(0, c - kScaleSlots); i < c; ++i)
-        mbar_wait_drain(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1, kDrainCycles);
+        drain_on(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1);
 }
 
 // A launch that may begin while the kernel before it on the stream is ending (it waits for
