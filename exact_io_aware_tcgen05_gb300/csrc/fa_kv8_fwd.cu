@@ -38,7 +38,10 @@
 //                tile's 16 scales by 4-byte asynchronous copies
 //   warp 1       tcgen05 issuer; owns the TMEM allocation.  S^T of the next tile is issued
 //                before the weights of this one are ready (two S^T buffers)
-//   warps 2, 3   the items' queries: scaled, cut into pieces, into shared memory
+//   warp 2       the items' queries: scaled, cut into pieces, into shared memory
+//   warp 3       relay: waits for what the issuer's next products read, so that the issuer
+//                itself meets only named barriers (a shared-memory access by the issuing warp
+//                holds the products that follow back)
 //   warps 4..7   softmax: a lane has a key
 // The second CTA of the SM works while this one waits at the ends of items.
 #include "fa_kv8_work.cuh"
@@ -118,6 +121,7 @@ constexpr int kv8_smem_bytes() {
 
 // named barriers (0 is __syncthreads)
 constexpr int kBarP = 1;      // weights written, or not fitting; the softmax warps and the issuer
+constexpr int kBarK = 3;      // the next tile's keys (and queries) and this one's values are there
 constexpr int kBarMax = 2;    // the softmax warps' maxima (or a part's sums) written
 
 // Sums of v[0 .. N) over the warp's lanes, by halving: lane l ends with the sum of column
@@ -251,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
         for (int i = 0; i < kParts; ++i) {
             mbar_init(smem_addr(&sm.part_full[i]), 1);
-            mbar_init(smem_addr(&sm.part_empty[i]), 5);   // the issuer, 4 softmax warps
+            mbar_init(smem_addr(&sm.part_empty[i]), 6);   // the issuer, the relay, 4 softmax warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sm.q_full[i]), 64);
+            mbar_init(smem_addr(&sm.q_full[i]), 32);
             mbar_init(smem_addr(&sm.q_empty[i]), 5);    // the last S^T of the part, 4 softmax warps
             mbar_init(smem_addr(&sm.s_full[i]), 1);
         }
@@ -319,68 +323,60 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             --left;
             return true;
         };
-        auto issue_s = [&](int T) {   // lane 0: S^T of the tile that advance() came to, number T
-            const int st = (2 * T) % kSlots;
-            if (first) wait(&sm.q_full[np & 1], np >> 1);
-            wait(&sm.kv_full[st], (2 * T) / kSlots);
-            tc_fence_after();
-            const uint64_t kd = kv0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
-            const uint64_t qd = qd0 + static_cast<uint64_t>(((np & 1) * K::kQBytes) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-                mma_ss_f8(tmem + (T & 1) * K::kSCols, kd + 2 * kk, qd + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
-            mma_commit(smem_addr(&sm.s_full[T & 1]));
-            mma_commit(smem_addr(&sm.kv_empty[st]));
-            if (left == 0) mma_commit(smem_addr(&sm.q_empty[np & 1]));
-        };
-        int T = 0;
-        bool more = advance();
-        if (more && lane == 0) issue_s(0);
+        bool more = advance(), fresh = true;
+        if (more) named_bar_sync(kBarK, 64);
+        // Step T: S^T of tile T + 1, then (for T >= 0) the product with tile T's weights.
 #pragma unroll 1
-        while (more) {
-            const bool fresh = first;   // tile T is its part's first
+        for (int T = -1; more || T >= 0; ++T) {
+            if (lane == 0 && more) {
+                const int st = (2 * T + 2) % kSlots, buf = (T + 1) & 1;
+                tc_fence_after();
+                const uint64_t kd = kv0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
+                const uint64_t qd = qd0 + static_cast<uint64_t>(((np & 1) * K::kQBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                    mma_ss_f8(tmem + buf * K::kSCols, kd + 2 * kk, qd + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
+                mma_commit(smem_addr(&sm.s_full[buf]));
+                mma_commit(smem_addr(&sm.kv_empty[st]));
+                if (left == 0) mma_commit(smem_addr(&sm.q_empty[np & 1]));
+            }
+            __syncwarp();
+            if (T >= 0) {
+#pragma unroll 1
+                while (!named_bar_all(kBarP, 160, true)) {}   // until the weights fit
+                if (lane == 0) {
+                    const int st = (2 * T + 1) % kSlots;
+                    tc_fence_after();
+                    const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
+                    const uint64_t pd = pd0 + static_cast<uint64_t>((T % K::kPBufs * K::kPBytes) >> 4);
+#pragma unroll
+                    for (int q = 0; q < (K::kWideO ? 1 : K::kP); ++q)
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 32; ++kk)
+                            mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4),
+                                      pd + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
+                                      (!fresh || q > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(smem_addr(&sm.pv_done));
+                    mma_commit(smem_addr(&sm.kv_empty[st]));
+                }
+                __syncwarp();
+                if (!more) break;
+            }
+            fresh = first;   // tile T + 1 is its part's first
             first = false;
             more = advance();
-            // S^T of tile T + 1 first if its keys are there already
-            bool issued = false;
-            if (more && lane == 0 &&
-                mbar_try_wait(smem_addr(&sm.kv_full[(2 * T + 2) % kSlots]), ((2 * T + 2) / kSlots) & 1)) {
-                issue_s(T + 1);
-                issued = true;
-            }
-            __syncwarp();
-#pragma unroll 1
-            while (!named_bar_all(kBarP, 160, true)) {}   // until the weights fit
-            if (lane == 0) {
-                const int st = (2 * T + 1) % kSlots;
-                wait(&sm.kv_full[st], (2 * T + 1) / kSlots);
-                tc_fence_after();
-                const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
-                const uint64_t pd = pd0 + static_cast<uint64_t>((T % K::kPBufs * K::kPBytes) >> 4);
-#pragma unroll
-                for (int q = 0; q < (K::kWideO ? 1 : K::kP); ++q)
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 32; ++kk)
-                        mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4),
-                                  pd + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
-                                  (!fresh || q > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(smem_addr(&sm.pv_done));
-                mma_commit(smem_addr(&sm.kv_empty[st]));
-                if (more && !issued) issue_s(T + 1);
-            }
-            __syncwarp();
-            ++T;
+            named_bar_sync(kBarK, 64);   // keys of tile T + 2, values of tile T + 1
         }
         if (lane == 0) {
             mma_commit(smem_addr(&sm.all_done));
             mbar_wait_drain(smem_addr(&sm.all_done), 0, kDrainCycles);
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         // -------------------------------------------------------------- queries
         constexpr int kLanes = D / 8;         // threads of a row
-        constexpr int kRows = 64 / kLanes;    // rows at a time
-        const int t = threadIdx.x - 64, sub = t % kLanes;
+        constexpr int kRows = 32 / kLanes;    // rows at a time
+        const int t = lane, sub = t % kLanes;
         bool ok = true;
 #pragma unroll 1
         for (int np = 0; take(np, part); ++np) {
@@ -418,6 +414,29 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&sm.q_full[buf]));
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- relay
+        int T = 0;
+#pragma unroll 1
+        for (int np = 0; take(np, part); ++np) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
+#pragma unroll 1
+            for (int i = 0; i < part.tiles; ++i, ++T) {
+                if (lane == 0) {
+                    if (T > 0) wait(&sm.kv_full[(2 * T - 1) % kSlots], (2 * T - 1) / kSlots);
+                    wait(&sm.kv_full[(2 * T) % kSlots], (2 * T) / kSlots);
+                    if (i == 0) wait(&sm.q_full[np & 1], np >> 1);
+                }
+                __syncwarp();
+                named_bar_sync(kBarK, 64);
+            }
+        }
+        if (T > 0) {
+            if (lane == 0) wait(&sm.kv_full[(2 * T - 1) % kSlots], (2 * T - 1) / kSlots);
+            __syncwarp();
+            named_bar_sync(kBarK, 64);
         }
     } else {
         // -------------------------------------------------------------- softmax
