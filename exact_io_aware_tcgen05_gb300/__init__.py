@@ -646,8 +646,7 @@ def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
     zero: the request has ended and gives its pages back), for int32 CUDA tensors lens and
     grow [B], table [B, width], ring [num_pages] and state [3] (first free page's place in
     the ring, free pages, refused requests).  table and ring are updated in place; the
-    outputs are new tensors (parts of one), slots of ``tokens`` elements (-1 for tokens that
-    get no place)."""
+    outputs are new tensors, slots of ``tokens`` elements (-1 for tokens that get no place)."""
     dev = lens.get_device()
     if dev >= 0 and _elsewhere(dev, stream):
         return _there(kv8_plan, dev, stream, lens, grow, table, ring, state, page=page, tokens=tokens)
@@ -663,13 +662,15 @@ def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
     _int32("table", table, (B, width), dev)
     _int32("ring", ring, ring.shape, dev)
     _int32("state", state, (3,), dev)
-    lens_out, cu, slots, state_out = torch.split_with_sizes(
-        lens.new_empty(2 * B + tokens + 4), (B, B + 1, tokens, 3))
-    at = lens_out.data_ptr()
+    empty, int32, device = torch.empty, torch.int32, lens.device
+    lens_out = empty(B, dtype=int32, device=device)
+    cu = empty(B + 1, dtype=int32, device=device)
+    slots = empty(tokens, dtype=int32, device=device)
+    state_out = empty(3, dtype=int32, device=device)
     _check(load().fa_kv8_plan(lens.data_ptr(), grow.data_ptr(), B, table.data_ptr(), width,
-                              ring.data_ptr(), ring.shape[0], page, state.data_ptr(), at, at + 4 * B,
-                              at + 8 * B + 4, tokens, at + 8 * B + 4 + 4 * tokens,
-                              torch._C._cuda_getCurrentRawStream(dev)))
+                              ring.data_ptr(), ring.shape[0], page, state.data_ptr(),
+                              lens_out.data_ptr(), cu.data_ptr(), slots.data_ptr(), tokens,
+                              state_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
     return lens_out, cu, slots, state_out
 
 
@@ -742,15 +743,15 @@ def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, windo
             raise ValueError(f"q has {shape[0]} requests, lens {B}")
         N, T, lse_shape = shape[1], 0, (B, Hq, shape[1])
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be contiguous, of q's shape, type and device")
     if lse is None:
-        lse = q.new_empty(lse_shape, dtype=torch.float32)
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
     elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError(f"lse must be contiguous float32 {lse_shape} on q's device")
     if workspace is None:
-        workspace = lens.new_empty(_kv8_workspace(dev, B, Hq, Hkv, N, d, T), dtype=torch.uint8)
+        workspace = torch.empty(_kv8_workspace(dev, B, Hq, Hkv, N, d, T), dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on q's device")
     k8, k_scale, v8, v_scale = cache

@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -1068,8 +1069,10 @@ fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long 
     p.Hkv = Hkv;
     p.num_slots = num_pages * page;
     p.elem = static_cast<int>(dtype);
-    // a warp a token while there are few, one for the blocks of 16 tokens beyond that
-    p.chunk = T <= 1024 ? 1 : kKv8Block;
+    // tokens of a warp: all of a block's 16 where there are warps enough for the GPU (64 an SM)
+    // all the same, fewer where there are not, since a warp takes its blocks in turn
+    const long long warps = 2LL * T * Hkv, want = 64LL * sm_count();
+    p.chunk = static_cast<int>(std::min(std::max(warps / want, 1LL), static_cast<long long>(kKv8Block)));
     const cudaError_t e = launch_kv8_append(p, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append launch");
 }

@@ -1,8 +1,7 @@
 // fa_kv8_cache.cu -- the paged 8-bit cache's bookkeeping (block tables, slots, free
 // pages) and its writer.  The formats and rules are those of fa_kv8_plan and
 // fa_kv8_append in include/fa.h.
-#include "fa_kernels.h"
-#include "fa_ptx.cuh"
+#include "fa_kv8_work.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -16,22 +15,22 @@ namespace {
 // `warp_sums` holds one value per warp (32 at most).
 __device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    auto scan = [&](long long x) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += u;
+        }
+        return x;
+    };
+    v = scan(v);
     __syncthreads();   // the last scan's sums have been read
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    long long before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const long long s = warp_sums[w];
-        if (w < warp) before += s;
-        all += s;
-    }
-    *total = all;
-    return v + before;
+    // every warp scans the warps' sums for itself
+    const long long sums = scan(lane < warps ? warp_sums[lane] : 0);
+    *total = __shfl_sync(0xffffffffu, sums, 31);
+    return v + (warp > 0 ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0);
 }
 
 // What every CTA knows of each request after the scans.
@@ -51,6 +50,10 @@ struct PlanRequest {
 __global__ void __launch_bounds__(1024) kv8_plan_kernel(const Kv8PlanParams p) {
     extern __shared__ PlanRequest req[];   // [B]
     __shared__ long long warp_sums[32];
+    __shared__ int used;     // pages taken from the ring: the served requests with the largest sum
+    if (threadIdx.x == 0) used = 0;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int page = 1 << p.page_log2;
     const int cap = p.num_pages;
     int head = p.state[0] % cap;
@@ -58,7 +61,7 @@ __global__ void __launch_bounds__(1024) kv8_plan_kernel(const Kv8PlanParams p) {
     const int count = min(max(p.state[1], 0), cap);
     const long long room = static_cast<long long>(p.width) << p.page_log2;
 
-    long long tokens = 0, wanted = 0, used = 0, gone = 0, refused = 0;
+    long long tokens = 0, wanted = 0, gone = 0, refused = 0;
     for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         const bool in = b < p.B;
@@ -77,10 +80,8 @@ __global__ void __launch_bounds__(1024) kv8_plan_kernel(const Kv8PlanParams p) {
         const long long freed = in && g < 0 ? have : 0;
         const long long back = gone + block_scan(freed, warp_sums, &sum) - freed;
         gone += sum;
-        block_scan(served ? need : 0, warp_sums, &sum);
-        used += sum;
-        block_scan(in && g >= 0 && !served ? 1 : 0, warp_sums, &sum);
-        refused += sum;
+        if (served && need > 0) atomicMax(&used, static_cast<int>(last));
+        refused += __syncthreads_count(in && g >= 0 && !served);
         if (in) {
             PlanRequest r;
             r.end = static_cast<int>(min(end, static_cast<long long>(INT_MAX)));
@@ -177,6 +178,8 @@ __device__ __forceinline__ void unpack4_e4m3(uint32_t w, float (&f)[4]) {
 // eight codes leave a lane in one store.
 template <int D, int E>
 __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     constexpr int kLanes = D / 8;          // lanes of one token
     constexpr int kRows = 32 / kLanes;     // tokens the warp loads at a time
     constexpr int kSteps = kKv8Block / kRows;
@@ -283,8 +286,7 @@ cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream
             kv8_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    kv8_plan_kernel<<<grid, threads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return kv8::launch_dependent(kv8_plan_kernel, grid, threads, smem, stream, p);
 }
 
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stream) {
@@ -293,12 +295,9 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stre
     const long long warps = chunks * p.Hkv * 2;
     const long long grid = (warps * 32 + kThreads - 1) / kThreads;
     if (grid > INT_MAX) return cudaErrorInvalidValue;
-    const dim3 g(static_cast<unsigned>(grid));
-    if (d == 128 && p.elem == kElemBf16Code) kv8_append_kernel<128, kElemBf16><<<g, kThreads, 0, stream>>>(p);
-    else if (d == 128) kv8_append_kernel<128, kElemF16><<<g, kThreads, 0, stream>>>(p);
-    else if (p.elem == kElemBf16Code) kv8_append_kernel<64, kElemBf16><<<g, kThreads, 0, stream>>>(p);
-    else kv8_append_kernel<64, kElemF16><<<g, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    auto kern = d == 128 ? (p.elem == kElemBf16Code ? kv8_append_kernel<128, kElemBf16> : kv8_append_kernel<128, kElemF16>)
+                         : (p.elem == kElemBf16Code ? kv8_append_kernel<64, kElemBf16> : kv8_append_kernel<64, kElemF16>);
+    return kv8::launch_dependent(kern, static_cast<int>(grid), kThreads, 0, stream, p);
 }
 
 }  // namespace fa

@@ -14,13 +14,13 @@
 // maximum crosses lanes.
 //
 // Bound by the tensor cores and the exponentials together: a 128 x 128 tile at d = 128 takes
-// 1024 cycles of MMAs for bf16 (2 x 4 of 128 x 128 x 32 8-bit, 8 of 128 x 128 x 16), and 16384
-// exponentials, 1024 cycles at 16 a cycle.  So that neither waits for the other, a tile goes
-// in two halves of 64 keys, each with its own S columns, which its P takes over: while the
-// softmax is on one half, the tensor cores multiply the other one's P and the next tile's
-// keys; and two CTAs share the SM.
+// 1024 cycles of MMAs for bf16 (2 x 4 of 128 x 128 x 32 8-bit, 8 of 128 x 128 x 16; MMAs of 64
+// columns ran no faster than those of 128), and 16384 exponentials, 1024 cycles at 16 a cycle.
+// The softmax takes a tile in two halves of 64 keys, so that the first half's product runs
+// during the second's softmax; P takes the place of the scores in TMEM.  Between a tile's
+// second half and the next tile's scores the SM's other CTA has the exponentials to itself.
 //
-// One CTA (256 threads, two per SM, half the TMEM each: S and P 2 x 64 columns, O d):
+// One CTA (256 threads, two per SM, half the TMEM each: S and P 128 columns, O d):
 //   warp 0       producer (fa_kv8_work.cuh)
 //   warp 1       tcgen05 issuer; owns the TMEM allocation
 //   warps 2, 3   an item's queries, scaled and cut into pieces; then the tiles' values to fp16
@@ -69,7 +69,7 @@ struct RowsSmem {   // behind the tiles
     uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
     uint64_t ready_full[kScaleSlots];
     uint64_t part_full[kParts], part_empty[kParts];
-    uint64_t q_full, q_empty, s_full[2], v_full[2], o_half[2], all_done;
+    uint64_t q_full, q_empty, s_full, o_half[2], all_done;
     uint32_t tmem;
     int abort;
     int poison[2];                   // [part parity] NaN found among values that only some rows see
@@ -84,7 +84,7 @@ constexpr int rows_fixed_bytes() {
 template <int D, int E>
 constexpr int rows_slots() {
     const int n = (kCtaSmem - rows_fixed_bytes<D, E>()) / RowsCfg<D, E>::kSlotBytes;
-    return n < kMaxSlots ? n : kMaxSlots;
+    return (n < kMaxSlots ? n : kMaxSlots) / 2 * 2;   // (even: a tile's K units lie side by side)
 }
 
 template <int D, int E>
@@ -92,7 +92,7 @@ constexpr int rows_smem_bytes() {
     return rows_fixed_bytes<D, E>() + rows_slots<D, E>() * RowsCfg<D, E>::kSlotBytes;
 }
 
-constexpr int kBarP = 1;     // + half: weights written; the softmax warps and the issuer
+constexpr int kBarP = 1;     // + half: weights and values there; softmax warps, values' warps, issuer
 constexpr int kBarRows = 3;  // the softmax warps among themselves
 constexpr int kBarConv = 4;  // warps 2 and 3 among themselves
 
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     using K = RowsCfg<D, E>;
     constexpr int kSlots = rows_slots<D, E>();
     static_assert(kSlots >= 4 && kSlots / 4 + 2 < kScaleSlots, "ring of key/value tiles");
-    constexpr uint32_t kIdescS = idesc_f32acc(kRows, kHalf, false, false, kElemFp8);
+    constexpr uint32_t kIdescS = idesc_f32acc(kRows, kKeys, false, false, kElemFp8);
     constexpr uint32_t kIdescO = idesc_f32acc(kRows, D, false, true, kElemF16);
 
     extern __shared__ uint8_t smem_raw[];
@@ -165,10 +165,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         mbar_init(smem_addr(&sm.q_full), 64);
         mbar_init(smem_addr(&sm.q_empty), 5);             // the last S of the part, 4 softmax warps
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sm.s_full[i]), 1);
-            mbar_init(smem_addr(&sm.v_full[i]), 64);
             mbar_init(smem_addr(&sm.o_half[i]), 1);
         }
+        mbar_init(smem_addr(&sm.s_full), 1);
         mbar_init(smem_addr(&sm.all_done), 1);
         fence_barrier_init();
     }
@@ -214,54 +213,51 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             --left;
             return true;
         };
-        auto issue_s = [&](int T, int half) {   // lane 0: half of S of the tile advance() came to
-            const int it = 4 * T + half, st = it % kSlots;
-            if (half == 0 && first) wait(&sm.q_full, nq);
-            wait(&sm.kv_full[st], it / kSlots);
-            tc_fence_after();
-            const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
-#pragma unroll
-            for (int q = 0; q < K::kQ; ++q)
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                    mma_ss_f8(tmem + kHalf * half, q0 + ((q * K::kQPiece) >> 4) + 2 * kk, kd + 2 * kk, kIdescS,
-                              (q > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(smem_addr(&sm.s_full[half]));
-            mma_commit(smem_addr(&sm.kv_empty[st]));
-            if (half == 1 && left == 0) mma_commit(smem_addr(&sm.q_empty));
-        };
-        auto issue_o = [&](int T, int half, bool fresh) {   // lane 0: O += P V of tile T's half
-            wait(&sm.v_full[half], T);
-            tc_fence_after();
-            const uint64_t vd = v0 + static_cast<uint64_t>((half % K::kV16Bufs * K::kV16Bytes) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)
-                mma_ts(tmem + 128, tmem + kHalf * half + 8 * kk, vd + ((kk * 2048) >> 4), kIdescO,
-                       (!fresh || half > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(smem_addr(&sm.o_half[half]));
-        };
-        // Step (T, half): the product of tile T's half (none for T = -1), then S of tile T + 1's.
-        bool more = advance(), fresh = true, ahead = false;
+        // A shared-memory access by the issuing warp holds back the products that follow, so
+        // within a part it meets only named barriers: the warps of the values come to each
+        // half's barrier once those and (the second half's) the next tile's keys are there.
+        // Step T: the products of tile T's halves (none for T = -1), then S of tile T + 1.
+        bool more = advance(), fresh = true;
 #pragma unroll 1
-        for (int T = -1;; ++T) {
+        for (int T = -1; more || T >= 0; ++T) {
+            if (T >= 0) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (T >= 0) named_bar_sync(kBarP + half, 160);
-                if (lane == 0) {
-                    if (T >= 0) issue_o(T, half, fresh);
-                    // In the first half S of the next tile goes ahead unless its keys or its
-                    // part's queries are still on the way; what is left follows in the second.
-                    const int it = 4 * T + 4;
-                    if (half == 0)
-                        ahead = more && mbar_try_wait(smem_addr(&sm.kv_full[it % kSlots]), (it / kSlots) & 1) &&
-                                (!first || mbar_try_wait(smem_addr(&sm.q_full), nq & 1));
-#pragma unroll 1
-                    for (int h = half == 1 && !ahead ? 0 : half; more && h <= half && (half == 1 || ahead); ++h)
-                        issue_s(T + 1, h);
+                for (int half = 0; half < 2; ++half) {
+                    named_bar_sync(kBarP + half, 224);
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint64_t vd = v0 + static_cast<uint64_t>((half % K::kV16Bufs * K::kV16Bytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kHalf / 16; ++kk)
+                            mma_ts(tmem + 128, tmem + kHalf * half + 8 * kk, vd + ((kk * 2048) >> 4), kIdescO,
+                                   (!fresh || half > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(smem_addr(&sm.o_half[half]));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!more) break;
             }
-            if (!more) break;
+            if (lane == 0) {
+                const int it = 4 * T + 4, st = it % kSlots;   // the keys' two slots are neighbours
+                if (first) {
+                    wait(&sm.q_full, nq);
+                    wait(&sm.kv_full[st], it / kSlots);
+                    wait(&sm.kv_full[st + 1], it / kSlots);
+                }
+                tc_fence_after();
+                const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
+#pragma unroll
+                for (int q = 0; q < K::kQ; ++q)
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_ss_f8(tmem, q0 + ((q * K::kQPiece) >> 4) + 2 * kk, kd + 2 * kk, kIdescS,
+                                  (q > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(smem_addr(&sm.s_full));
+                mma_commit(smem_addr(&sm.kv_empty[st]));
+                mma_commit(smem_addr(&sm.kv_empty[st + 1]));
+                if (left == 0) mma_commit(smem_addr(&sm.q_empty));
+            }
+            __syncwarp();
             fresh = first;   // tile T + 1 is its part's first
             first = false;
             more = advance();
@@ -380,22 +376,31 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                 }
                             }
                         }
-#pragma unroll 2
-                        for (int key = t / kPer; key < kHalf; key += 64 / kPer) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(src + unit_offset<D>(key, vu));
+                        uint4 w[kPer];
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j)
+                            w[j] = *reinterpret_cast<const uint4*>(src + unit_offset<D>(t / kPer + j * (64 / kPer), vu));
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) {
+                            const int key = t / kPer + j * (64 / kPer);
                             uint4 x, y;
-                            widen4(w.x, x.x, x.y);
-                            widen4(w.y, x.z, x.w);
-                            widen4(w.z, y.x, y.y);
-                            widen4(w.w, y.z, y.w);
+                            widen4(w[j].x, x.x, x.y);
+                            widen4(w[j].y, x.z, x.w);
+                            widen4(w[j].z, y.x, y.y);
+                            widen4(w[j].w, y.z, y.w);
                             *swizzled_unit(dst, key, vu % 4 * 2) = x;
                             *swizzled_unit(dst, key, vu % 4 * 2 + 1) = y;
                         }
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(smem_addr(&sm.v_full[half]));
                     named_bar_sync(kBarConv, 64);   // both warps have read the slot
                     if (t == 0) mbar_arrive(smem_addr(&sm.kv_empty[st]));
+                    if (half == 1 && i + 1 < part.tiles && ok) {   // the next tile's keys, for the issuer
+                        const int ik = 4 * T + 4;
+                        ok = __all_sync(0xffffffffu, wait(&sm.kv_full[ik % kSlots], ik / kSlots) &&
+                                                         wait(&sm.kv_full[ik % kSlots + 1], ik / kSlots));
+                    }
+                    named_bar_signal(kBarP + half, 224, ok);
                 }
             }
         }
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                     const int kb = kt + kHalf * half;
                     const float4* ready = &sm.ready[sc][4 * half];
                     const bool edge = absent || kb < part.all_lo || kb + kHalf - 1 > part.all_hi;
-                    if (ok) ok = __all_sync(0xffffffffu, wait(&sm.s_full[half], T));
+                    if (ok && half == 0) ok = __all_sync(0xffffffffu, wait(&sm.s_full, T));
                     if (ok) {
                         tc_fence_after();
                         if (edge) {
@@ -511,9 +516,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                             l *= f;
                             if (moves) ref = base - by;
                             if (i > 0 || half > 0) {
-                                // The last tile's product of this half was complete before this S;
-                                // that of the half before this one is waited for.
-                                ok = __all_sync(0xffffffffu, wait(&sm.o_half[half ^ 1], half == 0 ? T - 1 : T));
+                                // The last tile's products were complete before this tile's S; the
+                                // first half's is waited for.
+                                if (half == 1) ok = __all_sync(0xffffffffu, wait(&sm.o_half[0], T));
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int c = 0; c < D; c += 16) {
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                         tmem_st_wait();
                         tc_fence_before();
                     }
-                    named_bar_signal(kBarP + half, 160, ok);
+                    named_bar_signal(kBarP + half, 224, ok);
                 }
             }
             // ------------------------------------------------ the part's end

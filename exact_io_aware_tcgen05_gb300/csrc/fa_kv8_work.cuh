@@ -546,8 +546,9 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
 
 // A launch that may begin while the kernel before it on the stream is ending (it waits for
 // that one's results itself).
-inline cudaError_t launch_dependent(void (*kern)(Kv8FwdParams), int grid, int threads, int smem,
-                             cudaStream_t stream, const Kv8FwdParams& p) {
+template <class Params>
+cudaError_t launch_dependent(void (*kern)(Params), int grid, int threads, int smem, cudaStream_t stream,
+                             const Params& p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
