@@ -23,8 +23,9 @@
 // One CTA (256 threads, two per SM, half the TMEM each: S and P 128 columns, O d):
 //   warp 0       producer (fa_kv8_work.cuh)
 //   warp 1       tcgen05 issuer; owns the TMEM allocation
-//   warps 2, 3   an item's queries, scaled and cut into pieces; then the tiles' values to fp16
+//   warps 2, 3   the tiles' values to fp16
 //   warps 4..7   softmax and output, a row per thread
+//   warps 2..7   an item's queries, scaled and cut into pieces
 #include "fa_kv8_work.cuh"
 
 namespace fa {
@@ -62,6 +63,7 @@ struct RowsSmem {   // behind the tiles
     float4 ready[kScaleSlots][8];
     int absent[kScaleSlots];         // whether a block is hidden
     float q_scale[kRows];
+    int q_next;                      // claims of rows to cut (cut_rows)
     int3 window[kWindow];
     Share share;
     Part parts[kParts];
@@ -103,6 +105,45 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+// A part's queries into their pieces, by the warps that have nothing else to do: each claims
+// a warp's load of rows at a time, the next one's load on its way while it cuts the last one,
+// until there are none left.  `next` counts the claims of all parts, for each part kClaims
+// and one more (too many) for each of the 6 warps.
+template <int D, int E>
+__device__ __noinline__ void cut_rows(const Kv8FwdParams& p, int& next, float* q_scale, uint8_t* sQ, int start,
+                                      int n, int h, int row0) {
+    using K = RowsCfg<D, E>;
+    constexpr int kLanes = D / 8;          // threads of a row
+    constexpr int kPass = 32 / kLanes;     // rows of a warp's load
+    constexpr int kClaims = kRows / kPass;
+    const int lane = threadIdx.x & 31, sub = lane % kLanes, G = p.seq.group, rows = n * G;
+    const int tok0 = row0 / G, rem0 = row0 - tok0 * G;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    int r = -1;
+#pragma unroll 1
+    while (true) {
+        int c = lane == 0 ? atomicAdd(&next, 1) : 0;
+        c = __shfl_sync(0xffffffffu, c, 0) % (kClaims + 6);
+        const int r2 = c * kPass + lane / kLanes;
+        uint4 w2 = make_uint4(0, 0, 0, 0);
+        if (c < kClaims && row0 + r2 < rows) {
+            const int more = small_div(rem0 + r2, G, p.group_inv);
+            const int head = h * G + rem0 + r2 - more * G;
+            const long long token = start + tok0 + more;
+            w2 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + token * p.q_stride +
+                                                      head * D + sub * 8));
+        }
+        if (r >= 0) {
+            const float scale = cut_queries<D, E, K::kQ>(
+                w, sQ + unit_offset<D>(r, sub >> 1) + (sub & 1) * 8, K::kQPiece);
+            if (sub == 0) q_scale[r] = scale;
+        }
+        if (c >= kClaims) return;
+        w = w2;
+        r = r2;
+    }
+}
+
 // NaN for the channels in which a row sees a NaN code among the part's values that not every
 // row sees.  Rare: the codes are read again.
 template <int D>
@@ -118,6 +159,7 @@ __device__ __noinline__ void spoil_row(const Kv8FwdParams& p, const Part& part, 
         if (id < 0 || id >= p.num_pages) continue;
         const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
                             (j & ((1 << p.page_log2) - 1));
+#pragma unroll 1
         for (int c = 0; c < D; ++c) {
             if ((__ldg(p.v8 + r * D + c) & 0x7f) != 0x7f) continue;
             if (out) out[c] = 0x7fff;   // a NaN of either type
@@ -148,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     if (threadIdx.x == 0) {
         sm.abort = 0;
         sm.poison[0] = sm.poison[1] = 0;
+        sm.q_next = 0;
 #pragma unroll 1
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_addr(&sm.kv_full[i]), 1);
@@ -162,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             mbar_init(smem_addr(&sm.part_full[i]), 1);
             mbar_init(smem_addr(&sm.part_empty[i]), 7);   // every warp but the producer
         }
-        mbar_init(smem_addr(&sm.q_full), 64);
+        mbar_init(smem_addr(&sm.q_full), 192);            // warps 2 .. 7
         mbar_init(smem_addr(&sm.q_empty), 5);             // the last S of the part, 4 softmax warps
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sm.o_half[i]), 1);
@@ -269,10 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         __syncwarp();
     } else if (warp < 4) {
         // ----------------------------------------------------- queries and values
-        constexpr int kLanes = D / 8;         // threads of a row of queries
-        constexpr int kPass = 64 / kLanes;    // rows at a time
-        constexpr int kAhead = 4;
-        const int t = threadIdx.x - 64, sub = t % kLanes;
+        const int t = threadIdx.x - 64;
         int nq = 0, T = 0;
         bool ok = true;
 #pragma unroll 1
@@ -280,34 +320,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
             if (part.tiles == 0) continue;
-            const int G = p.seq.group, rows = part.req.n * G;
-            const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
-            // (rows' loads are kAhead passes ahead of the cutting into pieces)
-            auto load = [&](int n) {
-                const int more = small_div(rem0 + n, G, p.group_inv);
-                const int head = part.h * G + rem0 + n - more * G;
-                const long long token = part.req.start + tok0 + more;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (n < kRows && part.row0 + n < rows)
-                    x = __ldg(reinterpret_cast<const uint4*>(
-                        static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
-                return x;
-            };
-            uint4 w[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) w[i] = load(t / kLanes + i * kPass);
-            // the last part's products with its queries
             if (nq > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, nq - 1));
-#pragma unroll 1
-            for (int n = t / kLanes; n < kRows; n += kPass) {
-                const uint4 x = w[0];
-#pragma unroll
-                for (int i = 0; i + 1 < kAhead; ++i) w[i] = w[i + 1];
-                w[kAhead - 1] = load(n + kAhead * kPass);
-                const float scale = cut_queries<D, E, K::kQ>(
-                    x, sQ + unit_offset<D>(n, sub >> 1) + (sub & 1) * 8, K::kQPiece);
-                if (sub == 0) sm.q_scale[n] = scale;
-            }
+            cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&sm.q_full));
             ++nq;
@@ -423,6 +437,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             const int lo = p.seq.window > 0 ? max(pos_row - p.seq.window + 1, 0) : 0;
             float rowc = 0.f;   // the row's scale, and the exponent's
             if (part.tiles > 0) {
+                if (nq > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, nq - 1));
+                cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
+                fence_proxy_async_smem();
+                mbar_arrive(smem_addr(&sm.q_full));
                 ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full, nq));
                 rowc = sm.q_scale[row] * p.scale_log2;
                 __syncwarp();

@@ -57,7 +57,7 @@ static __device__ __noinline__ Request load_request(const Kv8FwdParams& p, int b
 }
 
 template <int C>
-constexpr int kItemCost = C <= 16 ? 2 : 2;
+constexpr int kItemCost = C <= 16 ? 1 : 4;
 
 // The items of a request for one key/value head: `blocks` blocks of C rows in `pairs`
 // pairs of `cost` units each.
