@@ -1117,6 +1117,10 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     p.group_inv = static_cast<uint32_t>(((1ull << 32) + g.seq.group - 1) / g.seq.group);
     if (static_cast<long long>(g.tokens) * g.seq.group > INT_MAX - 128)
         return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: problem too large for one launch");
+    // (the narrow kernels count key tiles of all items in 32 bits)
+    if (static_cast<long long>(B) * Hkv * ((static_cast<long long>(width) * page + 127) / 128 + 1) > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: B * Hkv * width * page = %lld is too large for one launch",
+                    static_cast<long long>(B) * Hkv * width * page);
     p.columns = kv8_columns(N, g.seq.group);
     p.ctas = 2 * sm_count();
     const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);

@@ -385,23 +385,22 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             if (ok) {
                 uint8_t* dst = sQ + buf * K::kQBytes;
                 const int G = p.seq.group, rows = part.req.n * G;
-                const int tok0 = part.row0 / G, rem0 = part.row0 - tok0 * G;
                 constexpr int kPasses = C / kRows;
                 uint4 w[kPasses];
 #pragma unroll
                 for (int i = 0; i < kPasses; ++i) {
                     const int n = t / kLanes + i * kRows;
-                    const int more = small_div(rem0 + n, G, p.group_inv);
-                    const long long token = part.req.start + tok0 + more;
-                    const int head = part.h * G + rem0 + n - more * G;
+                    const int tok = small_div(n, G, p.group_inv);   // (a request's rows are one item)
+                    const long long token = part.req.start + tok;
+                    const int head = part.h * G + n - tok * G;
                     w[i] = make_uint4(0, 0, 0, 0);
-                    if (part.row0 + n < rows)
+                    if (n < rows)
                         w[i] = __ldg(reinterpret_cast<const uint4*>(
                             static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
                     if (sub == 0) {
-                        sm.row_pos[buf][n] = part.row0 + n < rows ? part.req.len - part.req.n + tok0 + more : INT_MIN;
+                        sm.row_pos[buf][n] = n < rows ? part.req.len - part.req.n + tok : INT_MIN;
                         sm.out_at[buf][n] = (token * p.seq.Hq + head) * D;
-                        sm.lse_at[buf][n] = row_stat_index(p.seq, part.b, head, part.req.start, tok0 + more);
+                        sm.lse_at[buf][n] = row_stat_index(p.seq, part.b, head, part.req.start, tok);
                     }
                 }
 #pragma unroll

@@ -8,6 +8,7 @@
 #include "fa_seq.cuh"
 
 #include <climits>
+#include <type_traits>
 
 namespace fa {
 
@@ -48,7 +49,7 @@ struct Request {
     int len;        // tokens in the cache, the new ones among them
 };
 
-static __device__ __noinline__ Request load_request(const Kv8FwdParams& p, int b) {
+__device__ __forceinline__ Request load_request(const Kv8FwdParams& p, int b) {
     Request r;
     seq_bounds(p.seq, b, r.start, r.n);
     const long long room = static_cast<long long>(p.width) << p.page_log2;
@@ -65,10 +66,17 @@ struct Items {
     int blocks, pairs, cost;
 };
 
+// A request's rows are one block where items are narrow (kv8_columns chose them so), and its
+// units fit 32 bits (fa_fwd_kv8 sees to it).
+template <int C>
+constexpr bool kOneBlock = C <= 16;
+template <int C>
+using Units = std::conditional_t<kOneBlock<C>, int, long long>;
+
 // (Out of line, like the division: the kernels' many roles make much code, and what does not
 // fit the SM's instruction cache has to be fetched again and again.)
 template <int C>
-static __device__ __noinline__ Items items_of(const Kv8FwdParams& p, int n, int len) {
+static __device__ __noinline__ Items items_of_blocks(const Kv8FwdParams& p, int n, int len) {
     Items it;
     const int G = p.seq.group;
     it.blocks = (n * G + C - 1) / C;
@@ -93,8 +101,28 @@ static __device__ __noinline__ Items items_of(const Kv8FwdParams& p, int n, int 
     return it;
 }
 
+template <int C>
+__device__ __forceinline__ Items items_of(const Kv8FwdParams& p, int n, int len) {
+    if constexpr (!kOneBlock<C>) {
+        return items_of_blocks<C>(p, n, len);
+    } else {
+        Items it;
+        it.blocks = it.pairs = n > 0 ? 1 : 0;
+        int tiles = (len + kKeys - 1) / kKeys;
+        if (p.seq.window > 0) {
+            const long long span = static_cast<long long>(p.seq.window) + p.seq.N;
+            tiles = static_cast<int>(min(static_cast<long long>(tiles), (span + kKeys - 2) / kKeys + 1));
+        }
+        it.cost = tiles + kItemCost<C>;
+        return it;
+    }
+}
+
 static __device__ __noinline__ long long divide_long(long long a, long long b) { return a / b; }
 
+__device__ __forceinline__ int divide(int a, int b) {
+    return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
 // 64-bit division that mostly is a 32-bit one.
 __device__ __forceinline__ long long divide(long long a, long long b) {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
@@ -103,12 +131,14 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 
 // CTA c of the first G takes units [c total / G, (c + 1) total / G) of `total`; G is the
 // number of CTAs, or of units where there are fewer, so that no share among them is empty.
-__device__ __forceinline__ int sharers(long long total, int ctas) {
-    return static_cast<int>(min(total, static_cast<long long>(ctas)));
+template <class U>
+__device__ __forceinline__ int sharers(U total, int ctas) {
+    return static_cast<int>(min(total, static_cast<U>(ctas)));
 }
-__device__ __forceinline__ long long share_begin(long long total, int c, int G) {
-    const long long q = divide(total, G);
-    return q * c + divide((total - q * G) * c, G);
+template <class U>
+__device__ __forceinline__ U share_begin(U total, int c, int G) {   // (G < 2^10)
+    const U q = static_cast<U>(divide(total, static_cast<U>(G)));
+    return q * c + static_cast<U>(static_cast<uint32_t>((total - q * G) * c) / static_cast<uint32_t>(G));
 }
 __device__ __forceinline__ int share_of(long long total, long long unit, int G) {
     return static_cast<int>(divide((unit + 1) * G - 1, total));
@@ -162,10 +192,15 @@ struct Walk {
     }
     // The keys that the rows of block `blk` see.
     __device__ __forceinline__ void see(int blk, Part& part) const {
-        const int G = p.seq.group;
         part.row0 = blk * C;
-        const int first = req.len - req.n + part.row0 / G;   // positions of its first and last token
-        const int last = req.len - req.n + min((part.row0 + C - 1) / G, req.n - 1);
+        int first = req.len - req.n, last = first;   // positions of its first and last token
+        if constexpr (kOneBlock<C>) {
+            last += min(req.n, C) - 1;
+        } else {
+            const int G = p.seq.group;
+            first += part.row0 / G;
+            last += min((part.row0 + C - 1) / G, req.n - 1);
+        }
         const bool win = p.seq.window > 0;
         part.hi_key = p.seq.causal ? last : req.len - 1;
         part.all_hi = p.seq.causal ? first : req.len - 1;
@@ -173,6 +208,8 @@ struct Walk {
         part.all_lo = win ? max(last - p.seq.window + 1, 0) : 0;
         part.tile0 = part.lo_key / kKeys;
         part.item_tiles = part.hi_key >= part.lo_key ? part.hi_key / kKeys - part.tile0 + 1 : 0;
+        // (more new tokens than the call announced: no more keys than there are units for)
+        if (kOneBlock<C>) part.item_tiles = min(part.item_tiles, it.cost - kItemCost<C>);
     }
     __device__ __forceinline__ bool next(Part& part) {
 #pragma unroll 1
@@ -192,7 +229,7 @@ struct Walk {
             }
             int before = 0;   // units of the pair before this item's
             see(pair, part);
-            if (off >= part.item_tiles + kItemCost<C> && it.blocks - 1 - pair != pair) {
+            if (!kOneBlock<C> && off >= part.item_tiles + kItemCost<C> && it.blocks - 1 - pair != pair) {
                 before = part.item_tiles + kItemCost<C>;
                 see(it.blocks - 1 - pair, part);
             }
@@ -301,20 +338,22 @@ __device__ __forceinline__ int small_div(int a, int b, uint32_t inv) {
 }
 
 // Inclusive sums over the block of one value per thread, and the block's total.
-__device__ __forceinline__ long long block_units(long long v, long long* warp_sums, long long* total) {
+template <class U>
+__device__ __forceinline__ U block_units(U v, long long* warp_sums, U* total) {
+    U* sums = reinterpret_cast<U*>(warp_sums);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        const U u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
     __syncthreads();
-    if (lane == 31) warp_sums[warp] = v;
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
-    long long before = 0, all = 0;
+    U before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        const long long x = warp_sums[w];
+        const U x = sums[w];
         if (w < warp) before += x;
         all += x;
     }
@@ -326,31 +365,32 @@ __device__ __forceinline__ long long block_units(long long v, long long* warp_su
 template <int C, class Smem>
 __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Smem& sm) {
     const int cta = blockIdx.x, B = p.seq.B;
-    long long begin = 0, before = 0, total = 0;
+    using U = Units<C>;
+    U begin = 0, before = 0, total = 0;
     Request r{0, 0, 0};
-    auto units = [&](int b) -> long long {
+    auto units = [&](int b) -> U {
         if (b >= B) return 0;
         r = load_request(p, b);
         const Items it = items_of<C>(p, r.n, r.len);
-        return static_cast<long long>(it.pairs) * p.seq.Hkv * it.cost;
+        return static_cast<U>(it.pairs) * p.seq.Hkv * it.cost;
     };
     // request b's units end at `end`, `mine` of them: does the share begin there?
-    auto look = [&](int b, long long mine, long long end) {
+    auto look = [&](int b, U mine, U end) {
         if (begin >= end - mine && begin < end) {
             const Items it = items_of<C>(p, r.n, r.len);
-            const long long at = begin - (end - mine), item = divide(at, it.cost);
-            const int h = static_cast<int>(divide(item, it.pairs));
+            const U at = begin - (end - mine), item = static_cast<U>(divide(at, static_cast<U>(it.cost)));
+            const int h = kOneBlock<C> ? static_cast<int>(item) : static_cast<int>(divide(item, static_cast<U>(it.pairs)));
             sm.share.b0 = b;
             sm.share.off = static_cast<int>(at - item * it.cost);
             sm.share.h = h;
-            sm.share.pair = static_cast<int>(item - static_cast<long long>(h) * it.pairs);
+            sm.share.pair = static_cast<int>(item - static_cast<U>(h) * it.pairs);
         }
     };
-    const long long first = units(threadIdx.x);
-    long long sum = first;
+    const U first = units(threadIdx.x);
+    U sum = first;
 #pragma unroll 1
     for (int b = threadIdx.x + kThreads; b < B; b += kThreads) sum += units(b);
-    const long long upto = block_units(sum, sm.warp_sums, &total);
+    const U upto = block_units(sum, sm.warp_sums, &total);
     const int G = sharers(total, gridDim.x);
     begin = cta < G ? share_begin(total, cta, G) : total;
     if (threadIdx.x == 0) {
@@ -367,9 +407,9 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Smem& sm) {
 #pragma unroll 1
         for (int b0 = 0; b0 < B; b0 += kThreads) {
             const int b = b0 + threadIdx.x;
-            const long long mine = units(b);
-            long long all;
-            const long long end = before + block_units(mine, sm.warp_sums, &all);
+            const U mine = units(b);
+            U all;
+            const U end = before + block_units(mine, sm.warp_sums, &all);
             look(b, mine, end);
             before += all;
         }
