@@ -446,12 +446,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty));
             }
+            // a warp without rows leaves its part of P as it is (rows of O that nobody reads)
+            const bool idle = part.row0 + quad * 32 >= part.req.n * G;
             float l = 0.f, ref = kNone;   // the exponents' offset: M - kShift
 #pragma unroll 1
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
                 const int kt = (part.tile0 + i) * kKeys;
-                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.ready_full[sc], T / kScaleSlots));
+                if (ok && !idle) ok = __all_sync(0xffffffffu, wait(&sm.ready_full[sc], T / kScaleSlots));
                 const bool absent = sm.absent[sc] != 0;   // a block on a page that the cache does not have, or behind the last key
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -459,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                     const int kb = kt + kHalf * half;
                     const float4* ready = &sm.ready[sc][4 * half];
                     const bool edge = absent || kb < part.all_lo || kb + kHalf - 1 > part.all_hi;
-                    if (ok && half == 0) ok = __all_sync(0xffffffffu, wait(&sm.s_full, T));
-                    if (ok) {
+                    if (ok && !idle && half == 0) ok = __all_sync(0xffffffffu, wait(&sm.s_full, T));
+                    if (ok && !idle) {
                         tc_fence_after();
                         if (edge) {
                             // hidden keys' products become -inf
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                         tmem_st_wait();
                         tc_fence_before();
                     }
-                    named_bar_signal(kBarP + half, 224, ok);
+                    named_bar_signal(kBarP + half, 224, ok && !idle);
                 }
             }
             // ------------------------------------------------ the part's end
