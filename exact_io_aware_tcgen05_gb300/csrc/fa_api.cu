@@ -1153,7 +1153,7 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     p.num_pages = num_pages;
     p.scale_log2 = scale * kLog2e;
     p.elem = static_cast<int>(dtype);
-    p.timeout_cycles = g_wait_limit.load();
+    p.timeout_cycles = std::min(g_wait_limit.load(), kKv8MaxWaitCycles);
     p.status = status_word_ptr();
     if (!p.status) return fail(FA_ERR_CUDA, "fa_fwd_kv8: cannot resolve the device status word");
     const cudaError_t e = launch_fwd_kv8(p, d, ev, stream);

@@ -156,6 +156,9 @@ struct Kv8Join {
     int pad[2];
 };
 
+// The longest wait limit that the kernel of fa_fwd_kv8 is given (about three seconds).
+constexpr long long kKv8MaxWaitCycles = 6000000000LL;
+
 struct Kv8FwdParams {
     CUtensorMap tm_k, tm_v;   // codes as (d, page, num_pages * Hkv); the box is a page of one head
     SeqInfo seq;        // the new tokens (queries); N: the most of a request

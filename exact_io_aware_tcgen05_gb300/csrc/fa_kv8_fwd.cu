@@ -101,7 +101,7 @@ struct Kv8Smem {   // behind the tiles
     uint64_t all_done;
     uint32_t tmem;
     int abort;
-    int poison;                      // NaN found among values that only some rows see
+    int poison[2];                   // [part parity] NaN found among values that only some rows see
 };
 
 template <int D, int E, int C>
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         sm.abort = 0;
-        sm.poison = 0;
+        sm.poison[0] = sm.poison[1] = 0;
 #pragma unroll 1
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_addr(&sm.kv_full[i]), 1);
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                                     w.z &= ~(e | (e - (e >> 7)));
                                     w.w &= ~(f | (f - (f >> 7)));
                                     vrow[u] = w;
-                                    sm.poison = 1;
+                                    sm.poison[buf] = 1;
                                 }
                             }
                         }
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             constexpr int kSame = 32 / C;   // lanes that hold the same column's sum
             if (lane % kSame == 0) sm.part_sum[buf][quad][lane / kSame] = l[0];
             named_bar_sync(kBarMax, 128);
-            const bool poison = sm.poison != 0;
+            const bool poison = sm.poison[buf] != 0;
             if (ok) {
                 // lane n: column n's sum, and what its accumulators are multiplied by
                 const long long slot = 2LL * blockIdx.x + (part.begins ? 1 : 0);
@@ -664,10 +664,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 }
             }
             tc_fence_before();
-            if (poison) {   // (uniform) taken back once all have read it, before any sets it again
+            if (poison) {   // (uniform) taken back once all have read it; not set again before part np + 2
                 named_bar_sync(kBarMax, 128);
-                if (key == 0) sm.poison = 0;
-                named_bar_sync(kBarMax, 128);
+                if (key == 0) sm.poison[buf] = 0;
             }
             __syncwarp();
             if (lane == 0) {

@@ -327,8 +327,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             ++nq;
             // Values: a unit of 16 codes becomes two of 8 fp16 numbers.  A key's D / 16 units
             // are D / 16 threads', so that a warp reads whole rows.
+            // (the threads of the upper 64 channels have the neighbouring row: 8 lanes' stores
+            // then fall into different banks)
             constexpr int kPer = D / 16;
-            const int vu = t % kPer;
+            const int vu = t % kPer, row0 = t / kPer ^ vu / 4;
 #pragma unroll 1
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                             // zero too, and its channel becomes NaN at the part's end for the rows
                             // that see it.
 #pragma unroll 1
-                            for (int key = t / kPer; key < kHalf; key += 64 / kPer) {
+                            for (int key = row0; key < kHalf; key += 64 / kPer) {
                                 uint4* at = reinterpret_cast<uint4*>(src + unit_offset<D>(key, vu));
                                 const int pos = kt + half * kHalf + key;
                                 const bool hidden = sm.scales[sc][8 + half * 4 + key / 16] < 0.f ||
@@ -393,10 +395,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                         uint4 w[kPer];
 #pragma unroll
                         for (int j = 0; j < kPer; ++j)
-                            w[j] = *reinterpret_cast<const uint4*>(src + unit_offset<D>(t / kPer + j * (64 / kPer), vu));
+                            w[j] = *reinterpret_cast<const uint4*>(src + unit_offset<D>(row0 + j * (64 / kPer), vu));
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) {
-                            const int key = t / kPer + j * (64 / kPer);
+                            const int key = row0 + j * (64 / kPer);
                             uint4 x, y;
                             widen4(w[j].x, x.x, x.y);
                             widen4(w[j].y, x.z, x.w);

@@ -457,9 +457,14 @@ __device__ __forceinline__ bool wait_for(const Kv8FwdParams& p, Smem& sm, uint64
         return mbar_wait(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
 }
 
-// mbar_wait_drain, out of line.
+// A wait that ignores the abort flag, out of line: for what still comes after an abort.  It
+// comes at the latest when every other wait has given up, so this one waits for longer than
+// any of those may.  (A limit out of the parameters costs 3 to 5 % of the 128-row kernel's
+// time, by the registers that the call then takes: hence a constant, above a bound that the
+// host keeps.)
+constexpr long long kKv8DrainCycles = 2 * kKv8MaxWaitCycles + 2 * kDrainCycles;
 static __device__ __noinline__ void drain_on(uint32_t bar, uint32_t parity) {
-    mbar_wait_drain(bar, parity, kDrainCycles);
+    mbar_wait_drain(bar, parity, kKv8DrainCycles);
 }
 
 // Part number np, in registers; false behind the last.  After an abort too every role goes
@@ -488,7 +493,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
     const int box = min(page, U), boxes = U / box;   // keys of a copy, copies of a unit
     const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
     const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
-    int c = 0, items = 0;                      // tiles, units of the ring
+    int c = 0, items = 0, scales = 0;          // tiles, units of the ring, tiles whose scales are on the way
     bool ok = true, joined = false;
     Part part;
     Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
@@ -570,6 +575,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
                     }
                     if (plain) mbar_arrive(sbar);
                     else cp_async_arrive(sbar);
+                    scales = c + 1;
                 }
             }
         }
@@ -580,7 +586,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
     for (int i = max(0, items - kSlots); i < items; ++i)
         drain_on(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1);
 #pragma unroll 1
-    for (int i = max(0, c - kScaleSlots); i < c; ++i)
+    for (int i = max(0, scales - kScaleSlots); i < scales; ++i)
         drain_on(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1);
 }
 
