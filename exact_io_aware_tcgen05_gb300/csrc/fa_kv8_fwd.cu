@@ -2,8 +2,8 @@
 // include/fa.h) on sm_103a.
 //
 // A request's rows are its (new token, head of the group) pairs: they share a key/value
-// head and take one pass over its keys together, C = 8, 16 or 32 rows to an item.  With so
-// few rows the cache's bytes bound the pass (16 operations a byte at 8 rows and d = 128, too
+// head and take one pass over its keys together, up to C = 8 or 16 rows.  (Requests with more
+// rows go to the kernel of fa_kv8_rows.cu; this file launches both.)  With so few rows the cache's bytes bound the pass (16 operations a byte at 8 rows and d = 128, too
 // many for the CUDA cores, few for the tensor cores), so nothing is done to a code but to
 // load it: TMA copies pages into shared memory and tcgen05 (kind::f8f6f4) multiplies them
 // as they are.  The products are transposed, keys and channels on the 128 rows of an MMA
@@ -61,27 +61,21 @@ struct Kv8Cfg {
     static constexpr int kP = E == kElemBf16 ? 3 : 4;    // pieces of P
     // With few columns an MMA costs the reading of its 128 rows, so the pieces of q and of P
     // go side by side into one MMA of more columns (a multiple of 16, the rest zeros) and
-    // are added up when read.  (256 TMEM columns a CTA: where they do not hold P's pieces,
-    // the tensor cores add them up, an MMA each.)
+    // are added up when read.
     static constexpr int kSCols = (kQ * C + 15) / 16 * 16;
     static constexpr int kPCols = (kP * C + 15) / 16 * 16;
-    static constexpr bool kWideO = 2 * kSCols + kPCols <= 256;
-    static constexpr int kOCols = kWideO ? kPCols : C;
-    static constexpr int kTmemUsed = 2 * kSCols + kOCols;
+    static constexpr int kTmemUsed = 2 * kSCols + kPCols;
     static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : 256;
     static_assert(kTmemUsed <= 256, "TMEM columns, two CTAs per SM");
     static constexpr int kSlotBytes = kKeys * D;         // K or V of a tile
     static constexpr int kQBytes = kSCols * D;           // one item's queries
     static constexpr int kPBytes = kPCols * kKeys;       // a tile's weights
-    // two tiles' weights, unless they leave the ring fewer than 4 slots
-    static constexpr int kPBufs = D == 64 || kQBytes + kPBytes <= 20480 ? 2 : 1;
     static constexpr int kSwizzle = D == 128 ? 2 : 4;    // descriptor code of the D-byte swizzle
     static constexpr int kGroup = 8 * D;                 // bytes of 8 rows
 };
 
 template <int C>
 struct Kv8Smem {   // behind the tiles
-    static constexpr bool kOutOfLine = true;
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
     alignas(16) float q_scale[2][C];
     int row_pos[2][C];               // position of the row's token; INT_MIN: no row
@@ -107,7 +101,7 @@ struct Kv8Smem {   // behind the tiles
 template <int D, int E, int C>
 constexpr int kv8_slots() {
     using K = Kv8Cfg<D, E, C>;
-    const int left = kCtaSmem - 1024 - 2 * K::kQBytes - K::kPBufs * K::kPBytes - static_cast<int>(sizeof(Kv8Smem<C>));
+    const int left = kCtaSmem - 1024 - 2 * (K::kQBytes + K::kPBytes) - static_cast<int>(sizeof(Kv8Smem<C>));
     const int n = left / K::kSlotBytes;
     return n < kMaxSlots ? n : kMaxSlots;
 }
@@ -115,7 +109,7 @@ constexpr int kv8_slots() {
 template <int D, int E, int C>
 constexpr int kv8_smem_bytes() {
     using K = Kv8Cfg<D, E, C>;
-    return 1024 + kv8_slots<D, E, C>() * K::kSlotBytes + 2 * K::kQBytes + K::kPBufs * K::kPBytes +
+    return 1024 + kv8_slots<D, E, C>() * K::kSlotBytes + 2 * (K::kQBytes + K::kPBytes) +
            static_cast<int>(sizeof(Kv8Smem<C>));
 }
 
@@ -231,15 +225,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     // S^T: K e4m3 (K-major) times q's pieces e4m3 (K-major); O^T: V e4m3 (MN-major) times P's
     // pieces e5m2 (MN-major; operand format code 1)
     constexpr uint32_t kIdescS = idesc_f32acc(kKeys, K::kSCols, false, false, kElemFp8);
-    constexpr uint32_t kIdescO = idesc_f32acc(128, K::kOCols, true, true, kElemFp8) | (1u << 10);
+    constexpr uint32_t kIdescO = idesc_f32acc(128, K::kPCols, true, true, kElemFp8) | (1u << 10);
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sKV = smem;                                  // [slots]
     uint8_t* sQ = smem + kSlots * K::kSlotBytes;          // [2][pieces and rows][D]
-    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [kPBufs][blocks of 16 columns][keys][16]
-    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + K::kPBufs * K::kPBytes);
+    uint8_t* sP = sQ + 2 * K::kQBytes;                    // [2][blocks of 16 columns][keys][16]
+    Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + 2 * K::kPBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     grid_launch_dependents();
 
@@ -348,14 +342,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                     const int st = (2 * T + 1) % kSlots;
                     tc_fence_after();
                     const uint64_t vd = v0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
-                    const uint64_t pd = pd0 + static_cast<uint64_t>((T % K::kPBufs * K::kPBytes) >> 4);
+                    const uint64_t pd = pd0 + static_cast<uint64_t>(((T & 1) * K::kPBytes) >> 4);
 #pragma unroll
-                    for (int q = 0; q < (K::kWideO ? 1 : K::kP); ++q)
-#pragma unroll
-                        for (int kk = 0; kk < kKeys / 32; ++kk)
-                            mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4),
-                                      pd + ((q * C * kKeys) >> 4) + ((kk * 512) >> 4), kIdescO,
-                                      (!fresh || q > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < kKeys / 32; ++kk)
+                        mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4), pd + ((kk * 512) >> 4), kIdescO,
+                                  (!fresh || kk > 0) ? 1u : 0u);
                     mma_commit(smem_addr(&sm.pv_done));
                     mma_commit(smem_addr(&sm.kv_empty[st]));
                 }
@@ -412,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(smem_addr(&sm.q_full[buf]));
+            // (after an abort the rows' places are not written: nobody may take them for these)
+            if (ok) mbar_arrive(smem_addr(&sm.q_full[buf]));
         }
     } else if (warp == 3) {
         // ---------------------------------------------------------------- relay
@@ -551,10 +543,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                                 for (int j = 0; j < 4; ++j) w[n4 + j] = 0.f;
                             }
                         fits = attempt > 0 || top <= kShift + kGrow;
-                        // Two buffers: tile T - 2's product was complete before this tile's
-                        // S^T was.  One: the last tile's has to be.
-                        if (K::kPBufs == 1 && T > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
-                        store_weights<K::kP, C>(sP + T % K::kPBufs * K::kPBytes + key * 16, w);
+                        // (tile T - 2's product was complete before this tile's S^T was)
+                        store_weights<K::kP, C>(sP + (T & 1) * K::kPBytes + key * 16, w);
                         tc_fence_before();
                         fence_proxy_async_smem();
                     }
@@ -595,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll
                             for (int n = 0; n < C; ++n) l[n] *= sm.fac[quad][n];
 #pragma unroll 1
-                            for (int cc = 0; cc < K::kOCols; cc += 16) {
+                            for (int cc = 0; cc < K::kPCols; cc += 16) {
                                 uint32_t r[16];
                                 tmem_ld16(tO + cc, r);
                                 tmem_ld_wait();
@@ -644,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                     float o[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] = 0.f;
-                    if (part.tiles > 0) load_sum8<K::kWideO ? K::kP : 1>(tO + n0, C, o);
+                    if (part.tiles > 0) load_sum8<K::kP>(tO + n0, C, o);
                     uint32_t spoilt = 0;   // columns of these 8 that see a NaN in this channel
                     if (poison && key < D) spoilt = find_nan<D, C>(p, part, sm, buf, n0, key);
 #pragma unroll

@@ -57,7 +57,6 @@ struct RowsCfg {
 };
 
 struct RowsSmem {   // behind the tiles
-    static constexpr bool kOutOfLine = true;
     float scales[kScaleSlots][16];   // of a tile: K's 8 blocks, V's 8 (V < 0: hidden)
     // the same, ready for the exponents: K's scale, log2 of V's, 1 / V's (-1: hidden)
     float4 ready[kScaleSlots][8];

@@ -424,8 +424,9 @@ __device__ __forceinline__ void find_share(const Kv8FwdParams& p, Smem& sm) {
 }
 
 // The part of a wait that is not over at once, out of line: the kernels' roles wait in many
-// places.  The hardware suspends the thread for up to 20 us at a time, so that waiting warps
-// take no issue slots from the others; gives up as mbar_wait does.
+// places.  The hardware suspends the thread for up to 0.5 us at a time, so that waiting warps
+// take no issue slots from the others; gives up as mbar_wait does.  (More registers here, for a
+// time worked out from the limit, cost the 128-row kernel 1 to 5 % in its callers.)
 static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, long long limit,
                                             int* status) {
     const long long t0 = clock64();
@@ -436,7 +437,7 @@ static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volat
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(20000u)
+            : "r"(bar), "r"(parity), "r"(500u)
             : "memory");
         if (done) return true;
         if (*abort) return false;
@@ -450,11 +451,8 @@ static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volat
 
 template <class Smem>
 __device__ __forceinline__ bool wait_for(const Kv8FwdParams& p, Smem& sm, uint64_t* bar, int phase) {
-    if constexpr (Smem::kOutOfLine)
-        return mbar_try_wait(smem_addr(bar), phase & 1) ||
-               wait_on(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
-    else   // (a kernel that moves registers between its warps cannot call functions there)
-        return mbar_wait(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
+    return mbar_try_wait(smem_addr(bar), phase & 1) ||
+           wait_on(smem_addr(bar), phase & 1, &sm.abort, p.timeout_cycles, p.status);
 }
 
 // A wait that ignores the abort flag, out of line: for what still comes after an abort.  It

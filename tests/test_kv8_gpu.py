@@ -530,3 +530,23 @@ def test_attention_over_a_cache_against_the_16_bit_forward(fa):
     # each rounds its probabilities (half a step of bf16 at most) and its output (likewise)
     far = (o.float() - o2.reshape(B * N, Hq, d).float()).abs()
     assert far.max() <= 4 * 2.0 ** -8 * v.float().abs().max()
+
+
+@pytest.mark.parametrize("n,d", [(1, 128), (1, 64), (40, 128), (40, 64)])
+def test_wait_budget_expiry_reports_timeout_then_recovers(fa, n, d):
+    """Waits that give up end the kernels, whatever the other warps were at."""
+    rng = np.random.default_rng(15)
+    lens = [3000, 700, 90, 200] * 6
+    c = make(rng, len(lens), lens, [min(n, x) for x in lens], 8, 2, d, 64, "bf16")
+    want = fa_out(fa, c)
+    fa.fa_device_status()
+    fa.fa_set_wait_limit_cycles(1)
+    try:
+        fa_out(fa, c)
+        assert fa.fa_device_status(check=False) == fa.FA_ERR_TIMEOUT
+    finally:
+        fa.fa_set_wait_limit_cycles(0)
+    assert fa.fa_device_status(check=False) == fa.FA_OK
+    got = fa_out(fa, c)
+    fa.fa_device_status()
+    assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
