@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 if (lane == 0) {
                     if (T > 0) wait(&sm.kv_full[(2 * T - 1) % kSlots], (2 * T - 1) / kSlots);
                     wait(&sm.kv_full[(2 * T) % kSlots], (2 * T) / kSlots);
+                    wait(&sm.scales_full[T % kScaleSlots], T / kScaleSlots);
                     if (i == 0) wait(&sm.q_full[np & 1], np >> 1);
                 }
                 __syncwarp();
@@ -447,9 +448,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll 1
             for (int i = 0; i < part.tiles; ++i, ++T) {
                 const int sc = T % kScaleSlots;
-                if (ok)
-                    ok = __all_sync(0xffffffffu, wait(&sm.scales_full[sc], T / kScaleSlots) &&
-                                                     wait(&sm.s_full[T & 1], T >> 1));
+                // (the relay waited for the scales before it let S^T be issued)
+                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.s_full[T & 1], T >> 1));
                 float v[C], kc = 0.f, lvs = 0.f, inv_vs = 0.f;
                 uint32_t seen = ~0u;   // a bit per column
                 const float4* qs = reinterpret_cast<const float4*>(sm.q_scale[buf]);
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                         tc_fence_before();
                         fence_proxy_async_smem();
                     }
-                    if (named_bar_all(kBarP, 160, !ok || fits)) break;
+                    if ((i > 0 || attempt > 0) && named_bar_all(kBarP, 160, !ok || fits)) break;
                     // the maxima over the tile's keys
                     float mine = kNegInf;
                     if (ok) {

@@ -479,6 +479,13 @@ __device__ __forceinline__ bool take_part(Smem& sm, int np, Part& part) {
 // TMA, rows of d bytes swizzled over d bytes), and with the first of them the tile's 16
 // scales (K's, then V's; -1 for V's where a block's tokens are hidden: behind the last key
 // that is seen, or on a page that the cache does not have).
+//
+// One warp's instructions for a tile take about as long as a narrow tile does, so what its
+// copies have in common is worked out once and the table is read while the part is handed
+// over.  (A lane has a copy; the lanes' copies are issued one by one, some 80 cycles each, 16 a
+// tile with pages of 16 tokens.  A second producer warp, for V, made that case slower, 42.7 ->
+// 50.3 us for 128 requests of up to 2048 tokens at d = 64: the kernel's roles share the
+// instruction cache, and more code in flight costs more than the wait.)
 template <int D, int C, int U, int kSlots, class Smem>
 __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t* sKV) {
     constexpr int kUnits = kKeys / U;          // of a side
@@ -488,20 +495,31 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
         tma_prefetch_desc(&p.tm_v);
     }
     const int page = 1 << p.page_log2, per_tile = kKeys >> p.page_log2;
-    const int box = min(page, U), boxes = U / box;   // keys of a copy, copies of a unit
+    const int box_log2 = min(p.page_log2, U == 128 ? 7 : 6);
+    const int key = lane << box_log2;          // this lane's copy: keys from here on (none from 128 on)
+    const int unit_boxes = U >> box_log2;
     const int blocks_log2 = p.page_log2 - 4;   // scale blocks of a page
     const int side_blk = lane & 7;             // lanes 0..7: K's scales, 8..15: V's
-    int c = 0, items = 0, scales = 0;          // tiles, units of the ring, tiles whose scales are on the way
+    int c = 0;                                 // tiles
+    int slot = 0, use = 0;                     // the next unit's slot, how often it was used
     bool ok = true, joined = false;
     Part part;
     Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
 #pragma unroll 1
     for (int np = 0;; ++np) {
+        const bool more = walk.next(part);
+        if (!more) part.tiles = -1;
+        const int* row = p.table + static_cast<long long>(part.b) * p.width;
+        const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
+        const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
+        // the table's entries, 32 at a time, the next ones on their way
+        int base = part.tile0 * per_tile;
+        auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
+        int cur = part.tiles > 0 ? entry(base + lane) : -1;
+        int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
         if (np >= kParts)
             drain_on(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1);
-        const bool more = walk.next(part);
         if (lane == 0) {
-            if (!more) part.tiles = -1;
             sm.parts[np % kParts] = part;
             mbar_arrive(smem_addr(&sm.part_full[np % kParts]));
             if (more && part.begins && !part.whole) {
@@ -519,14 +537,6 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
         }
         __syncwarp();
         if (!more) break;
-        const int* row = p.table + static_cast<long long>(part.b) * p.width;
-        const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
-        const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
-        // the table's entries, 32 at a time, the next ones on their way
-        int base = part.tile0 * per_tile;
-        auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
-        int cur = part.tiles > 0 ? entry(base + lane) : -1;
-        int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
 #pragma unroll 1
         for (int i = 0; i < part.tiles && ok; ++i, ++c) {
             const int tile = part.tile0 + i;
@@ -536,27 +546,32 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
                 nxt = entry(base + 32 + lane);
             }
             const int first = tile * per_tile - base;
-            // the scales of the tile's 8 blocks (their slot's last tile is long done)
+            const int id = __shfl_sync(0xffffffffu, cur, (first + (key >> p.page_log2)) & 31);
+            const bool load = key < kKeys && id >= 0 && id < p.num_pages && tile * kKeys + key < lim;
+            const uint32_t loads = __ballot_sync(0xffffffffu, load);
+            const int page_row = id * p.seq.Hkv + part.h;
             const int sid = __shfl_sync(0xffffffffu, cur, (first + (side_blk >> blocks_log2)) & 31);
 #pragma unroll 1
-            for (int unit = 0; unit < 2 * kUnits; ++unit, ++items) {
-                // this lane's copy: keys from `key` of the tile on
-                const int key = (unit % kUnits) * U + (lane & (boxes - 1)) * box;
-                const int id = __shfl_sync(0xffffffffu, cur, (first + (key >> p.page_log2)) & 31);
-                const bool load = lane < boxes && id >= 0 && id < p.num_pages && tile * kKeys + key < lim;
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * D;
-                const int st = items % kSlots, use = items / kSlots;
+            for (int unit = 0; unit < 2 * kUnits; ++unit) {
                 if (use > 0) {
-                    ok = __all_sync(0xffffffffu, wait_for(p, sm, &sm.kv_empty[st], use - 1));
+                    ok = __all_sync(0xffffffffu, wait_for(p, sm, &sm.kv_empty[slot], use - 1));
                     if (!ok) break;
                 }
-                const uint32_t full = smem_addr(&sm.kv_full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                const uint32_t full = smem_addr(&sm.kv_full[slot]);
+                if (lane == 0) {
+                    const uint32_t n = __popc(loads >> (unit % kUnits * unit_boxes) & ((1u << unit_boxes) - 1u));
+                    mbar_arrive_expect_tx(full, (n << box_log2) * D);
+                }
                 __syncwarp();
-                if (load)
-                    tma_load_3d(smem_addr(sKV + st * U * D + lane * box * D), unit < kUnits ? &p.tm_k : &p.tm_v,
-                                full, 0, key & (page - 1), id * p.seq.Hkv + part.h);
+                if (load && (kUnits == 1 || key / U == unit % kUnits))
+                    tma_load_3d(smem_addr(sKV + (slot * U + key % U) * D), unit < kUnits ? &p.tm_k : &p.tm_v, full,
+                                0, key & (page - 1), page_row);
+                if (++slot == kSlots) {
+                    slot = 0;
+                    ++use;
+                }
                 if (unit == 0) {
+                    // the scales (their slot's last tile is long done)
                     const uint32_t sbar = smem_addr(&sm.scales_full[c % kScaleSlots]);
                     bool plain = true;
                     if (lane < 16) {
@@ -573,7 +588,6 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
                     }
                     if (plain) mbar_arrive(sbar);
                     else cp_async_arrive(sbar);
-                    scales = c + 1;
                 }
             }
         }
@@ -581,10 +595,14 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
     if (lane == 0 && !joined) p.joins[blockIdx.x].last = 0;
     // every copy lands before the CTA exits, whatever became of the other roles
 #pragma unroll 1
-    for (int i = max(0, items - kSlots); i < items; ++i)
-        drain_on(smem_addr(&sm.kv_full[i % kSlots]), (i / kSlots) & 1);
+    for (int i = 0; i < kSlots; ++i) {
+        const int last = i < slot ? use : use - 1;
+        if (last >= 0) drain_on(smem_addr(&sm.kv_full[i]), last & 1);
+    }
+    // (a tile has its scales from its first unit on)
+    const int tiles = (use * kSlots + slot + 2 * kUnits - 1) / (2 * kUnits);
 #pragma unroll 1
-    for (int i = max(0, scales - kScaleSlots); i < scales; ++i)
+    for (int i = max(0, tiles - kScaleSlots); i < tiles; ++i)
         drain_on(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1);
 }
 
