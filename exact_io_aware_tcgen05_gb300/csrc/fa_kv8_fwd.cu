@@ -671,9 +671,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     if (warp == 1) tmem_dealloc(tmem, K::kTmemCols);
 }
 
-// Joins the parts of the item that begins at the end of CTA c's share, c = blockIdx.x: a
-// warp per row.  Its lanes take 32 parts' references and sums at a time, then the warp adds
-// those parts' accumulators up in their order.
+// Joins the parts of the item that begins at the end of CTA c's share, c = blockIdx.x: a warp
+// per row, 8 rows a block (16 rows a warp, one behind the other, took 36 us behind a chunk of
+// 2048 tokens: a row's loads wait for one another, so rows have to be on their way together).
+// Its lanes take 32 parts' references and sums at a time, then the warp adds those parts'
+// accumulators up in their order; the first two parts' (there are always two) are on their way
+// before their weights are known.
 template <int D, int E>
 __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
     grid_launch_dependents();
@@ -682,46 +685,61 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     const Kv8Join j = p.joins[cta];
     if (j.last <= cta) return;
     const int C = p.columns, G = p.seq.group, lane = threadIdx.x & 31;
+    const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (j.row0 + n >= j.n * G) return;
     constexpr int kPer = D / 32;
     // the parts: this CTA's second slot, the first slots of the ones behind it
     const int parts = j.last - cta + 1;
-    for (int n = threadIdx.x >> 5; n < C && j.row0 + n < j.n * G; n += 8) {
-        auto row_of = [&](int part) { return (2LL * (cta + part) + (part == 0 ? 1 : 0)) * C + n; };
-        float m = kNegInf, sum = 0.f, o[kPer];
+    auto row_of = [&](int part) { return (2LL * (cta + part) + (part == 0 ? 1 : 0)) * C + n; };
+    float early[2][kPer];
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) o[c] = 0.f;
-        for (int p0 = 0; p0 < parts; p0 += 32) {
-            float2 st = make_float2(kNegInf, 0.f);
-            if (p0 + lane < parts) st = p.part_stat[row_of(p0 + lane)];
-            const float top = fmaxf(m, warp_max(st.x)), ref = top == kNegInf ? 0.f : top;
-            const float old = ex2_approx(m - ref), mine = ex2_approx(st.x - ref);
-            float s = mine * st.y;
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            sum = old * sum + s;
+        for (int c = 0; c < kPer; ++c) early[q][c] = p.part_o[row_of(q) * D + lane + 32 * c];
+    float m = kNegInf, sum = 0.f, o[kPer];
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) o[c] *= old;
-            const int here = min(32, parts - p0);
-#pragma unroll 4
-            for (int q = 0; q < here; ++q) {
+    for (int c = 0; c < kPer; ++c) o[c] = 0.f;
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+        float2 st = make_float2(kNegInf, 0.f);
+        if (p0 + lane < parts) st = p.part_stat[row_of(p0 + lane)];
+        const float top = fmaxf(m, warp_max(st.x)), ref = top == kNegInf ? 0.f : top;
+        const float old = ex2_approx(m - ref), mine = ex2_approx(st.x - ref);
+        float s = mine * st.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        sum = old * sum + s;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] *= old;
+        const int here = min(32, parts - p0);
+        int q = 0;
+        if (p0 == 0) {
+#pragma unroll
+            for (; q < 2; ++q) {
                 const float f = __shfl_sync(0xffffffffu, mine, q);
-                const float* x = p.part_o + row_of(p0 + q) * D + lane;
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, x[32 * c], o[c]);
+                for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, early[q][c], o[c]);
             }
-            m = top;
         }
-        const int r = j.row0 + n, tok = r / G, head = j.h * G + r % G;
-        const long long row = j.start + tok;
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll 4
+        for (; q < here; ++q) {
+            const float f = __shfl_sync(0xffffffffu, mine, q);
+            const float* x = p.part_o + row_of(p0 + q) * D + lane;
 #pragma unroll
-        for (int c = 0; c < kPer; ++c)
-            static_cast<uint16_t*>(p.o)[(row * p.seq.Hq + head) * D + lane + 32 * c] =
-                static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
-        if (lane == 0)
-            p.lse[row_stat_index(p.seq, j.b, head, j.start, tok)] =
-                sum != 0.f ? ((m == kNegInf ? 0.f : m) - kShift + log2f(sum)) * kLn2 : kNegInf;
+            for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, x[32 * c], o[c]);
+        }
+        m = top;
     }
+    const int r = j.row0 + n, tok = r / G, head = j.h * G + r % G;
+    const long long row = j.start + tok;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+        static_cast<uint16_t*>(p.o)[(row * p.seq.Hq + head) * D + lane + 32 * c] =
+            static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
+    if (lane == 0)
+        p.lse[row_stat_index(p.seq, j.b, head, j.start, tok)] =
+            sum != 0.f ? ((m == kNegInf ? 0.f : m) - kShift + log2f(sum)) * kLn2 : kNegInf;
 }
 
 template <int D, int E, int C>
@@ -743,7 +761,7 @@ cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream
                               : launch_fwd_kv8_rows(p, D, stream);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, p.ctas, 256, 0, stream, p);
+    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, dim3(p.ctas, p.columns / 8), 256, 0, stream, p);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[2], stream);
     return e;
 }

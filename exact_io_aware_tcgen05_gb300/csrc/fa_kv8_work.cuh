@@ -609,10 +609,10 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
 // A launch that may begin while the kernel before it on the stream is ending (it waits for
 // that one's results itself).
 template <class Params>
-cudaError_t launch_dependent(void (*kern)(Params), int grid, int threads, int smem, cudaStream_t stream,
+cudaError_t launch_dependent(void (*kern)(Params), dim3 grid, int threads, int smem, cudaStream_t stream,
                              const Params& p) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
