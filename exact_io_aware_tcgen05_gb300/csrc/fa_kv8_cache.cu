@@ -212,19 +212,32 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
             const int r = i * kRows + lane / kLanes;
             w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(x + (t + r) * p.stride)) : make_uint4(0, 0, 0, 0);
         }
-        // amax of the finite values, as integers (the order of magnitudes)
-        uint32_t top = 0;
+        // amax of the finite values, as integers (the order of magnitudes): of pairs of 16-bit
+        // ones, or one by one where there is an infinity or NaN to leave out
+        uint32_t pairs = 0;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack2<E>(u[j]);
-                const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu, b = __float_as_uint(f.y) & 0x7fffffffu;
-                top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
-            }
+            for (int j = 0; j < 4; ++j) pairs = __vmaxu2(pairs, u[j] & 0x7fff7fffu);
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        const uint32_t largest = __reduce_max_sync(0xffffffffu, max(pairs & 0xffffu, pairs >> 16));
+        const bool finite = largest < (E == kElemBf16 ? 0x7f80u : 0x7c00u);
+        uint32_t top = __float_as_uint(unpack2<E>(largest).x);
+        if (!finite) {
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack2<E>(u[j]);
+                    const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu, b = __float_as_uint(f.y) & 0x7fffffffu;
+                    top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+                }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+        }
         const int need = scale_exponent(top);
         const int page = slot >> p.page_log2;
         const int in_page = slot & ((1 << p.page_log2) - 1);
@@ -259,9 +272,12 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 g = unpack2<E>(u[j]);
-                // inf * 0 is NaN and 0 elsewhere: infinities become NaN codes
-                f[2 * j] = __fmaf_rn(g.x, inv, g.x * 0.f);
-                f[2 * j + 1] = __fmaf_rn(g.y, inv, g.y * 0.f);
+                f[2 * j] = g.x * inv;
+                f[2 * j + 1] = g.y * inv;
+                if (!finite) {   // inf * 0 is NaN: infinities become NaN codes
+                    f[2 * j] += g.x * 0.f;
+                    f[2 * j + 1] += g.y * 0.f;
+                }
             }
             if (r < n)
                 *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) =
