@@ -943,8 +943,9 @@ fa_status check_table(const char* who, int B, int width, int page) {
         return fail(FA_ERR_INVALID_ARG, "%s: B and width must be >= 1 (got %d, %d)", who, B, width);
     if (B > kKv8MaxRequests)
         return fail(FA_ERR_UNSUPPORTED, "%s: B = %d above %d", who, B, kKv8MaxRequests);
-    if (static_cast<long long>(width) * page > INT_MAX)
-        return fail(FA_ERR_UNSUPPORTED, "%s: table rows of %d pages hold 2^31 tokens or more", who, width);
+    // (the kernels round positions up to whole tiles of 128 in 32 bits)
+    if (static_cast<long long>(width) * page > INT_MAX - 128)
+        return fail(FA_ERR_UNSUPPORTED, "%s: table rows of %d pages hold more than 2^31 - 129 tokens", who, width);
     return FA_OK;
 }
 

@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     }
     const int r = j.row0 + n, tok = r / G, head = j.h * G + r % G;
     const long long row = j.start + tok;
+    if (!fa_index_ok(row, p.seq.total_tokens, p.status)) return;
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int c = 0; c < kPer; ++c)

@@ -346,7 +346,9 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  *   lens              device, int32 [B]: the tokens that each request holds (clamped to
  *                     0 .. width page)
  * A slot is a token's place in the cache, page id * page + offset in the page.
- * Limits: num_pages * page < 2^31, B <= 8192 (FA_ERR_UNSUPPORTED beyond).
+ * Limits (FA_ERR_UNSUPPORTED beyond): num_pages * page < 2^31, width * page < 2^31 - 128,
+ * B <= 8192; for fa_fwd_kv8 also num_pages * Hkv < 2^31, T * (Hq / Hkv) < 2^31 - 128 for T
+ * new tokens, and B * Hkv * (ceil(width * page / 128) + 1) < 2^31.
  *
  * fa_kv8_plan: request b gains grow[b] >= 0 tokens, or, where grow[b] < 0, it has ended.
  * Free pages queue in a ring: ring[(head + i) mod num_pages], 0 <= i < count, with
@@ -371,7 +373,8 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  * fa_kv8_append: token t of k and v ([T, Hkv, d], bf16 or fp16, tokens `stride` elements
  * apart, a multiple of 8) goes to slots[t]; a slot outside the cache (-1) leaves the token
  * out.  The tokens of one block of 16 slots must be neighbours in the batch with
- * consecutive slots, as fa_kv8_plan gives them.  For each block and head, with amax the
+ * consecutive slots, as fa_kv8_plan gives them (otherwise, and where a slot is given twice,
+ * what that block of 16 slots holds afterwards is not defined).  For each block and head, with amax the
  * largest finite magnitude among its new values and k >= -64 the least whole number with
  * amax <= 448 2^k, the block's scale becomes 2^k where its first new token is the block's
  * first, and max(old scale, 2^k) where the block held tokens before; those are then
@@ -390,13 +393,16 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  * key gets O = 0 and LSE = -inf; rows of a packed batch behind cu_seqlens[B] are left as
  * they were.  A table entry outside 0 .. num_pages - 1 hides its page's tokens.  A value
  * in a place hidden from a row (NaN included) does not reach that row.
- * N must be >= the most new tokens of a request.  The scores use the codes and q
- * unrounded; the probabilities are rounded to 9 bits (bf16) or 11 bits (fp16).
+ * N must be >= the most new tokens of a request (the rows of a request with more may be left
+ * as they were).  The scores use the codes and q unrounded.  The probabilities are rounded to
+ * 11 bits, or to 9 for bf16 where N * Hq / Hkv <= 16.
  *   workspace    device, >= fa_fwd_kv8_workspace_size(...) bytes, 256-byte aligned,
  *                contents ignored; not to be shared by calls in flight together
  *                (calls captured into graphs that replay at the same time among them)
  * The size does not depend on lens.  The result does not depend on anything but the
- * inputs, the geometry and the device's SM count.
+ * inputs, the geometry and the device's SM count.  Enqueues two kernels (L = 2 for
+ * fa_set_launch_events).  A wait inside them gives up after fa_set_wait_limit_cycles' budget
+ * or 6e9 cycles, whichever is less.
  */
 #define FA_KV8_BLOCK 16
 fa_status fa_kv8_plan(const int* lens, const int* grow, int B, int* table, int width, int* ring,

@@ -80,6 +80,22 @@ def test_attention_refuses(lib, over, status):
     assert _fwd(lib, **over) == status and lib.fa_last_error()
 
 
+@pytest.mark.parametrize("over", [
+    # num_pages * Hkv, new tokens * group, table rows of nearly 2^31 tokens, key tiles of all requests
+    dict(num_pages=1 << 23, page=16, Hkv=256, Hq=256, q_stride=256 * 128),
+    dict(cu_seqlens=16, total_tokens=1 << 26, Hq=64, Hkv=2, q_stride=64 * 128, N=1),
+    dict(width=(1 << 24) - 1, page=128),
+    dict(B=8192, Hkv=64, Hq=64, q_stride=64 * 128, width=1 << 12, page=128),
+])
+def test_attention_refuses_what_32_bits_do_not_count(lib, over):
+    assert _fwd(lib, **over) == 2 and lib.fa_last_error()
+    smaller = {k: v for k, v in over.items() if k not in ("num_pages", "total_tokens", "width")}
+    if "total_tokens" in over:
+        smaller["total_tokens"] = 7
+    # the same call is sound with a smaller count: only the workspace is missing
+    assert _fwd(lib, workspace=None, **smaller) == 3
+
+
 def test_workspace_size(lib):
     f = lib.fa_fwd_kv8_workspace_size
     assert f(1, 4, 2, 1, 128, 0) > 0 and f(1, 4, 2, 1, 128, 0) % 256 == 0
