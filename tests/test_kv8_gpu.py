@@ -249,6 +249,81 @@ def test_attention(fa, case):
     check(fa, c, d, dtype, causal, window)
 
 
+@pytest.mark.parametrize("B,most", [(257, 1), (700, 1), (700, 9), (300, 40)])
+def test_attention_of_many_requests(fa, B, most):
+    """More requests than a CTA has threads, long runs of requests without tokens among them."""
+    rng = np.random.default_rng(B + most)
+    lens = rng.integers(0, 150, B)
+    lens[40:200] = 0
+    lens[B - 1] = 900
+    new = np.minimum(rng.integers(0, most + 1, B), lens)
+    new[B - 1] = most
+    c = make(rng, B, lens.tolist(), new.tolist(), 4, 2, 64, 16, "bf16")
+    check(fa, c, 64, "bf16")
+
+
+@pytest.mark.parametrize("window", [0, 100])
+def test_more_new_tokens_than_announced(fa, window):
+    """The rows of max_seqlen tokens of each request are right whatever the others hold."""
+    rng = np.random.default_rng(16)
+    c = make(rng, 3, [600, 450, 300], [1, 9, 1], 4, 2, 128, 64, "bf16")
+    want = fa_out(fa, c, window=window)
+    got = fa_out(fa, c, window=window, max_seqlen=1)
+    fa.fa_device_status()
+    for t in (0, 1, 10):
+        # probabilities rounded to 9 and to 11 bits (2^-9 together at most), each output to bf16;
+        # values are 448 / 128 at most
+        assert (got[0][t].float() - want[0][t].float()).abs().max() <= 3 * 2.0 ** -8 * 3.5
+
+
+def test_calls_and_graphs_at_once(fa):
+    """Calls on two streams, each with its own workspace, and graphs of them that replay together."""
+    import torch
+    rng = np.random.default_rng(17)
+    want, args = [], []
+    for new, lens in ((1, [4000, 3000, 100] * 5), (50, [900, 2000] * 3)):
+        c = make(rng, len(lens), lens, [new] * len(lens), 8, 2, 128, 64, "bf16")
+        want.append(fa_out(fa, c))
+        cache = to_cache(fa, c["codes"][0], c["scales"][0], c["codes"][1], c["scales"][1])
+        args.append((c["q"].cuda(), cache, dev(c["table"]), dev(c["lens"]),
+                     dict(cu_seqlens=dev(c["cu"]), max_seqlen=new)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    graphs, outs = [], []
+    for s, (q, cache, table, lens, kw) in zip(streams, args):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(fa.attention_forward_kv8(q, cache, table, lens, **kw))
+        graphs.append(g)
+    for _ in range(20):
+        got = [fa.attention_forward_kv8(q, cache, table, lens, stream=s, **kw)
+               for s, (q, cache, table, lens, kw) in zip(streams, args)]
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for w, a, b in zip(want, got, outs):
+            assert all(torch.equal(x, y) for x, y in zip(w, a)) and all(torch.equal(x, y) for x, y in zip(w, b))
+    fa.fa_device_status()
+
+
+def test_suite_under_the_bounds_checking_build(fa):
+    """This file's tests again with the library that checks its indices; the status word has to be
+    clear after each."""
+    import os
+    import subprocess
+    import sys
+    if fa.fa_debug_checks_enabled():
+        pytest.skip("this is the checking build")
+    from exact_io_aware_tcgen05_gb300 import build as b
+    env = dict(os.environ, FA_GB300_LIBRARY=b.build(debug=True), FA_GB300_CHECK_STATUS="1")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", "-p", "no:cacheprovider",
+                        os.path.join("tests", "test_kv8_gpu.py")], cwd=root, env=env, capture_output=True,
+                       text=True, timeout=1200)
+    assert r.returncode == 0 and " passed" in r.stdout, (r.stdout[-4000:], r.stderr[-2000:])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("n", [1, 3, 70])
 def test_attention_dense(fa, n, dtype):
