@@ -563,6 +563,8 @@ class Kv8Cache(tuple):
 def kv8_cache(num_pages, Hkv, d, *, page=64, device="cuda") -> Kv8Cache:
     """A cache with no tokens in it (zero codes, scales of one)."""
     import torch
+    if page not in (16, 32, 64, 128) or d not in (64, 128):
+        raise ValueError(f"page must be 16, 32, 64 or 128 and d 64 or 128, got {page} and {d}")
     codes = [torch.zeros((num_pages, Hkv, page, d), dtype=torch.uint8, device=device)
              .view(torch.float8_e4m3fn) for _ in range(2)]
     scales = [torch.ones((num_pages, Hkv, page // FA_KV8_BLOCK), device=device) for _ in range(2)]

@@ -153,7 +153,7 @@ struct Kv8Join {
     int b, h;        // request, key/value head
     int start, n;    // the request's first new token in the batch, and their count
     int row0;        // the item's first row (rows are (token, head of the group) pairs)
-    int pad[2];
+    int pad[2];      // (32 bytes: two loads of 16)
 };
 
 // The longest wait limit that the kernel of fa_fwd_kv8 is given (about three seconds).

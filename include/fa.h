@@ -501,11 +501,11 @@ fa_status fa_device_status(cudaStream_t stream);
 void fa_set_wait_limit_cycles(long long cycles);
 
 /*
- * Per-kernel timing hook.  Arms the calling thread's NEXT fa_fwd or fa_bwd
+ * Per-kernel timing hook.  Arms the calling thread's NEXT fa_fwd, fa_bwd or fa_fwd_kv8
  * call (one call, then it disarms itself): events[i] is recorded on that
  * call's stream just before the call enqueues its i-th kernel, and events[L]
  * just after the last one, L being the number of kernels the call enqueues
- * (fa_fwd: 1; fa_bwd: 3 -- row statistics D, then dK/dV and dQ on the split
+ * (fa_fwd: 1; fa_fwd_kv8: 2; fa_bwd: 3 -- row statistics D, then dK/dV and dQ on the split
  * path, or the fused kernel and the dQ conversion on the fused one).  The
  * events are created and owned by the caller (cudaEventCreate); count must be
  * >= L + 1, otherwise that call fails with FA_ERR_INVALID_ARG before enqueuing

@@ -96,6 +96,14 @@ def test_attention_refuses_what_32_bits_do_not_count(lib, over):
     assert _fwd(lib, workspace=None, **smaller) == 3
 
 
+def test_cache_of_other_shapes_is_refused(lib):
+    for kw in (dict(d=128, page=24), dict(d=96, page=64), dict(d=64, page=256), dict(d=64, page=8)):
+        with pytest.raises(ValueError):
+            lib.kv8_cache(4, 2, device="cpu", **kw)
+    k8, k_scale, v8, v_scale = lib.kv8_cache(4, 2, 64, page=32, device="cpu")
+    assert k8.shape == v8.shape == (4, 2, 32, 64) and k_scale.shape == v_scale.shape == (4, 2, 2)
+
+
 def test_workspace_size(lib):
     f = lib.fa_fwd_kv8_workspace_size
     assert f(1, 4, 2, 1, 128, 0) > 0 and f(1, 4, 2, 1, 128, 0) % 256 == 0
