@@ -310,19 +310,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         int np = -1, left = 0;   // the part of the next tile, its tiles from that one on
         bool first = true;
         auto advance = [&]() {   // to the next tile; false at the end
-#pragma unroll 1
-            while (left == 0) {
+            if (left == 0) {
                 if (!take(np + 1, part)) return false;
                 ++np;
                 left = part.tiles;
                 first = true;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
-                if (left == 0 && lane == 0) {
-                    // (its queries are laid out all the same)
-                    wait(&sm.q_full[np & 1], np >> 1);
-                    mma_commit(smem_addr(&sm.q_empty[np & 1]));
-                }
             }
             --left;
             return true;
@@ -616,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 }
             }
             // ------------------------------------------------ the part's end
-            if (ok && part.tiles > 0) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
+            if (ok) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
             tc_fence_after();
             warp_sums(l, lane);
             constexpr int kSame = 32 / C;   // lanes that hold the same column's sum
@@ -642,9 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll 1
                 for (int n0 = 0; n0 < nrows; n0 += 8) {
                     float o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = 0.f;
-                    if (part.tiles > 0) load_sum8<K::kP>(tO + n0, C, o);
+                    load_sum8<K::kP>(tO + n0, C, o);
                     uint32_t spoilt = 0;   // columns of these 8 that see a NaN in this channel
                     if (poison && key < D) spoilt = find_nan<D, C>(p, part, sm, buf, n0, key);
 #pragma unroll

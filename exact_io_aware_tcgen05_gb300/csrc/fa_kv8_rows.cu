@@ -248,16 +248,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         const uint64_t k0 = sdesc<K::kSwizzle>(smem_addr(sKV), 16, K::kGroup);
         const uint64_t v0 = sdesc_sw128(smem_addr(sV), K::kV16Chunk, 1024);
         const uint64_t q0 = sdesc<K::kSwizzle>(smem_addr(sQ), 16, K::kGroup);
-        int np = -1, nq = -1, left = 0;   // the next tile's part, its number among those with tiles
-        bool first = true;                // the next tile is its part's first
-        auto advance = [&]() {            // to the next tile; false at the end
-#pragma unroll 1
-            while (left == 0) {
+        int np = -1, left = 0;   // the next tile's part, its tiles from that one on
+        bool first = true;       // the next tile is its part's first
+        auto advance = [&]() {   // to the next tile; false at the end
+            if (left == 0) {
                 if (!take_part(sm, np + 1, part)) return false;
                 ++np;
                 left = part.tiles;
                 first = true;
-                if (left > 0) ++nq;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
             }
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             if (lane == 0) {
                 const int it = 4 * T + 4, st = it % kSlots;   // the keys' two slots are neighbours
                 if (first) {
-                    wait(&sm.q_full, nq);
+                    wait(&sm.q_full, np);
                     wait(&sm.kv_full[st], it / kSlots);
                     wait(&sm.kv_full[st + 1], it / kSlots);
                 }
@@ -321,18 +319,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     } else if (warp < 4) {
         // ----------------------------------------------------- queries and values
         const int t = threadIdx.x - 64;
-        int nq = 0, T = 0;
+        int T = 0;
         bool ok = true;
 #pragma unroll 1
         for (int np = 0; take_part(sm, np, part); ++np) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
-            if (part.tiles == 0) continue;
-            if (nq > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, nq - 1));
+            if (np > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, np - 1));
             cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&sm.q_full));
-            ++nq;
             // Values: a unit of 16 codes becomes two of 8 fp16 numbers.  A key's D / 16 units
             // are D / 16 threads', so that a warp reads whole rows.
             // (the threads of the upper 64 channels have the neighbouring row: 8 lanes' stores
@@ -395,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                         w.z &= ~(e | (e - (e >> 7)));
                                         w.w &= ~(f | (f - (f >> 7)));
                                         *at = w;
-                                        sm.poison[(nq - 1) & 1] = 1;
+                                        sm.poison[np & 1] = 1;
                                     }
                                 }
                             }
@@ -433,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         const int quad = warp - 4, row = quad * 32 + lane;   // TMEM lane
         const uint32_t tS0 = tmem + (static_cast<uint32_t>(quad * 32) << 16), tO = tS0 + 128;
         const int G = p.seq.group;
-        int T = 0, nq = 0;   // tiles, parts with tiles
+        int T = 0;   // tiles
         bool ok = true;
 #pragma unroll 1
         for (int np = 0; take_part(sm, np, part); ++np) {
@@ -445,17 +441,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             // keys [lo, hi] are this row's
             const int hi = !real ? -1 : p.seq.causal ? pos_row : part.req.len - 1;
             const int lo = p.seq.window > 0 ? max(pos_row - p.seq.window + 1, 0) : 0;
-            float rowc = 0.f;   // the row's scale, and the exponent's
-            if (part.tiles > 0) {
-                if (nq > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, nq - 1));
-                cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
-                fence_proxy_async_smem();
-                mbar_arrive(smem_addr(&sm.q_full));
-                ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full, nq));
-                rowc = sm.q_scale[row] * p.scale_log2;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty));
-            }
+            if (np > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, np - 1));
+            cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
+            fence_proxy_async_smem();
+            mbar_arrive(smem_addr(&sm.q_full));
+            ok = __all_sync(0xffffffffu, ok && wait(&sm.q_full, np));
+            const float rowc = sm.q_scale[row] * p.scale_log2;   // the row's scale, and the exponent's
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sm.q_empty));
             // a warp without rows leaves its part of P as it is (rows of O that nobody reads)
             const bool idle = part.row0 + quad * 32 >= part.req.n * G;
             float l = 0.f, ref = kNone;   // the exponents' offset: M - kShift
@@ -572,19 +565,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                 }
             }
             // ------------------------------------------------ the part's end
-            if (part.tiles > 0) {
-                if (ok) ok = __all_sync(0xffffffffu, wait(&sm.o_half[1], T - 1));
-                ++nq;
-            }
+            if (ok) ok = __all_sync(0xffffffffu, wait(&sm.o_half[1], T - 1));
             tc_fence_after();
             bool poison = false;
-            if (part.tiles > 0 && (part.tile0 * kKeys < part.all_lo ||
-                                   (part.tile0 + part.tiles) * kKeys - 1 > part.all_hi)) {
+            if (part.tile0 * kKeys < part.all_lo || (part.tile0 + part.tiles) * kKeys - 1 > part.all_hi) {
                 // (parts with no such edge set no poison)
                 named_bar_sync(kBarRows, 128);
-                poison = sm.poison[(nq - 1) & 1] != 0;
+                poison = sm.poison[np & 1] != 0;
                 named_bar_sync(kBarRows, 128);
-                if (row == 0) sm.poison[(nq - 1) & 1] = 0;
+                if (row == 0) sm.poison[np & 1] = 0;
             }
             if (ok) {
                 const bool whole = part.whole;
@@ -596,14 +585,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t x[32];
-                    if (part.tiles > 0) {
-                        tmem_ld32(tO + c, x);
-                        tmem_ld_wait();
-                        reg_fence(x);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = 0;
-                    }
+                    tmem_ld32(tO + c, x);
+                    tmem_ld_wait();
+                    reg_fence(x);
                     if (in && whole) {
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {

@@ -148,7 +148,7 @@ __device__ __forceinline__ int share_of(long long total, long long unit, int G) 
 struct Part {
     Request req;
     int b, h, row0;     // request, key/value head, first row
-    int tile0, tiles;   // the part's key tiles (absolute), tiles may be 0: rows that see nothing
+    int tile0, tiles;   // the part's key tiles (absolute); 0: an item whose rows see nothing
     bool whole;         // all of the item's tiles
     bool begins;        // the item's first tile is the part's
     long long unit0;    // the item's first unit
@@ -474,11 +474,33 @@ __device__ __forceinline__ bool take_part(Smem& sm, int np, Part& part) {
     return part.tiles >= 0;
 }
 
+// O = 0 and LSE = -inf for an item that sees no keys: `rows` rows from row0 on, by a warp.
+template <int D>
+static __device__ __noinline__ void rows_without_keys(const Kv8FwdParams& p, int b, int h, int start, int row0,
+                                                      int rows) {
+    const int lane = threadIdx.x & 31, G = p.seq.group;
+#pragma unroll 1
+    for (int r = row0; r < row0 + rows; ++r) {
+        const int tok = r / G, head = h * G + r % G;
+        const long long token = start + tok;
+        if (!fa_index_ok(token, p.seq.total_tokens, p.status)) continue;
+        uint16_t* out = static_cast<uint16_t*>(p.o) + (token * p.seq.Hq + head) * D;
+        if (lane < D / 8) *reinterpret_cast<uint4*>(out + 8 * lane) = make_uint4(0, 0, 0, 0);
+        if (lane == 0) p.lse[row_stat_index(p.seq, b, head, start, tok)] = kNegInf;
+    }
+}
+
 // The producer warp: walks the CTA's share, hands its parts out, and for each part's tiles
 // copies K and V in units of U keys (K's units, then V's) through the ring of slots (pages by
 // TMA, rows of d bytes swizzled over d bytes), and with the first of them the tile's 16
 // scales (K's, then V's; -1 for V's where a block's tokens are hidden: behind the last key
 // that is seen, or on a page that the cache does not have).
+//
+// An item whose rows see nothing (an idle seat, a refused prompt) it writes itself and does not
+// hand out.  The issuer looks one tile ahead, into the next part, before it issues this part's
+// last product, so a part that it waits for there must not depend on that product.  A part with
+// tiles does not: its place among the parts and its queries' place were given back by parts
+// before this one.  Without tiles any number of parts could follow, and would.
 //
 // One warp's instructions for a tile take about as long as a narrow tile does, so what its
 // copies have in common is worked out once and the table is read while the part is handed
@@ -506,8 +528,13 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
     Part part;
     Walk<C> walk(p, sm.share, sm.window);      // (a CTA without a share has no parts)
 #pragma unroll 1
-    for (int np = 0;; ++np) {
+    for (int np = 0;;) {
         const bool more = walk.next(part);
+        if (more && part.tiles == 0) {
+            rows_without_keys<D>(p, part.b, part.h, part.req.start, part.row0,
+                                 min(C, part.req.n * p.seq.group - part.row0));
+            continue;
+        }
         if (!more) part.tiles = -1;
         const int* row = p.table + static_cast<long long>(part.b) * p.width;
         const int lim = min(part.hi_key + 1, part.req.len);   // tokens from here on are not needed
@@ -515,8 +542,8 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
         // the table's entries, 32 at a time, the next ones on their way
         int base = part.tile0 * per_tile;
         auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
-        int cur = part.tiles > 0 ? entry(base + lane) : -1;
-        int nxt = part.tiles > 0 ? entry(base + 32 + lane) : -1;
+        int cur = more ? entry(base + lane) : -1;
+        int nxt = more ? entry(base + 32 + lane) : -1;
         if (np >= kParts)
             drain_on(smem_addr(&sm.part_empty[np % kParts]), (np / kParts - 1) & 1);
         if (lane == 0) {
@@ -537,6 +564,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
         }
         __syncwarp();
         if (!more) break;
+        ++np;
 #pragma unroll 1
         for (int i = 0; i < part.tiles && ok; ++i, ++c) {
             const int tile = part.tile0 + i;

@@ -1,0 +1,69 @@
+"""The 8-bit paged cache on the GPU where a call can go wrong: rows that see nothing between long
+requests, and others that come up in a server's batches."""
+import pytest
+
+import kv8_ref64 as r64
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- items without keys
+
+# Long requests with requests that see nothing between them, one and several in a row, so many
+# that every CTA has items of both kinds: (tokens, new tokens) of one stretch, repeated.
+SEATS = {
+    "one": [(4096, 1), (0, 1), (3000, 1)],
+    "six": [(2048, 1)] + [(0, 1)] * 6 + [(129, 1)],
+    "ends": [(0, 1)] * 5 + [(5000, 1)] + [(0, 1)] * 2,
+    "short": [(1, 1), (0, 1), (128, 1), (0, 1), (0, 1)],
+}
+
+
+@pytest.mark.parametrize("Hkv", [1, 8])
+@pytest.mark.parametrize("group", [1, 8, 16, 24])
+@pytest.mark.parametrize("kind", list(SEATS))
+def test_idle_seats_between_long_requests(fa, kind, group, Hkv):
+    """Single tokens (up to 8 and up to 16 rows, and items of 128)."""
+    times = 40 if Hkv == 1 else 10
+    stretch = SEATS[kind] * times
+    lens, new = [x[0] for x in stretch], [x[1] for x in stretch]
+    c = r64.make(3, lens, new, group * Hkv, Hkv, 64 if group == 8 else 128, 64, "f16" if group == 1 else "bf16")
+    r64.close(c, *r64.run(fa, c), r64.attend(c))
+
+
+@pytest.mark.parametrize("Hkv", [1, 8])
+@pytest.mark.parametrize("group,new", [(2, 4), (4, 4), (8, 20), (1, 300)])
+def test_refused_prompts_between_long_requests(fa, group, new, Hkv):
+    """Requests with more new tokens than keys: their first blocks of rows see nothing."""
+    stretch = [(2500, new), (0, new), (3, new), (new // 2, new), (700, new), (0, new), (0, new), (0, new),
+               (0, new), (0, new), (1500, 1)] * (8 if Hkv == 1 else 3)
+    c = r64.make(4, [x[0] for x in stretch], [x[1] for x in stretch], group * Hkv, Hkv, 128, 32, "bf16")
+    r64.close(c, *r64.run(fa, c), r64.attend(c))
+    r64.close(c, *r64.run(fa, c, window=100), r64.attend(c, window=100))
+
+
+def test_nothing_but_idle_seats(fa):
+    for n, group in ((1, 8), (2, 8), (40, 8)):
+        c = r64.make(5, [0] * 50, [n] * 50, group * 2, 2, 128, 64, "bf16")
+        o, lse = r64.run(fa, c)
+        assert (o == 0).all() and (lse == -float("inf")).all()
+
+
+def test_a_refused_prompt_in_a_step(fa):
+    """A prompt that kv8_plan refuses keeps its place in cu_seqlens; the others' rows are right."""
+    import torch
+    H, Hq, d, page, pages = 2, 8, 128, 64, 160
+    cache = fa.kv8_cache(pages, H, d, page=page)
+    grow = [3000, 500, 2500, 1, 400]
+    T = sum(grow)
+    table = torch.zeros(5, 60, dtype=torch.int32, device="cuda")
+    ring = torch.arange(pages, dtype=torch.int32, device="cuda")
+    state = torch.tensor([0, 100, 0], dtype=torch.int32, device="cuda")   # 100 free pages: 47 + 8 + 40 + 1
+    lens = torch.zeros(5, dtype=torch.int32, device="cuda")
+    x = torch.randn(T, Hq + 2 * H, d, device="cuda").bfloat16()
+    ln, cu, slots, st = fa.kv8_plan(lens, torch.tensor(grow, dtype=torch.int32, device="cuda"), table, ring, state,
+                                    page=page, tokens=T)
+    assert ln.tolist() == [3000, 500, 2500, 1, 0] and st.tolist()[2] == 1
+    fa.kv8_append(cache, x[:, Hq:Hq + H], x[:, Hq + H:], slots)
+    c = dict(q=x[:, :Hq].contiguous(), cache=tuple(cache), table=table, lens=ln, cu=cu, new=grow, dtype="bf16")
+    r64.close(c, *r64.run(fa, c), r64.attend(c))
