@@ -609,18 +609,19 @@ def _int32(name, x, shape, device):
 
 def _rows(name, x, heads, d):
     """Elements between the tokens of a [..., heads, d] tensor whose tokens are evenly spaced
-    (a slice of a wider projection's output, say)."""
+    (a slice of a wider projection's output, say) and do not overlap (an expanded tensor's do)."""
     shape, strides = x.shape, x.stride()
-    stride = strides[-3] if shape[-3] > 1 else 0
     ok = shape[-2] == heads and shape[-1] == d and strides[-1] == 1 and (heads == 1 or strides[-2] == d)
-    if len(shape) == 4 and shape[0] > 1:
-        n, outer = shape[1], strides[0]
-        ok = ok and outer % max(n, 1) == 0 and (n <= 1 or outer == stride * n)
-        stride = outer // max(n, 1)
+    n, outer = shape[-3], shape[0] if len(shape) == 4 else 1
+    if n * outer <= 1:
+        stride = heads * d
+    else:
+        stride = strides[-3] if n > 1 else strides[0]
+        ok = ok and stride >= heads * d and (n == 1 or outer == 1 or strides[0] == stride * n)
     if not ok:
         raise ValueError(f"{name} must be [..., {heads}, {d}] with contiguous heads and evenly "
                          "spaced tokens")
-    return stride or heads * d
+    return stride
 
 
 def _elsewhere(device, stream) -> bool:

@@ -1,0 +1,79 @@
+"""The 8-bit cache's entry points on the host, at the edges (no GPU needed)."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from exact_io_aware_tcgen05_gb300 import build as b
+    b.build()
+    import exact_io_aware_tcgen05_gb300 as fa
+    fa.load()
+    return fa
+
+
+def _q(*shape):
+    import torch
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+# q of 4 heads, d 64, whose tokens lie in the same place, or overlap
+OVERLAPPING = {
+    "requests": lambda: _q(1, 1, 4, 64).expand(6, 1, 4, 64),
+    "tokens": lambda: _q(2, 1, 4, 64).expand(2, 5, 4, 64),
+    "both": lambda: _q(1, 1, 4, 64).expand(6, 5, 4, 64),
+    "requests of several tokens": lambda: _q(1, 5, 4, 64).expand(6, 5, 4, 64),
+    "one request": lambda: _q(1, 1, 4, 64).expand(1, 5, 4, 64),
+    "packed": lambda: _q(1, 4, 64).expand(5, 4, 64),
+    "shifted": lambda: _q(4096).as_strided((5, 4, 64), (64, 64, 1)),
+    "shifted requests": lambda: _q(4096).as_strided((6, 1, 4, 64), (128, 256, 64, 1)),
+    "no heads' distance": lambda: _q(5, 1, 64).expand(5, 4, 64),
+}
+
+
+@pytest.mark.parametrize("kind", list(OVERLAPPING))
+def test_expanded_queries_are_refused(lib, kind):
+    import torch
+    q = OVERLAPPING[kind]()
+    B = 1 if q.dim() == 3 else q.shape[0]
+    kw = dict(cu_seqlens=torch.tensor([0, 5], dtype=torch.int32), max_seqlen=5) if q.dim() == 3 else {}
+    cache = lib.kv8_cache(4, 2, 64, page=16, device="cpu")
+    with pytest.raises(ValueError, match="evenly"):
+        lib.attention_forward_kv8(q, cache, torch.zeros(B, 3, dtype=torch.int32),
+                                  torch.ones(B, dtype=torch.int32), **kw)
+
+
+@pytest.mark.parametrize("side", ["k", "v", "both"])
+def test_expanded_keys_and_values_are_refused(lib, side, monkeypatch):
+    import torch
+    monkeypatch.setattr(lib, "_kv8_shape", lambda cache, device: tuple(cache.k8.shape))   # (tensors on the CPU)
+    cache = lib.kv8_cache(4, 4, 64, page=16, device="cpu")
+    x = dict(k=_q(5, 4, 64), v=_q(5, 4, 64))
+    for name in x if side == "both" else side:
+        x[name] = _q(1, 4, 64).expand(5, 4, 64)
+    with pytest.raises(ValueError, match="evenly|same distance"):
+        lib.kv8_append(cache, x["k"], x["v"], torch.zeros(5, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("make,stride", [
+    (lambda: _q(5, 4, 64), 256),
+    (lambda: _q(5, 9, 64)[:, 2:6], 576),                    # slices of a wider tensor
+    (lambda: _q(10, 9, 64)[::2, 2:6], 1152),
+    (lambda: _q(3, 5, 9, 64)[:, :, 2:6], 576),
+    (lambda: _q(6, 5, 4, 64)[:, :1], 1280),                 # one token of each request
+    (lambda: _q(6, 5, 4, 64)[2:3, ::2], 512),               # one request
+    (lambda: _q(1, 4, 64), 256),                            # single tokens, wherever they lie
+    (lambda: _q(1, 1, 4, 64), 256),
+    (lambda: _q(8, 4, 64)[3:4].expand(1, 4, 64), 256),
+    (lambda: _q(0, 4, 64), 256),                            # no token
+    (lambda: _q(3, 0, 4, 64), 256),
+])
+def test_distance_of_tokens(lib, make, stride):
+    assert lib._rows("q", make(), 4, 64) == stride
+
+
+def test_distance_of_tokens_of_one_head(lib):
+    assert lib._rows("q", _q(5, 3, 64)[:, 1:2], 1, 64) == 192
+    with pytest.raises(ValueError):
+        lib._rows("q", _q(5, 3, 64)[:, 1:2], 4, 64)
+    with pytest.raises(ValueError):
+        lib._rows("q", _q(3, 5, 4, 64)[:, ::2], 4, 64)       # requests and tokens at odds
