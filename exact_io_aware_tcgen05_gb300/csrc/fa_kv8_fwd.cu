@@ -101,7 +101,7 @@ struct Kv8Smem {   // behind the tiles
     uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], scales_full[kScaleSlots];
     uint64_t part_full[kParts], part_empty[kParts];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], pv_done;
+    uint64_t s_full[2], pv_done[2];  // [tile parity]
     uint64_t all_done;
     uint32_t tmem;
     int abort;
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
             mbar_init(smem_addr(&sm.q_full[i]), 32);
             mbar_init(smem_addr(&sm.q_empty[i]), 5);    // the last S^T of the part, 4 softmax warps
             mbar_init(smem_addr(&sm.s_full[i]), 1);
+            mbar_init(smem_addr(&sm.pv_done[i]), 1);
         }
-        mbar_init(smem_addr(&sm.pv_done), 1);
         mbar_init(smem_addr(&sm.all_done), 1);
         fence_barrier_init();
     }
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                     for (int kk = 0; kk < kKeys / 32; ++kk)
                         mma_ss_f8(colO, vd + ((kk * 32 * D) >> 4), pd + ((kk * 512) >> 4), kIdescO,
                                   (!fresh || kk > 0) ? 1u : 0u);
-                    mma_commit(smem_addr(&sm.pv_done));
+                    mma_commit(smem_addr(&sm.pv_done[T & 1]));
                     mma_commit(smem_addr(&sm.kv_empty[st]));
                 }
                 __syncwarp();
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                         }
                         __syncwarp();
                         if (i > 0) {
-                            ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
+                            ok = __all_sync(0xffffffffu, wait(&sm.pv_done[(T - 1) & 1], (T - 1) >> 1));
                             tc_fence_after();
 #pragma unroll
                             for (int n = 0; n < C; ++n) l[n] *= sm.fac[quad][n];
@@ -610,7 +610,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                 }
             }
             // ------------------------------------------------ the part's end
-            if (ok) ok = __all_sync(0xffffffffu, wait(&sm.pv_done, T - 1));
+            // (The last tile's scores were issued before the product of the tile before it, so
+            // that one may be running still.  A wait looks at a phase's parity: with one barrier
+            // for all products it could take the one before those two for the last.)
+            if (ok) ok = __all_sync(0xffffffffu, wait(&sm.pv_done[(T - 1) & 1], (T - 1) >> 1));
             tc_fence_after();
             warp_sums(l, lane);
             constexpr int kSame = 32 / C;   // lanes that hold the same column's sum

@@ -77,3 +77,22 @@ def test_distance_of_tokens_of_one_head(lib):
         lib._rows("q", _q(5, 3, 64)[:, 1:2], 4, 64)
     with pytest.raises(ValueError):
         lib._rows("q", _q(3, 5, 4, 64)[:, ::2], 4, 64)       # requests and tokens at odds
+
+
+def test_wait_for_a_parts_last_product():
+    """The narrow kernel's wait at a part's end, for every state that its products can be in then.
+
+    The scores of tile t are issued before the product of tile t - 1, so when a part's last tile t
+    has had its scores, products up to t - 2 are known to be complete and t - 1 and t may be running.
+    A wait for a phase passes where the barrier's last completed phase has its parity."""
+    import os
+    import re
+    import exact_io_aware_tcgen05_gb300 as fa
+    with open(os.path.join(os.path.dirname(fa.__file__), "csrc", "fa_kv8_fwd.cu")) as f:
+        m = re.search(r"uint64_t [^;]*pv_done(?:\[(\d+)\])?;", f.read())
+    bars = int(m.group(1) or 1)                             # product t completes phase t // bars of one of them
+    for t in range(9):
+        for complete in range(max(t - 1, 0), t + 2):       # products that are complete when the wait begins
+            phases = len(range(t % bars, complete, bars))   # completed ones of the barrier waited for
+            passes = (phases - 1) % 2 == t // bars % 2
+            assert passes == (complete > t), (bars, t, complete)
