@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             const int pos_row = part.req.len - part.req.n + tok;
             // keys [lo, hi] are this row's
             const int hi = !real ? -1 : p.seq.causal ? pos_row : part.req.len - 1;
-            const int lo = p.seq.window > 0 ? max(pos_row - p.seq.window + 1, 0) : 0;
+            const int lo = first_key(p.seq.window, pos_row);
             if (np > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, np - 1));
             cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
             fence_proxy_async_smem();

@@ -60,6 +60,13 @@ __device__ __forceinline__ Request load_request(const Kv8FwdParams& p, int b) {
 template <int C>
 constexpr int kItemCost = C <= 16 ? 1 : 4;
 
+// The first key that a token at position `pos` sees, max(pos - window + 1, 0) with a window.
+// (A request with more new tokens than keys has positions below 0, and a window may be as
+// large as an int: their difference need not be one.)
+__device__ __forceinline__ int first_key(int window, int pos) {
+    return window > 0 ? max(pos, window - 1) - (window - 1) : 0;
+}
+
 // The items of a request for one key/value head: `blocks` blocks of C rows in `pairs`
 // pairs of `cost` units each.
 struct Items {
@@ -201,11 +208,10 @@ struct Walk {
             first += part.row0 / G;
             last += min((part.row0 + C - 1) / G, req.n - 1);
         }
-        const bool win = p.seq.window > 0;
         part.hi_key = p.seq.causal ? last : req.len - 1;
         part.all_hi = p.seq.causal ? first : req.len - 1;
-        part.lo_key = win ? max(first - p.seq.window + 1, 0) : 0;
-        part.all_lo = win ? max(last - p.seq.window + 1, 0) : 0;
+        part.lo_key = first_key(p.seq.window, first);
+        part.all_lo = first_key(p.seq.window, last);
         part.tile0 = part.lo_key / kKeys;
         part.item_tiles = part.hi_key >= part.lo_key ? part.hi_key / kKeys - part.tile0 + 1 : 0;
         // (more new tokens than the call announced: no more keys than there are units for)

@@ -67,3 +67,13 @@ def test_a_refused_prompt_in_a_step(fa):
     fa.kv8_append(cache, x[:, Hq:Hq + H], x[:, Hq + H:], slots)
     c = dict(q=x[:, :Hq].contiguous(), cache=tuple(cache), table=table, lens=ln, cu=cu, new=grow, dtype="bf16")
     r64.close(c, *r64.run(fa, c), r64.attend(c))
+
+
+# ------------------------------------------------------------------------- windows
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 50, 2 ** 30, 140, 1])
+@pytest.mark.parametrize("group,new", [(1, 9), (2, 8), (4, 200)])
+def test_any_window_with_more_tokens_than_keys(fa, group, new, window):
+    """Positions below 0 and windows as long as an int, in items of up to 8, 16 and 128 rows."""
+    c = r64.make(6, [5, 300, 0, new // 2], [new, 1, new, new], group * 2, 2, 128, 16, "bf16")
+    r64.close(c, *r64.run(fa, c, window=window), r64.attend(c, window=window))
