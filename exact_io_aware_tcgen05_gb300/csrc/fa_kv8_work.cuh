@@ -286,7 +286,9 @@ __device__ __forceinline__ float pow2f(int k) { return __uint_as_float(static_ca
 // of them take part), cut into KQ e4m3 pieces for `dst` (pieces `piece` bytes apart): the row
 // times the power of two that brings its largest element into (224, 448], as fp16 numbers
 // (exact: 8 or 11 bits), each piece the rounding of what the ones before it leave.  Returns
-// the row's scale; an infinity or NaN makes it NaN, and with it the row.
+// the row's scale.  An infinity or NaN makes all the row's pieces NaN, and with them its
+// products (its scale stays a number: masked products must stay -inf whatever they are
+// multiplied by, so that a row that sees nothing comes out as one).
 template <int D, int E, int KQ>
 __device__ __forceinline__ float cut_queries(uint4 w, uint8_t* dst, int piece) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -304,7 +306,7 @@ __device__ __forceinline__ float cut_queries(uint4 w, uint8_t* dst, int piece) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 f = unpack2<E>(u[j]);
-        h[j] = pack2<kElemF16>(f.x * inv, f.y * inv);
+        h[j] = fine ? pack2<kElemF16>(f.x * inv, f.y * inv) : 0x7fff7fffu;
     }
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
@@ -328,7 +330,7 @@ __device__ __forceinline__ float cut_queries(uint4 w, uint8_t* dst, int piece) {
             }
         }
     }
-    return fine ? pow2f(k) : __uint_as_float(0x7fc00000u);
+    return pow2f(k);
 }
 
 // Bytes of a word that are e4m3 NaN (0x7f or 0xff), as 0x80 in each.

@@ -77,3 +77,32 @@ def test_any_window_with_more_tokens_than_keys(fa, group, new, window):
     """Positions below 0 and windows as long as an int, in items of up to 8, 16 and 128 rows."""
     c = r64.make(6, [5, 300, 0, new // 2], [new, 1, new, new], group * 2, 2, 128, 16, "bf16")
     r64.close(c, *r64.run(fa, c, window=window), r64.attend(c, window=window))
+
+
+# ------------------------------------------------------- queries that are not finite
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,group,new", [(128, 1, 6), (64, 2, 7), (128, 4, 6), (64, 1, 150)])
+def test_queries_that_are_not_finite_and_rows_that_see_nothing(fa, d, group, new, dtype):
+    """An infinity or NaN in a query makes its row NaN where the row sees a key, and no other row; a
+    row that sees none has O = 0 and LSE = -inf, whatever its query holds."""
+    import torch
+    # positions from -3 on; pages that the cache does not have in the second and third
+    c = r64.make(7, [new - 3, 200, 64 + new], [new, new, new], group * 2, 2, d, 16, dtype)
+    c["table"][1, :] = -1
+    c["table"][2, 4:] = 2 ** 30
+    clean = r64.run(fa, c)
+    want = r64.attend(c)
+    r64.close(c, *clean, want)
+    bad = torch.zeros(c["q"].shape[:2], dtype=torch.bool, device="cuda")
+    for b in range(3):
+        for i, (h, x) in zip((0, 2, 3, new - 1), ((0, "nan"), (1, "inf"), (group * 2 - 1, "-inf"), (0, "inf"))):
+            c["q"][b * new + i, h, 5 * i % d] = float(x)
+            bad[b * new + i, h] = True
+    o, lse = r64.run(fa, c)
+    sees = (want[1] > -float("inf")).T                     # [T, Hq]
+    assert bool((sees & bad).any()) and bool((~sees & bad).any())
+    assert torch.isnan(o[sees & bad]).all() and torch.isnan(lse.T[sees & bad]).all()
+    assert (o[~sees] == 0).all() and (lse.T[~sees] == -float("inf")).all()
+    fine = ~(sees & bad)
+    assert torch.equal(o[fine], clean[0][fine]) and torch.equal(lse.T[fine], clean[1].T[fine])
