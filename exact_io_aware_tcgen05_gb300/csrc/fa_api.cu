@@ -1103,7 +1103,7 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     Kv8FwdParams p;
     if ((st = check_pages("fa_fwd_kv8", num_pages, page, &p.page_log2)) != FA_OK) return st;
     if ((st = check_table("fa_fwd_kv8", B, width, page)) != FA_OK) return st;
-    if (!q || !k8 || !k_scale || !v8 || !v_scale || !table || !lens || !o || !lse)
+    if (!k8 || !k_scale || !v8 || !v_scale || !table || !lens || (g.tokens > 0 && (!q || !o || !lse)))
         return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: every pointer must be non-null");
     if (!aligned16(q) || !aligned16(k8) || !aligned16(v8) || !aligned16(o) || !aligned16(lse) ||
         !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(table) || !aligned4(lens))
@@ -1122,6 +1122,7 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     if (static_cast<long long>(B) * Hkv * ((static_cast<long long>(width) * page + 127) / 128 + 1) > INT_MAX)
         return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: B * Hkv * width * page = %lld is too large for one launch",
                     static_cast<long long>(B) * Hkv * width * page);
+    if (g.tokens == 0) return FA_OK;
     p.columns = kv8_columns(N, g.seq.group);
     p.ctas = 2 * sm_count();
     const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);
@@ -1131,7 +1132,6 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
                     need, workspace_bytes, workspace ? "" : " (null)");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return fail(FA_ERR_WORKSPACE, "fa_fwd_kv8: workspace must be 256-byte aligned");
-    if (g.tokens == 0) return FA_OK;
     p.seq = g.seq;
     p.q = q;
     p.q_stride = q_stride;

@@ -106,3 +106,22 @@ def test_queries_that_are_not_finite_and_rows_that_see_nothing(fa, d, group, new
     assert (o[~sees] == 0).all() and (lse.T[~sees] == -float("inf")).all()
     fine = ~(sees & bad)
     assert torch.equal(o[fine], clean[0][fine]) and torch.equal(lse.T[fine], clean[1].T[fine])
+
+
+def test_a_step_without_tokens(fa):
+    """Plan, append and attend of a packed batch that holds no token."""
+    import torch
+    cache = fa.kv8_cache(8, 2, 128, page=16)
+    was = [t.view(torch.uint8).clone() for t in cache]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, table = torch.tensor([20, 0, 7], **i32), torch.tensor([[1, 2], [0, 0], [3, 0]], **i32)
+    ln, cu, slots, st = fa.kv8_plan(lens, torch.zeros(3, **i32), table, torch.arange(8, **i32),
+                                    torch.tensor([4, 4, 0], **i32), page=16, tokens=0)
+    assert ln.tolist() == [20, 0, 7] and cu.tolist() == [0] * 4 and slots.numel() == 0 and st.tolist() == [4, 4, 0]
+    x = torch.empty(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    fa.kv8_append(cache, x[:, 4:6], x[:, 6:], slots)
+    for n in (1, 2 ** 30):
+        o, lse = fa.attention_forward_kv8(x[:, :4], cache, table, ln, cu_seqlens=cu, max_seqlen=n)
+        assert o.shape == (0, 4, 128) and lse.shape == (4, 0)
+    assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(was, cache))
+    fa.fa_device_status()

@@ -96,3 +96,17 @@ def test_wait_for_a_parts_last_product():
             phases = len(range(t % bars, complete, bars))   # completed ones of the barrier waited for
             passes = (phases - 1) % 2 == t // bars % 2
             assert passes == (complete > t), (bars, t, complete)
+
+
+def test_a_step_without_tokens(lib):
+    """Empty tensors have no address: no token, none needed (nor a workspace)."""
+    def fwd(**over):
+        a = dict(dtype=0, q=None, q_stride=512, k8=16, k_scale=16, v8=16, v_scale=16, num_pages=8, page=64,
+                 table=16, width=4, lens=16, o=None, lse=None, B=2, Hq=4, Hkv=2, N=3, d=128, causal=1, window=0,
+                 cu_seqlens=16, total_tokens=0, scale=0.1, workspace=None, workspace_bytes=0)
+        a.update(over)
+        return lib.fa_fwd_kv8(*a.values(), None, check=False)
+    assert fwd() == 0
+    for name in ("k8", "k_scale", "v8", "v_scale", "table", "lens"):
+        assert fwd(**{name: None}) == 1
+    assert fwd(total_tokens=1) == 1 and fwd(page=24) == 2 and fwd(q_stride=516) == 1
