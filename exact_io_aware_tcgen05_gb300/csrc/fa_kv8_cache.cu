@@ -170,6 +170,40 @@ __device__ __forceinline__ void unpack4_e4m3(uint32_t w, float (&f)[4]) {
     f[3] = y.y;
 }
 
+// a * b and a / b in fp32, rounded to odd: toward zero, and the last bit set where that was not
+// exact.  A value so rounded rounds on to e4m3's 4 bits as the exact one does (the 20 bits
+// between hold whether it lies above, below or on a tie).  An exact one stays as it is.
+__device__ __forceinline__ float to_odd(float x, bool exact) {
+    return exact ? x : __uint_as_float(__float_as_uint(x) | 1u);
+}
+__device__ __forceinline__ float mul_odd(float a, float b) {
+    const float x = __fmul_rz(a, b);
+    return to_odd(x, __fmaf_rn(a, b, -x) == 0.f);
+}
+__device__ __forceinline__ float div_odd(float a, float b) {
+    const float x = __fdiv_rz(a, b);
+    return to_odd(x, __fmaf_rn(-x, b, a) == 0.f);
+}
+
+// The codes of n new tokens of a block whose scale is not a power of two, by a warp: a block that
+// another writer began (this one's scales are powers of two).  `x` and `row` are the lane's 8
+// values of the first token.
+template <int D, int E>
+__device__ __noinline__ void append_by_division(const uint16_t* x, long long stride, uint8_t* row, int n, float scale) {
+    for (int r = (threadIdx.x & 31) / (D / 8); r < n; r += 32 / (D / 8)) {
+        const uint4 w = *reinterpret_cast<const uint4*>(x + r * stride);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 g = unpack2<E>(u[j]);
+            f[2 * j] = div_odd(g.x, scale) + g.x * 0.f;   // (inf * 0 is NaN: infinities become NaN codes)
+            f[2 * j + 1] = div_odd(g.y, scale) + g.y * 0.f;
+        }
+        *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) = make_uint2(pack4_e4m3(f[0], f[1], f[2], f[3]), pack4_e4m3(f[4], f[5], f[6], f[7]));
+    }
+}
+
 // One warp takes the blocks of 16 slots whose first new token is among its `chunk`
 // tokens, for one head of K or V, one block after the other: D / 8 lanes hold one token
 // (8 values, a 16-byte load), so the warp holds the block's new tokens at once and reads
@@ -254,38 +288,42 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
             scale = fmaxf(old, scale);
             if (scale > old) {
                 // the tokens that the block held, rounded again to the larger scale
-                const float ratio = old / scale;
+                const float ratio = old / scale;   // (exact, the new scale being a power of two, or too small for any code)
                 for (int r = lane / kLanes; r < off; r += kRows) {
                     uint2* at = reinterpret_cast<uint2*>(row + static_cast<long long>(r - off) * D);
                     uint2 c = *at;
                     float f[4];
                     unpack4_e4m3(c.x, f);
-                    c.x = pack4_e4m3(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+                    c.x = pack4_e4m3(mul_odd(f[0], ratio), mul_odd(f[1], ratio), mul_odd(f[2], ratio), mul_odd(f[3], ratio));
                     unpack4_e4m3(c.y, f);
-                    c.y = pack4_e4m3(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+                    c.y = pack4_e4m3(mul_odd(f[0], ratio), mul_odd(f[1], ratio), mul_odd(f[2], ratio), mul_odd(f[3], ratio));
                     *at = c;
                 }
             }
         }
-        const float inv = 1.f / scale;   // exact for a power of two
+        if ((__float_as_uint(scale) & 0x7fffffu) != 0) {
+            append_by_division<D, E>(x + t * p.stride, p.stride, row, n, scale);
+        } else {
+            const float inv = 1.f / scale;   // exact for a power of two
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int r = i * kRows + lane / kLanes;
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            float f[8];
+            for (int i = 0; i < kSteps; ++i) {
+                const int r = i * kRows + lane / kLanes;
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                float f[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 g = unpack2<E>(u[j]);
-                f[2 * j] = g.x * inv;
-                f[2 * j + 1] = g.y * inv;
-                if (!finite) {   // inf * 0 is NaN: infinities become NaN codes
-                    f[2 * j] += g.x * 0.f;
-                    f[2 * j + 1] += g.y * 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 g = unpack2<E>(u[j]);
+                    f[2 * j] = g.x * inv;
+                    f[2 * j + 1] = g.y * inv;
+                    if (!finite) {   // inf * 0 is NaN: infinities become NaN codes
+                        f[2 * j] += g.x * 0.f;
+                        f[2 * j + 1] += g.y * 0.f;
+                    }
                 }
+                if (r < n)
+                    *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) =
+                        make_uint2(pack4_e4m3(f[0], f[1], f[2], f[3]), pack4_e4m3(f[4], f[5], f[6], f[7]));
             }
-            if (r < n)
-                *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) =
-                    make_uint2(pack4_e4m3(f[0], f[1], f[2], f[3]), pack4_e4m3(f[4], f[5], f[6], f[7]));
         }
         __syncwarp();   // every lane has read the old scale
         if (lane == 0) *scale_at = scale;

@@ -1,7 +1,9 @@
 """The 8-bit paged cache on the GPU where a call can go wrong: rows that see nothing between long
 requests, and others that come up in a server's batches."""
+import numpy as np
 import pytest
 
+import kv8_ref as ref
 import kv8_ref64 as r64
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +127,79 @@ def test_a_step_without_tokens(fa):
         assert o.shape == (0, 4, 128) and lse.shape == (4, 0)
     assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(was, cache))
     fa.fa_device_status()
+
+
+# --------------------------------------------------------------- scales in the writer
+
+def _blocks(rng, dtype, n, d):
+    """n blocks that hold some tokens at scales that are no powers of two, and tokens for the places
+    behind them: codes [n, 1, 16, d], scales [n], offsets and values [n][new, d].  Many values lie so
+    near the middle between two codes that a rounding on the way there decides otherwise."""
+    import torch
+    mid = (ref.VALUES[8:126] + ref.VALUES[9:127]) / 2           # ties of normal codes
+    codes = rng.integers(0, 256, (n, 1, 16, d)).astype(np.uint8)
+    scales, offs, new = np.empty(n), rng.integers(1, 16, n), []
+    for i in range(n):
+        x = torch.from_numpy(rng.normal(0, 1, (16 - offs[i], d))).to(r64.TYPES[dtype]).double().numpy()
+        if i % 2:
+            # the block keeps its scale: some value over it is a tie, but for 32 bits
+            m = rng.choice(mid)
+            s = np.float32(x.flat[0] / m if x.flat[0] else 1.0)
+            s = abs(s) if abs(s) * 448 >= np.abs(x).max() else np.float32(abs(x.flat[0]) / mid[rng.integers(0, 9)])
+            while s * 448 < np.abs(x).max():
+                s = np.float32(s * 2)
+        else:
+            # the scale grows: some code held is a tie at the new one, but for 32 bits
+            grown = ref.scale_of_amax(np.abs(x).max())
+            c = rng.integers(16, 126)
+            s = np.float32(rng.choice(mid[mid < ref.VALUES[c]]) * grown / ref.VALUES[c])
+            codes[i, 0, :, ::3] = c
+        scales[i] = s
+        new.append(x)
+    return codes, scales, offs, new
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_append_to_blocks_of_any_scale(fa, d, dtype):
+    """Blocks that another writer began: e4m3(x / scale) and e4m3(code old / new), rounded once."""
+    import torch
+    rng = np.random.default_rng(d)
+    n = 400
+    codes, scales, offs, new = _blocks(rng, dtype, n, d)
+    scales = scales.reshape(n, 1, 1)
+    slots = np.concatenate([16 * i + np.arange(o, 16) for i, o in enumerate(offs)]).astype(np.int32)
+    x = np.concatenate(new)[:, None]
+    # rounding twice gives other codes
+    keeps = np.arange(n) % 2 == 1
+    with np.errstate(over="ignore"):
+        twice = np.concatenate([(np.float32(v) * (np.float32(1) / np.float32(s))).astype(np.float64).ravel()
+                                for v, s, k in zip(new, scales.ravel(), keeps) if k])
+    once = np.concatenate([(v / s).ravel() for v, s, k in zip(new, scales.ravel(), keeps) if k])
+    assert (ref.e4m3_codes(np.clip(twice, -448, 448)) != ref.e4m3_codes(once)).sum() > 10
+    cache = []
+    for _ in range(2):
+        cache += [torch.from_numpy(codes.copy()).cuda().view(torch.float8_e4m3fn),
+                  torch.from_numpy(scales.astype(np.float32)).cuda()]
+    k = torch.from_numpy(x).to(r64.TYPES[dtype]).cuda()
+    fa.kv8_append(fa.Kv8Cache(cache), k, k, torch.from_numpy(slots).cuda())
+    ref.append(codes, scales, x, slots)
+    for c, s in (cache[:2], cache[2:]):
+        assert np.array_equal(s.double().cpu().numpy(), scales)
+        got = c.view(torch.uint8).cpu().numpy()
+        assert np.array_equal(ref.VALUES[got], ref.VALUES[codes], equal_nan=True), int((got != codes).sum())
+
+
+def test_append_of_infinities_to_a_block_of_any_scale(fa):
+    import torch
+    cache = fa.kv8_cache(1, 1, 64, page=16)
+    for s in (cache.k_scale, cache.v_scale):
+        s.fill_(0.3)
+    x = torch.zeros(3, 1, 64, dtype=torch.bfloat16, device="cuda")
+    x[0, 0, 1], x[1, 0, 2], x[2, 0, 3], x[2, 0, 4], x[2, 0, 5] = 3.0, float("inf"), float("-inf"), float("nan"), -0.3
+    fa.kv8_append(cache, x, x, torch.arange(5, 8, dtype=torch.int32, device="cuda"))
+    got = cache.k8.float()[0, 0, 5:8]
+    assert torch.equal(cache.k_scale.flatten(), torch.full((1,), 0.3, device="cuda"))
+    assert torch.isnan(got).nonzero().tolist() == [[1, 2], [2, 3], [2, 4]]
+    assert got[0, 1] == 10 and got[2, 5] == -1 and torch.nan_to_num(got).abs().sum() == 11
+    assert torch.equal(cache.k8.view(torch.uint8), cache.v8.view(torch.uint8))
