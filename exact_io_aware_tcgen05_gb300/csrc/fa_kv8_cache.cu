@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = i * kRows + lane / kLanes;
-            w[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(x + (t + r) * p.stride)) : make_uint4(0, 0, 0, 0);
+            w[i] = r < n ? *reinterpret_cast<const uint4*>(x + (t + r) * p.stride) : make_uint4(0, 0, 0, 0);
         }
         // amax of the finite values, as integers (the order of magnitudes): of pairs of 16-bit
         // ones, or one by one where there is an infinity or NaN to leave out

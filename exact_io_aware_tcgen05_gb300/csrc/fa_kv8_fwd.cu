@@ -214,11 +214,11 @@ __device__ __noinline__ uint32_t find_nan(const Kv8FwdParams& p, const Part& par
             j = part.all_hi;   // seen by all: the product has it
             continue;
         }
-        const int id = __ldg(p.table + static_cast<long long>(part.b) * p.width + (j >> p.page_log2));
+        const int id = p.table[static_cast<long long>(part.b) * p.width + (j >> p.page_log2)];
         if (id < 0 || id >= p.num_pages) continue;
         const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
                             (j & ((1 << p.page_log2) - 1));
-        if ((__ldg(p.v8 + r * D + channel) & 0x7f) != 0x7f) continue;
+        if ((p.v8[r * D + channel] & 0x7f) != 0x7f) continue;
         for (int n = 0; n < 8; ++n) {
             const int rp = sm.row_pos[buf][n0 + n];
             if (j <= rp && (p.seq.window <= 0 || rp - j < p.seq.window)) spoilt |= 1u << n;
@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                     const int head = part.h * G + n - tok * G;
                     w[i] = make_uint4(0, 0, 0, 0);
                     if (n < rows)
-                        w[i] = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8));
+                        w[i] = *reinterpret_cast<const uint4*>(
+                            static_cast<const uint16_t*>(p.q) + token * p.q_stride + head * D + sub * 8);
                     if (sub == 0) {
                         sm.row_pos[buf][n] = n < rows ? part.req.len - part.req.n + tok : INT_MIN;
                         sm.out_at[buf][n] = (token * p.seq.Hq + head) * D;

@@ -138,8 +138,8 @@ __device__ __noinline__ void cut_rows(const Kv8FwdParams& p, int& next, float* q
             const int more = small_div(rem0 + r2, G, p.group_inv);
             const int head = h * G + rem0 + r2 - more * G;
             const long long token = start + tok0 + more;
-            w2 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + token * p.q_stride +
-                                                      head * D + sub * 8));
+            w2 = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + token * p.q_stride +
+                                                 head * D + sub * 8);
         }
         if (r >= 0) {
             const float scale = cut_queries<D, E, K::kQ>(
@@ -163,13 +163,13 @@ __device__ __noinline__ void spoil_row(const Kv8FwdParams& p, const Part& part, 
             j = part.all_hi;   // seen by all: the product has it
             continue;
         }
-        const int id = __ldg(p.table + static_cast<long long>(part.b) * p.width + (j >> p.page_log2));
+        const int id = p.table[static_cast<long long>(part.b) * p.width + (j >> p.page_log2)];
         if (id < 0 || id >= p.num_pages) continue;
         const long long r = ((static_cast<long long>(id) * p.seq.Hkv + part.h) << p.page_log2) +
                             (j & ((1 << p.page_log2) - 1));
 #pragma unroll 1
         for (int c = 0; c < D; ++c) {
-            if ((__ldg(p.v8 + r * D + c) & 0x7f) != 0x7f) continue;
+            if ((p.v8[r * D + c] & 0x7f) != 0x7f) continue;
             if (out) out[c] = 0x7fff;   // a NaN of either type
             else partial[c] = __uint_as_float(0x7fc00000u);
         }

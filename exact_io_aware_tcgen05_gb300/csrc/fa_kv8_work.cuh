@@ -49,11 +49,20 @@ struct Request {
     int len;        // tokens in the cache, the new ones among them
 };
 
+// (As seq_bounds of fa_seq.cuh.  These kernels begin while the ones before them, which write
+// lengths, bounds, table, cache and queries, may be running, so they read nothing through the
+// read-only path, which is for data that nobody writes while a kernel lives.)
 __device__ __forceinline__ Request load_request(const Kv8FwdParams& p, int b) {
     Request r;
-    seq_bounds(p.seq, b, r.start, r.n);
+    if (p.seq.cu_seqlens) {
+        r.start = min(max(p.seq.cu_seqlens[b], 0), p.seq.total_tokens);
+        r.n = min(max(p.seq.cu_seqlens[b + 1], r.start), p.seq.total_tokens) - r.start;
+    } else {
+        r.start = b * p.seq.N;
+        r.n = p.seq.N;
+    }
     const long long room = static_cast<long long>(p.width) << p.page_log2;
-    r.len = static_cast<int>(min(max(static_cast<long long>(__ldg(p.lens + b)), 0LL), room));
+    r.len = static_cast<int>(min(max(static_cast<long long>(p.lens[b]), 0LL), room));
     return r;
 }
 
@@ -549,7 +558,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
         const int last_page = min((lim + page - 1) >> p.page_log2, p.width);
         // the table's entries, 32 at a time, the next ones on their way
         int base = part.tile0 * per_tile;
-        auto entry = [&](int i) { return i < last_page ? __ldg(row + i) : -1; };
+        auto entry = [&](int i) { return i < last_page ? row[i] : -1; };
         int cur = more ? entry(base + lane) : -1;
         int nxt = more ? entry(base + 32 + lane) : -1;
         if (np >= kParts)

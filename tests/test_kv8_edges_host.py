@@ -110,3 +110,17 @@ def test_a_step_without_tokens(lib):
     for name in ("k8", "k_scale", "v8", "v_scale", "table", "lens"):
         assert fwd(**{name: None}) == 1
     assert fwd(total_tokens=1) == 1 and fwd(page=24) == 2 and fwd(q_stride=516) == 1
+
+
+def test_kernels_that_begin_early_read_nothing_as_constant():
+    """These kernels are launched while the ones before them, which write what they read, may still
+    run.  The read-only path (__ldg, and what the compiler makes of const __restrict__) is for data
+    that nothing writes while a kernel lives."""
+    import os
+    import re
+    import exact_io_aware_tcgen05_gb300 as fa
+    csrc = os.path.join(os.path.dirname(fa.__file__), "csrc")
+    for name in ("fa_kv8_work.cuh", "fa_kv8_cache.cu", "fa_kv8_fwd.cu", "fa_kv8_rows.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//.*", "", f.read())
+        assert not re.search(r"__ldg|__restrict__|\.nc\b|ld\.global\.nc|\bseq_bounds\s*\(", code), name
