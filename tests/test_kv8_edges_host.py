@@ -124,3 +124,31 @@ def test_kernels_that_begin_early_read_nothing_as_constant():
         with open(os.path.join(csrc, name)) as f:
             code = re.sub(r"//.*", "", f.read())
         assert not re.search(r"__ldg|__restrict__|\.nc\b|ld\.global\.nc|\bseq_bounds\s*\(", code), name
+
+
+@pytest.mark.parametrize("over", [dict(tokens=2 ** 32 + 3), dict(tokens=2 ** 31), dict(page=2 ** 32 + 16),
+                                  dict(tokens=-2 ** 32)])
+def test_plan_refuses_numbers_beyond_32_bits(lib, over):
+    import torch
+    i32 = dict(dtype=torch.int32)
+    args = dict(page=16, tokens=3) | over
+    with pytest.raises(ValueError, match="32 bits"):
+        lib.kv8_plan(torch.zeros(2, **i32), torch.zeros(2, **i32), torch.zeros(2, 4, **i32), torch.zeros(8, **i32),
+                     torch.zeros(3, **i32), **args)
+
+
+@pytest.mark.parametrize("over", [dict(window=2 ** 32 + 1), dict(window=2 ** 31), dict(window=-2 ** 32),
+                                  dict(max_seqlen=2 ** 32 + 1), dict(max_seqlen=2 ** 31)])
+def test_attention_refuses_numbers_beyond_32_bits(lib, over):
+    """(A window of 2^32 + 1 would be one of 1.)"""
+    import torch
+    kw = dict(cu_seqlens=torch.tensor([0, 2, 5], dtype=torch.int32), max_seqlen=3) | over
+    args = _q(5, 4, 64), lib.kv8_cache(4, 2, 64, page=16, device="cpu")
+    tables = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits" if "window" in over else "32 bits|device"):
+        lib.attention_forward_kv8(*args, *tables, **kw)
+    assert lib._c_int("window", 2 ** 31 - 1) == 2 ** 31 - 1
+    with pytest.raises(ValueError, match="32 bits"):
+        lib._c_int("window", 2 ** 31)
+    with pytest.raises(TypeError):
+        lib._c_int("window", 7.5)
