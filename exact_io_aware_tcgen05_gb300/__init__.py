@@ -15,7 +15,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import operator
 import os
 
 __all__ = [
@@ -597,12 +596,14 @@ def _kv8_shape(cache, device):
 _ONE_DEVICE = "all tensors must be on one CUDA device"
 
 
-def _c_int(name, x):
-    """x as an int that a C int holds (ctypes would take its lowest 32 bits without a word)."""
-    x = operator.index(x)
-    if not -2 ** 31 <= x < 2 ** 31:
-        raise ValueError(f"{name} must fit 32 bits, got {x}")
-    return x
+def _beyond(**numbers):
+    """The error for whole numbers that a C int does not hold (ctypes would take their lowest 32
+    bits without a word)."""
+    wrong = [f"{name} = {x}" for name, x in numbers.items() if not -_INT <= x < _INT]
+    return ValueError(f"{', '.join(wrong)} must fit 32 bits")
+
+
+_INT = 2 ** 31
 
 
 def _int32(name, x, shape, device):
@@ -665,8 +666,9 @@ def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
     import torch
     if lens.dim() != 1 or table.dim() != 2 or ring.dim() != 1:
         raise ValueError("lens must be [B], table [B, width], ring [num_pages]")
-    B, width = lens.shape[0], _c_int("width", table.shape[1])
-    page, tokens = _c_int("page", page), _c_int("tokens", int(tokens))
+    B, width, num_pages, tokens = lens.shape[0], table.shape[1], ring.shape[0], int(tokens)
+    if not (-_INT <= tokens < _INT and -_INT <= page < _INT and width < _INT and num_pages < _INT):
+        raise _beyond(tokens=tokens, page=page, width=width, num_pages=num_pages)
     if tokens < 0:
         raise ValueError(f"tokens must be >= 0, got {tokens}")
     _int32("lens", lens, (B,), dev)
@@ -680,7 +682,7 @@ def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):
     slots = empty(tokens, dtype=int32, device=device)
     state_out = empty(3, dtype=int32, device=device)
     _check(load().fa_kv8_plan(lens.data_ptr(), grow.data_ptr(), B, table.data_ptr(), width,
-                              ring.data_ptr(), _c_int("num_pages", ring.shape[0]), page, state.data_ptr(),
+                              ring.data_ptr(), num_pages, page, state.data_ptr(),
                               lens_out.data_ptr(), cu.data_ptr(), slots.data_ptr(), tokens,
                               state_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
     return lens_out, cu, slots, state_out
@@ -739,7 +741,7 @@ def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, windo
         raise ValueError("lens must be [B], table [B, width]")
     Hq, d = shape[-2], shape[-1]
     stride = _rows("q", q, Hq, d)
-    B, width, window = lens.shape[0], _c_int("width", table.shape[1]), _c_int("window", window)
+    B, width = lens.shape[0], table.shape[1]
     _int32("lens", lens, (B,), dev)
     _int32("table", table, (B, width), dev)
     num_pages, Hkv, page, dk = _kv8_shape(cache, dev)
@@ -749,11 +751,13 @@ def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, windo
         if max_seqlen is None:
             raise ValueError("packed batches need max_seqlen")
         _int32("cu_seqlens", cu_seqlens, (B + 1,), dev)
-        N, T, lse_shape = _c_int("max_seqlen", int(max_seqlen)), _c_int("tokens", shape[0]), (Hq, shape[0])
+        N, T, lse_shape = int(max_seqlen), shape[0], (Hq, shape[0])
     else:
         if shape[0] != B:
             raise ValueError(f"q has {shape[0]} requests, lens {B}")
-        N, T, lse_shape = _c_int("N", shape[1]), 0, (B, Hq, shape[1])
+        N, T, lse_shape = shape[1], 0, (B, Hq, shape[1])
+    if not (-_INT <= window < _INT and -_INT <= N < _INT and T < _INT and width < _INT):
+        raise _beyond(window=window, max_seqlen=N, tokens=T, width=width)
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
     elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
