@@ -203,3 +203,80 @@ def test_append_of_infinities_to_a_block_of_any_scale(fa):
     assert torch.isnan(got).nonzero().tolist() == [[1, 2], [2, 3], [2, 4]]
     assert got[0, 1] == 10 and got[2, 5] == -1 and torch.nan_to_num(got).abs().sum() == 11
     assert torch.equal(cache.k8.view(torch.uint8), cache.v8.view(torch.uint8))
+
+
+# --------------------------------------------------------------------- hidden values
+
+import test_kv8_gpu as base   # noqa: E402  (its cases, with a comparison that a NaN fails)
+
+
+@pytest.mark.parametrize("case", base.CASES, ids=[str(i) for i in range(len(base.CASES))])
+def test_no_nan_of_a_free_place_comes_out(fa, case):
+    lens, new, Hq, Hkv, d, page, dtype, causal, window = case
+    c = r64.make(8, lens, new, Hq, Hkv, d, page, dtype, spread=1.0)
+    r64.close(c, *r64.run(fa, c, causal=causal, window=window), r64.attend(c, causal=causal, window=window))
+
+
+NAN_CASES = [
+    # (lens, new, Hq, Hkv, d, page, dtype, causal, window): up to 8, 16 and 128 rows, whole and split items
+    ([300, 77], [4, 2], 4, 2, 128, 64, "bf16", True, 0),
+    ([300, 77], [4, 2], 4, 2, 64, 16, "f16", True, 0),
+    ([4000], [4], 4, 2, 128, 128, "bf16", True, 0),
+    ([300, 77], [7, 3], 2, 2, 128, 32, "f16", True, 40),
+    ([300, 200], [6, 8], 2, 2, 64, 32, "bf16", True, 3),
+    ([300, 77], [4, 4], 8, 2, 128, 64, "bf16", True, 0),
+    ([9000], [2], 16, 2, 64, 64, "f16", True, 0),
+    ([300, 600], [5, 15], 2, 2, 128, 16, "bf16", True, 130),
+    ([300, 77], [4, 2], 4, 2, 128, 64, "bf16", False, 0),
+    ([300, 77], [20, 77], 4, 2, 128, 64, "f16", True, 0),
+    ([300, 77], [20, 77], 4, 2, 64, 32, "f16", True, 40),
+    ([3000, 700], [140, 40], 4, 2, 64, 64, "f16", True, 0),
+    ([3000, 700], [140, 40], 4, 2, 128, 128, "bf16", True, 200),
+    ([300, 77], [50, 77], 4, 2, 128, 16, "f16", False, 0),
+]
+
+
+@pytest.mark.parametrize("case", NAN_CASES, ids=[str(i) for i in range(len(NAN_CASES))])
+def test_nan_reaches_the_rows_that_see_it(fa, case):
+    """NaN codes among the values of some tokens: those channels of the rows that see them, of that
+    head's queries, and nothing else; among the keys: those rows."""
+    import torch
+    lens, new, Hq, Hkv, d, page, dtype, causal, window = case
+    c = r64.make(9, lens, new, Hq, Hkv, d, page, dtype, spread=1.0)
+    kw = dict(causal=causal, window=window)
+    clean = r64.run(fa, c, **kw)
+    r64.close(c, *clean, r64.attend(c, **kw))
+    spots = []                                             # (request, token, key/value head, channel)
+    for b, (n, m) in enumerate(zip(lens, new)):
+        first = n - m
+        for i, j in enumerate({n - 1, n - 2, max(first, 0), max(first - window + 2, 0), n // 2, 0}):
+            spots.append((b, j, i % Hkv, (37 * i + 5) % d))
+    cu = c["cu"].tolist()
+
+    def sees(b, j):
+        pos = torch.arange(lens[b] - new[b], lens[b], device="cuda")
+        see = torch.full_like(pos, j < lens[b], dtype=torch.bool)
+        if causal:
+            see = see & (j <= pos)
+        if window:
+            see = see & (pos - j < window)
+        return see
+
+    G = Hq // Hkv
+    for side in (2, 0):                                    # values, then keys
+        cache = list(c["cache"])
+        cache[side] = codes = cache[side].view(torch.uint8).clone()
+        want = torch.zeros(c["q"].shape, dtype=torch.bool, device="cuda")
+        for b, j, h, ch in spots:
+            codes[int(c["table"][b, j // page]), h, j % page, ch] = 127 if j % 2 else 255
+            for g in range(h * G, h * G + G):
+                want[cu[b]:cu[b + 1], g, ch if side else slice(None)] |= sees(b, j) if side else sees(b, j)[:, None]
+        cache[side] = codes.view(torch.float8_e4m3fn)
+        o, lse = r64.run(fa, c | dict(cache=tuple(cache)), **kw)
+        assert torch.equal(torch.isnan(o), want)
+        assert torch.equal(o[~want], clean[0][~want])
+        if side:
+            assert torch.equal(lse, clean[1])
+        else:
+            assert torch.equal(torch.isnan(lse), want[..., 0].T)
+            assert torch.equal(lse[~want[..., 0].T], clean[1][~want[..., 0].T])
