@@ -17,14 +17,21 @@
 // than a code, so each goes in as a sum of codes:
 //   q   each row times a power of two, so that its largest element is in (224, 448], as 2
 //       (bf16) or 3 (fp16) e4m3 pieces of 4 bits, each piece the rounding of what the ones
-//       before it left: exact down to 2^-18 of the row's largest element;
+//       before it left.  The last piece's least step is 2^-9, so an element whose last bit is
+//       2^-9 or more is exact (elements of 2^-2 or more for bf16's 8 bits, of 2 or more for
+//       fp16's 11), and a smaller one is off by 2^-10 at most, 2^-17.8 of the row's largest;
 //   P   as fp16 (11 bits), cut into e5m2 pieces of 3 bits (the high byte of an fp16 number
 //       is an e5m2 number): 3 pieces for bf16 outputs, the last one rounded (9 bits, one
 //       more than bf16 holds), 4 for fp16 (all 11).  e5m2 rather than e4m3 because long
 //       contexts need its range: weights are kept down to 2^-28 of the largest.
 // V's scale joins the exponent: with t_j = s_j + log2(v_scale_j) and M the running maximum
 // of t (or a little less, see kGrow), the weights 2^(t_j - M) are near 1 at most whatever the
-// scales, and the sum of the probabilities is that of 2^(t_j - M) / v_scale_j.
+// scales, and the sum of the probabilities is that of 2^(t_j - M) / v_scale_j.  In 32 bits that
+// bounds V's scales.  With R = log2(largest / least scale), a key whose t is 123 or more below
+// the largest (as far as a weight, or the factor that moves a reference, stays a normal number)
+// has at most 2^(R - 123) of the probability of the key with the largest, so n such keys are
+// nothing beside it (2^-24) up to R = 99 - log2(n); and a sum of n weights of up to 2^15 over
+// scales of 2^-80 or more stays below 2^(95 + log2(n)).
 //
 // Work split.  The key tiles of all items (request, key/value head, C rows) lie one behind
 // the other and every CTA, two per SM, takes an equal share of them (kItemCost more tiles
@@ -47,12 +54,17 @@
 //
 // Measured (one GB300; bytes of the codes and scales that are seen): 2 requests of 131072 tokens
 // (Hkv 16, d = 128) 163 us, 97 % of the measured copy rate; 64 requests of up to 8192 (Hkv 8)
-// 78 us, 84 %; 128 of up to 2048 at d = 64, fp16, pages of 16, 41 us, 36 %; one request of 1000
-// 10 us.  Long contexts are bound by the cache's bytes.  Short ones are bound by a tile's and an
-// item's instructions in the warps that handle them, at d = 64 twice as many for each byte: the
-// producer has some 2000 cycles of work a tile (fa_kv8_work.cuh), the softmax 1700, and an
-// item's start and end 5000.  A third CTA per SM (80 registers a thread) took 59 us in place of
-// 44 there, items of 32 rows in this kernel more than the 128-row kernel for the same rows.
+// 79 us, 84 %; 128 of up to 2048 at d = 64, fp16, pages of 16, 41 us, 36 %; one request of 1000
+// 10 us on the GPU, 24 to 32 for the whole call from Python, whose host side is the longer one.
+// With 16 rows in place of 8 a tile's softmax takes twice the instructions and keeps some 50
+// bytes a thread in local memory: 64 requests of up to 8192 with 16 heads a group 93 us (60 % of
+// the measured copy rate; 67 us, 79 %, with 8 heads; 113 us with 17, in the 128-row kernel), 128
+// of up to 2048 at d = 64, fp16, 69 us (40 with 8).  Long contexts are bound by the cache's bytes.
+// Short ones are bound by a tile's and an item's instructions in the warps that handle them, at
+// d = 64 twice as many for each byte: the producer has some 2000 cycles of work a tile
+// (fa_kv8_work.cuh), the softmax 1700, and an item's start and end 5000.  A third CTA per SM (80
+// registers a thread) took 59 us in place of 44 there, items of 32 rows in this kernel more than
+// the 128-row kernel for the same rows.
 // One request: two launches, the search for the shares, one item's chain and the join.
 #include "fa_kv8_work.cuh"
 

@@ -339,6 +339,7 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  *   k8, v8            device, e4m3 [num_pages, Hkv, page, d]
  *   k_scale, v_scale  device, fp32 [num_pages, Hkv, page / 16]: one per block of 16
  *                     tokens and head, positive and finite; a value is code * scale.
+ *                     (V's have bounds in fa_fwd_kv8, below.)
  *   table             device, int32 [B, width]: page k of request b holds its tokens
  *                     k page .. k page + page - 1.  Entries past a request's tokens are
  *                     not used and may hold anything, and so may the cache's bytes and
@@ -394,8 +395,17 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  * they were.  A table entry outside 0 .. num_pages - 1 hides its page's tokens.  A value
  * in a place hidden from a row (NaN included) does not reach that row.
  * N must be >= the most new tokens of a request (what the rows of a request's further tokens
- * then hold is not defined).  The scores use the codes and q unrounded.  The probabilities are rounded to
- * 11 bits, or to 9 for bf16 where N * Hq / Hkv <= 16.
+ * then hold is not defined).
+ * Besides 32-bit sums, exponentials and O itself, these are rounded:
+ *   q              an element is held to 2^-17 of its row's largest, exactly from 2^-9 (bf16) or
+ *                  2^-6 (fp16) of that one on
+ *   probabilities  to 11 bits, or to 9 for bf16 where N * Hq / Hkv <= 16; for O a key counts as
+ *                  nothing where its probability times V's scale is below 2^-28 of the row's
+ *                  largest such product
+ * V's scales must be 2^-80 or more where a request's tokens are, and its largest no more than
+ * 2^99 / lens[b] times its least; beyond that the sum of the probabilities, and with it O and
+ * LSE, may miss keys or overflow.  fa_kv8_append's are never below 2^-64, so what it writes is
+ * within this as long as no value exceeds 2^43 / lens[b] (8e6 for a million tokens).
  *   workspace    device, >= fa_fwd_kv8_workspace_size(...) bytes, 256-byte aligned,
  *                contents ignored; not to be shared by calls in flight together
  *                (calls captured into graphs that replay at the same time among them)
@@ -517,7 +527,8 @@ void fa_set_launch_events(const cudaEvent_t* events, int count);
  * Bounds-checking build.  The library built with FA_DEBUG_CHECKS defined
  * (exact_io_aware_tcgen05_gb300.build.build(debug=True), libfa_gb300_debug.so)
  * checks, inside every kernel, each computed global index and TMA store box
- * against its tensor; a failing check skips the access and records device
+ * against its tensor (in the paged cache's kernels, the rows of O and LSE only);
+ * a failing check skips the access and records device
  * status 7, which fa_device_status() reports as FA_ERR_CUDA with a message.
  * Nothing traps.  (A stand-in for a memory checker; the kernels are otherwise
  * identical.)

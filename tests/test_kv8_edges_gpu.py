@@ -280,3 +280,63 @@ def test_nan_reaches_the_rows_that_see_it(fa, case):
         else:
             assert torch.equal(torch.isnan(lse), want[..., 0].T)
             assert torch.equal(lse[~want[..., 0].T], clean[1][~want[..., 0].T])
+
+
+# ------------------------------------------------------- ranges that the header states
+
+ROWS = [(2, 4), (8, 2), (4, 20)]        # (heads a group, new tokens): up to 8, 16 and 128 rows
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group,new", ROWS)
+def test_queries_with_one_large_element(fa, group, new, dtype):
+    """Elements of q far below the row's largest, and keys that are small where that one is: an
+    element is held to 2^-17 of the largest."""
+    import torch
+    for large in (2.0 ** 10, 2.0 ** 13):
+        c = r64.make(10, [700, 90], [new, new], group * 2, 2, 128, 64, dtype)
+        c["q"][..., 7] = torch.where(torch.rand(c["q"].shape[:2], device="cuda") < 0.7, large, 1.0).to(c["q"].dtype)
+        k8 = c["cache"][0].view(torch.uint8)
+        k8[..., 7] = torch.where(k8[..., 7] & 127 == 127, k8[..., 7], 0)
+        r64.close(c, *r64.run(fa, c), r64.attend(c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("n", [200, 8192])
+@pytest.mark.parametrize("first", [True, False])
+def test_value_scales_far_apart(fa, first, n, group, new, dtype):
+    """Blocks of values 2^99 / tokens apart, scores that are about the same: every key counts in the
+    sum of the probabilities, wherever the large ones are (the first half of the blocks, every other
+    one, and the last)."""
+    import torch
+    far = 99 - (n - 1).bit_length()
+    for low in (-64, -80, 0):
+        high = low + far
+        if high > 120 or dtype == "f16" and high > 4:
+            high = 4 if dtype == "f16" else 120
+            low = high - far
+            if low < -80:
+                low = -80
+        c = r64.make(11, [n], [new], group, 1, 64, 16, dtype)
+        vs = c["cache"][3]
+        blocks = c["table"][0, :-(-n // 16)].long()
+        half = torch.zeros(len(blocks), dtype=torch.bool)
+        if first:
+            half[:len(half) // 2] = True
+        else:
+            half[1::2] = True
+        half[-1] = not first
+        vs[blocks, 0, 0] = torch.where(half.cuda(), 2.0 ** high, 2.0 ** low)
+        if low == -64 and first:                           # blocks of zeros, as kv8_append writes them
+            c["cache"][2].view(torch.uint8)[blocks[~half]] = 0
+        c["q"] *= 0.25
+        r64.close(c, *r64.run(fa, c), r64.attend(c))
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("exponent", [-80, -64, 0, 100])
+def test_value_scales_at_their_bounds(fa, exponent, group, new):
+    c = r64.make(12, [3000, 40], [new, new], group * 2, 2, 128, 32, "bf16")
+    c["cache"][3].mul_(2.0 ** 7 * 2.0 ** exponent)
+    r64.close(c, *r64.run(fa, c), r64.attend(c))
