@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         };
         // A shared-memory access by the issuing warp holds back the products that follow, so
         // within a part it meets only named barriers: the warps of the values come to each
-        // half's barrier once those and (the second half's) the next tile's keys are there.
+        // half's barrier once those and (the second half's) the next tile's keys are there, and
+        // give the part's queries free once its first keys are.
         // Step T: the products of tile T's halves (none for T = -1), then S of tile T + 1.
         bool more = advance(), fresh = true;
 #pragma unroll 1
@@ -288,11 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             }
             if (lane == 0) {
                 const int it = 4 * T + 4, st = it % kSlots;   // the keys' two slots are neighbours
-                if (first) {
-                    wait(&sm.q_full, np);
-                    wait(&sm.kv_full[st], it / kSlots);
-                    wait(&sm.kv_full[st + 1], it / kSlots);
-                }
+                if (first) wait(&sm.q_full, np);   // (the part's first keys too)
                 tc_fence_after();
                 const uint64_t kd = k0 + static_cast<uint64_t>((st * K::kSlotBytes) >> 4);
 #pragma unroll
@@ -327,6 +324,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
             if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
             if (np > 0) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty, np - 1));
             cut_rows<D, E>(p, sm.q_next, sm.q_scale, sQ, part.req.start, part.req.n, part.h, part.row0);
+            // All keys are waited for here, tile after tile, so that no wait can take an older phase
+            // of their place for theirs (it looks at the parity; the first keys may land behind the
+            // first values, so having those is not enough), and before S gives the place back.
+            auto keys = [&](int ik) {
+                return __all_sync(0xffffffffu, wait(&sm.kv_full[ik % kSlots], ik / kSlots) &&
+                                                   wait(&sm.kv_full[ik % kSlots + 1], ik / kSlots));
+            };
+            if (ok) ok = keys(4 * T);
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&sm.q_full));
             // Values: a unit of 16 codes becomes two of 8 fp16 numbers.  A key's D / 16 units
@@ -415,11 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                     fence_proxy_async_smem();
                     named_bar_sync(kBarConv, 64);   // both warps have read the slot
                     if (t == 0) mbar_arrive(smem_addr(&sm.kv_empty[st]));
-                    if (half == 1 && i + 1 < part.tiles && ok) {   // the next tile's keys, for the issuer
-                        const int ik = 4 * T + 4;
-                        ok = __all_sync(0xffffffffu, wait(&sm.kv_full[ik % kSlots], ik / kSlots) &&
-                                                         wait(&sm.kv_full[ik % kSlots + 1], ik / kSlots));
-                    }
+                    if (half == 1 && i + 1 < part.tiles && ok) ok = keys(4 * T + 4);   // for the issuer
                     named_bar_signal(kBarP + half, 224, ok);
                 }
             }
