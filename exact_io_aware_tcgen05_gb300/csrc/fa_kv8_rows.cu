@@ -102,9 +102,19 @@ constexpr int rows_smem_bytes() {
     return rows_fixed_bytes<D, E>() + rows_slots<D, E>() * RowsCfg<D, E>::kSlotBytes;
 }
 
-constexpr int kBarP = 1;     // + half: weights and values there; softmax warps, values' warps, issuer
+// + half: weights and values there; softmax warps, values' warps, issuer.  Only the issuer waits
+// there (and a warp without rows).  The others come again once the issuer has been there, or they
+// would be counted twice: they wait for what it issued behind it, the softmax for a tile's scores,
+// the values' warps for the products of a half, after an abort too (it goes on issuing).
+constexpr int kBarP = 1;
 constexpr int kBarRows = 3;  // the softmax warps among themselves
 constexpr int kBarConv = 4;  // warps 2 and 3 among themselves
+
+// A wait, by a warp, for what the issuer commits in any case.
+__device__ __forceinline__ void wait_for_issuer(uint64_t* bar, int phase) {
+    if (!mbar_try_wait(smem_addr(bar), phase & 1)) drain_on(smem_addr(bar), phase & 1);
+    __syncwarp();
+}
 
 // Four e4m3 codes to fp16 (exact; NaN stays NaN).
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -366,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                 for (int half = 0; half < 2; ++half) {
                     const int it = 4 * T + 2 + half, st = it % kSlots;
                     if (ok) ok = __all_sync(0xffffffffu, wait(&sm.kv_full[st], it / kSlots));
-                    // the place's last values have been multiplied
+                    // the place's last values have been multiplied (see there, kBarP)
                     const int o = K::kV16Bufs == 2 ? half : half ^ 1, use = K::kV16Bufs == 2 || half == 0 ? T - 1 : T;
-                    if (ok && use >= 0) ok = __all_sync(0xffffffffu, wait(&sm.o_half[o], use));
+                    if (use >= 0) wait_for_issuer(&sm.o_half[o], use);
                     if (ok) {
                         uint8_t* src = sKV + st * K::kSlotBytes;
                         uint8_t* dst = sV + half % K::kV16Bufs * K::kV16Bytes + vu / 4 * K::kV16Chunk;
@@ -421,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                     named_bar_sync(kBarConv, 64);   // both warps have read the slot
                     if (t == 0) mbar_arrive(smem_addr(&sm.kv_empty[st]));
                     if (half == 1 && i + 1 < part.tiles && ok) ok = keys(4 * T + 4);   // for the issuer
-                    named_bar_signal(kBarP + half, 224, ok);
+                    named_bar_arrive(kBarP + half, 224);
                 }
             }
         }
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                     const int kb = kt + kHalf * half;
                     const float4* ready = &sm.ready[sc][4 * half];
                     const bool edge = absent || kb < part.all_lo || kb + kHalf - 1 > part.all_hi;
-                    if (ok && !idle && half == 0) ok = __all_sync(0xffffffffu, wait(&sm.s_full, T));
+                    if (!idle && half == 0) wait_for_issuer(&sm.s_full, T);
                     if (ok && !idle) {
                         tc_fence_after();
                         if (edge) {
@@ -562,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                         tmem_st_wait();
                         tc_fence_before();
                     }
-                    named_bar_signal(kBarP + half, 224, ok && !idle);
+                    named_bar_signal(kBarP + half, 224, !idle);
                 }
             }
             // ------------------------------------------------ the part's end

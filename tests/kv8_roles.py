@@ -14,7 +14,8 @@ twice at a barrier, roles that wait for one another for good.
   two products    the product barriers alternate by tile (narrow)
   first keys      the values' warps wait for a part's first keys too, before its queries (128 rows)
   queries' part   the queries' warp gives parts back, as the others do (narrow)
-  tile barriers   the barriers between values, softmax and issuer alternate by tile (128 rows)
+  issuer's waits  after an abort too, scores and products are waited for before a barrier's next turn
+                  (128 rows)
   abort seen      the producer looks at the abort flag once a place is free
 """
 from __future__ import annotations
@@ -106,12 +107,19 @@ class Cta:
         while bar.turn == turn:
             yield
 
-    def signal(self, name, count, who, live):
-        """Comes without waiting while all is well, and waits after an abort."""
-        if live:
-            self.meetings.setdefault(name, Meeting(count)).come(who)
+    def come_to_half(self, half, ok, who):
+        if ok or "issuer's waits" not in self.without:
+            self.meetings.setdefault(half, Meeting(3)).come(who)
         else:
-            yield from self.meet(name, count, who)
+            yield from self.meet(half, 3, who)
+
+    def wait_for_issuer(self, bar, phase, ok):
+        if "issuer's waits" in self.without:
+            return ok and (yield from self.wait(bar, phase))
+        yield from self.drain(bar, phase)
+        if bar.done != phase + 1:
+            raise Wrong("a wait passed for another phase")
+        return ok
 
     def take(self, np):
         yield from self.drain(self.part_full[np % PARTS], np // PARTS)
@@ -263,9 +271,6 @@ class Cta:
 
     # ------------------------------------------------------------------ 128 rows
 
-    def half(self, T, half):
-        return ("half", half, T % 2 if "tile barriers" not in self.without else 0)
-
     def rows_issuer(self):
         np, with_tiles, left, T, first = -1, -1, 0, -1, True
 
@@ -285,7 +290,7 @@ class Cta:
         while more or T >= 0:
             if T >= 0:
                 for half in range(2):
-                    yield from self.meet(self.half(T, half), 3, "issuer")
+                    yield from self.meet(half, 3, "issuer")
                     self.queue.append(("product", 2 * T + half))
                     self.commit(self.product[half])
                 if not more:
@@ -326,8 +331,8 @@ class Cta:
                     n = 4 * T + 2 + half
                     if ok:
                         ok = yield from self.wait(*self.unit(n))
-                    if ok and T > 0:
-                        ok = yield from self.wait(self.product[half], T - 1)
+                    if T > 0:
+                        ok = yield from self.wait_for_issuer(self.product[half], T - 1, ok)
                     if ok:
                         self.use(n)
                     self.empty[n % self.slots].arrive()
@@ -335,7 +340,7 @@ class Cta:
                         for m in (4 * T + 4, 4 * T + 5):
                             if ok:
                                 ok = yield from self.wait(*self.unit(m))
-                    yield from self.signal(self.half(T, half), 3, "values", ok)
+                    yield from self.come_to_half(half, ok, "values")
                 T += 1
 
     def rows_softmax(self):
@@ -351,9 +356,9 @@ class Cta:
                 cut += 1
             for _ in range(tiles):
                 for half in range(2):
-                    if ok and half == 0:
-                        ok = yield from self.wait(self.s_full[0], T)
-                    yield from self.signal(self.half(T, half), 3, "softmax", ok)
+                    if half == 0:
+                        ok = yield from self.wait_for_issuer(self.s_full[0], T, ok)
+                    yield from self.come_to_half(half, ok, "softmax")
                     yield
                 T += 1
             if ok and tiles:

@@ -17,9 +17,10 @@ NEEDED = [
     ("rows", "empty parts", "stuck", dict(empty=True, slots=(4,))),
     ("narrow", "two products", "a wait passed for an older phase", {}),
     ("rows", "first keys", "a wait passed for an older phase", dict(slots=(4,))),
+    ("rows", "issuer's waits", "twice at a barrier", dict(abort=True)),
 ]
 
 
 @pytest.mark.parametrize("kind,what,wrong,kw", NEEDED, ids=[f"{n[0]}-{n[1]}" for n in NEEDED])
 def test_what_goes_wrong_without(kind, what, wrong, kw):
-    assert roles.outcomes(kind, 60, what, **kw).get(wrong, 0) > 0
+    assert roles.outcomes(kind, 120, what, **kw).get(wrong, 0) > 0
