@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_addr(&sm.scales_full[i]), 32);
         for (int i = 0; i < kParts; ++i) {
             mbar_init(smem_addr(&sm.part_full[i]), 1);
-            mbar_init(smem_addr(&sm.part_empty[i]), 6);   // the issuer, the relay, 4 softmax warps
+            mbar_init(smem_addr(&sm.part_empty[i]), 7);   // every warp but the producer
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sm.q_full[i]), 32);
@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 #pragma unroll 1
         for (int np = 0; take(np, part); ++np) {
             const int buf = np & 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[np % kParts]));
             if (np >= 2) ok = __all_sync(0xffffffffu, ok && wait(&sm.q_empty[buf], (np >> 1) - 1));
             if (ok) {
                 uint8_t* dst = sQ + buf * K::kQBytes;

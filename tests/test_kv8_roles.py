@@ -18,6 +18,7 @@ NEEDED = [
     ("narrow", "two products", "a wait passed for an older phase", {}),
     ("rows", "first keys", "a wait passed for an older phase", dict(slots=(4,))),
     ("rows", "issuer's waits", "twice at a barrier", dict(abort=True)),
+    ("narrow", "queries' part", "stuck", dict(abort=True)),
 ]
 
 
