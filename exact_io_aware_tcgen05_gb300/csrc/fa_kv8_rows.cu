@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                     }
                     fence_proxy_async_smem();
                     named_bar_sync(kBarConv, 64);   // both warps have read the slot
-                    if (t == 0) mbar_arrive(smem_addr(&sm.kv_empty[st]));
+                    if (t == 0 && ok) mbar_arrive(smem_addr(&sm.kv_empty[st]));   // (its copy has landed)
                     if (half == 1 && i + 1 < part.tiles && ok) ok = keys(4 * T + 4);   // for the issuer
                     named_bar_arrive(kBarP + half, 224);
                 }

@@ -456,7 +456,7 @@ static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volat
             : "=r"(done)
             : "r"(bar), "r"(parity), "r"(500u)
             : "memory");
-        if (done) return true;
+        if (done) return *abort == 0;   // (produce: a place given back for an abort is not free)
         if (*abort) return false;
         if (clock64() - t0 > limit) {
             *abort = 1;
@@ -599,7 +599,15 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
 #pragma unroll 1
             for (int unit = 0; unit < 2 * kUnits; ++unit) {
                 if (use > 0) {
-                    ok = __all_sync(0xffffffffu, wait_for(p, sm, &sm.kv_empty[slot], use - 1));
+                    // After an abort the issuer gives places back whatever became of their copies,
+                    // and nothing may be copied to one that has a copy on its way.  (Both loads are on
+                    // their way together; the abort comes long before a place given back for it.)
+                    const int abort = *const_cast<volatile int*>(&sm.abort);
+                    const uint32_t bar = smem_addr(&sm.kv_empty[slot]);
+                    const int phase = (use - 1) & 1;
+                    ok = mbar_try_wait(bar, phase) ? abort == 0
+                                                   : wait_on(bar, phase, &sm.abort, p.timeout_cycles, p.status);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
                 const uint32_t full = smem_addr(&sm.kv_full[slot]);

@@ -340,3 +340,27 @@ def test_value_scales_at_their_bounds(fa, exponent, group, new):
     c = r64.make(12, [3000, 40], [new, new], group * 2, 2, 128, 32, "bf16")
     c["cache"][3].mul_(2.0 ** 7 * 2.0 ** exponent)
     r64.close(c, *r64.run(fa, c), r64.attend(c))
+
+
+# ------------------------------------------------------------------------ timeouts
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_waits_that_run_out_over_many_short_items(fa, dtype, group, new):
+    """Waits that give up, at once or later, in CTAs of some hundred items of a tile or two, requests
+    without keys among them: the kernels end, and the next call is right."""
+    import torch
+    lens = [100, 200, 0, 30, 129, 0, 0, 64] * 500
+    c = r64.make(13, lens, [min(new, max(n, 1)) for n in lens], group * 8, 8, 64, 16, dtype)
+    want = r64.run(fa, c)
+    args = c["q"], fa.Kv8Cache(c["cache"]), c["table"], c["lens"]
+    for limit in (1, 300, 2000, 5000):
+        fa.fa_set_wait_limit_cycles(limit)
+        try:
+            fa.attention_forward_kv8(*args, cu_seqlens=c["cu"], max_seqlen=new)
+            status = fa.fa_device_status(check=False)
+        finally:
+            fa.fa_set_wait_limit_cycles(0)
+        assert status in (fa.FA_OK, fa.FA_ERR_TIMEOUT) and (limit > 1 or status == fa.FA_ERR_TIMEOUT)
+    got = r64.run(fa, c)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

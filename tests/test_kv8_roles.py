@@ -7,8 +7,9 @@ import kv8_roles as roles
 
 @pytest.mark.parametrize("kind", ["narrow", "rows"])
 @pytest.mark.parametrize("empty", [False, True])
-def test_every_schedule_ends_well(kind, empty):
-    assert roles.outcomes(kind, 400, empty=empty) == {"fine": 400}
+@pytest.mark.parametrize("abort", [False, True])
+def test_every_schedule_ends_well(kind, empty, abort):
+    assert roles.outcomes(kind, 400, empty=empty, abort=abort) == {"fine": 400}
 
 
 # what is left out, and what then goes wrong in some schedules
@@ -19,6 +20,8 @@ NEEDED = [
     ("rows", "first keys", "a wait passed for an older phase", dict(slots=(4,))),
     ("rows", "issuer's waits", "twice at a barrier", dict(abort=True)),
     ("narrow", "queries' part", "stuck", dict(abort=True)),
+    ("narrow", "abort seen", "a copy into a place with a copy in flight", dict(abort=True)),
+    ("rows", "abort seen", "a copy into a place with a copy in flight", dict(abort=True)),
 ]
 
 
