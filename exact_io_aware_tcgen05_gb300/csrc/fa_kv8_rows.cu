@@ -20,8 +20,8 @@
 // during the second's softmax; P takes the place of the scores in TMEM.  Between a tile's
 // second half and the next tile's scores the SM's other CTA has the units to itself.
 //
-// Measured (one GB300, bf16, Hq 32, Hkv 8): 2048 new tokens over 16384 keys at d = 128 464 us,
-// 1110 TFLOP/s, 59 % of the measured bf16 rate; 16 whole prompts of up to 2048 at d = 64 232 us,
+// Measured (one GB300, bf16, Hq 32, Hkv 8): 2048 new tokens over 16384 keys at d = 128 463 us,
+// 1110 TFLOP/s, 59 % of the measured bf16 rate; 16 whole prompts of up to 2048 at d = 64 229 us,
 // twice what its exponentials and MMAs take.  Bound by the chain of a tile in its CTA (scores,
 // two halves of softmax of some 1000 cycles each, product), two CTAs deep: the tensor pipe is
 // active 48 % (d = 128) and the issue slots half used, so neither unit is the limit.  A softmax in
