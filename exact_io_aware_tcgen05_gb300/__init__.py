@@ -621,8 +621,10 @@ def _rows(name, x, heads, d):
     """Elements between the tokens of a [..., heads, d] tensor whose tokens are evenly spaced
     (a slice of a wider projection's output, say) and do not overlap (an expanded tensor's do)."""
     shape, strides = x.shape, x.stride()
-    ok = shape[-2] == heads and shape[-1] == d and strides[-1] == 1 and (heads == 1 or strides[-2] == d)
     n, outer = shape[-3], shape[0] if len(shape) == 4 else 1
+    ok = shape[-2] == heads and shape[-1] == d
+    if n * outer > 0:   # (an empty tensor's strides are anything)
+        ok = ok and strides[-1] == 1 and (heads == 1 or strides[-2] == d)
     if n * outer <= 1:
         stride = heads * d
     else:

@@ -66,6 +66,7 @@ def test_expanded_keys_and_values_are_refused(lib, side, monkeypatch):
     (lambda: _q(8, 4, 64)[3:4].expand(1, 4, 64), 256),
     (lambda: _q(0, 4, 64), 256),                            # no token
     (lambda: _q(3, 0, 4, 64), 256),
+    (lambda: _q(0).as_strided((0, 4, 64), (0, 0, 0)), 256),
 ])
 def test_distance_of_tokens(lib, make, stride):
     assert lib._rows("q", make(), 4, 64) == stride
