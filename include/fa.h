@@ -380,9 +380,10 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  * amax <= 448 2^k, the block's scale becomes 2^k where its first new token is the block's
  * first, and max(old scale, 2^k) where the block held tokens before; those are then
  * rounded again to the new scale, code = e4m3(code old / new).  A new code is
- * e4m3(x / scale), to nearest, ties to even.  Scales are powers of two, so the
- * divisions are exact, and so is the second rounding for codes that stay normal e4m3
- * numbers.  Infinities and NaN become NaN codes.
+ * e4m3(x / scale), to nearest, ties to even, rounded once.  (The scales made here are powers
+ * of two, and rounding to a larger one again is exact for codes that stay normal e4m3 numbers;
+ * a block begun by another writer may have any positive scale.)  Infinities and NaN become NaN
+ * codes.
  *
  * fa_fwd_kv8: O and LSE of the new tokens' attention over the cache.
  *   q            device, read: bf16 or fp16; dense [B, N, Hq, d] or packed [T, Hq, d],
