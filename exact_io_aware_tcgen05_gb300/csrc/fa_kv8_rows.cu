@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                 }
             }
             // ------------------------------------------------ the part's end
-            if (ok) ok = __all_sync(0xffffffffu, wait(&sm.o_half[1], T - 1));
+            wait_for_issuer(&sm.o_half[1], T - 1);   // (a warp may have no rows in the next part: kBarP)
             tc_fence_after();
             bool poison = false;
             if (part.tile0 * kKeys < part.all_lo || (part.tile0 + part.tiles) * kKeys - 1 > part.all_hi) {

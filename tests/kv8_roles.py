@@ -7,7 +7,8 @@ mbarrier looks at the parity of its last complete phase only, a named barrier co
 whoever they are from.  The warps of one role walk together here (their own barriers see to that).
 `run` returns what went wrong first: a wait that passed for an older phase, keys or values used before
 they landed or overwritten before they were read, a copy into a place with a copy in flight, a role
-twice at a barrier, roles that wait for one another for good.
+twice at a barrier, roles that wait for one another for good.  (With 128 rows there is a second warp
+of the softmax, `tail`, that has no rows in some parts.)
 
 `without` leaves out one of what the kernels do against these:
   empty parts     items whose rows see nothing are not handed out
@@ -16,6 +17,7 @@ twice at a barrier, roles that wait for one another for good.
   queries' part   the queries' warp gives parts back, as the others do (narrow)
   issuer's waits  after an abort too, scores and products are waited for before a barrier's next turn
                   (128 rows)
+  parts' ends     after an abort too, the softmax waits for a part's last product (128 rows)
   abort seen      the producer looks at the abort flag once a place is free
 """
 from __future__ import annotations
@@ -68,7 +70,8 @@ class Cta:
         self.parts = parts if "empty parts" in self.without else [p for p in parts if p]
         self.slots, self.abort_at, self.abort = slots, abort_at, False
         self.units = 1 if self.narrow else 2            # units of a tile's keys, and of its values
-        roles = 4 if self.narrow else 3                 # that give parts back
+        self.without_rows = [self.rng.random() < 0.4 for _ in parts]   # of the softmax's second warp
+        roles = 4                                       # that give parts back
         if "queries' part" in self.without and self.narrow:
             roles -= 1
         self.handed = [None] * PARTS
@@ -76,8 +79,8 @@ class Cta:
         self.part_empty = [Phases(roles) for _ in range(PARTS)]
         self.full = [Phases(1) for _ in range(slots)]
         self.empty = [Phases(1) for _ in range(slots)]
-        self.q_full = [Phases(1 if self.narrow else 2) for _ in range(2)]
-        self.q_empty = [Phases(2) for _ in range(2)]
+        self.q_full = [Phases(1 if self.narrow else 3) for _ in range(2)]
+        self.q_empty = [Phases(2 if self.narrow else 3) for _ in range(2)]
         self.s_full = [Phases(1), Phases(1)]
         self.product = [Phases(1), Phases(1)]           # of a tile (narrow) or of a half
         self.meetings, self.flight, self.queue = {}, [], []
@@ -107,11 +110,11 @@ class Cta:
         while bar.turn == turn:
             yield
 
-    def come_to_half(self, half, ok, who):
-        if ok or "issuer's waits" not in self.without:
-            self.meetings.setdefault(half, Meeting(3)).come(who)
+    def come_to_half(self, half, ok, who, idle=False):
+        if not idle and (ok or "issuer's waits" not in self.without):
+            self.meetings.setdefault(half, Meeting(4)).come(who)
         else:
-            yield from self.meet(half, 3, who)
+            yield from self.meet(half, 4, who)
 
     def wait_for_issuer(self, bar, phase, ok):
         if "issuer's waits" in self.without:
@@ -290,7 +293,7 @@ class Cta:
         while more or T >= 0:
             if T >= 0:
                 for half in range(2):
-                    yield from self.meet(half, 3, "issuer")
+                    yield from self.meet(half, 4, "issuer")
                     self.queue.append(("product", 2 * T + half))
                     self.commit(self.product[half])
                 if not more:
@@ -343,7 +346,10 @@ class Cta:
                     yield from self.come_to_half(half, ok, "values")
                 T += 1
 
-    def rows_softmax(self):
+    def rows_tail(self):
+        yield from self.rows_softmax("tail")
+
+    def rows_softmax(self, who="softmax"):
         np, cut, T, ok = 0, 0, 0, True
         while (tiles := (yield from self.take(np))) >= 0:
             if tiles:
@@ -354,15 +360,19 @@ class Cta:
                     ok = yield from self.wait(self.q_full[0], cut)
                 self.q_empty[0].arrive()
                 cut += 1
+            idle = who == "tail" and self.without_rows[np]
             for _ in range(tiles):
                 for half in range(2):
-                    if half == 0:
+                    if half == 0 and not idle:
                         ok = yield from self.wait_for_issuer(self.s_full[0], T, ok)
-                    yield from self.come_to_half(half, ok, "softmax")
+                    yield from self.come_to_half(half, ok, who, idle)
                     yield
                 T += 1
-            if ok and tiles:
-                ok = yield from self.wait(self.product[1], T - 1)
+            if tiles and (ok or "parts' ends" not in self.without):
+                if "parts' ends" in self.without:
+                    ok = yield from self.wait(self.product[1], T - 1)
+                else:
+                    ok = yield from self.wait_for_issuer(self.product[1], T - 1, ok)
                 if ok and self.products_done < 2 * T and not self.abort:
                     raise Wrong("a product that is not complete")
             self.give(np)
@@ -372,7 +382,7 @@ class Cta:
     # ------------------------------------------------------------------ the schedule
 
     def run(self, most=60000):
-        names = ["queries", "relay", "softmax", "issuer"] if self.narrow else ["values", "softmax", "issuer"]
+        names = ["queries", "relay", "softmax", "issuer"] if self.narrow else ["values", "softmax", "tail", "issuer"]
         prefix = "narrow_" if self.narrow else "rows_"
         roles = {"producer": self.producer(), **{n: getattr(self, prefix + n)() for n in names}}
         speed = {n: self.rng.choice([1, 3, 10]) for n in roles}

@@ -19,6 +19,7 @@ NEEDED = [
     ("narrow", "two products", "a wait passed for an older phase", {}),
     ("rows", "first keys", "a wait passed for an older phase", dict(slots=(4,))),
     ("rows", "issuer's waits", "twice at a barrier", dict(abort=True)),
+    ("rows", "parts' ends", "twice at a barrier", dict(abort=True)),
     ("narrow", "queries' part", "stuck", dict(abort=True)),
     ("narrow", "abort seen", "a copy into a place with a copy in flight", dict(abort=True)),
     ("rows", "abort seen", "a copy into a place with a copy in flight", dict(abort=True)),
@@ -27,4 +28,4 @@ NEEDED = [
 
 @pytest.mark.parametrize("kind,what,wrong,kw", NEEDED, ids=[f"{n[0]}-{n[1]}" for n in NEEDED])
 def test_what_goes_wrong_without(kind, what, wrong, kw):
-    assert roles.outcomes(kind, 120, what, **kw).get(wrong, 0) > 0
+    assert roles.outcomes(kind, 150, what, **kw).get(wrong, 0) > 0
