@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 __all__ = [
@@ -27,6 +28,8 @@ __all__ = [
     "fa_fp8_quantize_qk_incoherent", "fa_bwd_set_dq_heads", "fa_fwd_set_heads", "fa_fwd_heads",
     "fa_bwd_dq_heads",
     "fa_fwd_fp8", "Fp8Operands", "quantize_fp8", "attention_forward_fp8",
+    "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_rope_bwd_workspace_size", "fa_kv8_append_norm_rope",
+    "RopePlan", "rope_plan", "norm_rope_forward", "norm_rope_backward", "kv8_append_norm_rope",
     "fa_kv8_plan", "fa_kv8_append", "fa_fwd_kv8", "fa_fwd_kv8_workspace_size", "FA_KV8_BLOCK",
     "Kv8Cache", "kv8_cache", "kv8_plan", "kv8_append", "attention_forward_kv8",
     "fa_device_status",
@@ -119,6 +122,17 @@ def load(path: str | None = None):
     lib.fa_kv8_plan.restype = _i
     lib.fa_kv8_append.argtypes = [_i, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp]
     lib.fa_kv8_append.restype = _i
+    _rope = [_vp, _vp, _i, _vp, _i, _i]   # positions, axes, num_axes, turns, rot, interleaved
+    lib.fa_norm_rope.argtypes = ([_i] + 4 * [_vp, _ll] + [_i] * 5 + [_vp, _vp, _i, _f] + _rope + [_vp])
+    lib.fa_norm_rope.restype = _i
+    lib.fa_norm_rope_bwd_workspace_size.argtypes = [_i] * 4
+    lib.fa_norm_rope_bwd_workspace_size.restype = _sz
+    lib.fa_norm_rope_bwd.argtypes = ([_i] + 6 * [_vp, _ll] + [_i] * 5 + [_vp, _vp, _i, _f, _vp, _vp] + _rope
+                                     + [_vp, _sz, _vp])
+    lib.fa_norm_rope_bwd.restype = _i
+    lib.fa_kv8_append_norm_rope.argtypes = ([_i] + 4 * [_vp, _ll] + [_vp] * 4 + [_i] * 5 + [_vp, _i, _i, _vp, _vp, _i, _f]
+                                            + _rope + [_vp])
+    lib.fa_kv8_append_norm_rope.restype = _i
     lib.fa_fwd_kv8_workspace_size.argtypes = [_i] * 6
     lib.fa_fwd_kv8_workspace_size.restype = _sz
     lib.fa_fwd_kv8.argtypes = [_i, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i,
@@ -423,6 +437,55 @@ def fa_kv8_append(dtype, k, v, stride, k8, k_scale, v8, v_scale, num_pages, page
     return st
 
 
+def fa_norm_rope(dtype, q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, T, Hq, Hkv, d, norm,
+                 q_weight, k_weight, weights_f32, eps, positions, axes, num_axes, turns, rot, interleaved,
+                 stream=None, check: bool = True) -> int:
+    """Norms of queries and keys for each head and their rotation by position (see include/fa.h)."""
+    st = load().fa_norm_rope(int(dtype), _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(q_out),
+                             int(q_out_stride), _ptr(k_out), int(k_out_stride), T, Hq, Hkv, d, int(bool(norm)),
+                             _ptr(q_weight), _ptr(k_weight), int(bool(weights_f32)), float(eps), _ptr(positions),
+                             _ptr(axes), num_axes, _ptr(turns), rot, int(bool(interleaved)), _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def fa_norm_rope_bwd_workspace_size(T, Hq, Hkv, d) -> int:
+    """Workspace bytes of fa_norm_rope_bwd with a weight's gradient (0 for invalid sizes)."""
+    return int(load().fa_norm_rope_bwd_workspace_size(T, Hq, Hkv, d))
+
+
+def fa_norm_rope_bwd(dtype, q, q_stride, k, k_stride, dq_out, dq_out_stride, dk_out, dk_out_stride, dq, dq_stride, dk,
+                     dk_stride, T, Hq, Hkv, d, norm, q_weight, k_weight, weights_f32, eps, dq_weight, dk_weight,
+                     positions, axes, num_axes, turns, rot, interleaved, workspace, workspace_bytes, stream=None,
+                     check: bool = True) -> int:
+    """The gradients of fa_norm_rope (see include/fa.h)."""
+    st = load().fa_norm_rope_bwd(int(dtype), _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(dq_out),
+                                 int(dq_out_stride), _ptr(dk_out), int(dk_out_stride), _ptr(dq), int(dq_stride),
+                                 _ptr(dk), int(dk_stride), T, Hq, Hkv, d, int(bool(norm)), _ptr(q_weight),
+                                 _ptr(k_weight), int(bool(weights_f32)), float(eps), _ptr(dq_weight),
+                                 _ptr(dk_weight), _ptr(positions), _ptr(axes), num_axes, _ptr(turns), rot,
+                                 int(bool(interleaved)), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def fa_kv8_append_norm_rope(dtype, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, k8, k_scale, v8, v_scale,
+                            num_pages, page, Hq, Hkv, d, slots, T, norm, q_weight, k_weight, weights_f32, eps,
+                            positions, axes, num_axes, turns, rot, interleaved, stream=None, check: bool = True) -> int:
+    """fa_norm_rope and fa_kv8_append in one kernel (see include/fa.h)."""
+    st = load().fa_kv8_append_norm_rope(int(dtype), _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v),
+                                        int(v_stride), _ptr(q_out), int(q_out_stride), _ptr(k8), _ptr(k_scale),
+                                        _ptr(v8), _ptr(v_scale), num_pages, page, Hq, Hkv, d, _ptr(slots), T,
+                                        int(bool(norm)), _ptr(q_weight), _ptr(k_weight), int(bool(weights_f32)),
+                                        float(eps), _ptr(positions), _ptr(axes), num_axes, _ptr(turns), rot,
+                                        int(bool(interleaved)), _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
 def fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, total_tokens) -> int:
     """Workspace bytes of fa_fwd_kv8 (total_tokens: T for a packed batch, 0 for a dense one)."""
     return int(load().fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, int(total_tokens)))
@@ -654,6 +717,228 @@ def _there(call, device, stream, *args, **kwargs):
             stream = torch.cuda.ExternalStream(_stream(stream), device=device)
         with torch.cuda.stream(stream):
             return call(*args, **kwargs)
+
+
+class RopePlan(tuple):
+    """(turns, axes, num_axes, interleaved), the frequencies of a rotation by position as the
+    kernels take them (:func:`rope_plan`): int64 CUDA tensor [rot / 2] and, with several axes,
+    int32 CUDA tensor [rot / 2]."""
+    __slots__ = ()
+    _fields = ("turns", "axes", "num_axes", "interleaved")
+
+    def __getattr__(self, name):
+        try:
+            return self[self._fields.index(name)]
+        except ValueError:
+            raise AttributeError(name) from None
+
+
+# 2^64 / (2 pi) as a fraction
+_TURN = (2 ** 64 * 10 ** 60, 2 * 3141592653589793238462643383279502884197169399375105820974945)
+
+
+def rope_plan(frequencies, *, axes=None, interleaved=False, device="cuda") -> RopePlan:
+    """The plan of a rotation that turns channel pair f by position * frequencies[f] radians (a
+    sequence of numbers or a tensor, a multiple of 8 of them, for twice as many channels).  Pair f
+    is the channels (f, f + n) of the first 2 n = rot, or (2 f, 2 f + 1) with ``interleaved``.
+    ``axes``: for positions on several axes (up to 4), the axis that each frequency goes by."""
+    import torch
+    f = [float(x) for x in (frequencies.tolist() if isinstance(frequencies, torch.Tensor) else frequencies)]
+    if not f or len(f) % 8 or len(f) > 64:
+        raise ValueError(f"the number of frequencies must be a multiple of 8 from 8 to 64, got {len(f)}")
+    if not all(math.isfinite(x) for x in f):
+        raise ValueError("frequencies must be finite")
+    turns = []
+    for x in f:
+        n, m = x.as_integer_ratio()
+        t = (2 * n * _TURN[0] + m * _TURN[1]) // (2 * m * _TURN[1]) % 2 ** 64   # to nearest
+        turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    num_axes = 1
+    if axes is not None:
+        axes = [int(a) for a in (axes.tolist() if isinstance(axes, torch.Tensor) else axes)]
+        if len(axes) != len(f) or not all(0 <= a < 4 for a in axes):
+            raise ValueError("axes must name an axis from 0 to 3 for each frequency")
+        num_axes = max(axes) + 1
+    axes = torch.tensor(axes, dtype=torch.int32, device=device) if num_axes > 1 else None
+    return RopePlan((torch.tensor(turns, dtype=torch.int64, device=device), axes, num_axes, bool(interleaved)))
+
+
+def _norm_rope(dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps):
+    """What the calls that norm and rotate have in common, checked, as the C ABI takes it: (norm,
+    weights, weights_f32, eps) and (positions, axes, num_axes, turns, rot, interleaved)."""
+    import torch
+    wide = False
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if not norm:
+            raise ValueError(f"{name} without a norm")
+        if w.dtype != dtype and w.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32 or of q's type, got {w.dtype}")
+        if w.shape != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and have the shape ({d},), got {tuple(w.shape)}")
+        if w.get_device() != dev:
+            raise ValueError(_ONE_DEVICE)
+        wide = w.dtype == torch.float32
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must be of one type")
+    first = (1 if norm else 0, q_weight.data_ptr() if q_weight is not None else None,
+             k_weight.data_ptr() if k_weight is not None else None, wide, eps if norm else 0.0)
+    if rope is None:
+        if positions is not None:
+            raise ValueError("positions without a rope plan")
+        return first, (None, None, 1, None, 0, 0)
+    turns, axes, num_axes, interleaved = rope
+    if positions is None:
+        raise ValueError("a rope plan needs positions")
+    _int32("positions", positions, lead if num_axes == 1 else (num_axes, *lead), dev)
+    if turns.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    rot = 2 * turns.shape[0]
+    if rot > d:
+        raise ValueError(f"the plan turns {rot} channels of {d}")
+    return first, (positions.data_ptr(), axes.data_ptr() if axes is not None else None, num_axes, turns.data_ptr(), rot,
+                   interleaved)
+
+
+def _heads_of(name, x, lead, d, dev, dtype):
+    """Heads of, and elements between the tokens of, a tensor [*lead, heads, d]."""
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    shape = x.shape
+    if shape[:-2] != lead or shape[-1] != d:
+        raise ValueError(f"{name} must have the shape {tuple(lead)} + (heads, {d}), got {tuple(shape)}")
+    if x.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    return shape[-2], _rows(name, x, shape[-2], d)
+
+
+def _qk_shape(q, k):
+    """The leading dimensions, tokens and head dimension of q, and heads and strides of both."""
+    shape, dev = q.shape, q.get_device()
+    if len(shape) not in (3, 4):
+        raise ValueError("q and k must be [B, N, heads, d] or [T, heads, d]")
+    if dev < 0:
+        raise ValueError(_ONE_DEVICE)
+    lead, d = shape[:-2], shape[-1]
+    T = lead.numel()
+    if T >= _INT:
+        raise _beyond(tokens=T)
+    return (lead, T, d, *_heads_of("q", q, lead, d, dev, q.dtype), *_heads_of("k", k, lead, d, dev, q.dtype))
+
+
+def _like(name, x, like, dev):
+    """`x` as an output of `like`'s shape and type (a new tensor for None), and its tokens' distance."""
+    import torch
+    shape = like.shape
+    if x is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device), shape[-2] * shape[-1]
+    heads, stride = _heads_of(name, x, shape[:-2], shape[-1], dev, like.dtype)
+    if heads != shape[-2]:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(x.shape)}")
+    return x, stride
+
+
+def norm_rope_forward(q, k, positions=None, rope: RopePlan | None = None, *, q_weight=None, k_weight=None, norm=True,
+                      eps=1e-6, out=None, stream=None):
+    """q and k ([B, N, heads, d] or [T, heads, d], both bf16 or both fp16, evenly spaced tokens) after
+    the norm of each head's row, with ``q_weight`` and ``k_weight`` ([d], float32 or of q's type), and
+    the rotation by ``positions`` (int32, the shape of q without heads and d; [axes, ...] with a plan
+    of several axes).  ``norm=False`` rotates only, no plan norms only.  ``out``: a pair of tensors
+    to write, q and k themselves among them."""
+    dev = q.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(norm_rope_forward, dev, stream, q, k, positions, rope, q_weight=q_weight, k_weight=k_weight,
+                      norm=norm, eps=eps, out=out)
+    import torch
+    dtype = _dtype_code(q, k)
+    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk_shape(q, k)
+    norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
+    q_out, k_out = (None, None) if out is None else out
+    q_out, q_out_stride = _like("out[0]", q_out, q, dev)
+    k_out, k_out_stride = _like("out[1]", k_out, k, dev)
+    _check(load().fa_norm_rope(dtype, q.data_ptr(), q_stride, k.data_ptr(), k_stride, q_out.data_ptr(), q_out_stride,
+                               k_out.data_ptr(), k_out_stride, T, Hq, Hkv, d, *norms, *turned,
+                               torch._C._cuda_getCurrentRawStream(dev)))
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_rope_workspace(device, T, Hq, Hkv, d):
+    """fa_norm_rope_bwd_workspace_size on CUDA device number `device`, the current one."""
+    return fa_norm_rope_bwd_workspace_size(T, Hq, Hkv, d)
+
+
+def norm_rope_backward(q, k, dq_out, dk_out, positions=None, rope: RopePlan | None = None, *, q_weight=None,
+                       k_weight=None, norm=True, eps=1e-6, out=None, workspace=None, stream=None):
+    """dq, dk, dq_weight, dk_weight of :func:`norm_rope_forward` on q and k, for the gradients dq_out
+    and dk_out of its outputs (attention_backward's dq and dk).  The weights' gradients are float32,
+    None for weights that are not given.  ``out``: a pair of tensors for dq and dk (slices of the
+    projection's gradient, say, or dq_out and dk_out themselves); ``workspace``: uint8,
+    fa_norm_rope_bwd_workspace_size bytes, allocated if not given."""
+    dev = q.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(norm_rope_backward, dev, stream, q, k, dq_out, dk_out, positions, rope, q_weight=q_weight,
+                      k_weight=k_weight, norm=norm, eps=eps, out=out, workspace=workspace)
+    import torch
+    dtype = _dtype_code(q, k, dq_out, dk_out)
+    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk_shape(q, k)
+    norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
+    heads, dq_out_stride = _heads_of("dq_out", dq_out, lead, d, dev, q.dtype)
+    heads_k, dk_out_stride = _heads_of("dk_out", dk_out, lead, d, dev, q.dtype)
+    if heads != Hq or heads_k != Hkv:
+        raise ValueError(f"dq_out and dk_out must have q's and k's heads, {Hq} and {Hkv}, got {heads} and {heads_k}")
+    dq, dk = (None, None) if out is None else out
+    dq, dq_stride = _like("out[0]", dq, q, dev)
+    dk, dk_stride = _like("out[1]", dk, k, dev)
+    dq_weight = dk_weight = None
+    if q_weight is not None:
+        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    if k_weight is not None:
+        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on q's device")
+    elif q_weight is not None or k_weight is not None:
+        workspace = torch.empty(_norm_rope_workspace(dev, T, Hq, Hkv, d), dtype=torch.uint8, device=q.device)
+    _check(load().fa_norm_rope_bwd(
+        dtype, q.data_ptr(), q_stride, k.data_ptr(), k_stride, dq_out.data_ptr(), dq_out_stride, dk_out.data_ptr(),
+        dk_out_stride, dq.data_ptr(), dq_stride, dk.data_ptr(), dk_stride, T, Hq, Hkv, d, *norms, _ptr(dq_weight),
+        _ptr(dk_weight), *turned, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        torch._C._cuda_getCurrentRawStream(dev)))
+    return dq, dk, dq_weight, dk_weight
+
+
+def kv8_append_norm_rope(cache: Kv8Cache, q, k, v, slots, positions=None, rope: RopePlan | None = None, *, q_weight=None,
+                         k_weight=None, norm=True, eps=1e-6, out=None, stream=None):
+    """:func:`norm_rope_forward` and :func:`kv8_append` in one pass, for the tokens q [T, Hq, d], k and v
+    [T, Hkv, d] of a serving step: returns q normed and rotated (``out``, or a new tensor), writes k,
+    normed and rotated, and v into the cache at ``slots``."""
+    dev = q.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(kv8_append_norm_rope, dev, stream, cache, q, k, v, slots, positions, rope, q_weight=q_weight,
+                      k_weight=k_weight, norm=norm, eps=eps, out=out)
+    import torch
+    dtype = _dtype_code(q, k, v)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d]")
+    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk_shape(q, k)
+    num_pages, heads, page, dk = _kv8_shape(cache, dev)
+    if heads != Hkv or dk != d:
+        raise ValueError(f"the cache has {heads} heads of {dk} channels, k {Hkv} of {d}")
+    heads, v_stride = _heads_of("v", v, lead, d, dev, q.dtype)
+    if heads != Hkv:
+        raise ValueError(f"v must have k's {Hkv} heads, got {heads}")
+    _int32("slots", slots, lead, dev)
+    norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
+    out, out_stride = _like("out", out, q, dev)
+    k8, k_scale, v8, v_scale = cache
+    _check(load().fa_kv8_append_norm_rope(
+        dtype, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, out.data_ptr(), out_stride,
+        k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(), v_scale.data_ptr(), num_pages, page, Hq, Hkv, d,
+        slots.data_ptr(), T, *norms, *turned, torch._C._cuda_getCurrentRawStream(dev)))
+    return out
 
 
 def kv8_plan(lens, grow, table, ring, state, *, page, tokens, stream=None):

@@ -919,6 +919,181 @@ fa_status fa_debug_check_selftest(cudaStream_t stream) {
 
 }  // extern "C"
 
+// ------------------------------------------------------- norms and rotation of q and k
+
+namespace fa {
+namespace {
+
+bool tokens_ok(const void* x, long long stride, int heads, int d) {
+    return aligned16(x) && stride % 8 == 0 && stride >= static_cast<long long>(heads) * d;
+}
+
+// Checks and takes over what the calls that norm and rotate have in common.
+fa_status take_norm_rope(const char* who, fa_dtype dtype, int T, int Hq, int Hkv, int d, int norm,
+                         const void* q_weight, const void* k_weight, int weights_f32, float eps,
+                         const int* positions, const int* axes, int num_axes,
+                         const unsigned long long* turns, int rot, int interleaved, NormRopeParams* p) {
+    *p = NormRopeParams{};
+    const fa_status st = check_dtype(dtype, who);
+    if (st != FA_OK) return st;
+    if (T < 0 || Hq < 1 || Hkv < 1)
+        return fail(FA_ERR_INVALID_ARG, "%s: T >= 0, Hq >= 1 and Hkv >= 1 needed (got %d, %d, %d)", who, T, Hq, Hkv);
+    if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "%s: head dim %d not in {64, 128}", who, d);
+    if (static_cast<long long>(Hq) * d > INT_MAX || static_cast<long long>(Hkv) * d > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "%s: too many heads", who);
+    if (rot < 0 || rot > d || rot % 16 != 0)
+        return fail(FA_ERR_INVALID_ARG, "%s: rot %d must be a multiple of 16 from 0 to d", who, rot);
+    if (rot > 0 && (!turns || (T > 0 && !positions)))
+        return fail(FA_ERR_INVALID_ARG, "%s: a rotation needs turns and positions", who);
+    if (num_axes < 1 || num_axes > 4 || (num_axes > 1 && !axes))
+        return fail(FA_ERR_INVALID_ARG, "%s: num_axes %d must be 1 to 4, and axes given from 2 on", who, num_axes);
+    if (!aligned4(positions) || !aligned4(axes) || (reinterpret_cast<uintptr_t>(turns) & 7u))
+        return fail(FA_ERR_INVALID_ARG, "%s: positions and axes must be 4-byte aligned, turns 8-byte", who);
+    if (norm && (!(eps > 0.f) || !std::isfinite(eps)))
+        return fail(FA_ERR_INVALID_ARG, "%s: eps must be finite and > 0", who);
+    if (!norm && (q_weight || k_weight))
+        return fail(FA_ERR_INVALID_ARG, "%s: weights without a norm", who);
+    if (!aligned16(q_weight) || !aligned16(k_weight))
+        return fail(FA_ERR_INVALID_ARG, "%s: weights must be 16-byte aligned", who);
+    p->w[0] = q_weight;
+    p->w[1] = k_weight;
+    p->wide = weights_f32 ? 1 : 0;
+    p->norm = norm ? 1 : 0;
+    p->eps = eps;
+    p->rope.turns = turns;
+    p->rope.axes = num_axes > 1 ? axes : nullptr;
+    p->rope.positions = positions;
+    p->rope.axis_stride = T;
+    p->rope.num_axes = num_axes;
+    p->rope.rot = rot;
+    p->rope.interleaved = interleaved ? 1 : 0;
+    p->heads[0] = Hq;
+    p->heads[1] = Hkv;
+    p->T = T;
+    p->elem = static_cast<int>(dtype);
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_norm_rope(fa_dtype dtype, const void* q, long long q_stride, const void* k,
+                       long long k_stride, void* q_out, long long q_out_stride, void* k_out,
+                       long long k_out_stride, int T, int Hq, int Hkv, int d, int norm,
+                       const void* q_weight, const void* k_weight, int weights_f32, float eps,
+                       const int* positions, const int* axes, int num_axes,
+                       const unsigned long long* turns, int rot, int interleaved,
+                       cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    NormRopeParams p;
+    const fa_status st = take_norm_rope("fa_norm_rope", dtype, T, Hq, Hkv, d, norm, q_weight, k_weight, weights_f32,
+                                        eps, positions, axes, num_axes, turns, rot, interleaved, &p);
+    if (st != FA_OK) return st;
+    if (T == 0) return FA_OK;
+    if (!q || !k || !q_out || !k_out)
+        return fail(FA_ERR_INVALID_ARG, "fa_norm_rope: every tensor must be non-null");
+    if (!tokens_ok(q, q_stride, Hq, d) || !tokens_ok(k, k_stride, Hkv, d) ||
+        !tokens_ok(q_out, q_out_stride, Hq, d) || !tokens_ok(k_out, k_out_stride, Hkv, d))
+        return fail(FA_ERR_INVALID_ARG, "fa_norm_rope: tensors must be 16-byte aligned, strides multiples of 8 "
+                    "and at least heads * d");
+    p.x[0] = q;
+    p.x[1] = k;
+    p.y[0] = q_out;
+    p.y[1] = k_out;
+    p.x_stride[0] = q_stride;
+    p.x_stride[1] = k_stride;
+    p.y_stride[0] = q_out_stride;
+    p.y_stride[1] = k_out_stride;
+    p.status = status_word_ptr();
+    if (!p.status) return fail(FA_ERR_CUDA, "fa_norm_rope: cannot resolve the device status word");
+    if (norm_rope_plan(p, d, sm_count(), false) == 0)
+        return fail(FA_ERR_UNSUPPORTED, "fa_norm_rope: problem too large for one launch");
+    const cudaError_t e = launch_norm_rope(p, d, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_norm_rope launch");
+}
+
+size_t fa_norm_rope_bwd_workspace_size(int T, int Hq, int Hkv, int d) {
+    using namespace fa;
+    if (T < 1 || Hq < 1 || Hkv < 1 || (d != 64 && d != 128)) return 0;
+    NormRopeParams p{};
+    p.T = T;
+    p.heads[0] = Hq;
+    p.heads[1] = Hkv;
+    return static_cast<size_t>(norm_rope_plan(p, d, sm_count(), true)) * d * sizeof(float);
+}
+
+fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, const void* k,
+                           long long k_stride, const void* dq_out, long long dq_out_stride,
+                           const void* dk_out, long long dk_out_stride, void* dq,
+                           long long dq_stride, void* dk, long long dk_stride, int T, int Hq,
+                           int Hkv, int d, int norm, const void* q_weight, const void* k_weight,
+                           int weights_f32, float eps, float* dq_weight, float* dk_weight,
+                           const int* positions, const int* axes, int num_axes,
+                           const unsigned long long* turns, int rot, int interleaved,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    NormRopeParams p;
+    const fa_status st = take_norm_rope("fa_norm_rope_bwd", dtype, T, Hq, Hkv, d, norm, q_weight, k_weight,
+                                        weights_f32, eps, positions, axes, num_axes, turns, rot, interleaved, &p);
+    if (st != FA_OK) return st;
+    if (!norm && (dq_weight || dk_weight))
+        return fail(FA_ERR_INVALID_ARG, "fa_norm_rope_bwd: weights' gradients without a norm");
+    if (!aligned4(dq_weight) || !aligned4(dk_weight))
+        return fail(FA_ERR_INVALID_ARG, "fa_norm_rope_bwd: the weights' gradients must be 4-byte aligned");
+    if (T > 0) {
+        if ((norm && (!q || !k)) || !dq_out || !dk_out || !dq || !dk)
+            return fail(FA_ERR_INVALID_ARG, "fa_norm_rope_bwd: every tensor must be non-null");
+        if ((norm && (!tokens_ok(q, q_stride, Hq, d) || !tokens_ok(k, k_stride, Hkv, d))) ||
+            !tokens_ok(dq_out, dq_out_stride, Hq, d) || !tokens_ok(dk_out, dk_out_stride, Hkv, d) ||
+            !tokens_ok(dq, dq_stride, Hq, d) || !tokens_ok(dk, dk_stride, Hkv, d))
+            return fail(FA_ERR_INVALID_ARG, "fa_norm_rope_bwd: tensors must be 16-byte aligned, strides multiples "
+                        "of 8 and at least heads * d");
+        if (dq_weight || dk_weight) {
+            const size_t need = fa_norm_rope_bwd_workspace_size(T, Hq, Hkv, d);
+            if (!workspace || workspace_bytes < need)
+                return fail(FA_ERR_WORKSPACE, "fa_norm_rope_bwd: workspace of at least %zu bytes needed, got %zu%s",
+                            need, workspace_bytes, workspace ? "" : " (null)");
+            if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+                return fail(FA_ERR_WORKSPACE, "fa_norm_rope_bwd: workspace must be 256-byte aligned");
+            p.partial = static_cast<float*>(workspace);
+        }
+    } else {
+        // no tokens: the weights' gradients are sums of nothing
+        for (float* w : {dq_weight, dk_weight})
+            if (w) {
+                const cudaError_t e = cudaMemsetAsync(w, 0, d * sizeof(float), stream);
+                if (e != cudaSuccess) return cuda_fail(e, "fa_norm_rope_bwd");
+            }
+        return FA_OK;
+    }
+    p.x[0] = q;
+    p.x[1] = k;
+    p.dy[0] = dq_out;
+    p.dy[1] = dk_out;
+    p.y[0] = dq;
+    p.y[1] = dk;
+    p.x_stride[0] = q_stride;
+    p.x_stride[1] = k_stride;
+    p.dy_stride[0] = dq_out_stride;
+    p.dy_stride[1] = dk_out_stride;
+    p.y_stride[0] = dq_stride;
+    p.y_stride[1] = dk_stride;
+    p.dw[0] = dq_weight;
+    p.dw[1] = dk_weight;
+    p.status = status_word_ptr();
+    if (!p.status) return fail(FA_ERR_CUDA, "fa_norm_rope_bwd: cannot resolve the device status word");
+    if (norm_rope_plan(p, d, sm_count(), true) == 0)
+        return fail(FA_ERR_UNSUPPORTED, "fa_norm_rope_bwd: problem too large for one launch");
+    const cudaError_t e = launch_norm_rope_bwd(p, d, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_norm_rope_bwd launch");
+}
+
+}  // extern "C"
+
 // ------------------------------------------------------------- paged 8-bit cache
 
 namespace fa {
@@ -935,6 +1110,34 @@ fa_status check_pages(const char* who, int num_pages, int page, int* page_log2) 
     int l = 4;
     while ((1 << l) < page) ++l;
     *page_log2 = l;
+    return FA_OK;
+}
+
+// Checks and takes over what the calls that write the cache have in common.
+fa_status take_cache(const char* who, const void* k, const void* v, void* k8, float* k_scale, void* v8,
+                     float* v_scale, int num_pages, int page, int Hkv, const int* slots, int T, Kv8AppendParams* p) {
+    const fa_status st = check_pages(who, num_pages, page, &p->page_log2);
+    if (st != FA_OK) return st;
+    if (!k8 || !v8 || !k_scale || !v_scale || (T > 0 && (!k || !v || !slots)))
+        return fail(FA_ERR_INVALID_ARG, "%s: every pointer must be non-null", who);
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || !aligned4(slots))
+        return fail(FA_ERR_INVALID_ARG, "%s: k, v, k8 and v8 must be 16-byte aligned, the scales and slots 4-byte "
+                    "aligned", who);
+    p->x[0] = k;
+    p->x[1] = v;
+    p->codes[0] = static_cast<uint8_t*>(k8);
+    p->codes[1] = static_cast<uint8_t*>(v8);
+    p->scales[0] = k_scale;
+    p->scales[1] = v_scale;
+    p->slots = slots;
+    p->T = T;
+    p->Hkv = Hkv;
+    p->num_slots = num_pages * page;
+    // tokens of a warp: all of a block's 16 where there are warps enough for the GPU (64 an SM)
+    // all the same, fewer where there are not, since a warp takes its blocks in turn
+    const long long warps = 2LL * T * Hkv, want = 64LL * sm_count();
+    p->chunk = static_cast<int>(std::min(std::max(warps / want, 1LL), static_cast<long long>(kKv8Block)));
     return FA_OK;
 }
 
@@ -1047,35 +1250,56 @@ fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long 
         return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: T >= 0 and Hkv >= 1 needed (got %d, %d)", T, Hkv);
     if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "fa_kv8_append: head dim %d not in {64, 128}", d);
     Kv8AppendParams p;
-    if ((st = check_pages("fa_kv8_append", num_pages, page, &p.page_log2)) != FA_OK) return st;
-    if (!k8 || !v8 || !k_scale || !v_scale || (T > 0 && (!k || !v || !slots)))
-        return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: every pointer must be non-null");
-    if (!aligned16(k) || !aligned16(v) || !aligned16(k8) || !aligned16(v8) || !aligned4(k_scale) ||
-        !aligned4(v_scale) || !aligned4(slots))
-        return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: k, v, k8 and v8 must be 16-byte aligned, the "
-                    "scales and slots 4-byte aligned");
+    if ((st = take_cache("fa_kv8_append", k, v, k8, k_scale, v8, v_scale, num_pages, page, Hkv, slots, T, &p)) != FA_OK)
+        return st;
     if (stride % 8 != 0 || stride < static_cast<long long>(Hkv) * d)
         return fail(FA_ERR_INVALID_ARG, "fa_kv8_append: stride %lld must be a multiple of 8 and at "
                     "least Hkv * d", stride);
     if (T == 0) return FA_OK;
-    p.x[0] = k;
-    p.x[1] = v;
-    p.codes[0] = static_cast<uint8_t*>(k8);
-    p.codes[1] = static_cast<uint8_t*>(v8);
-    p.scales[0] = k_scale;
-    p.scales[1] = v_scale;
-    p.slots = slots;
     p.stride = stride;
-    p.T = T;
-    p.Hkv = Hkv;
-    p.num_slots = num_pages * page;
     p.elem = static_cast<int>(dtype);
-    // tokens of a warp: all of a block's 16 where there are warps enough for the GPU (64 an SM)
-    // all the same, fewer where there are not, since a warp takes its blocks in turn
-    const long long warps = 2LL * T * Hkv, want = 64LL * sm_count();
-    p.chunk = static_cast<int>(std::min(std::max(warps / want, 1LL), static_cast<long long>(kKv8Block)));
     const cudaError_t e = launch_kv8_append(p, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append launch");
+}
+
+fa_status fa_kv8_append_norm_rope(fa_dtype dtype, const void* q, long long q_stride, const void* k,
+                                  long long k_stride, const void* v, long long v_stride, void* q_out,
+                                  long long q_out_stride, void* k8, float* k_scale, void* v8,
+                                  float* v_scale, int num_pages, int page, int Hq, int Hkv, int d,
+                                  const int* slots, int T, int norm, const void* q_weight,
+                                  const void* k_weight, int weights_f32, float eps,
+                                  const int* positions, const int* axes, int num_axes,
+                                  const unsigned long long* turns, int rot, int interleaved,
+                                  cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    constexpr const char* who = "fa_kv8_append_norm_rope";
+    NormRopeParams n;
+    fa_status st = take_norm_rope(who, dtype, T, Hq, Hkv, d, norm, q_weight, k_weight, weights_f32, eps, positions,
+                                  axes, num_axes, turns, rot, interleaved, &n);
+    if (st != FA_OK) return st;
+    Kv8AppendParams p;
+    if ((st = take_cache(who, k, v, k8, k_scale, v8, v_scale, num_pages, page, Hkv, slots, T, &p)) != FA_OK) return st;
+    if (T == 0) return FA_OK;
+    if (!q || !q_out) return fail(FA_ERR_INVALID_ARG, "%s: every tensor must be non-null", who);
+    if (!tokens_ok(q, q_stride, Hq, d) || !tokens_ok(k, k_stride, Hkv, d) || !tokens_ok(v, v_stride, Hkv, d) ||
+        !tokens_ok(q_out, q_out_stride, Hq, d))
+        return fail(FA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned, strides multiples of 8 and at least "
+                    "heads * d", who);
+    p.stride = v_stride;
+    p.elem = static_cast<int>(dtype);
+    n.x[0] = q;
+    n.x[1] = k;
+    n.y[0] = q_out;
+    n.x_stride[0] = q_stride;
+    n.x_stride[1] = k_stride;
+    n.y_stride[0] = q_out_stride;
+    n.status = status_word_ptr();
+    if (!n.status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
+    if (norm_rope_plan(n, d, sm_count(), false) == 0)
+        return fail(FA_ERR_UNSUPPORTED, "%s: problem too large for one launch", who);
+    const cudaError_t e = launch_kv8_append_norm_rope(p, n, d, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append_norm_rope launch");
 }
 
 size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens) {

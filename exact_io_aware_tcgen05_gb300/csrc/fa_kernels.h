@@ -145,6 +145,37 @@ struct Kv8AppendParams {
     int elem;
 };
 
+// Rotation by position (fa_norm_rope in fa.h).
+struct RopeParams {
+    const unsigned long long* turns;   // [rot / 2], a position's share of a turn in units of 2^-64
+    const int* axes;        // [rot / 2], or null: all frequencies go by axis 0
+    const int* positions;   // [num_axes, T]
+    long long axis_stride;  // T
+    int num_axes;
+    int rot;                // channels rotated (0: none)
+    int interleaved;        // pairs (2 f, 2 f + 1), else (f, f + rot / 2)
+};
+
+// Norms and rotation of queries (side 0) and keys (side 1), forward and backward.
+struct NormRopeParams {
+    const void* x[2];       // 16-bit [T, heads, d], tokens x_stride elements apart
+    const void* dy[2];      // backward: the outputs' gradients
+    void* y[2];             // the outputs; backward: the inputs' gradients
+    long long x_stride[2], dy_stride[2], y_stride[2];
+    const void* w[2];       // weights [d], or null
+    float* dw[2];           // backward: their gradients, or null
+    float* partial;         // backward: [ctas, d], the CTAs' sums; null where no gradient is wanted
+    RopeParams rope;
+    int heads[2];
+    int run[2];             // heads of a unit of work, a divisor of heads (norm_rope_plan)
+    int ctas[2];
+    int T;
+    int norm, wide;         // whether there is a norm; whether the weights are fp32
+    float eps;
+    int elem;
+    int* status;
+};
+
 // What the attention kernel's CTA c leaves for the joining kernel where its range ends
 // inside an item: the item's first part is CTA c's second slot, the others are the first
 // slots of CTAs c + 1 .. last (0: the range ends between two items).
@@ -202,6 +233,13 @@ cudaError_t launch_fp8_quant_qk(const Fp8QuantParams& p, int d, int grid, cudaSt
 cudaError_t launch_fp8_quant_v(const Fp8QuantParams& p, int d, int grid, cudaStream_t stream);
 cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stream);
+// norm_rope_plan fills in run and ctas and returns the CTAs of both sides (0: too many).
+int norm_rope_plan(NormRopeParams& p, int d, int sms, bool backward);
+cudaError_t launch_norm_rope(NormRopeParams& p, int d, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(NormRopeParams& p, int d, cudaStream_t stream);
+// kv8_append whose keys, and the queries beside them, go through norm and rotation first
+// (a.x[0] and n's key output are not used).
+cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRopeParams& n, int d, cudaStream_t stream);
 cudaError_t launch_fwd_kv8_rows(const Kv8FwdParams& p, int d, cudaStream_t stream);
 // launch_fwd_kv8 records ev[0..2] (if not null) around its two kernels.
 cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, cudaStream_t stream);

@@ -2,6 +2,7 @@
 // pages) and its writer.  The formats and rules are those of fa_kv8_plan and
 // fa_kv8_append in include/fa.h.
 #include "fa_kv8_work.cuh"
+#include "fa_norm_rope.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -206,6 +207,42 @@ __device__ __noinline__ void append_by_division(const uint16_t* x, long long str
     }
 }
 
+// The next run of consecutive slots of one block among a batch's tokens, from token t on.
+struct BlockRun {
+    int slot, off, n;   // its first slot, that one's place in the block, its tokens
+    bool skip;          // no place in the cache, or a block that an earlier warp began
+};
+__device__ __forceinline__ BlockRun next_run(const Kv8AppendParams& p, int t, long long c0) {
+    const int lane = threadIdx.x & 31;
+    BlockRun r;
+    r.slot = p.slots[t];
+    r.off = r.slot & (kKv8Block - 1);
+    const bool real = r.slot >= 0 && r.slot < p.num_slots;
+    const int mine = lane < kKv8Block && t + lane < p.T ? p.slots[t + lane] : -1;
+    const uint32_t follows = __ballot_sync(
+        0xffffffffu, real && r.off + lane < kKv8Block && mine == r.slot + lane);
+    r.n = real ? __ffs(~follows) - 1 : 1;   // lane 16 never follows
+    r.skip = !real || (r.off > 0 && t == c0 && t > 0 && p.slots[t - 1] == r.slot - 1);
+    return r;
+}
+
+// The `off` tokens that a block held, rounded again to a larger scale, by a warp; `row` is the
+// lane's 8 codes of the block's first token, `ratio` the old scale by the new one (exact, the new
+// scale being a power of two, or too small for any code).
+template <int D>
+__device__ __forceinline__ void round_again(uint8_t* row, int off, float ratio) {
+    for (int r = (threadIdx.x & 31) / (D / 8); r < off; r += 32 / (D / 8)) {
+        uint2* at = reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D);
+        uint2 c = *at;
+        float f[4];
+        unpack4_e4m3(c.x, f);
+        c.x = pack4_e4m3(mul_odd(f[0], ratio), mul_odd(f[1], ratio), mul_odd(f[2], ratio), mul_odd(f[3], ratio));
+        unpack4_e4m3(c.y, f);
+        c.y = pack4_e4m3(mul_odd(f[0], ratio), mul_odd(f[1], ratio), mul_odd(f[2], ratio), mul_odd(f[3], ratio));
+        *at = c;
+    }
+}
+
 // One warp takes the blocks of 16 slots whose first new token is among its `chunk`
 // tokens, for one head of K or V, one block after the other: D / 8 lanes hold one token
 // (8 values, a 16-byte load), so the warp holds the block's new tokens at once and reads
@@ -217,17 +254,11 @@ __device__ __noinline__ void append_by_division(const uint16_t* x, long long str
 // an infinity on its own: then the ALUs were as busy as the memory); 64 single tokens 3.2 us, a
 // launch and the loads that wait for one another (slot, then values and scale).
 template <int D, int E>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p) {
-    grid_launch_dependents();
-    grid_dependency_wait();
+__device__ __forceinline__ void append_chunk(const Kv8AppendParams& p, int side, int h, long long c0) {
     constexpr int kLanes = D / 8;          // lanes of one token
     constexpr int kRows = 32 / kLanes;     // tokens the warp loads at a time
     constexpr int kSteps = kKv8Block / kRows;
     const int lane = threadIdx.x & 31;
-    const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int h = static_cast<int>(item % p.Hkv);
-    const int side = static_cast<int>(item / p.Hkv % 2);
-    const long long c0 = item / p.Hkv / 2 * p.chunk;
     if (c0 >= p.T) return;
     const int c1 = static_cast<int>(min(c0 + p.chunk, static_cast<long long>(p.T)));
     const uint16_t* x = static_cast<const uint16_t*>(p.x[side]) + static_cast<long long>(h) * D +
@@ -235,15 +266,10 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
     int t = static_cast<int>(c0);
     while (t < c1) {
         // the run of consecutive slots from t on, to the end of its block
-        const int slot = p.slots[t];
-        const int off = slot & (kKv8Block - 1);
-        const bool real = slot >= 0 && slot < p.num_slots;
-        const int mine = lane < kKv8Block && t + lane < p.T ? p.slots[t + lane] : -1;
-        const uint32_t follows = __ballot_sync(
-            0xffffffffu, real && off + lane < kKv8Block && mine == slot + lane);
-        const int n = real ? __ffs(~follows) - 1 : 1;   // lane 16 never follows
-        if (!real || (off > 0 && t == c0 && t > 0 && p.slots[t - 1] == slot - 1)) {
-            t += n;    // no place in the cache, or a block that an earlier warp began
+        const BlockRun run = next_run(p, t, c0);
+        const int slot = run.slot, off = run.off, n = run.n;
+        if (run.skip) {
+            t += n;
             continue;
         }
         uint4 w[kSteps];
@@ -288,20 +314,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
         if (off > 0) {
             const float old = *scale_at;
             scale = fmaxf(old, scale);
-            if (scale > old) {
-                // the tokens that the block held, rounded again to the larger scale
-                const float ratio = old / scale;   // (exact, the new scale being a power of two, or too small for any code)
-                for (int r = lane / kLanes; r < off; r += kRows) {
-                    uint2* at = reinterpret_cast<uint2*>(row + static_cast<long long>(r - off) * D);
-                    uint2 c = *at;
-                    float f[4];
-                    unpack4_e4m3(c.x, f);
-                    c.x = pack4_e4m3(mul_odd(f[0], ratio), mul_odd(f[1], ratio), mul_odd(f[2], ratio), mul_odd(f[3], ratio));
-                    unpack4_e4m3(c.y, f);
-                    c.y = pack4_e4m3(mul_odd(f[0], ratio), mul_odd(f[1], ratio), mul_odd(f[2], ratio), mul_odd(f[3], ratio));
-                    *at = c;
-                }
-            }
+            if (scale > old) round_again<D>(row - static_cast<long long>(off) * D, off, old / scale);
         }
         if ((__float_as_uint(scale) & 0x7fffffu) != 0) {
             append_by_division<D, E>(x + t * p.stride, p.stride, row, n, scale);
@@ -333,6 +346,116 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
     }
 }
 
+template <int D, int E>
+__global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    append_chunk<D, E>(p, static_cast<int>(item / p.Hkv % 2), static_cast<int>(item % p.Hkv),
+                       item / p.Hkv / 2 * p.chunk);
+}
+
+// append_chunk for keys that are normed and rotated on their way: the block's new tokens are in
+// registers as 32-bit numbers, from which its scale and codes come, so a key is rounded once.
+template <int D, int E, bool IL>
+__device__ __forceinline__ void append_rotated_chunk(const Kv8AppendParams& p, const NormRopeParams& q, int h,
+                                                     long long c0) {
+    constexpr int kLanes = D / 16;         // lanes of one token
+    constexpr int kRows = 32 / kLanes;     // tokens the warp loads at a time
+    constexpr int kSteps = kKv8Block / kRows;
+    const int lane = threadIdx.x & 31;
+    if (c0 >= p.T) return;
+    const int c1 = static_cast<int>(min(c0 + p.chunk, static_cast<long long>(p.T)));
+    const RowLane<D, IL> at(lane % kLanes, q.rope.rot);
+    const uint16_t* x = static_cast<const uint16_t*>(q.x[1]) + static_cast<long long>(h) * D;
+    float w[16];
+    if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
+    int t = static_cast<int>(c0);
+    while (t < c1) {
+        const BlockRun run = next_run(p, t, c0);
+        const int off = run.off, n = run.n;
+        if (run.skip) {
+            t += n;
+            continue;
+        }
+        float v[kSteps][16];
+        uint32_t top = 0;   // the largest finite magnitude, as an integer
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = i * kRows + lane / kLanes;
+            const long long token = t + min(r, n - 1);   // (rows behind the run are not stored)
+            const uint16_t* from = x + token * q.x_stride[1];
+            widen<E>(*reinterpret_cast<const uint4*>(from + 8 * at.unit[0]),
+                     *reinterpret_cast<const uint4*>(from + 8 * at.unit[1]), v[i]);
+            if (q.norm) {
+                const float f = inverse_norm<D>(v[i], q.eps);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * f * w[j];
+            }
+            float c[8], s[8];
+            rotation_of<D, IL>(q.rope, at, token, c, s);
+            rotate<D, IL, false>(at, c, s, v[i]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
+                if (a < 0x7f800000u) top = max(top, a);
+                else finite = false;
+            }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int page = run.slot >> p.page_log2;
+        const int in_page = run.slot & ((1 << p.page_log2) - 1);
+        const long long row0 = (static_cast<long long>(page) * p.Hkv + h) << p.page_log2;
+        float* scale_at = p.scales[0] + (row0 + in_page) / kKv8Block;
+        uint8_t* row = p.codes[0] + (row0 + in_page) * D;
+        float scale = pow2f(scale_exponent(top));
+        if (off > 0) {
+            const float old = *scale_at;
+            scale = fmaxf(old, scale);
+            if (scale > old) round_again<D>(row - static_cast<long long>(off) * D + lane % (D / 8) * 8, off, old / scale);
+        }
+        const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
+        const float inv = 1.f / scale;   // exact for a power of two
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = i * kRows + lane / kLanes;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float f = v[i][j];
+                v[i][j] = power ? f * inv : div_odd(f, scale);
+                if (!finite) v[i][j] += f * 0.f;   // inf * 0 is NaN: infinities become NaN codes
+            }
+            if (r >= n) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D + 8 * at.unit[j]) =
+                    make_uint2(pack4_e4m3(v[i][8 * j], v[i][8 * j + 1], v[i][8 * j + 2], v[i][8 * j + 3]),
+                               pack4_e4m3(v[i][8 * j + 4], v[i][8 * j + 5], v[i][8 * j + 6], v[i][8 * j + 7]));
+        }
+        __syncwarp();   // every lane has read the old scale
+        if (lane == 0) *scale_at = scale;
+        t += n;
+    }
+}
+
+// The first q.ctas[0] CTAs prepare the queries, the others take chunks of keys and values.
+template <int D, int E, bool IL>
+__global__ void __launch_bounds__(kNormThreads) kv8_append_norm_rope_kernel(const Kv8AppendParams p,
+                                                                            const __grid_constant__ NormRopeParams q) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (static_cast<int>(blockIdx.x) < q.ctas[0]) {
+        norm_rope_rows<D, E, IL>(q, 0, blockIdx.x);
+        return;
+    }
+    const long long item = (static_cast<long long>(blockIdx.x - q.ctas[0]) * kNormThreads + threadIdx.x) >> 5;
+    const int h = static_cast<int>(item % p.Hkv);
+    const long long c0 = item / p.Hkv / 2 * p.chunk;
+    if (item / p.Hkv % 2 == 0) append_rotated_chunk<D, E, IL>(p, q, h, c0);
+    else append_chunk<D, E>(p, 1, h, c0);
+}
+
 }  // namespace
 
 cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream) {
@@ -358,6 +481,18 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stre
     auto kern = d == 128 ? (p.elem == kElemBf16Code ? kv8_append_kernel<128, kElemBf16> : kv8_append_kernel<128, kElemF16>)
                          : (p.elem == kElemBf16Code ? kv8_append_kernel<64, kElemBf16> : kv8_append_kernel<64, kElemF16>);
     return kv8::launch_dependent(kern, static_cast<int>(grid), kThreads, 0, stream, p);
+}
+
+cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRopeParams& n, int d, cudaStream_t stream) {
+    const long long chunks = (static_cast<long long>(a.T) + a.chunk - 1) / a.chunk;
+    const long long grid = n.ctas[0] + (chunks * a.Hkv * 2 * 32 + kNormThreads - 1) / kNormThreads;
+    if (grid > INT_MAX) return cudaErrorInvalidValue;
+    const bool f16 = a.elem == kElemF16Code, il = n.rope.interleaved != 0;
+    auto kern = d == 128 ? (f16 ? (il ? kv8_append_norm_rope_kernel<128, kElemF16, true> : kv8_append_norm_rope_kernel<128, kElemF16, false>)
+                                : (il ? kv8_append_norm_rope_kernel<128, kElemBf16, true> : kv8_append_norm_rope_kernel<128, kElemBf16, false>))
+                         : (f16 ? (il ? kv8_append_norm_rope_kernel<64, kElemF16, true> : kv8_append_norm_rope_kernel<64, kElemF16, false>)
+                                : (il ? kv8_append_norm_rope_kernel<64, kElemBf16, true> : kv8_append_norm_rope_kernel<64, kElemBf16, false>));
+    return kv8::launch_dependent(kern, static_cast<int>(grid), kNormThreads, 0, stream, a, n);
 }
 
 }  // namespace fa

@@ -661,9 +661,9 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
 
 // A launch that may begin while the kernel before it on the stream is ending (it waits for
 // that one's results itself).
-template <class Params>
-cudaError_t launch_dependent(void (*kern)(Params), dim3 grid, int threads, int smem, cudaStream_t stream,
-                             const Params& p) {
+template <class... Params>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                             const Params&... p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -674,7 +674,7 @@ cudaError_t launch_dependent(void (*kern)(Params), dim3 grid, int threads, int s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, p...);
 }
 
 }  // namespace kv8

@@ -328,6 +328,68 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
                      const int* cu_seqlens, int total_tokens, float scale, cudaStream_t stream);
 
 /*
+ * Norms of queries and keys for each head, and their rotation by position, in one pass over
+ * the output of a projection: what stands between it and the attention calls above.
+ *
+ * Each head's row x of d channels becomes
+ *   n_c = x_c r w_c,  r = 1 / sqrt(mean of the x_c^2 + eps)      (norm != 0; else n = x)
+ * with q_weight or k_weight for w (null: 1), and its first `rot` channels are turned in pairs:
+ * pair f = 0 .. rot / 2 - 1 is the channels (a, b) = (f, f + rot / 2), or (2 f, 2 f + 1) with
+ * interleaved != 0, and
+ *   y_a = n_a cos t - n_b sin t,  y_b = n_b cos t + n_a sin t;   other channels: y = n.
+ * The angle t is position times frequency.  turns[f] is frequency f as a share of a turn in
+ * units of 2^-64, round(2^64 frequency / (2 pi)) mod 2^64 for a frequency in radians a
+ * position, and t = 2 pi ((position * turns[f]) mod 2^64) / 2^64: no rounding grows with the
+ * position, which may be any int32.  With several axes (time, height, width of images and
+ * video) frequency f goes by axis axes[f].
+ *   q, k            device, read: T tokens of Hq and Hkv heads of d channels, bf16 or fp16,
+ *                   heads contiguous, tokens `stride` elements apart (a multiple of 8, heads * d
+ *                   if contiguous; slices of a wider projection's output, say).  Hq need not
+ *                   be a multiple of Hkv.
+ *   q_out, k_out    device, written: the same type and shapes; may be q and k themselves
+ *                   (with their strides), and must not overlap them otherwise
+ *   q_weight, k_weight   device, [d], 16-byte aligned, of the type of q, or fp32 with
+ *                   weights_f32 != 0; each may be null; null both without a norm
+ *   eps             finite and > 0 (ignored without a norm)
+ *   positions       device, int32 [num_axes, T] (num_axes rows of T); null if rot is 0
+ *   axes            device, int32 [rot / 2], each 0 .. num_axes - 1 (others count as 0); only
+ *                   read if num_axes > 1 (up to 4)
+ *   turns           device, uint64 [rot / 2]; null if rot is 0
+ *   rot             a multiple of 16 from 0 to d
+ * All arithmetic is in fp32 (squares of values beyond 2^63 overflow), the cosines and sines are
+ * those of sincospif, and each output is rounded once.  Infinities and NaN go where the formula
+ * takes them: into their own row only.  d in {64, 128}.  Enqueues one kernel.
+ *
+ * fa_norm_rope_bwd: the gradients dq, dk of q and k, and dq_weight, dk_weight (fp32 [d], each
+ * may be null) of the weights, from the outputs' gradients dq_out, dk_out.  With dn the output's
+ * gradient turned back, xh = x r and g = dn w:
+ *   dx = r (g - xh mean(g xh)),   dw = sum over tokens and heads of dn xh    (no norm: dx = dn).
+ * q and k are fa_norm_rope's inputs (not read, and may be null, without a norm); dq and dk may be
+ * dq_out and dk_out.  The sums of dw are in fp32 within a CTA and fp64 across them, in one order
+ * for given sizes: the same inputs give the same bits.  The workspace (256-byte aligned,
+ * fa_norm_rope_bwd_workspace_size bytes, contents ignored; not to be shared by calls in flight
+ * together) is needed only for a weight's gradient.  Enqueues one kernel, and a second one
+ * for the weights' gradients.  T = 0 writes zeros to them.
+ */
+fa_status fa_norm_rope(fa_dtype dtype, const void* q, long long q_stride, const void* k,
+                       long long k_stride, void* q_out, long long q_out_stride, void* k_out,
+                       long long k_out_stride, int T, int Hq, int Hkv, int d, int norm,
+                       const void* q_weight, const void* k_weight, int weights_f32, float eps,
+                       const int* positions, const int* axes, int num_axes,
+                       const unsigned long long* turns, int rot, int interleaved,
+                       cudaStream_t stream);
+size_t fa_norm_rope_bwd_workspace_size(int T, int Hq, int Hkv, int d);
+fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, const void* k,
+                           long long k_stride, const void* dq_out, long long dq_out_stride,
+                           const void* dk_out, long long dk_out_stride, void* dq,
+                           long long dq_stride, void* dk, long long dk_stride, int T, int Hq,
+                           int Hkv, int d, int norm, const void* q_weight, const void* k_weight,
+                           int weights_f32, float eps, float* dq_weight, float* dk_weight,
+                           const int* positions, const int* axes, int num_axes,
+                           const unsigned long long* turns, int rot, int interleaved,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Attention over a paged cache held in 8 bits: the serving form.  Three entry points
  * make one step of a server: fa_kv8_plan gives the requests' new tokens their places,
  * fa_kv8_append writes the new keys and values there, fa_fwd_kv8 attends to them.  All
@@ -385,6 +447,12 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  * a block begun by another writer may have any positive scale.)  Infinities and NaN become NaN
  * codes.
  *
+ * fa_kv8_append_norm_rope: fa_norm_rope and fa_kv8_append in one kernel.  q goes to q_out as
+ * in fa_norm_rope; k is normed and rotated in fp32, and the block's scale and codes come from
+ * those numbers as above (rounded once, where the two calls would round them to 16 bits in
+ * between); v goes to the cache as it is.  T tokens of each, with strides of their own; the
+ * tokens without a slot get their q_out too.  Arguments otherwise as there.
+ *
  * fa_fwd_kv8: O and LSE of the new tokens' attention over the cache.
  *   q            device, read: bf16 or fp16; dense [B, N, Hq, d] or packed [T, Hq, d],
  *                tokens `q_stride` elements apart (a multiple of 8, Hq d if contiguous)
@@ -422,6 +490,15 @@ fa_status fa_kv8_plan(const int* lens, const int* grow, int B, int* table, int w
 fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long stride, void* k8,
                         float* k_scale, void* v8, float* v_scale, int num_pages, int page, int Hkv,
                         int d, const int* slots, int T, cudaStream_t stream);
+fa_status fa_kv8_append_norm_rope(fa_dtype dtype, const void* q, long long q_stride, const void* k,
+                                  long long k_stride, const void* v, long long v_stride, void* q_out,
+                                  long long q_out_stride, void* k8, float* k_scale, void* v8,
+                                  float* v_scale, int num_pages, int page, int Hq, int Hkv, int d,
+                                  const int* slots, int T, int norm, const void* q_weight,
+                                  const void* k_weight, int weights_f32, float eps,
+                                  const int* positions, const int* axes, int num_axes,
+                                  const unsigned long long* turns, int rot, int interleaved,
+                                  cudaStream_t stream);
 size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens);
 fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
                      const float* k_scale, const void* v8, const float* v_scale, int num_pages,
