@@ -29,6 +29,7 @@ __all__ = [
     "fa_bwd_dq_heads",
     "fa_fwd_fp8", "Fp8Operands", "quantize_fp8", "attention_forward_fp8",
     "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_rope_bwd_workspace_size", "fa_kv8_append_norm_rope",
+    "fa_fwd_kv8_prefix", "fa_fwd_kv8_prefix_workspace_size", "attention_forward_kv8_prefix",
     "RopePlan", "rope_plan", "norm_rope_forward", "norm_rope_backward", "kv8_append_norm_rope",
     "fa_kv8_plan", "fa_kv8_append", "fa_fwd_kv8", "fa_fwd_kv8_workspace_size", "FA_KV8_BLOCK",
     "Kv8Cache", "kv8_cache", "kv8_plan", "kv8_append", "attention_forward_kv8",
@@ -138,6 +139,11 @@ def load(path: str | None = None):
     lib.fa_fwd_kv8.argtypes = [_i, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i,
                                _i, _i, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]
     lib.fa_fwd_kv8.restype = _i
+    lib.fa_fwd_kv8_prefix_workspace_size.argtypes = [_i] * 6
+    lib.fa_fwd_kv8_prefix_workspace_size.restype = _sz
+    lib.fa_fwd_kv8_prefix.argtypes = [_i, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _vp, _vp,
+                                      _vp, _i, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]
+    lib.fa_fwd_kv8_prefix.restype = _i
     lib.fa_device_status.argtypes = [_vp]
     lib.fa_device_status.restype = _i
     lib.fa_set_wait_limit_cycles.argtypes = [_ll]
@@ -500,6 +506,25 @@ def fa_fwd_kv8(dtype, q, q_stride, k8, k_scale, v8, v_scale, num_pages, page, ta
                            _ptr(lse), B, Hq, Hkv, N, d, int(bool(causal)), int(window),
                            _ptr(cu_seqlens), int(total_tokens), float(scale), _ptr(workspace),
                            int(workspace_bytes), _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def fa_fwd_kv8_prefix_workspace_size(B, Hq, Hkv, N, d, total_tokens) -> int:
+    """Workspace bytes of fa_fwd_kv8_prefix (total_tokens: T for a packed batch, 0 for a dense one)."""
+    return int(load().fa_fwd_kv8_prefix_workspace_size(B, Hq, Hkv, N, d, int(total_tokens)))
+
+
+def fa_fwd_kv8_prefix(dtype, q, q_stride, k8, k_scale, v8, v_scale, num_pages, page, prefix_table, prefix_width,
+                      prefix_lens, prefix_cu, groups, table, width, lens, o, lse, B, Hq, Hkv, N, d, cu_seqlens,
+                      total_tokens, scale, workspace, workspace_bytes, stream=None, check: bool = True) -> int:
+    """Attention of new tokens over shared prefixes and their own keys in the 8-bit cache (see include/fa.h)."""
+    st = load().fa_fwd_kv8_prefix(int(dtype), _ptr(q), int(q_stride), _ptr(k8), _ptr(k_scale), _ptr(v8), _ptr(v_scale),
+                                  num_pages, page, _ptr(prefix_table), prefix_width, _ptr(prefix_lens), _ptr(prefix_cu),
+                                  groups, _ptr(table), width, _ptr(lens), _ptr(o), _ptr(lse), B, Hq, Hkv, N, d,
+                                  _ptr(cu_seqlens), int(total_tokens), float(scale), _ptr(workspace),
+                                  int(workspace_bytes), _stream(stream))
     if check:
         _check(st)
     return st
@@ -1005,19 +1030,9 @@ def _kv8_workspace(device, B, Hq, Hkv, N, d, total_tokens):
     return fa_fwd_kv8_workspace_size(B, Hq, Hkv, N, d, total_tokens)
 
 
-def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, window=0, scale=None,
-                          cu_seqlens=None, max_seqlen=None, stream=None, out=None, lse=None,
-                          workspace=None):
-    """O, LSE of new tokens' attention over the paged 8-bit cache, which holds their own keys
-    and values already.  q: bf16 or fp16, dense [B, N, Hq, d] or packed [T, Hq, d] with
-    cu_seqlens (int32 [B + 1]) and max_seqlen; its tokens may lie apart (a slice of a wider
-    tensor).  table: int32 [B, width], lens: int32 [B], as kv8_plan keeps them.  Allocates
-    what of the outputs and the workspace (uint8, fa_fwd_kv8_workspace_size) is not given."""
-    dev = q.get_device()
-    if dev >= 0 and _elsewhere(dev, stream):
-        return _there(attention_forward_kv8, dev, stream, q, cache, table, lens, causal=causal,
-                      window=window, scale=scale, cu_seqlens=cu_seqlens, max_seqlen=max_seqlen, out=out,
-                      lse=lse, workspace=workspace)
+def _kv8_call(q, cache, table, lens, cu_seqlens, max_seqlen, out, lse, workspace, dev):
+    """What the attention calls over the 8-bit cache have in common, checked, outputs allocated:
+    (dtype, stride, num_pages, page, width, B, Hq, Hkv, N, d, T, out, lse)."""
     import torch
     dtype = _dtype_code(q)
     packed = cu_seqlens is not None
@@ -1043,8 +1058,8 @@ def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, windo
         if shape[0] != B:
             raise ValueError(f"q has {shape[0]} requests, lens {B}")
         N, T, lse_shape = shape[1], 0, (B, Hq, shape[1])
-    if not (-_INT <= window < _INT and -_INT <= N < _INT and T < _INT and width < _INT):
-        raise _beyond(window=window, max_seqlen=N, tokens=T, width=width)
+    if not (-_INT <= N < _INT and T < _INT and width < _INT):
+        raise _beyond(max_seqlen=N, tokens=T, width=width)
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
     elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
@@ -1053,18 +1068,80 @@ def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, windo
         lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
     elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError(f"lse must be contiguous float32 {lse_shape} on q's device")
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous, on q's device")
+    return dtype, stride, num_pages, page, width, B, Hq, Hkv, N, d, T, out, lse
+
+
+def attention_forward_kv8(q, cache: Kv8Cache, table, lens, *, causal=True, window=0, scale=None,
+                          cu_seqlens=None, max_seqlen=None, stream=None, out=None, lse=None,
+                          workspace=None):
+    """O, LSE of new tokens' attention over the paged 8-bit cache, which holds their own keys
+    and values already.  q: bf16 or fp16, dense [B, N, Hq, d] or packed [T, Hq, d] with
+    cu_seqlens (int32 [B + 1]) and max_seqlen; its tokens may lie apart (a slice of a wider
+    tensor).  table: int32 [B, width], lens: int32 [B], as kv8_plan keeps them.  Allocates
+    what of the outputs and the workspace (uint8, fa_fwd_kv8_workspace_size) is not given."""
+    dev = q.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(attention_forward_kv8, dev, stream, q, cache, table, lens, causal=causal,
+                      window=window, scale=scale, cu_seqlens=cu_seqlens, max_seqlen=max_seqlen, out=out,
+                      lse=lse, workspace=workspace)
+    import torch
+    dtype, stride, num_pages, page, width, B, Hq, Hkv, N, d, T, out, lse = _kv8_call(
+        q, cache, table, lens, cu_seqlens, max_seqlen, out, lse, workspace, dev)
+    if not -_INT <= window < _INT:
+        raise _beyond(window=window)
     if workspace is None:
         workspace = torch.empty(_kv8_workspace(dev, B, Hq, Hkv, N, d, T), dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous, on q's device")
     k8, k_scale, v8, v_scale = cache
     _check(load().fa_fwd_kv8(
         dtype, q.data_ptr(), stride, k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(),
         v_scale.data_ptr(), num_pages, page, table.data_ptr(), width, lens.data_ptr(), out.data_ptr(),
         lse.data_ptr(), B, Hq, Hkv, N, d, 1 if causal else 0, window,
-        cu_seqlens.data_ptr() if packed else None, T, d ** -0.5 if scale is None else scale,
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), T, d ** -0.5 if scale is None else scale,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         torch._C._cuda_getCurrentRawStream(dev)))
+    return out, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace(device, B, Hq, Hkv, N, d, total_tokens):
+    """fa_fwd_kv8_prefix_workspace_size on CUDA device number `device`, the current one."""
+    return fa_fwd_kv8_prefix_workspace_size(B, Hq, Hkv, N, d, total_tokens)
+
+
+def attention_forward_kv8_prefix(q, cache: Kv8Cache, prefix_table, prefix_lens, prefix_cu, table, lens, *, scale=None,
+                                 cu_seqlens=None, max_seqlen=None, stream=None, out=None, lse=None, workspace=None):
+    """:func:`attention_forward_kv8` (causal, no window) for a batch whose requests share prefixes: the
+    new tokens prefix_cu[p] .. prefix_cu[p + 1] - 1 (int32 [groups + 1]; dense batches: token b N + i) see
+    all of the first prefix_lens[p] tokens of row p of prefix_table (int32 [groups], [groups, width]),
+    which are read once for all of them, and then their request's own, ``table`` and ``lens``."""
+    dev = q.get_device()
+    if dev >= 0 and _elsewhere(dev, stream):
+        return _there(attention_forward_kv8_prefix, dev, stream, q, cache, prefix_table, prefix_lens, prefix_cu, table,
+                      lens, scale=scale, cu_seqlens=cu_seqlens, max_seqlen=max_seqlen, out=out, lse=lse,
+                      workspace=workspace)
+    import torch
+    dtype, stride, num_pages, page, width, B, Hq, Hkv, N, d, T, out, lse = _kv8_call(
+        q, cache, table, lens, cu_seqlens, max_seqlen, out, lse, workspace, dev)
+    if prefix_lens.dim() != 1 or prefix_table.dim() != 2:
+        raise ValueError("prefix_lens must be [groups], prefix_table [groups, width]")
+    groups, prefix_width = prefix_lens.shape[0], prefix_table.shape[1]
+    _int32("prefix_lens", prefix_lens, (groups,), dev)
+    _int32("prefix_table", prefix_table, (groups, prefix_width), dev)
+    _int32("prefix_cu", prefix_cu, (groups + 1,), dev)
+    if prefix_width >= _INT:
+        raise _beyond(prefix_width=prefix_width)
+    if workspace is None:
+        size = _prefix_workspace(dev, B, Hq, Hkv, N, d, T) if q.numel() else 0
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    k8, k_scale, v8, v_scale = cache
+    _check(load().fa_fwd_kv8_prefix(
+        dtype, q.data_ptr(), stride, k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(), v_scale.data_ptr(), num_pages,
+        page, prefix_table.data_ptr(), prefix_width, prefix_lens.data_ptr(), prefix_cu.data_ptr(), groups,
+        table.data_ptr(), width, lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, N, d,
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), T, d ** -0.5 if scale is None else scale,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), torch._C._cuda_getCurrentRawStream(dev)))
     return out, lse
 
 

@@ -1196,6 +1196,102 @@ fa_status make_page_map(CUtensorMap* map, const void* base, int num_pages, int H
     return FA_OK;
 }
 
+fa_status check_workspace(const char* who, const void* workspace, size_t bytes, size_t need) {
+    if (!workspace || bytes < need)
+        return fail(FA_ERR_WORKSPACE, "%s: workspace of at least %zu bytes needed, got %zu%s", who, need, bytes,
+                    workspace ? "" : " (null)");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(FA_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", who);
+    return FA_OK;
+}
+
+// Checks and takes over what attention over the cache needs to know, but for the workspace.
+fa_status take_kv8_fwd(const char* who, fa_dtype dtype, const Geometry& g, const void* q, long long q_stride,
+                       const void* k8, const float* k_scale, const void* v8, const float* v_scale, int num_pages,
+                       int page, const int* table, int width, const int* lens, void* o, float* lse, int d, float scale,
+                       Kv8FwdParams* p) {
+    const int B = g.seq.B, Hq = g.seq.Hq, Hkv = g.seq.Hkv;
+    fa_status st;
+    if ((st = check_pages(who, num_pages, page, &p->page_log2)) != FA_OK) return st;
+    if ((st = check_table(who, B, width, page)) != FA_OK) return st;
+    if (!k8 || !k_scale || !v8 || !v_scale || !table || !lens || (g.tokens > 0 && (!q || !o || !lse)))
+        return fail(FA_ERR_INVALID_ARG, "%s: every pointer must be non-null", who);
+    if (!aligned16(q) || !aligned16(k8) || !aligned16(v8) || !aligned16(o) || !aligned16(lse) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(table) || !aligned4(lens))
+        return fail(FA_ERR_INVALID_ARG, "%s: q, k8, v8, o and lse must be 16-byte aligned, the scales, table and "
+                    "lens 4-byte aligned", who);
+    if (q_stride % 8 != 0 || q_stride < static_cast<long long>(Hq) * d)
+        return fail(FA_ERR_INVALID_ARG, "%s: q_stride %lld must be a multiple of 8 and at least Hq * d", who, q_stride);
+    if (static_cast<long long>(num_pages) * Hkv > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "%s: num_pages * Hkv = %lld is 2^31 or more", who,
+                    static_cast<long long>(num_pages) * Hkv);
+    p->group_inv = static_cast<uint32_t>(((1ull << 32) + g.seq.group - 1) / g.seq.group);
+    if (static_cast<long long>(g.tokens) * g.seq.group > INT_MAX - 128)
+        return fail(FA_ERR_UNSUPPORTED, "%s: problem too large for one launch", who);
+    // (the narrow kernels count key tiles of all items in 32 bits)
+    if (static_cast<long long>(B) * Hkv * ((static_cast<long long>(width) * page + 127) / 128 + 1) > INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "%s: B * Hkv * width * page = %lld is too large for one launch", who,
+                    static_cast<long long>(B) * Hkv * width * page);
+    p->columns = kv8_columns(g.seq.N, g.seq.group);
+    p->ctas = 2 * sm_count();
+    p->seq = g.seq;
+    p->q = q;
+    p->q_stride = q_stride;
+    p->v8 = static_cast<const uint8_t*>(v8);
+    p->k_scale = k_scale;
+    p->v_scale = v_scale;
+    p->table = table;
+    p->lens = lens;
+    p->o = o;
+    p->lse = lse;
+    p->o_f32 = 0;
+    p->width = width;
+    p->num_pages = num_pages;
+    p->scale_log2 = scale * kLog2e;
+    p->elem = static_cast<int>(dtype);
+    p->timeout_cycles = std::min(g_wait_limit.load(), kKv8MaxWaitCycles);
+    return FA_OK;
+}
+
+// The tensor maps, the parts of the workspace and the status word.
+fa_status place_kv8_fwd(Kv8FwdParams* p, const void* k8, const void* v8, int Hkv, int page, int d, void* workspace) {
+    // the kernel for items of 128 rows copies 64 keys at a time
+    const int box = p->columns == 128 && page > 64 ? 64 : page;
+    fa_status st;
+    if ((st = make_page_map(&p->tm_k, k8, p->num_pages, Hkv, page, d, box, "k8")) != FA_OK) return st;
+    if ((st = make_page_map(&p->tm_v, v8, p->num_pages, Hkv, page, d, box, "v8")) != FA_OK) return st;
+    const Kv8Workspace w = kv8_workspace(p->ctas, p->columns, d);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p->joins = reinterpret_cast<Kv8Join*>(ws);
+    p->part_stat = reinterpret_cast<float2*>(ws + w.stat);
+    p->part_o = reinterpret_cast<float*>(ws + w.o);
+    p->status = status_word_ptr();
+    if (!p->status) return fail(FA_ERR_CUDA, "attention over the 8-bit cache: cannot resolve the device status word");
+    return FA_OK;
+}
+
+// Byte layout of fa_fwd_kv8_prefix's workspace: that of the prefixes' pass, that of the own keys'
+// (at `own`), and O (fp32) and LSE of each.
+struct PrefixWorkspace {
+    size_t own, part[2], lse[2], full;
+};
+PrefixWorkspace prefix_workspace(const Geometry& g, int d) {
+    auto pad = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    const int ctas = 2 * sm_count();
+    const size_t rows = static_cast<size_t>(g.tokens) * g.seq.Hq;
+    PrefixWorkspace w;
+    w.own = kv8_workspace(ctas, kv8_columns(g.tokens, g.seq.group), d).full;
+    size_t at = w.own + kv8_workspace(ctas, kv8_columns(g.seq.N, g.seq.group), d).full;
+    for (int i = 0; i < 2; ++i) {
+        w.part[i] = at;
+        at += pad(rows * d * sizeof(float));
+        w.lse[i] = at;
+        at += pad(rows * sizeof(float));
+    }
+    w.full = at;
+    return w;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -1325,64 +1421,78 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
     st = check_common(B, Hq, Hkv, N, d, causal, window, cu_seqlens, total_tokens, scale, &g);
     if (st != FA_OK) return st;
     Kv8FwdParams p;
-    if ((st = check_pages("fa_fwd_kv8", num_pages, page, &p.page_log2)) != FA_OK) return st;
-    if ((st = check_table("fa_fwd_kv8", B, width, page)) != FA_OK) return st;
-    if (!k8 || !k_scale || !v8 || !v_scale || !table || !lens || (g.tokens > 0 && (!q || !o || !lse)))
-        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: every pointer must be non-null");
-    if (!aligned16(q) || !aligned16(k8) || !aligned16(v8) || !aligned16(o) || !aligned16(lse) ||
-        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(table) || !aligned4(lens))
-        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: q, k8, v8, o and lse must be 16-byte aligned, "
-                    "the scales, table and lens 4-byte aligned");
-    if (q_stride % 8 != 0 || q_stride < static_cast<long long>(Hq) * d)
-        return fail(FA_ERR_INVALID_ARG, "fa_fwd_kv8: q_stride %lld must be a multiple of 8 and at "
-                    "least Hq * d", q_stride);
-    if (static_cast<long long>(num_pages) * Hkv > INT_MAX)
-        return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: num_pages * Hkv = %lld is 2^31 or more",
-                    static_cast<long long>(num_pages) * Hkv);
-    p.group_inv = static_cast<uint32_t>(((1ull << 32) + g.seq.group - 1) / g.seq.group);
-    if (static_cast<long long>(g.tokens) * g.seq.group > INT_MAX - 128)
-        return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: problem too large for one launch");
-    // (the narrow kernels count key tiles of all items in 32 bits)
-    if (static_cast<long long>(B) * Hkv * ((static_cast<long long>(width) * page + 127) / 128 + 1) > INT_MAX)
-        return fail(FA_ERR_UNSUPPORTED, "fa_fwd_kv8: B * Hkv * width * page = %lld is too large for one launch",
-                    static_cast<long long>(B) * Hkv * width * page);
-    if (g.tokens == 0) return FA_OK;
-    p.columns = kv8_columns(N, g.seq.group);
-    p.ctas = 2 * sm_count();
-    const Kv8Workspace w = kv8_workspace(p.ctas, p.columns, d);
-    const size_t need = w.full;
-    if (!workspace || workspace_bytes < need)
-        return fail(FA_ERR_WORKSPACE, "fa_fwd_kv8: workspace of at least %zu bytes needed, got %zu%s",
-                    need, workspace_bytes, workspace ? "" : " (null)");
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
-        return fail(FA_ERR_WORKSPACE, "fa_fwd_kv8: workspace must be 256-byte aligned");
-    p.seq = g.seq;
-    p.q = q;
-    p.q_stride = q_stride;
-    // the kernel for items of 128 rows copies 64 keys at a time
-    const int box = p.columns == 128 && page > 64 ? 64 : page;
-    if ((st = make_page_map(&p.tm_k, k8, num_pages, Hkv, page, d, box, "k8")) != FA_OK) return st;
-    if ((st = make_page_map(&p.tm_v, v8, num_pages, Hkv, page, d, box, "v8")) != FA_OK) return st;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.joins = reinterpret_cast<Kv8Join*>(ws);
-    p.part_stat = reinterpret_cast<float2*>(ws + w.stat);
-    p.part_o = reinterpret_cast<float*>(ws + w.o);
-    p.v8 = static_cast<const uint8_t*>(v8);
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.table = table;
-    p.lens = lens;
-    p.o = o;
-    p.lse = lse;
-    p.width = width;
-    p.num_pages = num_pages;
-    p.scale_log2 = scale * kLog2e;
-    p.elem = static_cast<int>(dtype);
-    p.timeout_cycles = std::min(g_wait_limit.load(), kKv8MaxWaitCycles);
-    p.status = status_word_ptr();
-    if (!p.status) return fail(FA_ERR_CUDA, "fa_fwd_kv8: cannot resolve the device status word");
+    st = take_kv8_fwd("fa_fwd_kv8", dtype, g, q, q_stride, k8, k_scale, v8, v_scale, num_pages, page, table, width, lens,
+                      o, lse, d, scale, &p);
+    if (st != FA_OK || g.tokens == 0) return st;
+    const size_t need = kv8_workspace(p.ctas, p.columns, d).full;
+    if ((st = check_workspace("fa_fwd_kv8", workspace, workspace_bytes, need)) != FA_OK) return st;
+    if ((st = place_kv8_fwd(&p, k8, v8, Hkv, page, d, workspace)) != FA_OK) return st;
     const cudaError_t e = launch_fwd_kv8(p, d, ev, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_kv8 launch");
+}
+
+size_t fa_fwd_kv8_prefix_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens) {
+    fa::Geometry g;
+    if (!fa::query_geometry(B, Hq, Hkv, N, d, 0, 0, total_tokens, &g)) return 0;
+    return fa::prefix_workspace(g, d).full;
+}
+
+fa_status fa_fwd_kv8_prefix(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
+                            const float* k_scale, const void* v8, const float* v_scale,
+                            int num_pages, int page, const int* prefix_table, int prefix_width,
+                            const int* prefix_lens, const int* prefix_cu, int groups,
+                            const int* table, int width, const int* lens, void* o, float* lse,
+                            int B, int Hq, int Hkv, int N, int d, const int* cu_seqlens,
+                            int total_tokens, float scale, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+    using namespace fa;
+    t_last_error[0] = '\0';
+    constexpr const char* who = "fa_fwd_kv8_prefix";
+    fa_status st = check_dtype(dtype, who);
+    if (st != FA_OK) return st;
+    // the requests' own keys, and the groups' rows (any number of them up to all) over the prefixes
+    Geometry g, g0;
+    st = check_common(B, Hq, Hkv, N, d, 1, 0, cu_seqlens, total_tokens, scale, &g);
+    if (st != FA_OK) return st;
+    if (!prefix_cu || !prefix_table || !prefix_lens)
+        return fail(FA_ERR_INVALID_ARG, "%s: every pointer must be non-null", who);
+    if (groups < 1) return fail(FA_ERR_INVALID_ARG, "%s: groups must be >= 1 (got %d)", who, groups);
+    if (static_cast<long long>(g.tokens) * Hq > 8LL * INT_MAX)
+        return fail(FA_ERR_UNSUPPORTED, "%s: problem too large for one launch", who);
+    st = check_common(groups, Hq, Hkv, std::max(g.tokens, 1), d, 0, 0, prefix_cu, g.tokens, scale, &g0);
+    if (st != FA_OK) return st;
+    Kv8FwdParams p, p0;
+    st = take_kv8_fwd(who, dtype, g, q, q_stride, k8, k_scale, v8, v_scale, num_pages, page, table, width, lens, o, lse,
+                      d, scale, &p);
+    if (st != FA_OK) return st;
+    st = take_kv8_fwd(who, dtype, g0, q, q_stride, k8, k_scale, v8, v_scale, num_pages, page, prefix_table, prefix_width,
+                      prefix_lens, o, lse, d, scale, &p0);
+    if (st != FA_OK || g.tokens == 0) return st;
+    const PrefixWorkspace w = prefix_workspace(g, d);
+    if ((st = check_workspace(who, workspace, workspace_bytes, w.full)) != FA_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if ((st = place_kv8_fwd(&p0, k8, v8, Hkv, page, d, ws)) != FA_OK) return st;
+    if ((st = place_kv8_fwd(&p, k8, v8, Hkv, page, d, ws + w.own)) != FA_OK) return st;
+    Kv8PrefixJoinParams j{};
+    j.seq = g.seq;
+    j.prefix_cu = prefix_cu;
+    j.groups = groups;
+    j.o = o;
+    j.out_lse = lse;
+    j.elem = p.elem;
+    int i = 0;
+    for (Kv8FwdParams* x : {&p0, &p}) {
+        x->o_f32 = 1;
+        x->o = ws + w.part[i];
+        x->lse = reinterpret_cast<float*>(ws + w.lse[i]);
+        j.part[i] = static_cast<const float*>(x->o);
+        j.lse[i] = x->lse;
+        ++i;
+    }
+    cudaError_t e = launch_fwd_kv8(p0, d, nullptr, stream);
+    if (e == cudaSuccess) e = launch_fwd_kv8(p, d, nullptr, stream);
+    if (e == cudaSuccess) e = launch_kv8_prefix_join(j, d, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_kv8_prefix launch");
 }
 
 }  // extern "C"

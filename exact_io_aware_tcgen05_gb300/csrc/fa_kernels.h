@@ -200,8 +200,9 @@ struct Kv8FwdParams {
     const float* v_scale;
     const int* table;   // [B, width]
     const int* lens;    // [B]
-    void* o;
+    void* o;            // 16-bit, or fp32 with o_f32
     float* lse;
+    int o_f32;
     int width, num_pages, page_log2;
     uint32_t group_inv; // ceil(2^32 / group)
     int columns;        // rows of an item (kv8_columns)
@@ -214,6 +215,19 @@ struct Kv8FwdParams {
     int elem;
     long long timeout_cycles;
     int* status;
+};
+
+// Attention with shared prefixes: the two parts, over the prefixes (0) and over the requests'
+// own keys (1), that fa_kv8_prefix_join_kernel puts together.
+struct Kv8PrefixJoinParams {
+    SeqInfo seq;             // as of the call
+    const int* prefix_cu;    // [groups + 1]
+    int groups;
+    const float* part[2];    // [tokens, Hq, d]
+    const float* lse[2];     // [Hq, tokens]; as out_lse
+    void* o;
+    float* out_lse;
+    int elem;
 };
 
 // Launchers (defined in the kernel translation units).  They only enqueue on
@@ -243,6 +257,8 @@ cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRope
 cudaError_t launch_fwd_kv8_rows(const Kv8FwdParams& p, int d, cudaStream_t stream);
 // launch_fwd_kv8 records ev[0..2] (if not null) around its two kernels.
 cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, cudaStream_t stream);
+
+cudaError_t launch_kv8_prefix_join(const Kv8PrefixJoinParams& p, int d, cudaStream_t stream);
 
 int* device_status_word();  // library-owned device status word (fa_api.cu)
 

@@ -239,7 +239,8 @@ __device__ __noinline__ uint32_t find_nan(const Kv8FwdParams& p, const Part& par
     return spoilt;
 }
 
-template <int D, int E, int C>
+// F32: O in fp32 (one of two parts that another kernel joins)
+template <int D, int E, int C, bool F32>
 __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_constant__ Kv8FwdParams p) {
     using K = Kv8Cfg<D, E, C>;
     constexpr int kSlots = kv8_slots<D, E, C>();
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     Part part;
 
     if (warp == 0) {
-        produce<D, C, kKeys, kSlots>(p, sm, sKV);
+        produce<D, C, kKeys, kSlots, F32>(p, sm, sKV);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
         // Walks the tiles of all parts one behind the other, one tile ahead with S^T.  After
@@ -664,8 +665,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
                         if (n >= nrows || key >= D) continue;
                         if (part.whole) {
                             const long long at = sm.out_at[buf][n] + key;
-                            if (fa_index_ok(at, static_cast<long long>(p.seq.total_tokens) * p.seq.Hq * D, p.status))
-                                static_cast<uint16_t*>(p.o)[at] = static_cast<uint16_t>(pack2<E>(x, 0.f));
+                            if (fa_index_ok(at, static_cast<long long>(p.seq.total_tokens) * p.seq.Hq * D, p.status)) {
+                                if (F32) static_cast<float*>(p.o)[at] = x;
+                                else static_cast<uint16_t*>(p.o)[at] = static_cast<uint16_t>(pack2<E>(x, 0.f));
+                            }
                         } else {
                             p.part_o[(slot * C + n) * D + key] = x;
                         }
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 // Its lanes take 32 parts' references and sums at a time, then the warp adds those parts'
 // accumulators up in their order; the first two parts' (there are always two) are on their way
 // before their weights are known.
-template <int D, int E>
+template <int D, int E, bool F32>
 __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -754,36 +757,89 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     if (!fa_index_ok(row, p.seq.total_tokens, p.status)) return;
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int c = 0; c < kPer; ++c)
-        static_cast<uint16_t*>(p.o)[(row * p.seq.Hq + head) * D + lane + 32 * c] =
-            static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
+    for (int c = 0; c < kPer; ++c) {
+        const long long at = (row * p.seq.Hq + head) * D + lane + 32 * c;
+        if (F32) static_cast<float*>(p.o)[at] = o[c] * inv;
+        else static_cast<uint16_t*>(p.o)[at] = static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
+    }
     if (lane == 0)
         p.lse[row_stat_index(p.seq, j.b, head, j.start, tok)] =
             sum != 0.f ? ((m == kNegInf ? 0.f : m) - kShift + log2f(sum)) * kLn2 : kNegInf;
 }
 
-template <int D, int E, int C>
+template <int D, int E, int C, bool F32>
 cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
     constexpr int smem = kv8_smem_bytes<D, E, C>();
     static_assert(smem <= kCtaSmem, "shared memory per CTA");
-    auto kern = fa_fwd_kv8_kernel<D, E, C>;
+    auto kern = fa_fwd_kv8_kernel<D, E, C, F32>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, p.ctas, kThreads, smem, stream, p);
 }
 
-template <int D, int E>
-cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
+template <int D, int E, bool F32>
+cudaError_t launch_both_as(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
     cudaError_t e = ev ? cudaEventRecord(ev[0], stream) : cudaSuccess;
     if (e == cudaSuccess)
-        e = p.columns == 8    ? launch_attend<D, E, 8>(p, stream)
-            : p.columns == 16 ? launch_attend<D, E, 16>(p, stream)
+        e = p.columns == 8    ? launch_attend<D, E, 8, F32>(p, stream)
+            : p.columns == 16 ? launch_attend<D, E, 16, F32>(p, stream)
                               : launch_fwd_kv8_rows(p, D, stream);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, dim3(p.ctas, p.columns / 8), 256, 0, stream, p);
+    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E, F32>, dim3(p.ctas, p.columns / 8), 256, 0, stream, p);
     if (e == cudaSuccess && ev) e = cudaEventRecord(ev[2], stream);
     return e;
+}
+
+template <int D, int E>
+cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
+    return p.o_f32 ? launch_both_as<D, E, true>(p, ev, stream) : launch_both_as<D, E, false>(p, ev, stream);
+}
+
+// Joins the two parts of attention with a shared prefix, O and LSE of each in fp32: a warp a row.
+// A row behind the last request is left as it was, one outside all groups has no first part.
+template <int D, int E>
+__global__ void __launch_bounds__(256) fa_kv8_prefix_join_kernel(const Kv8PrefixJoinParams p) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= static_cast<long long>(p.seq.total_tokens) * p.seq.Hq) return;
+    const int token = static_cast<int>(row / p.seq.Hq), h = static_cast<int>(row - static_cast<long long>(token) * p.seq.Hq);
+    long long at;   // of its LSE, as in fa_fwd
+    if (p.seq.cu_seqlens) {
+        if (token < p.seq.cu_seqlens[0] || token >= p.seq.cu_seqlens[p.seq.B]) return;
+        at = static_cast<long long>(h) * p.seq.total_tokens + token;
+    } else {
+        at = (static_cast<long long>(token / p.seq.N) * p.seq.Hq + h) * p.seq.N + token % p.seq.N;
+    }
+    const bool grouped = token >= p.prefix_cu[0] && token < p.prefix_cu[p.groups];
+    const float l0 = grouped ? p.lse[0][static_cast<long long>(h) * p.seq.total_tokens + token] : kNegInf;
+    const float l1 = p.lse[1][at];
+    const float top = fmaxf(l0, l1), ref = top == kNegInf ? 0.f : top;
+    const float w0 = expf(l0 - ref), w1 = expf(l1 - ref), sum = w0 + w1;
+    const float inv = sum > 0.f ? 1.f / sum : sum;   // (NaN stays; 0: nothing seen)
+    const float f0 = w0 * inv, f1 = w1 * inv;
+    constexpr int kPer = D / 32;
+    float x[kPer], y[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        x[i] = grouped ? p.part[0][row * D + kPer * lane + i] : 0.f;
+        y[i] = p.part[1][row * D + kPer * lane + i];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = f0 * x[i] + f1 * y[i];
+    uint32_t* out = static_cast<uint32_t*>(p.o) + (row * D + kPer * lane) / 2;
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) out[i] = pack2<E>(x[2 * i], x[2 * i + 1]);
+    if (lane == 0) p.out_lse[at] = sum > 0.f || sum != sum ? ref + logf(sum) : kNegInf;
+}
+
+template <int D, int E>
+cudaError_t launch_prefix_join(const Kv8PrefixJoinParams& p, cudaStream_t stream) {
+    const long long grid = (static_cast<long long>(p.seq.total_tokens) * p.seq.Hq + 7) / 8;
+    if (grid > INT_MAX) return cudaErrorInvalidValue;
+    return launch_dependent(fa_kv8_prefix_join_kernel<D, E>, dim3(static_cast<unsigned>(grid)), 256, 0, stream, p);
 }
 
 }  // namespace
@@ -794,6 +850,14 @@ cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, 
                                        : launch_both<128, kElemF16>(p, ev, stream);
     return p.elem == kElemBf16Code ? launch_both<64, kElemBf16>(p, ev, stream)
                                    : launch_both<64, kElemF16>(p, ev, stream);
+}
+
+cudaError_t launch_kv8_prefix_join(const Kv8PrefixJoinParams& p, int d, cudaStream_t stream) {
+    if (d == 128)
+        return p.elem == kElemBf16Code ? launch_prefix_join<128, kElemBf16>(p, stream)
+                                       : launch_prefix_join<128, kElemF16>(p, stream);
+    return p.elem == kElemBf16Code ? launch_prefix_join<64, kElemBf16>(p, stream)
+                                   : launch_prefix_join<64, kElemF16>(p, stream);
 }
 
 }  // namespace fa

@@ -186,7 +186,8 @@ __device__ __noinline__ void spoil_row(const Kv8FwdParams& p, const Part& part, 
     }
 }
 
-template <int D, int E>
+// F32: O in fp32 (one of two parts that another kernel joins)
+template <int D, int E, bool F32>
 __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __grid_constant__ Kv8FwdParams p) {
     using K = RowsCfg<D, E>;
     constexpr int kSlots = rows_slots<D, E>();
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     Part part;
 
     if (warp == 0) {
-        produce<D, kRows, kHalf, kSlots>(p, sm, sKV);
+        produce<D, kRows, kHalf, kSlots, F32>(p, sm, sKV);
     } else if (warp == 1) {
         // --------------------------------------------------------------- issuer
         // Walks the tiles of all parts one behind the other; S of a tile's half is issued
@@ -592,14 +593,18 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                 const long long slot = (2LL * blockIdx.x + (part.begins ? 1 : 0)) * kRows + row;
                 const bool in = real && fa_index_ok(token, p.seq.total_tokens, p.status);
                 uint16_t* out = static_cast<uint16_t*>(p.o) + (token * p.seq.Hq + head) * D;
-                float* partial = p.part_o + slot * D;
+                float* partial = F32 && whole ? static_cast<float*>(p.o) + (token * p.seq.Hq + head) * D : p.part_o + slot * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t x[32];
                     tmem_ld32(tO + c, x);
                     tmem_ld_wait();
                     reg_fence(x);
-                    if (in && whole) {
+                    if (F32 && in && whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * mul);
+                    }
+                    if (!F32 && in && whole) {
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             uint32_t y[4];
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
                                 make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
                     }
                 }
-                if (poison && in) spoil_row<D>(p, part, lo, hi, whole ? out : nullptr, whole ? nullptr : partial);
+                if (poison && in) spoil_row<D>(p, part, lo, hi, whole && !F32 ? out : nullptr, whole && !F32 ? nullptr : partial);
                 const float m = ref == kNone ? 0.f : ref + kShift;
                 if (in && whole)
                     p.lse[row_stat_index(p.seq, part.b, head, part.req.start, tok)] =
@@ -635,14 +640,19 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     if (warp == 1) tmem_dealloc(tmem, 256);
 }
 
-template <int D, int E>
-cudaError_t launch_rows(const Kv8FwdParams& p, cudaStream_t stream) {
+template <int D, int E, bool F32>
+cudaError_t launch_rows_as(const Kv8FwdParams& p, cudaStream_t stream) {
     constexpr int smem = rows_smem_bytes<D, E>();
     static_assert(smem <= kCtaSmem, "shared memory per CTA");
-    auto kern = fa_fwd_kv8_rows_kernel<D, E>;
+    auto kern = fa_fwd_kv8_rows_kernel<D, E, F32>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, p.ctas, kThreads, smem, stream, p);
+}
+
+template <int D, int E>
+cudaError_t launch_rows(const Kv8FwdParams& p, cudaStream_t stream) {
+    return p.o_f32 ? launch_rows_as<D, E, true>(p, stream) : launch_rows_as<D, E, false>(p, stream);
 }
 
 }  // namespace

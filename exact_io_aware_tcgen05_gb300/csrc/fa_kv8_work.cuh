@@ -492,7 +492,7 @@ __device__ __forceinline__ bool take_part(Smem& sm, int np, Part& part) {
 }
 
 // O = 0 and LSE = -inf for an item that sees no keys: `rows` rows from row0 on, by a warp.
-template <int D>
+template <int D, bool F32>
 static __device__ __noinline__ void rows_without_keys(const Kv8FwdParams& p, int b, int h, int start, int row0,
                                                       int rows) {
     const int lane = threadIdx.x & 31, G = p.seq.group;
@@ -501,8 +501,9 @@ static __device__ __noinline__ void rows_without_keys(const Kv8FwdParams& p, int
         const int tok = r / G, head = h * G + r % G;
         const long long token = start + tok;
         if (!fa_index_ok(token, p.seq.total_tokens, p.status)) continue;
-        uint16_t* out = static_cast<uint16_t*>(p.o) + (token * p.seq.Hq + head) * D;
-        if (lane < D / 8) *reinterpret_cast<uint4*>(out + 8 * lane) = make_uint4(0, 0, 0, 0);
+        constexpr int kUnits = D / (F32 ? 4 : 8);   // 16 bytes each
+        uint4* out = static_cast<uint4*>(p.o) + (token * p.seq.Hq + head) * kUnits;
+        if (lane < kUnits) out[lane] = make_uint4(0, 0, 0, 0);
         if (lane == 0) p.lse[row_stat_index(p.seq, b, head, start, tok)] = kNegInf;
     }
 }
@@ -525,7 +526,7 @@ static __device__ __noinline__ void rows_without_keys(const Kv8FwdParams& p, int
 // tile with pages of 16 tokens.  A second producer warp, for V, made that case slower, 42.7 ->
 // 50.3 us for 128 requests of up to 2048 tokens at d = 64: the kernel's roles share the
 // instruction cache, and more code in flight costs more than the wait.)
-template <int D, int C, int U, int kSlots, class Smem>
+template <int D, int C, int U, int kSlots, bool F32, class Smem>
 __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t* sKV) {
     constexpr int kUnits = kKeys / U;          // of a side
     const int lane = threadIdx.x & 31;
@@ -548,7 +549,7 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
     for (int np = 0;;) {
         const bool more = walk.next(part);
         if (more && part.tiles == 0) {
-            rows_without_keys<D>(p, part.b, part.h, part.req.start, part.row0,
+            rows_without_keys<D, F32>(p, part.b, part.h, part.req.start, part.row0,
                                  min(C, part.req.n * p.seq.group - part.row0));
             continue;
         }

@@ -478,6 +478,23 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
  *   workspace    device, >= fa_fwd_kv8_workspace_size(...) bytes, 256-byte aligned,
  *                contents ignored; not to be shared by calls in flight together
  *                (calls captured into graphs that replay at the same time among them)
+ *
+ * fa_fwd_kv8_prefix: the same for a batch whose requests share prefixes, each read once for
+ * all of its group.  Group p = 0 .. groups - 1 is the new tokens prefix_cu[p] .. prefix_cu[p + 1] - 1
+ * (dense: token b N + i), whole requests one behind the other, and its prefix the first
+ * prefix_lens[p] tokens of row p of prefix_table [groups, prefix_width].  A request's sequence is
+ * its group's prefix and then the lens[b] tokens of its own row of `table`, so a new token sees
+ * all of the prefix and, causally, its own request's tokens (no window).  Tokens outside all
+ * groups have no prefix, nor have groups of prefix_lens 0.
+ *   prefix_table, prefix_lens   device, int32, as table and lens
+ *   prefix_cu       device, int32 [groups + 1], non-decreasing, within 0 .. T
+ * Otherwise as fa_fwd_kv8, roundings included (probabilities to 11 bits, or to 9 for bf16 where
+ * the rows at hand, all T tokens' for the prefixes, are 16 or fewer), V's scales for prefix and own
+ * tokens each.  O and LSE of both parts are held in fp32 in the workspace of
+ * fa_fwd_kv8_prefix_workspace_size(...) bytes (8 Hq d bytes a token and 2 of fa_fwd_kv8's) and joined
+ * there: O = sum_i exp(LSE_i - LSE) O_i.  Limits: as fa_fwd_kv8's, for the prefixes with `groups`
+ * and prefix_width in place of B and width.  Enqueues five kernels; takes no launch events.
+ *
  * The size does not depend on lens.  The result does not depend on anything but the
  * inputs, the geometry and the device's SM count.  Enqueues two kernels (L = 2 for
  * fa_set_launch_events).  A wait inside them gives up after fa_set_wait_limit_cycles' budget
@@ -506,6 +523,15 @@ fa_status fa_fwd_kv8(fa_dtype dtype, const void* q, long long q_stride, const vo
                      int B, int Hq, int Hkv, int N, int d, int causal, int window,
                      const int* cu_seqlens, int total_tokens, float scale, void* workspace,
                      size_t workspace_bytes, cudaStream_t stream);
+size_t fa_fwd_kv8_prefix_workspace_size(int B, int Hq, int Hkv, int N, int d, int total_tokens);
+fa_status fa_fwd_kv8_prefix(fa_dtype dtype, const void* q, long long q_stride, const void* k8,
+                            const float* k_scale, const void* v8, const float* v_scale,
+                            int num_pages, int page, const int* prefix_table, int prefix_width,
+                            const int* prefix_lens, const int* prefix_cu, int groups,
+                            const int* table, int width, const int* lens, void* o, float* lse,
+                            int B, int Hq, int Hkv, int N, int d, const int* cu_seqlens,
+                            int total_tokens, float scale, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
 
 /*
  * Backward pass of fa_fwd for the loss gradient dO, recomputing S and P from
