@@ -1392,8 +1392,8 @@ fa_status fa_kv8_append_norm_rope(fa_dtype dtype, const void* q, long long q_str
     n.y_stride[0] = q_out_stride;
     n.status = status_word_ptr();
     if (!n.status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
-    if (norm_rope_plan(n, d, sm_count(), false) == 0)
-        return fail(FA_ERR_UNSUPPORTED, "%s: problem too large for one launch", who);
+    // tokens of a CTA: a block's where that leaves two CTAs or more for every SM
+    p.chunk = static_cast<int>(std::min(std::max(T / (2LL * sm_count()), 1LL), static_cast<long long>(kKv8Block)));
     const cudaError_t e = launch_kv8_append_norm_rope(p, n, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append_norm_rope launch");
 }

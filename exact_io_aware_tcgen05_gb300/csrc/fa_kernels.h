@@ -249,8 +249,8 @@ cudaError_t launch_kv8_plan(const Kv8PlanParams& p, int sms, cudaStream_t stream
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stream);
 // norm_rope_plan fills in run and ctas and returns the CTAs of both sides (0: too many).
 int norm_rope_plan(NormRopeParams& p, int d, int sms, bool backward);
-cudaError_t launch_norm_rope(NormRopeParams& p, int d, cudaStream_t stream);
-cudaError_t launch_norm_rope_bwd(NormRopeParams& p, int d, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams& p, int d, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, int d, cudaStream_t stream);
 // kv8_append whose keys, and the queries beside them, go through norm and rotation first
 // (a.x[0] and n's key output are not used).
 cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRopeParams& n, int d, cudaStream_t stream);

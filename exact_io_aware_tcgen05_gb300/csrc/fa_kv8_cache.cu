@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <climits>
 
+
 namespace fa {
 namespace {
 
@@ -357,19 +358,17 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
 
 // append_chunk for keys that are normed and rotated on their way: the block's new tokens are in
 // registers as 32-bit numbers, from which its scale and codes come, so a key is rounded once.
+// `cosines` and `sines`: rows of D / 2 for the tokens from c0 on.
 template <int D, int E, bool IL>
 __device__ __forceinline__ void append_rotated_chunk(const Kv8AppendParams& p, const NormRopeParams& q, int h,
-                                                     long long c0) {
+                                                     long long c0, const float* cosines, const float* sines) {
     constexpr int kLanes = D / 16;         // lanes of one token
     constexpr int kRows = 32 / kLanes;     // tokens the warp loads at a time
     constexpr int kSteps = kKv8Block / kRows;
     const int lane = threadIdx.x & 31;
-    if (c0 >= p.T) return;
     const int c1 = static_cast<int>(min(c0 + p.chunk, static_cast<long long>(p.T)));
     const RowLane<D, IL> at(lane % kLanes, q.rope.rot);
     const uint16_t* x = static_cast<const uint16_t*>(q.x[1]) + static_cast<long long>(h) * D;
-    float w[16];
-    if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
     int t = static_cast<int>(c0);
     while (t < c1) {
         const BlockRun run = next_run(p, t, c0);
@@ -378,30 +377,39 @@ __device__ __forceinline__ void append_rotated_chunk(const Kv8AppendParams& p, c
             t += n;
             continue;
         }
-        float v[kSteps][16];
-        uint32_t top = 0;   // the largest finite magnitude, as an integer
-        bool finite = true;
+        uint4 in[kSteps][2];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int r = i * kRows + lane / kLanes;
-            const long long token = t + min(r, n - 1);   // (rows behind the run are not stored)
-            const uint16_t* from = x + token * q.x_stride[1];
-            widen<E>(*reinterpret_cast<const uint4*>(from + 8 * at.unit[0]),
-                     *reinterpret_cast<const uint4*>(from + 8 * at.unit[1]), v[i]);
-            if (q.norm) {
-                const float f = inverse_norm<D>(v[i], q.eps);
+            // (rows behind the run are not stored)
+            const uint16_t* from = x + (t + min(i * kRows + lane / kLanes, n - 1)) * q.x_stride[1];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * f * w[j];
-            }
-            float c[8], s[8];
-            rotation_of<D, IL>(q.rope, at, token, c, s);
-            rotate<D, IL, false>(at, c, s, v[i]);
+            for (int j = 0; j < 2; ++j) in[i][j] = *reinterpret_cast<const uint4*>(from + 8 * at.unit[j]);
+        }
+        float w[16];
+        if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
+        float v[kSteps][16];
+        uint32_t top = 0;   // the largest magnitude, as an integer (the order of magnitudes)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
-                if (a < 0x7f800000u) top = max(top, a);
-                else finite = false;
-            }
+        for (int i = 0; i < kSteps; ++i) {
+            widen<E>(in[i][0], in[i][1], v[i]);
+            if (q.norm) scale_row(v[i], inverse_norm<D>(v[i], q.eps), w);
+            const int row = static_cast<int>(t - c0) + min(i * kRows + lane / kLanes, n - 1);
+            Rotation r;
+            rotation_from<D, IL>(cosines + row * (D / 2), sines + row * (D / 2), at, r);
+            rotate<D, IL, false>(at, r, v[i]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+        }
+        const bool finite = !__any_sync(0xffffffffu, top >= 0x7f800000u);
+        if (!finite) {   // infinities and NaN left out
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
+                    top = max(top, a < 0x7f800000u ? a : 0u);
+                }
         }
         top = __reduce_max_sync(0xffffffffu, top);
         const int page = run.slot >> p.page_log2;
@@ -420,18 +428,18 @@ __device__ __forceinline__ void append_rotated_chunk(const Kv8AppendParams& p, c
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = i * kRows + lane / kLanes;
+            float f[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float f = v[i][j];
-                v[i][j] = power ? f * inv : div_odd(f, scale);
-                if (!finite) v[i][j] += f * 0.f;   // inf * 0 is NaN: infinities become NaN codes
+                f[j] = power ? v[i][j] * inv : div_odd(v[i][j], scale);
+                if (!finite) f[j] += v[i][j] * 0.f;   // inf * 0 is NaN: infinities become NaN codes
             }
             if (r >= n) continue;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D + 8 * at.unit[j]) =
-                    make_uint2(pack4_e4m3(v[i][8 * j], v[i][8 * j + 1], v[i][8 * j + 2], v[i][8 * j + 3]),
-                               pack4_e4m3(v[i][8 * j + 4], v[i][8 * j + 5], v[i][8 * j + 6], v[i][8 * j + 7]));
+                    make_uint2(pack4_e4m3(f[8 * j], f[8 * j + 1], f[8 * j + 2], f[8 * j + 3]),
+                               pack4_e4m3(f[8 * j + 4], f[8 * j + 5], f[8 * j + 6], f[8 * j + 7]));
         }
         __syncwarp();   // every lane has read the old scale
         if (lane == 0) *scale_at = scale;
@@ -439,21 +447,72 @@ __device__ __forceinline__ void append_rotated_chunk(const Kv8AppendParams& p, c
     }
 }
 
-// The first q.ctas[0] CTAs prepare the queries, the others take chunks of keys and values.
+// A CTA takes `chunk` tokens: their cosines and sines into shared memory, then their blocks of
+// keys and of values, a warp for each head, and their queries, a group of D / 16 lanes for a token
+// and some of the heads.  (A block that begins among them may go on behind them: up to 15 tokens
+// more, whose angles are here too.)
 template <int D, int E, bool IL>
-__global__ void __launch_bounds__(kNormThreads) kv8_append_norm_rope_kernel(const Kv8AppendParams p,
-                                                                            const __grid_constant__ NormRopeParams q) {
+__global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
+    const __grid_constant__ Kv8AppendParams p, const __grid_constant__ NormRopeParams q) {
+    constexpr int kTokens = 2 * kKv8Block - 1;
+    __shared__ alignas(16) float cosines[kTokens][D / 2], sines[kTokens][D / 2];
     grid_launch_dependents();
     grid_dependency_wait();
-    if (static_cast<int>(blockIdx.x) < q.ctas[0]) {
-        norm_rope_rows<D, E, IL>(q, 0, blockIdx.x);
-        return;
+    const long long c0 = static_cast<long long>(blockIdx.x) * p.chunk;
+    const int tokens = static_cast<int>(min(static_cast<long long>(p.chunk), p.T - c0));   // the CTA's own
+    const int half = q.rope.rot / 2;
+    if (half > 0) {
+        const int last = p.slots[c0 + tokens - 1];
+        const int all = min(tokens + kKv8Block - 1 - (last & (kKv8Block - 1)), static_cast<int>(min(p.T - c0, 64LL)));
+        for (int i = threadIdx.x; i < all * half; i += kNormThreads) {
+            const int row = i / half, f = i - row * half;
+            if (row >= tokens && p.slots[c0 + row] != last + row - tokens + 1) continue;
+            cos_sin(q.rope, f, c0 + row, cosines[row][f], sines[row][f]);
+        }
     }
-    const long long item = (static_cast<long long>(blockIdx.x - q.ctas[0]) * kNormThreads + threadIdx.x) >> 5;
-    const int h = static_cast<int>(item % p.Hkv);
-    const long long c0 = item / p.Hkv / 2 * p.chunk;
-    if (item / p.Hkv % 2 == 0) append_rotated_chunk<D, E, IL>(p, q, h, c0);
-    else append_chunk<D, E>(p, 1, h, c0);
+    __syncthreads();
+    const int warp = threadIdx.x / 32;
+    for (int i = warp; i < 2 * p.Hkv; i += kNormThreads / 32) {
+        if (i < p.Hkv) append_rotated_chunk<D, E, IL>(p, q, i, c0, cosines[0], sines[0]);
+        else append_chunk<D, E>(p, 1, i - p.Hkv, c0);
+    }
+    constexpr int L = D / 16, kGroups = kNormThreads / L, kAhead = 4;
+    const int group = threadIdx.x / L, per = kGroups / p.chunk;   // groups for a token
+    const int row = group % p.chunk, first = group / p.chunk;
+    const bool real = row < tokens && first < per;
+    const long long token = c0 + (real ? row : 0);
+    const RowLane<D, IL> at(threadIdx.x % L, q.rope.rot);
+    const uint16_t* x = static_cast<const uint16_t*>(q.x[0]) + token * q.x_stride[0];
+    uint16_t* y = static_cast<uint16_t*>(q.y[0]) + token * q.y_stride[0];
+    Rotation rot;
+    float w[16];
+    rotation_from<D, IL>(cosines[token - c0], sines[token - c0], at, rot);
+    if (q.norm) load_weights<D, E, IL>(q.w[0], q.wide, at, w);
+#pragma unroll 1
+    for (int h0 = 0; h0 < q.heads[0]; h0 += per * kAhead) {
+        uint4 in[kAhead][2];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int h = h0 + u * per + first;
+                in[u][j] = real && h < q.heads[0] ? *reinterpret_cast<const uint4*>(x + h * D + 8 * at.unit[j])
+                                                  : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + u * per + first;
+            float v[16];
+            widen<E>(in[u][0], in[u][1], v);
+            if (q.norm) scale_row(v, inverse_norm<D>(v, q.eps), w);
+            rotate<D, IL, false>(at, rot, v);
+            if (real && h < q.heads[0] && fa_index_ok(token, p.T, q.status)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<uint4*>(y + h * D + 8 * at.unit[j]) = narrow<E>(v + 8 * j);
+            }
+        }
+    }
 }
 
 }  // namespace
@@ -484,9 +543,7 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stre
 }
 
 cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRopeParams& n, int d, cudaStream_t stream) {
-    const long long chunks = (static_cast<long long>(a.T) + a.chunk - 1) / a.chunk;
-    const long long grid = n.ctas[0] + (chunks * a.Hkv * 2 * 32 + kNormThreads - 1) / kNormThreads;
-    if (grid > INT_MAX) return cudaErrorInvalidValue;
+    const long long grid = (static_cast<long long>(a.T) + a.chunk - 1) / a.chunk;
     const bool f16 = a.elem == kElemF16Code, il = n.rope.interleaved != 0;
     auto kern = d == 128 ? (f16 ? (il ? kv8_append_norm_rope_kernel<128, kElemF16, true> : kv8_append_norm_rope_kernel<128, kElemF16, false>)
                                 : (il ? kv8_append_norm_rope_kernel<128, kElemBf16, true> : kv8_append_norm_rope_kernel<128, kElemBf16, false>))

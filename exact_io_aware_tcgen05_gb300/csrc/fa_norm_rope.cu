@@ -1,11 +1,6 @@
 // fa_norm_rope.cu -- norms of queries and keys for each head with the rotation by position in
 // the same pass, and its gradient.  The formulas are those of fa_norm_rope and fa_norm_rope_bwd
 // in include/fa.h, the layout in registers that of fa_norm_rope.cuh.
-//
-// Both are bound by memory: the forward reads and writes each value once (4 bytes), the backward
-// reads two and writes one (6 bytes).  A unit of work is one token's run of heads of one side (q
-// or k) for D / 16 lanes, which work out the token's cosines and sines once and keep two (the
-// backward) or four rows on their way.
 #include "fa_kv8_work.cuh"
 #include "fa_norm_rope.cuh"
 
@@ -14,46 +9,126 @@
 namespace fa {
 namespace {
 
-template <int D, int E, bool IL>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int side = static_cast<int>(blockIdx.x) >= p.ctas[0] ? 1 : 0;
-    norm_rope_rows<D, E, IL>(p, side, blockIdx.x - (side ? p.ctas[0] : 0));
-}
+// A unit of work is one token's run of heads of one side (q or k), for a group of D / 16 lanes; the
+// groups of a warp have neighbouring tokens.
+struct Unit {
+    long long token;
+    int head;
+    __device__ __forceinline__ Unit(const NormRopeParams& p, int side, long long unit) {
+        const long long part = unit / p.T;
+        token = unit - part * p.T;
+        head = static_cast<int>(part) * p.run[side];
+    }
+};
 
-// dn = dy turned back; with r the row's inverse norm, xh = x r and g = dn w:
-//   dx = r (g - xh mean(g xh)),  dw = sum over tokens and heads of dn xh.
-// A CTA keeps to one side and adds its rows' dn xh up in registers, then over its groups in
-// shared memory; norm_rope_weights_kernel adds the CTAs' sums up in their order, so the result
-// has one order of additions for a given shape and device.
+// This lane's two 16-byte units of the rows of a unit of work, kStep bytes from row to row.
+template <int D, bool IL>
+struct LaneRows {
+    static constexpr int kStep = D * 2;
+    char* unit[2];
+    __device__ __forceinline__ LaneRows(const void* x, long long stride, const Unit& u, const RowLane<D, IL>& at) {
+        char* first = static_cast<char*>(const_cast<void*>(x)) + 2 * (u.token * stride + u.head * D);
+        unit[0] = first + 16 * at.unit[0];
+        unit[1] = first + 16 * at.unit[1];
+    }
+    __device__ __forceinline__ void load(int row, uint4 (&v)[2]) const {
+        v[0] = *reinterpret_cast<const uint4*>(unit[0] + row * kStep);
+        v[1] = *reinterpret_cast<const uint4*>(unit[1] + row * kStep);
+    }
+    template <int E>
+    __device__ __forceinline__ void store(int row, const float (&v)[16]) const {
+        *reinterpret_cast<uint4*>(unit[0] + row * kStep) = narrow<E>(v);
+        *reinterpret_cast<uint4*>(unit[1] + row * kStep) = narrow<E>(v + 8);
+    }
+    __device__ __forceinline__ void advance(int rows) {
+        unit[0] += rows * kStep;
+        unit[1] += rows * kStep;
+    }
+};
+
 template <int D, int E, bool IL>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
-    constexpr int L = D / 16, kGroups = kNormThreads / L, kAhead = 2;
-    __shared__ float sums[kGroups][D];
+__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr int kAhead = 2, kLanes = RowLane<D, IL>::kLanes, kGroups = kNormThreads / kLanes;
     grid_launch_dependents();
     grid_dependency_wait();
     const int side = static_cast<int>(blockIdx.x) >= p.ctas[0] ? 1 : 0, run = p.run[side];
-    const int cta = blockIdx.x - (side ? p.ctas[0] : 0), in_warp = threadIdx.x / L % (32 / L);
-    const RowLane<D, IL> at(threadIdx.x % L, p.rope.rot);
     const long long units = static_cast<long long>(p.T) * (p.heads[side] / run);
+    const long long unit = static_cast<long long>(blockIdx.x - (side ? p.ctas[0] : 0)) * kGroups + threadIdx.x / kLanes;
+    const bool real = unit < units;   // (the others take part in the sums)
+    const Unit un(p, side, real ? unit : units - 1);
+    const RowLane<D, IL> at(threadIdx.x % kLanes, p.rope.rot);
+    LaneRows<D, IL> from(p.x[side], p.x_stride[side], un, at), to(p.y[side], p.y_stride[side], un, at);
+    Rotation rot;
+    float w[16];
+    if (p.norm) load_weights<D, E, IL>(p.w[side], p.wide, at, w);
+    // a batch of rows whose loads are on their way together; whole: all of them are there
+    auto batch = [&](bool fresh, auto whole, int left) {
+        uint4 in[kAhead][2];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (whole || u < left) from.load(u, in[u]);
+        if (fresh) lane_rotation<D, IL>(p.rope, at, un.token, rot);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (!whole && u >= left) break;
+            float v[16];
+            widen<E>(in[u][0], in[u][1], v);
+            if (p.norm) scale_row(v, inverse_norm<D>(v, p.eps), w);
+            rotate<D, IL, false>(at, rot, v);
+            if (real && fa_index_ok(un.token, p.T, p.status)) to.template store<E>(u, v);
+        }
+        from.advance(kAhead);
+        to.advance(kAhead);
+    };
+    int left = run;
+#pragma unroll 1
+    for (; left >= kAhead; left -= kAhead) batch(left == run, std::true_type{}, left);
+    if (left > 0) batch(left == run, std::false_type{}, left);
+}
+
+// A row's dn (in g) to dx, and its part of dw:
+//   xh = x r,  g = dn w,  dx = r (g - xh mean(g xh)),  dw += dn xh.
+template <int D>
+__device__ __forceinline__ void norm_back(float (&g)[16], float (&x)[16], float r, const float (&w)[16], float (&dw)[16]) {
+    float q[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        x[i] *= r;
+        dw[i] = fmaf(g[i], x[i], dw[i]);
+        g[i] *= w[i];
+        q[i & 1] = fmaf(g[i], x[i], q[i & 1]);
+    }
+    const float mean = row_sum<D>(q[0] + q[1]) * (-1.f / D);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = r * fmaf(x[i], mean, g[i]);
+}
+
+// A CTA keeps to one side and goes through many units; it adds its rows' parts of dw up in
+// registers, then over its groups of lanes in shared memory, and norm_rope_weights_kernel adds the
+// CTAs' sums up in their order, so the result has one order of additions for given sizes.
+template <int D, int E, bool IL>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr int kAhead = 2, kLanes = RowLane<D, IL>::kLanes, kGroups = kNormThreads / kLanes;
+    __shared__ alignas(16) float sums[kGroups][D];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int side = static_cast<int>(blockIdx.x) >= p.ctas[0] ? 1 : 0, run = p.run[side];
+    const long long units = static_cast<long long>(p.T) * (p.heads[side] / run);
+    const RowLane<D, IL> at(threadIdx.x % kLanes, p.rope.rot);
     float w[16], dw[16];
     if (p.norm) load_weights<D, E, IL>(p.w[side], p.wide, at, w);
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[i] = 0.f;
-    // (every lane of a warp goes through as many units: the sums shuffle)
 #pragma unroll 1
-    for (long long first = static_cast<long long>(cta) * kGroups + threadIdx.x / 32 * (32 / L); first < units;
+    for (long long first = static_cast<long long>(blockIdx.x - (side ? p.ctas[0] : 0)) * kGroups; first < units;
          first += static_cast<long long>(p.ctas[side]) * kGroups) {
-        const long long mine = first + in_warp;
-        const bool real = mine < units;
-        const long long unit = real ? mine : units - 1;
-        const long long part = unit / p.T, token = unit - part * p.T;
-        const uint16_t* x = static_cast<const uint16_t*>(p.x[side]) + token * p.x_stride[side] + part * run * D;
-        const uint16_t* dy = static_cast<const uint16_t*>(p.dy[side]) + token * p.dy_stride[side] + part * run * D;
-        uint16_t* y = static_cast<uint16_t*>(p.y[side]) + token * p.y_stride[side] + part * run * D;
-        float c[8], s[8];
-        rotation_of<D, IL>(p.rope, at, token, c, s);
+        const bool real = first + threadIdx.x / kLanes < units;   // (the others take part in the sums)
+        const Unit un(p, side, real ? first + threadIdx.x / kLanes : units - 1);
+        const uint16_t* x = static_cast<const uint16_t*>(p.x[side]) + un.token * p.x_stride[side] + un.head * D;
+        const uint16_t* dy = static_cast<const uint16_t*>(p.dy[side]) + un.token * p.dy_stride[side] + un.head * D;
+        uint16_t* y = static_cast<uint16_t*>(p.y[side]) + un.token * p.y_stride[side] + un.head * D;
+        Rotation rot;
+        lane_rotation<D, IL>(p.rope, at, un.token, rot);
 #pragma unroll 1
         for (int h0 = 0; h0 < run; h0 += kAhead) {
             uint4 gin[kAhead][2], in[kAhead][2];
@@ -70,36 +145,24 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const __gri
             for (int u = 0; u < kAhead; ++u) {
                 float g[16];
                 widen<E>(gin[u][0], gin[u][1], g);
-                rotate<D, IL, true>(at, c, s, g);
-                if (p.norm) {
-                    float xh[16];
-                    widen<E>(in[u][0], in[u][1], xh);
-                    const float r = inverse_norm<D>(xh, p.eps);
-                    float q[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        xh[i] *= r;
-                        dw[i] = fmaf(g[i], xh[i], dw[i]);
-                        g[i] *= w[i];
-                        q[i & 1] = fmaf(g[i], xh[i], q[i & 1]);
-                    }
-                    const float mean = row_sum<D>(q[0] + q[1]) * (1.f / D);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) g[i] = r * fmaf(-xh[i], mean, g[i]);
+                rotate<D, IL, true>(at, rot, g);
+                if (p.norm) {   // (a row that is not there is zeros, and adds nothing to dw)
+                    float v[16];
+                    widen<E>(in[u][0], in[u][1], v);
+                    norm_back<D>(g, v, inverse_norm<D>(v, p.eps), w, dw);
                 }
-                uint4 out[2];
-                narrow<E>(g, out[0], out[1]);
-                if (real && h0 + u < run && fa_index_ok(token, p.T, p.status)) {
+                if (real && h0 + u < run && fa_index_ok(un.token, p.T, p.status)) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<uint4*>(y + (h0 + u) * D + 8 * at.unit[j]) = out[j];
+                        *reinterpret_cast<uint4*>(y + (h0 + u) * D + 8 * at.unit[j]) = narrow<E>(g + 8 * j);
                 }
             }
         }
     }
     if (!p.partial) return;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sums[threadIdx.x / L][8 * at.unit[i / 8] + i % 8] = dw[i];
+    for (int i = 0; i < 16; ++i) sums[threadIdx.x / kLanes][8 * at.unit[i / 8] + i % 8] = dw[i];
     __syncthreads();
     if (threadIdx.x < D) {
         float v = 0.f;
@@ -133,23 +196,22 @@ __global__ void __launch_bounds__(1024) norm_rope_weights_kernel(const __grid_co
 }
 
 template <int D, int E>
-cudaError_t launch(NormRopeParams& p, cudaStream_t stream) {
-    const bool il = p.rope.interleaved != 0;
-    return kv8::launch_dependent(il ? norm_rope_kernel<D, E, true> : norm_rope_kernel<D, E, false>,
+cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
+    return kv8::launch_dependent(p.rope.interleaved ? norm_rope_kernel<D, E, true> : norm_rope_kernel<D, E, false>,
                                  p.ctas[0] + p.ctas[1], kNormThreads, 0, stream, p);
 }
 
 template <int D, int E>
-cudaError_t launch_bwd(NormRopeParams& p, cudaStream_t stream) {
-    const bool il = p.rope.interleaved != 0;
-    const cudaError_t e = kv8::launch_dependent(il ? norm_rope_bwd_kernel<D, E, true> : norm_rope_bwd_kernel<D, E, false>,
-                                                p.ctas[0] + p.ctas[1], kNormThreads, 0, stream, p);
+cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t stream) {
+    const cudaError_t e = kv8::launch_dependent(
+        p.rope.interleaved ? norm_rope_bwd_kernel<D, E, true> : norm_rope_bwd_kernel<D, E, false>, p.ctas[0] + p.ctas[1],
+        kNormThreads, 0, stream, p);
     if (e != cudaSuccess || !p.partial) return e;
     return kv8::launch_dependent(norm_rope_weights_kernel<D>, 2 * (D / 32), 1024, 0, stream, p);
 }
 
-// The heads of a unit: the largest divisor of `heads` that leaves `want` units or more (1 where
-// even single heads do not).
+// The heads of a unit: the largest divisor of `heads` that leaves `want` units or more (1 where even
+// single heads do not).
 int heads_of_unit(long long T, int heads, long long want) {
     int best = 1;
     for (int r = 2; r <= heads; ++r)
@@ -159,20 +221,26 @@ int heads_of_unit(long long T, int heads, long long want) {
 
 }  // namespace
 
-// Units of one token and a run of heads; enough of them for every SM, and runs no longer than
-// that allows, so that a token's angles serve many heads.
+// Units of one token and a run of heads.  A unit's start (its angles) costs about as much as four
+// heads, so few units are wanted, but enough for every SM: four CTAs' worth for each.  Where that
+// leaves runs of more than 8 heads, twice as many even out the last CTAs: 16384 tokens of 16 and 16
+// heads took 47.2 us with runs of 8 and 49.5 with 16; 5003 of 12 and 4 (d = 64) 4.3 us with runs of 2 and
+// 5.9 with 1.
 int norm_rope_plan(NormRopeParams& p, int d, int sms, bool backward) {
     const int groups = kNormThreads / (d / 16);   // of a CTA
-    const long long want = static_cast<long long>(sms) * 8 * groups;
-    long long ctas[2], all = 0;
+    const long long want = static_cast<long long>(sms) * 4 * groups;
+    long long ctas[2];
     for (int side = 0; side < 2; ++side) {
-        p.run[side] = heads_of_unit(p.T, p.heads[side], want * p.heads[side] / (p.heads[0] + p.heads[1]));
+        const long long mine = want * p.heads[side] / (p.heads[0] + p.heads[1]);
+        p.run[side] = heads_of_unit(p.T, p.heads[side], mine);
+        if (p.run[side] > 8) p.run[side] = std::max(heads_of_unit(p.T, p.heads[side], 2 * mine), std::min(p.run[side], 8));
+        while (p.heads[side] % p.run[side] != 0) --p.run[side];
         ctas[side] = (static_cast<long long>(p.T) * (p.heads[side] / p.run[side]) + groups - 1) / groups;
-        all += ctas[side];
     }
-    // the backward's CTAs go through several units each, so that few sums are left to add up
-    const long long most = 4LL * sms;
-    if (backward && all > most) {
+    // the backward's CTAs, as many as are resident, go through several units each, so that few sums
+    // are left to add up
+    const long long most = 2LL * sms;
+    if (backward && ctas[0] + ctas[1] > most) {
         ctas[0] = std::max(1LL, std::min(most - 1, most * p.heads[0] / (p.heads[0] + p.heads[1])));
         ctas[1] = most - ctas[0];
     }
@@ -182,13 +250,13 @@ int norm_rope_plan(NormRopeParams& p, int d, int sms, bool backward) {
     return p.ctas[0] + p.ctas[1];
 }
 
-cudaError_t launch_norm_rope(NormRopeParams& p, int d, cudaStream_t stream) {
+cudaError_t launch_norm_rope(const NormRopeParams& p, int d, cudaStream_t stream) {
     const bool f16 = p.elem == kElemF16Code;
     if (d == 128) return f16 ? launch<128, kElemF16>(p, stream) : launch<128, kElemBf16>(p, stream);
     return f16 ? launch<64, kElemF16>(p, stream) : launch<64, kElemBf16>(p, stream);
 }
 
-cudaError_t launch_norm_rope_bwd(NormRopeParams& p, int d, cudaStream_t stream) {
+cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, int d, cudaStream_t stream) {
     const bool f16 = p.elem == kElemF16Code;
     if (d == 128) return f16 ? launch_bwd<128, kElemF16>(p, stream) : launch_bwd<128, kElemBf16>(p, stream);
     return f16 ? launch_bwd<64, kElemF16>(p, stream) : launch_bwd<64, kElemBf16>(p, stream);
