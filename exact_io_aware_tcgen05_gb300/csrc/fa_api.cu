@@ -1245,6 +1245,7 @@ fa_status take_kv8_fwd(const char* who, fa_dtype dtype, const Geometry& g, const
     p->o = o;
     p->lse = lse;
     p->o_f32 = 0;
+    p->behind = 0;
     p->width = width;
     p->num_pages = num_pages;
     p->scale_log2 = scale * kLog2e;
@@ -1392,8 +1393,15 @@ fa_status fa_kv8_append_norm_rope(fa_dtype dtype, const void* q, long long q_str
     n.y_stride[0] = q_out_stride;
     n.status = status_word_ptr();
     if (!n.status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
-    // tokens of a CTA: a block's where that leaves two CTAs or more for every SM
+    // a chunk is a block's tokens where that leaves two CTAs or more for every SM, and then a CTA has two
     p.chunk = static_cast<int>(std::min(std::max(T / (2LL * sm_count()), 1LL), static_cast<long long>(kKv8Block)));
+    p.chunks = p.chunk == kKv8Block ? 2 : 1;
+    if (p.chunk == kKv8Block) {
+        // long batches: the queries by the kernel of fa_norm_rope, which needs fewer registers
+        n.heads[1] = 0;
+        if (norm_rope_plan(n, d, sm_count(), false) == 0)
+            return fail(FA_ERR_UNSUPPORTED, "%s: problem too large for one launch", who);
+    }
     const cudaError_t e = launch_kv8_append_norm_rope(p, n, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append_norm_rope launch");
 }
@@ -1489,9 +1497,16 @@ fa_status fa_fwd_kv8_prefix(fa_dtype dtype, const void* q, long long q_stride, c
         j.lse[i] = x->lse;
         ++i;
     }
-    cudaError_t e = launch_fwd_kv8(p0, d, nullptr, stream);
-    if (e == cudaSuccess) e = launch_fwd_kv8(p, d, nullptr, stream);
-    if (e == cudaSuccess) e = launch_kv8_prefix_join(j, d, stream);
+    p.behind = 1;
+    // Few key tiles for each CTA: one CTA per SM for each pass, so that both run at once and fewer parts
+    // are left to join.
+    const long long tiles = (static_cast<long long>(g.tokens) * g0.seq.group / p0.columns + groups) * Hkv *
+                            ((static_cast<long long>(prefix_width) * page + 127) / 128);
+    if (tiles < 16 * static_cast<long long>(p0.ctas)) {
+        p0.ctas /= 2;
+        p.ctas /= 2;
+    }
+    const cudaError_t e = launch_fwd_kv8_prefix(p0, p, j, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_kv8_prefix launch");
 }
 

@@ -142,6 +142,7 @@ struct Kv8AppendParams {
     int T, Hkv, num_slots;
     int page_log2;
     int chunk;          // tokens of one warp: the blocks that start among them are its own
+    int chunks;         // with norm and rotation: of a CTA
     int elem;
 };
 
@@ -202,7 +203,8 @@ struct Kv8FwdParams {
     const int* lens;    // [B]
     void* o;            // 16-bit, or fp32 with o_f32
     float* lse;
-    int o_f32;
+    int o_f32;          // a pass of attention with shared prefixes
+    int behind;         // the second of them
     int width, num_pages, page_log2;
     uint32_t group_inv; // ceil(2^32 / group)
     int columns;        // rows of an item (kv8_columns)
@@ -251,14 +253,16 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stre
 int norm_rope_plan(NormRopeParams& p, int d, int sms, bool backward);
 cudaError_t launch_norm_rope(const NormRopeParams& p, int d, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, int d, cudaStream_t stream);
-// kv8_append whose keys, and the queries beside them, go through norm and rotation first
-// (a.x[0] and n's key output are not used).
+// kv8_append whose keys, and the queries beside them, go through norm and rotation first (a.x[0] is
+// not used, nor n's key output).  With n.ctas[0] > 0 the queries have a kernel of their own.
 cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRopeParams& n, int d, cudaStream_t stream);
 cudaError_t launch_fwd_kv8_rows(const Kv8FwdParams& p, int d, cudaStream_t stream);
 // launch_fwd_kv8 records ev[0..2] (if not null) around its two kernels.
 cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, cudaStream_t stream);
 
-cudaError_t launch_kv8_prefix_join(const Kv8PrefixJoinParams& p, int d, cudaStream_t stream);
+// The passes over the prefixes (p0) and over the requests' own keys (p1), and their joins.
+cudaError_t launch_fwd_kv8_prefix(const Kv8FwdParams& p0, const Kv8FwdParams& p1, const Kv8PrefixJoinParams& j, int d,
+                                  cudaStream_t stream);
 
 int* device_status_word();  // library-owned device status word (fa_api.cu)
 

@@ -356,129 +356,209 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
                        item / p.Hkv / 2 * p.chunk);
 }
 
-// append_chunk for keys that are normed and rotated on their way: the block's new tokens are in
-// registers as 32-bit numbers, from which its scale and codes come, so a key is rounded once.
-// `cosines` and `sines`: rows of D / 2 for the tokens from c0 on.
+// The lane's part of a key, rotated but for its factor r (its inverse norm; rotation keeps factors).
 template <int D, int E, bool IL>
-__device__ __forceinline__ void append_rotated_chunk(const Kv8AppendParams& p, const NormRopeParams& q, int h,
-                                                     long long c0, const float* cosines, const float* sines) {
-    constexpr int kLanes = D / 16;         // lanes of one token
-    constexpr int kRows = 32 / kLanes;     // tokens the warp loads at a time
-    constexpr int kSteps = kKv8Block / kRows;
-    const int lane = threadIdx.x & 31;
-    const int c1 = static_cast<int>(min(c0 + p.chunk, static_cast<long long>(p.T)));
-    const RowLane<D, IL> at(lane % kLanes, q.rope.rot);
-    const uint16_t* x = static_cast<const uint16_t*>(q.x[1]) + static_cast<long long>(h) * D;
-    int t = static_cast<int>(c0);
+__device__ __forceinline__ void key_row(const NormRopeParams& q, const RowLane<D, IL>& at, const float* cosines,
+                                        const float* sines, uint4 a, uint4 b, const float (&w)[16], float (&v)[16],
+                                        float& r) {
+    widen<E>(a, b, v);
+    r = 1.f;
+    if (q.norm) {
+        r = inverse_norm<D>(v, q.eps);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= w[j];
+    }
+    Rotation rot;
+    rotation_from<D, IL>(cosines, sines, at, rot);
+    rotate<D, IL, false>(at, rot, v);
+}
+
+// append_chunk for keys that are normed and rotated on their way, from which 32-bit numbers the
+// block's scale and codes come, so that a key is rounded once.  With PAIR two warps have a block, the
+// first and the last 8 of its new tokens, and both walk the chunk's runs (one warp's 64 numbers a lane
+// did not fit its registers beside the rest: 322 us in place of 301 for 8 prompts of 8192 tokens, Hq 32,
+// Hkv 8, d = 128); `tops` is theirs, for two runs in turn.  Without, runs have 8 tokens at most.
+// `cosines` and `sines`: rows of D / 2 for the tokens from c0 on; w: the lane's weights.
+//
+// Returns the first token that is not done: c1, or, without RARE, where a run needs RARE: there are
+// infinities or NaN among its keys, or the block's scale is not a power of two (another writer began
+// it).
+template <int D, int E, bool IL, bool PAIR, bool RARE>
+__device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const NormRopeParams& q, const RowLane<D, IL>& at,
+                                              const float (&w)[16], int h, long long c0, int t, int c1,
+                                              const float* cosines, const float* sines, uint32_t (*tops)[2], int& turn) {
+    constexpr int kLanes = D / 16;               // lanes of one token
+    constexpr int kRows = 32 / kLanes;           // tokens the warp loads at a time
+    constexpr int kMine = kKv8Block / 2, kSteps = kMine / kRows;
+    const int lane = threadIdx.x & 31, pair = threadIdx.x / 64, second = PAIR ? threadIdx.x / 32 & 1 : 0;
+    const int mine = second * kMine + lane / kLanes;   // the lane's first token in a run
+    // the larger of both warps' numbers (the buffers take turns: a warp that writes one again has met
+    // the other since that one read it)
+    auto both = [&](uint32_t top) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (!PAIR) return top;
+        uint32_t* x = tops[turn & 1];
+        ++turn;
+        if (lane == 0) x[second] = top;
+        named_bar_sync(1 + pair, 64);
+        return max(x[0], x[1]);
+    };
     while (t < c1) {
         const BlockRun run = next_run(p, t, c0);
-        const int off = run.off, n = run.n;
         if (run.skip) {
-            t += n;
+            t += run.n;
             continue;
         }
+        const int off = run.off, n = run.n;
+        const uint16_t* x = static_cast<const uint16_t*>(q.x[1]) + (t + mine) * q.x_stride[1] + static_cast<long long>(h) * D;
         uint4 in[kSteps][2];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            // (rows behind the run are not stored)
-            const uint16_t* from = x + (t + min(i * kRows + lane / kLanes, n - 1)) * q.x_stride[1];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) in[i][j] = *reinterpret_cast<const uint4*>(from + 8 * at.unit[j]);
+            in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
+            if (i * kRows + mine < n) {
+                in[i][0] = *reinterpret_cast<const uint4*>(x + 8 * at.unit[0]);
+                in[i][1] = *reinterpret_cast<const uint4*>(x + 8 * at.unit[1]);
+            }
+            x += kRows * q.x_stride[1];
         }
-        float w[16];
-        if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
-        float v[kSteps][16];
-        uint32_t top = 0;   // the largest magnitude, as an integer (the order of magnitudes)
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            widen<E>(in[i][0], in[i][1], v[i]);
-            if (q.norm) scale_row(v[i], inverse_norm<D>(v[i], q.eps), w);
-            const int row = static_cast<int>(t - c0) + min(i * kRows + lane / kLanes, n - 1);
-            Rotation r;
-            rotation_from<D, IL>(cosines + row * (D / 2), sines + row * (D / 2), at, r);
-            rotate<D, IL, false>(at, r, v[i]);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
-        }
-        const bool finite = !__any_sync(0xffffffffu, top >= 0x7f800000u);
-        if (!finite) {   // infinities and NaN left out
-            top = 0;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
-                    top = max(top, a < 0x7f800000u ? a : 0u);
-                }
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
         const int page = run.slot >> p.page_log2;
         const int in_page = run.slot & ((1 << p.page_log2) - 1);
         const long long row0 = (static_cast<long long>(page) * p.Hkv + h) << p.page_log2;
         float* scale_at = p.scales[0] + (row0 + in_page) / kKv8Block;
         uint8_t* row = p.codes[0] + (row0 + in_page) * D;
-        float scale = pow2f(scale_exponent(top));
-        if (off > 0) {
-            const float old = *scale_at;
-            scale = fmaxf(old, scale);
-            if (scale > old) round_again<D>(row - static_cast<long long>(off) * D + lane % (D / 8) * 8, off, old / scale);
-        }
-        const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
-        const float inv = 1.f / scale;   // exact for a power of two
+        const float old = off > 0 ? *scale_at : 0.f;
+        float v[kSteps][16], r[kSteps];
+        float most = 0.f;   // the largest magnitude (NaN does not count)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int r = i * kRows + lane / kLanes;
-            float f[16];
+            const int place = static_cast<int>(t - c0) + min(i * kRows + mine, n - 1);
+            key_row<D, E, IL>(q, at, cosines + place * (D / 2), sines + place * (D / 2), in[i][0], in[i][1], w, v[i], r[i]);
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) m = fmax3(m, fabsf(v[i][j]), fabsf(v[i][j + 1]));
+            if (i * kRows + mine < n) most = fmaxf(most, m * r[i]);
+        }
+        uint32_t top = both(__float_as_uint(most));
+        if (RARE && top >= 0x7f800000u) {
+            top = 0;
+            for (int i = 0; i < kSteps; ++i)
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t a = __float_as_uint(v[i][j] * r[i]) & 0x7fffffffu;
+                    if (i * kRows + mine < n && a < 0x7f800000u) top = max(top, a);
+                }
+            top = both(top);
+        }
+        const float scale = fmaxf(pow2f(scale_exponent(top)), old);
+        if (!RARE && (top >= 0x7f800000u || (__float_as_uint(scale) & 0x7fffffu) != 0)) return t;
+        if (second == 0) {   // (both warps have read the old scale)
+            if (off > 0 && scale > old)
+                round_again<D>(row - static_cast<long long>(off) * D + lane % (D / 8) * 8, off, old / scale);
+            if (lane == 0) *scale_at = scale;
+        }
+        const float unscale = 1.f / scale;   // exact for a power of two
+        uint8_t* to = row + mine * D;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const float f = r[i] * unscale;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                f[j] = power ? v[i][j] * inv : div_odd(v[i][j], scale);
-                if (!finite) f[j] += v[i][j] * 0.f;   // inf * 0 is NaN: infinities become NaN codes
+                // (inf * 0 is NaN: infinities become NaN codes)
+                if (RARE) v[i][j] = div_odd(v[i][j] * r[i], scale) + v[i][j] * r[i] * 0.f;
+                else v[i][j] *= f;
             }
-            if (r >= n) continue;
+            if (i * kRows + mine < n) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D + 8 * at.unit[j]) =
-                    make_uint2(pack4_e4m3(f[8 * j], f[8 * j + 1], f[8 * j + 2], f[8 * j + 3]),
-                               pack4_e4m3(f[8 * j + 4], f[8 * j + 5], f[8 * j + 6], f[8 * j + 7]));
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<uint2*>(to + i * kRows * D + 8 * at.unit[j]) =
+                        make_uint2(pack4_e4m3(v[i][8 * j], v[i][8 * j + 1], v[i][8 * j + 2], v[i][8 * j + 3]),
+                                   pack4_e4m3(v[i][8 * j + 4], v[i][8 * j + 5], v[i][8 * j + 6], v[i][8 * j + 7]));
+            }
         }
-        __syncwarp();   // every lane has read the old scale
-        if (lane == 0) *scale_at = scale;
         t += n;
+    }
+    return c1;
+}
+
+template <int D, int E, bool IL, bool PAIR>
+__device__ __noinline__ int append_rotated_rare(const Kv8AppendParams& p, const NormRopeParams& q, int h, long long c0,
+                                                int t, int c1, const float* cosines, const float* sines,
+                                                uint32_t (*tops)[2], int turn) {
+    const RowLane<D, IL> at(threadIdx.x % (D / 16), q.rope.rot);
+    float w[16];
+    if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
+    append_rotated<D, E, IL, PAIR, true>(p, q, at, w, h, c0, t, c1, cosines, sines, tops, turn);
+    return turn;
+}
+
+// Items (a head and one of the CTA's chunks of tokens) by pairs of warps, or by single ones.
+template <int D, int E, bool IL, bool PAIR>
+__device__ __forceinline__ void append_keys(const Kv8AppendParams& p, const NormRopeParams& q, long long c0, int tokens,
+                                            const float (*cosines)[D / 2], const float (*sines)[D / 2],
+                                            uint32_t (*tops)[2][2]) {
+    constexpr int kTeams = kNormThreads / (PAIR ? 64 : 32);
+    const int team = threadIdx.x / (PAIR ? 64 : 32);
+    const RowLane<D, IL> at(threadIdx.x % (D / 16), q.rope.rot);
+    float w[16];
+    if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
+    int turn = 0;
+    for (int i = team; i < p.Hkv * p.chunks; i += kTeams) {
+        const int first = i / p.Hkv * p.chunk, h = i % p.Hkv;
+        const int t0 = static_cast<int>(c0) + first, t1 = static_cast<int>(c0) + min(first + p.chunk, tokens);
+        uint32_t (*mine)[2] = tops[PAIR ? team : 0];
+        const int t = append_rotated<D, E, IL, PAIR, false>(p, q, at, w, h, t0, t0, t1, cosines[first], sines[first], mine, turn);
+        if (t < t1) turn = append_rotated_rare<D, E, IL, PAIR>(p, q, h, t0, t, t1, cosines[first], sines[first], mine, turn);
     }
 }
 
-// A CTA takes `chunk` tokens: their cosines and sines into shared memory, then their blocks of
-// keys and of values, a warp for each head, and their queries, a group of D / 16 lanes for a token
-// and some of the heads.  (A block that begins among them may go on behind them: up to 15 tokens
-// more, whose angles are here too.)
+// What a CTA of kv8_append_norm_rope_kernel does (blockIdx.y), for some tokens: their blocks of keys
+// (two warps for a head and `chunk` tokens) or of values (a warp), or their queries, a group of D / 16 lanes for a
+// token and some of the heads.  For keys and queries the CTA first has the tokens' cosines and sines
+// in shared memory.  (A block that begins among them may go on behind them: up to 15 tokens more,
+// whose angles are there too.)
+constexpr int kAppendValues = 0, kAppendKeys = 1, kAppendQueries = 2;
+
 template <int D, int E, bool IL>
 __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
     const __grid_constant__ Kv8AppendParams p, const __grid_constant__ NormRopeParams q) {
-    constexpr int kTokens = 2 * kKv8Block - 1;
+    constexpr int kTokens = 3 * kKv8Block - 1, kWarps = kNormThreads / 32;
     __shared__ alignas(16) float cosines[kTokens][D / 2], sines[kTokens][D / 2];
+    __shared__ uint32_t tops[kWarps / 2][2][2];
     grid_launch_dependents();
     grid_dependency_wait();
-    const long long c0 = static_cast<long long>(blockIdx.x) * p.chunk;
-    const int tokens = static_cast<int>(min(static_cast<long long>(p.chunk), p.T - c0));   // the CTA's own
-    const int half = q.rope.rot / 2;
+    const int role = blockIdx.y, warp = threadIdx.x / 32;
+    const long long c0 = static_cast<long long>(blockIdx.x) * p.chunk * p.chunks;   // the CTA's first token
+    const int tokens = static_cast<int>(min(static_cast<long long>(p.chunk) * p.chunks, p.T - c0));
+    if (role == kAppendValues) {
+        for (int i = warp; i < p.Hkv * p.chunks; i += kWarps)
+            append_chunk<D, E>(p, 1, i % p.Hkv, c0 + i / p.Hkv * p.chunk);
+        return;
+    }
+    const int half = q.rope.rot / 2, lane = threadIdx.x % 32;
     if (half > 0) {
-        const int last = p.slots[c0 + tokens - 1];
-        const int all = min(tokens + kKv8Block - 1 - (last & (kKv8Block - 1)), static_cast<int>(min(p.T - c0, 64LL)));
-        for (int i = threadIdx.x; i < all * half; i += kNormThreads) {
-            const int row = i / half, f = i - row * half;
+        int all = tokens, last = 0;
+        if (role == kAppendKeys) {
+            last = p.slots[c0 + tokens - 1];
+            all = min(tokens + kKv8Block - 1 - (last & (kKv8Block - 1)), static_cast<int>(min(p.T - c0, 64LL)));
+        }
+        for (int row = warp; row < all; row += kWarps) {
             if (row >= tokens && p.slots[c0 + row] != last + row - tokens + 1) continue;
-            cos_sin(q.rope, f, c0 + row, cosines[row][f], sines[row][f]);
+#pragma unroll
+            for (int f = lane; f < D / 2; f += 32)
+                if (f < half) cos_sin(q.rope, f, c0 + row, cosines[row][f], sines[row][f]);
         }
     }
     __syncthreads();
-    const int warp = threadIdx.x / 32;
-    for (int i = warp; i < 2 * p.Hkv; i += kNormThreads / 32) {
-        if (i < p.Hkv) append_rotated_chunk<D, E, IL>(p, q, i, c0, cosines[0], sines[0]);
-        else append_chunk<D, E>(p, 1, i - p.Hkv, c0);
+    if (role == kAppendKeys) {
+        // (a decoding step's single tokens need no pairs of warps)
+        if (tokens == 1 && next_run(p, static_cast<int>(c0), c0).n <= kKv8Block / 2)
+            append_keys<D, E, IL, false>(p, q, c0, tokens, cosines, sines, tops);
+        else
+            append_keys<D, E, IL, true>(p, q, c0, tokens, cosines, sines, tops);
+        return;
     }
-    constexpr int L = D / 16, kGroups = kNormThreads / L, kAhead = 4;
-    const int group = threadIdx.x / L, per = kGroups / p.chunk;   // groups for a token
-    const int row = group % p.chunk, first = group / p.chunk;
+    constexpr int L = D / 16, kGroups = kNormThreads / L;
+    const int group = threadIdx.x / L, per = kGroups / (p.chunk * p.chunks);   // groups for a token
+    const int row = group % (p.chunk * p.chunks), first = group / (p.chunk * p.chunks);
     const bool real = row < tokens && first < per;
     const long long token = c0 + (real ? row : 0);
     const RowLane<D, IL> at(threadIdx.x % L, q.rope.rot);
@@ -489,10 +569,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
     rotation_from<D, IL>(cosines[token - c0], sines[token - c0], at, rot);
     if (q.norm) load_weights<D, E, IL>(q.w[0], q.wide, at, w);
 #pragma unroll 1
-    for (int h0 = 0; h0 < q.heads[0]; h0 += per * kAhead) {
-        uint4 in[kAhead][2];
+    for (int h0 = 0; h0 < q.heads[0]; h0 += 2 * per) {
+        uint4 in[2][2];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int h = h0 + u * per + first;
@@ -500,7 +580,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
                                                   : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < 2; ++u) {
             const int h = h0 + u * per + first;
             float v[16];
             widen<E>(in[u][0], in[u][1], v);
@@ -543,13 +623,16 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, int d, cudaStream_t stre
 }
 
 cudaError_t launch_kv8_append_norm_rope(const Kv8AppendParams& a, const NormRopeParams& n, int d, cudaStream_t stream) {
-    const long long grid = (static_cast<long long>(a.T) + a.chunk - 1) / a.chunk;
+    const long long tokens = static_cast<long long>(a.chunk) * a.chunks;
+    const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens), n.ctas[0] > 0 ? 2 : 3);
     const bool f16 = a.elem == kElemF16Code, il = n.rope.interleaved != 0;
     auto kern = d == 128 ? (f16 ? (il ? kv8_append_norm_rope_kernel<128, kElemF16, true> : kv8_append_norm_rope_kernel<128, kElemF16, false>)
                                 : (il ? kv8_append_norm_rope_kernel<128, kElemBf16, true> : kv8_append_norm_rope_kernel<128, kElemBf16, false>))
                          : (f16 ? (il ? kv8_append_norm_rope_kernel<64, kElemF16, true> : kv8_append_norm_rope_kernel<64, kElemF16, false>)
                                 : (il ? kv8_append_norm_rope_kernel<64, kElemBf16, true> : kv8_append_norm_rope_kernel<64, kElemBf16, false>));
-    return kv8::launch_dependent(kern, static_cast<int>(grid), kNormThreads, 0, stream, a, n);
+    cudaError_t e = kv8::launch_dependent(kern, grid, kNormThreads, 0, stream, a, n);
+    if (e == cudaSuccess && n.ctas[0] > 0) e = launch_norm_rope(n, d, stream);
+    return e;
 }
 
 }  // namespace fa

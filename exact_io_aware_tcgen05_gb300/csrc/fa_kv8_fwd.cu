@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     uint8_t* sP = sQ + 2 * K::kQBytes;                    // [2][blocks of 16 columns][keys][16]
     Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + 2 * K::kPBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    grid_launch_dependents();
+    if (!F32) grid_launch_dependents();
 
     if (threadIdx.x == 0) {
         sm.abort = 0;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         fence_proxy_async_smem();
     }
     // what the kernels before this one wrote is there from here on
-    grid_dependency_wait();
+    wait_and_launch<F32>(p);
     find_share<C>(p, sm);
     tc_fence_before();
     __syncthreads();
@@ -691,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, K::kTmemCols);
+    if (F32 && p.behind) grid_dependency_wait();
 }
 
 // Joins the parts of the item that begins at the end of CTA c's share, c = blockIdx.x: a warp
@@ -700,25 +701,26 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
 // accumulators up in their order; the first two parts' (there are always two) are on their way
 // before their weights are known.
 template <int D, int E, bool F32>
-__global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
-    grid_launch_dependents();
-    grid_dependency_wait();
+__device__ __forceinline__ void join_parts(const Kv8FwdParams& p) {
     const int cta = blockIdx.x;
     const Kv8Join j = p.joins[cta];
     if (j.last <= cta) return;
     const int C = p.columns, G = p.seq.group, lane = threadIdx.x & 31;
     const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (j.row0 + n >= j.n * G) return;
-    constexpr int kPer = D / 32;
+    constexpr int kPer = D / 32;   // channels of a lane, side by side
+    using Vec = std::conditional_t<kPer == 4, float4, float2>;
     // the parts: this CTA's second slot, the first slots of the ones behind it
     const int parts = j.last - cta + 1;
     auto row_of = [&](int part) { return (2LL * (cta + part) + (part == 0 ? 1 : 0)) * C + n; };
-    float early[2][kPer];
+    auto load = [&](int part, float (&x)[kPer]) {
+        *reinterpret_cast<Vec*>(x) = *reinterpret_cast<const Vec*>(p.part_o + row_of(part) * D + kPer * lane);
+    };
+    alignas(16) float early[2][kPer];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) early[q][c] = p.part_o[row_of(q) * D + lane + 32 * c];
-    float m = kNegInf, sum = 0.f, o[kPer];
+    for (int q = 0; q < 2; ++q) load(q, early[q]);
+    float m = kNegInf, sum = 0.f;
+    alignas(16) float o[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) o[c] = 0.f;
 #pragma unroll 1
@@ -743,12 +745,13 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
                 for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, early[q][c], o[c]);
             }
         }
-#pragma unroll 4
+#pragma unroll 8
         for (; q < here; ++q) {
             const float f = __shfl_sync(0xffffffffu, mine, q);
-            const float* x = p.part_o + row_of(p0 + q) * D + lane;
+            alignas(16) float x[kPer];
+            load(p0 + q, x);
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, x[32 * c], o[c]);
+            for (int c = 0; c < kPer; ++c) o[c] = fmaf(f, x[c], o[c]);
         }
         m = top;
     }
@@ -757,14 +760,35 @@ __global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_const
     if (!fa_index_ok(row, p.seq.total_tokens, p.status)) return;
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-        const long long at = (row * p.seq.Hq + head) * D + lane + 32 * c;
-        if (F32) static_cast<float*>(p.o)[at] = o[c] * inv;
-        else static_cast<uint16_t*>(p.o)[at] = static_cast<uint16_t>(pack2<E>(o[c] * inv, 0.f));
+    for (int c = 0; c < kPer; ++c) o[c] *= inv;
+    const long long at = (row * p.seq.Hq + head) * D + kPer * lane;
+    if (F32) {
+        *reinterpret_cast<Vec*>(static_cast<float*>(p.o) + at) = *reinterpret_cast<Vec*>(o);
+    } else {
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2)
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack2<E>(o[c], o[c + 1]);
     }
     if (lane == 0)
         p.lse[row_stat_index(p.seq, j.b, head, j.start, tok)] =
             sum != 0.f ? ((m == kNegInf ? 0.f : m) - kShift + log2f(sum)) * kLn2 : kNegInf;
+}
+
+template <int D, int E>
+__global__ void __launch_bounds__(256) fa_fwd_kv8_join_kernel(const __grid_constant__ Kv8FwdParams p) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    join_parts<D, E, false>(p);
+}
+
+// The joins of the pass over shared prefixes (z = 0) and of that over the requests' own keys.
+template <int D, int E>
+__global__ void __launch_bounds__(256) fa_kv8_prefix_parts_kernel(const __grid_constant__ Kv8FwdParams p0,
+                                                                  const __grid_constant__ Kv8FwdParams p1) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const Kv8FwdParams& p = blockIdx.z == 0 ? p0 : p1;
+    if (static_cast<int>(blockIdx.x) < p.ctas && 8 * static_cast<int>(blockIdx.y) < p.columns) join_parts<D, E, true>(p);
 }
 
 template <int D, int E, int C, bool F32>
@@ -778,22 +802,21 @@ cudaError_t launch_attend(const Kv8FwdParams& p, cudaStream_t stream) {
 }
 
 template <int D, int E, bool F32>
-cudaError_t launch_both_as(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
-    cudaError_t e = ev ? cudaEventRecord(ev[0], stream) : cudaSuccess;
-    if (e == cudaSuccess)
-        e = p.columns == 8    ? launch_attend<D, E, 8, F32>(p, stream)
-            : p.columns == 16 ? launch_attend<D, E, 16, F32>(p, stream)
-                              : launch_fwd_kv8_rows(p, D, stream);
-    if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E, F32>, dim3(p.ctas, p.columns / 8), 256, 0, stream, p);
-    if (e == cudaSuccess && ev) e = cudaEventRecord(ev[2], stream);
-    return e;
+cudaError_t launch_main(const Kv8FwdParams& p, cudaStream_t stream) {
+    return p.columns == 8    ? launch_attend<D, E, 8, F32>(p, stream)
+           : p.columns == 16 ? launch_attend<D, E, 16, F32>(p, stream)
+                             : launch_fwd_kv8_rows(p, D, stream);
 }
 
 template <int D, int E>
 cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream_t stream) {
-    return p.o_f32 ? launch_both_as<D, E, true>(p, ev, stream) : launch_both_as<D, E, false>(p, ev, stream);
+    cudaError_t e = ev ? cudaEventRecord(ev[0], stream) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_main<D, E, false>(p, stream);
+    if (e == cudaSuccess && ev) e = cudaEventRecord(ev[1], stream);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(fa_fwd_kv8_join_kernel<D, E>, dim3(p.ctas, p.columns / 8), 256, 0, stream, p);
+    if (e == cudaSuccess && ev) e = cudaEventRecord(ev[2], stream);
+    return e;
 }
 
 // Joins the two parts of attention with a shared prefix, O and LSE of each in fp32: a warp a row.
@@ -836,10 +859,17 @@ __global__ void __launch_bounds__(256) fa_kv8_prefix_join_kernel(const Kv8Prefix
 }
 
 template <int D, int E>
-cudaError_t launch_prefix_join(const Kv8PrefixJoinParams& p, cudaStream_t stream) {
-    const long long grid = (static_cast<long long>(p.seq.total_tokens) * p.seq.Hq + 7) / 8;
+cudaError_t launch_prefix(const Kv8FwdParams& p0, const Kv8FwdParams& p1, const Kv8PrefixJoinParams& j, cudaStream_t stream) {
+    const long long grid = (static_cast<long long>(j.seq.total_tokens) * j.seq.Hq + 7) / 8;
     if (grid > INT_MAX) return cudaErrorInvalidValue;
-    return launch_dependent(fa_kv8_prefix_join_kernel<D, E>, dim3(static_cast<unsigned>(grid)), 256, 0, stream, p);
+    cudaError_t e = launch_main<D, E, true>(p0, stream);
+    if (e == cudaSuccess) e = launch_main<D, E, true>(p1, stream);
+    if (e == cudaSuccess)
+        e = launch_dependent(fa_kv8_prefix_parts_kernel<D, E>,
+                             dim3(std::max(p0.ctas, p1.ctas), std::max(p0.columns, p1.columns) / 8, 2), 256, 0, stream, p0, p1);
+    if (e == cudaSuccess)
+        e = launch_dependent(fa_kv8_prefix_join_kernel<D, E>, dim3(static_cast<unsigned>(grid)), 256, 0, stream, j);
+    return e;
 }
 
 }  // namespace
@@ -852,12 +882,13 @@ cudaError_t launch_fwd_kv8(const Kv8FwdParams& p, int d, const cudaEvent_t* ev, 
                                    : launch_both<64, kElemF16>(p, ev, stream);
 }
 
-cudaError_t launch_kv8_prefix_join(const Kv8PrefixJoinParams& p, int d, cudaStream_t stream) {
+cudaError_t launch_fwd_kv8_prefix(const Kv8FwdParams& p0, const Kv8FwdParams& p1, const Kv8PrefixJoinParams& j, int d,
+                                  cudaStream_t stream) {
     if (d == 128)
-        return p.elem == kElemBf16Code ? launch_prefix_join<128, kElemBf16>(p, stream)
-                                       : launch_prefix_join<128, kElemF16>(p, stream);
-    return p.elem == kElemBf16Code ? launch_prefix_join<64, kElemBf16>(p, stream)
-                                   : launch_prefix_join<64, kElemF16>(p, stream);
+        return j.elem == kElemBf16Code ? launch_prefix<128, kElemBf16>(p0, p1, j, stream)
+                                       : launch_prefix<128, kElemF16>(p0, p1, j, stream);
+    return j.elem == kElemBf16Code ? launch_prefix<64, kElemBf16>(p0, p1, j, stream)
+                                   : launch_prefix<64, kElemF16>(p0, p1, j, stream);
 }
 
 }  // namespace fa

@@ -231,6 +231,9 @@ int norm_rope_plan(NormRopeParams& p, int d, int sms, bool backward) {
     const long long want = static_cast<long long>(sms) * 4 * groups;
     long long ctas[2];
     for (int side = 0; side < 2; ++side) {
+        p.run[side] = 1;
+        ctas[side] = 0;
+        if (p.heads[side] == 0) continue;
         const long long mine = want * p.heads[side] / (p.heads[0] + p.heads[1]);
         p.run[side] = heads_of_unit(p.T, p.heads[side], mine);
         if (p.run[side] > 8) p.run[side] = std::max(heads_of_unit(p.T, p.heads[side], 2 * mine), std::min(p.run[side], 8));

@@ -53,12 +53,18 @@ __device__ __forceinline__ int axis_of(const RopeParams& r, int f) {
     return static_cast<unsigned>(axis) < static_cast<unsigned>(r.num_axes) ? axis : 0;
 }
 
-// Cosine and sine of frequency f's angle for one token.
+// Cosine and sine of frequency f's angle for one token.  The nearest quarter turn is taken off as an
+// integer first: what is left, an eighth of a turn at most, is an fp32 number to 2^-28 of a turn, where
+// a whole turn would be one to 2^-26.
 __device__ __forceinline__ void cos_sin(const RopeParams& r, int f, long long token, float& c, float& s) {
     const long long pos = r.positions[axis_of(r, f) * r.axis_stride + token];
-    const unsigned long long t = static_cast<unsigned long long>(pos) * r.turns[f];
-    // the upper 32 bits as half turns, -1 <= x < 1
-    sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f, &s, &c);
+    const uint32_t turn = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * r.turns[f]) >> 32);
+    const uint32_t quarter = (turn + 0x20000000u) >> 30;
+    float x, y;
+    sincospif(static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 0x1p-31f, &y, &x);   // (half turns)
+    const uint32_t a = __float_as_uint(quarter & 1 ? y : x), b = __float_as_uint(quarter & 1 ? x : y);
+    c = __uint_as_float(a ^ ((quarter + 1) & 2) << 30);
+    s = __uint_as_float(b ^ (quarter & 2) << 30);
 }
 
 // A lane's cosines and sines: pair i is the lane's channels (i, 8 + i), or with IL (2 i, 2 i + 1).
@@ -137,7 +143,9 @@ __device__ __forceinline__ float inverse_norm(const float (&x)[16], float eps) {
     float q[2] = {x[0] * x[0], x[1] * x[1]};
 #pragma unroll
     for (int i = 2; i < 16; ++i) q[i & 1] = fmaf(x[i], x[i], q[i & 1]);
-    return rsqrtf(fmaf(row_sum<D>(q[0] + q[1]), 1.f / D, eps));
+    const float a = fmaf(row_sum<D>(q[0] + q[1]), 1.f / D, eps), r = rsqrtf(a);
+    // a step of Newton's: rsqrtf is good to two ulps (infinite squares: r = 0)
+    return r > 0.f ? fmaf(0.5f * r, fmaf(-a * r, r, 1.f), r) : r;
 }
 
 // x = x r w, in that order.
