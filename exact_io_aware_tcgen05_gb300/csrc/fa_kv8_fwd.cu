@@ -844,12 +844,12 @@ __global__ void __launch_bounds__(256) fa_kv8_prefix_join_kernel(const Kv8Prefix
     const float inv = sum > 0.f ? 1.f / sum : sum;   // (NaN stays; 0: nothing seen)
     const float f0 = w0 * inv, f1 = w1 * inv;
     constexpr int kPer = D / 32;
-    float x[kPer], y[kPer];
+    using Vec = std::conditional_t<kPer == 4, float4, float2>;
+    alignas(16) float x[kPer], y[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        x[i] = grouped ? p.part[0][row * D + kPer * lane + i] : 0.f;
-        y[i] = p.part[1][row * D + kPer * lane + i];
-    }
+    for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+    if (grouped) *reinterpret_cast<Vec*>(x) = *reinterpret_cast<const Vec*>(p.part[0] + row * D + kPer * lane);
+    *reinterpret_cast<Vec*>(y) = *reinterpret_cast<const Vec*>(p.part[1] + row * D + kPer * lane);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) x[i] = f0 * x[i] + f1 * y[i];
     uint32_t* out = static_cast<uint32_t*>(p.o) + (row * D + kPer * lane) / 2;

@@ -110,3 +110,11 @@ def check(name, got, want, bound, dtype):
         bound = bound + out_round(dtype) * (want.abs() + bound) + TINY[dtype]
     err = (got.double() - want).abs()
     assert (err <= bound).all(), (name, int((~(err <= bound)).sum()), float((err / bound.clamp(min=1e-300)).max()))
+
+
+def exact_angles(positions, freq):
+    """angles() for positions as far as an int32 goes, by whole numbers."""
+    from fractions import Fraction
+    two_pi = Fraction(2 * 3141592653589793238462643383279502884197169399375105820974945, 10 ** 60)
+    rows = [[float(Fraction(f) * p % two_pi) for f in freq] for p in positions]
+    return torch.tensor(rows, dtype=torch.float64)
