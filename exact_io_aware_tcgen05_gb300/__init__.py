@@ -708,7 +708,11 @@ def _int32(name, x, shape, device):
 def _rows(name, x, heads, d):
     """Elements between the tokens of a [..., heads, d] tensor whose tokens are evenly spaced
     (a slice of a wider projection's output, say) and do not overlap (an expanded tensor's do)."""
-    shape, strides = x.shape, x.stride()
+    return _rows_of(name, x.shape, x.stride(), heads, d)
+
+
+@functools.lru_cache(maxsize=4096)
+def _rows_of(name, shape, strides, heads, d):
     n, outer = shape[-3], shape[0] if len(shape) == 4 else 1
     ok = shape[-2] == heads and shape[-1] == d
     if n * outer > 0:   # (an empty tensor's strides are anything)
@@ -728,7 +732,7 @@ def _elsewhere(device, stream) -> bool:
     """Whether a call has to change the current device or stream to run on `stream` (None: the
     current one) of CUDA device number `device`."""
     import torch
-    return stream is not None or device != torch.cuda.current_device()
+    return stream is not None or device != torch._C._cuda_getDevice()
 
 
 def _there(call, device, stream, *args, **kwargs):
@@ -789,30 +793,25 @@ def rope_plan(frequencies, *, axes=None, interleaved=False, device="cuda") -> Ro
 
 
 def _norm_rope(dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps):
-    """What the calls that norm and rotate have in common, checked, as the C ABI takes it: (norm,
-    weights, weights_f32, eps) and (positions, axes, num_axes, turns, rot, interleaved)."""
-    import torch
+    """What the calls that norm and rotate have in common, checked, as the C ABI takes it: norm,
+    weights, weights_f32, eps, and positions, axes, num_axes, turns, rot, interleaved."""
+    q_ptr = k_ptr = None
     wide = False
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if not norm:
-            raise ValueError(f"{name} without a norm")
-        if w.dtype != dtype and w.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32 or of q's type, got {w.dtype}")
-        if w.shape != (d,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous and have the shape ({d},), got {tuple(w.shape)}")
-        if w.get_device() != dev:
-            raise ValueError(_ONE_DEVICE)
-        wide = w.dtype == torch.float32
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight must be of one type")
-    first = (1 if norm else 0, q_weight.data_ptr() if q_weight is not None else None,
-             k_weight.data_ptr() if k_weight is not None else None, wide, eps if norm else 0.0)
+    if q_weight is not None:
+        wide = _weight("q_weight", q_weight, dtype, d, dev, norm)
+        q_ptr = q_weight.data_ptr()
+    if k_weight is not None:
+        kind = _weight("k_weight", k_weight, dtype, d, dev, norm)
+        if q_weight is not None and kind != wide:
+            raise TypeError("q_weight and k_weight must be of one type")
+        wide = kind
+        k_ptr = k_weight.data_ptr()
+    if not norm:
+        eps = 0.0
     if rope is None:
         if positions is not None:
             raise ValueError("positions without a rope plan")
-        return first, (None, None, 1, None, 0, 0)
+        return (norm, q_ptr, k_ptr, wide, eps), (None, None, 1, None, 0, 0)
     turns, axes, num_axes, interleaved = rope
     if positions is None:
         raise ValueError("a rope plan needs positions")
@@ -822,46 +821,65 @@ def _norm_rope(dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, e
     rot = 2 * turns.shape[0]
     if rot > d:
         raise ValueError(f"the plan turns {rot} channels of {d}")
-    return first, (positions.data_ptr(), axes.data_ptr() if axes is not None else None, num_axes, turns.data_ptr(), rot,
-                   interleaved)
+    return ((norm, q_ptr, k_ptr, wide, eps),
+            (positions.data_ptr(), None if axes is None else axes.data_ptr(), num_axes, turns.data_ptr(), rot, interleaved))
 
 
-def _heads_of(name, x, lead, d, dev, dtype):
-    """Heads of, and elements between the tokens of, a tensor [*lead, heads, d]."""
-    if x.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    shape = x.shape
-    if shape[:-2] != lead or shape[-1] != d:
-        raise ValueError(f"{name} must have the shape {tuple(lead)} + (heads, {d}), got {tuple(shape)}")
-    if x.get_device() != dev:
+def _weight(name, w, dtype, d, dev, norm):
+    """Whether a norm's weights are float32 (or else of q's type)."""
+    import torch
+    kind = w.dtype
+    if not norm:
+        raise ValueError(f"{name} without a norm")
+    if kind != dtype and kind != torch.float32:
+        raise TypeError(f"{name} must be float32 or of q's type, got {kind}")
+    if w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and have the shape ({d},), got {tuple(w.shape)}")
+    if w.get_device() != dev:
         raise ValueError(_ONE_DEVICE)
-    return shape[-2], _rows(name, x, shape[-2], d)
+    return kind == torch.float32
 
 
-def _qk_shape(q, k):
-    """The leading dimensions, tokens and head dimension of q, and heads and strides of both."""
-    shape, dev = q.shape, q.get_device()
+@functools.lru_cache(maxsize=4096)
+def _tokens(name, shape, strides):
+    """The leading dimensions, tokens, heads, head dimension and elements between the tokens of a tensor
+    [B, N, heads, d] or [T, heads, d]."""
     if len(shape) not in (3, 4):
-        raise ValueError("q and k must be [B, N, heads, d] or [T, heads, d]")
-    if dev < 0:
-        raise ValueError(_ONE_DEVICE)
-    lead, d = shape[:-2], shape[-1]
-    T = lead.numel()
+        raise ValueError(f"{name} must be [B, N, heads, d] or [T, heads, d], got {tuple(shape)}")
+    lead, T = shape[:-2], 1
+    for n in lead:
+        T *= n
     if T >= _INT:
         raise _beyond(tokens=T)
-    return (lead, T, d, *_heads_of("q", q, lead, d, dev, q.dtype), *_heads_of("k", k, lead, d, dev, q.dtype))
+    return lead, T, shape[-2], shape[-1], _rows_of(name, shape, strides, shape[-2], shape[-1])
 
 
-def _like(name, x, like, dev):
-    """`x` as an output of `like`'s shape and type (a new tensor for None), and its tokens' distance."""
+def _beside(name, x, dtype, lead, d, dev, heads=0):
+    """Heads and tokens' distance of a tensor like q, and of `heads` heads if given."""
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    lead_x, _, heads_x, d_x, stride = _tokens(name, x.shape, x.stride())
+    if lead_x != lead or d_x != d or (heads and heads_x != heads):
+        raise ValueError(f"{name} must have the shape {tuple(lead)} + ({heads or 'heads'}, {d}), got {tuple(x.shape)}")
+    if x.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    return heads_x, stride
+
+
+def _qk(q, k, dev):
+    """fa_dtype, leading dimensions, tokens, head dimension, and heads and strides of q and k."""
+    dtype = _dtype_code(q, k)
+    if dev < 0:
+        raise ValueError(_ONE_DEVICE)
+    lead, T, Hq, d, q_stride = _tokens("q", q.shape, q.stride())
+    return (dtype, lead, T, d, Hq, q_stride, *_beside("k", k, q.dtype, lead, d, dev))
+
+
+def _fresh(like):
+    """A new tensor of `like`'s shape and type, contiguous, and its tokens' distance."""
     import torch
     shape = like.shape
-    if x is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device), shape[-2] * shape[-1]
-    heads, stride = _heads_of(name, x, shape[:-2], shape[-1], dev, like.dtype)
-    if heads != shape[-2]:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(x.shape)}")
-    return x, stride
+    return torch.empty_like(like, memory_format=torch.contiguous_format), shape[-2] * shape[-1]
 
 
 def norm_rope_forward(q, k, positions=None, rope: RopePlan | None = None, *, q_weight=None, k_weight=None, norm=True,
@@ -876,12 +894,15 @@ def norm_rope_forward(q, k, positions=None, rope: RopePlan | None = None, *, q_w
         return _there(norm_rope_forward, dev, stream, q, k, positions, rope, q_weight=q_weight, k_weight=k_weight,
                       norm=norm, eps=eps, out=out)
     import torch
-    dtype = _dtype_code(q, k)
-    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk_shape(q, k)
+    dtype, lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
     norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
-    q_out, k_out = (None, None) if out is None else out
-    q_out, q_out_stride = _like("out[0]", q_out, q, dev)
-    k_out, k_out_stride = _like("out[1]", k_out, k, dev)
+    if out is None:
+        q_out, q_out_stride = _fresh(q)
+        k_out, k_out_stride = _fresh(k)
+    else:
+        q_out, k_out = out
+        _, q_out_stride = _beside("out[0]", q_out, q.dtype, lead, d, dev, Hq)
+        _, k_out_stride = _beside("out[1]", k_out, q.dtype, lead, d, dev, Hkv)
     _check(load().fa_norm_rope(dtype, q.data_ptr(), q_stride, k.data_ptr(), k_stride, q_out.data_ptr(), q_out_stride,
                                k_out.data_ptr(), k_out_stride, T, Hq, Hkv, d, *norms, *turned,
                                torch._C._cuda_getCurrentRawStream(dev)))
@@ -906,16 +927,17 @@ def norm_rope_backward(q, k, dq_out, dk_out, positions=None, rope: RopePlan | No
         return _there(norm_rope_backward, dev, stream, q, k, dq_out, dk_out, positions, rope, q_weight=q_weight,
                       k_weight=k_weight, norm=norm, eps=eps, out=out, workspace=workspace)
     import torch
-    dtype = _dtype_code(q, k, dq_out, dk_out)
-    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk_shape(q, k)
+    dtype, lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
     norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
-    heads, dq_out_stride = _heads_of("dq_out", dq_out, lead, d, dev, q.dtype)
-    heads_k, dk_out_stride = _heads_of("dk_out", dk_out, lead, d, dev, q.dtype)
-    if heads != Hq or heads_k != Hkv:
-        raise ValueError(f"dq_out and dk_out must have q's and k's heads, {Hq} and {Hkv}, got {heads} and {heads_k}")
-    dq, dk = (None, None) if out is None else out
-    dq, dq_stride = _like("out[0]", dq, q, dev)
-    dk, dk_stride = _like("out[1]", dk, k, dev)
+    _, dq_out_stride = _beside("dq_out", dq_out, q.dtype, lead, d, dev, Hq)
+    _, dk_out_stride = _beside("dk_out", dk_out, q.dtype, lead, d, dev, Hkv)
+    if out is None:
+        dq, dq_stride = _fresh(q)
+        dk, dk_stride = _fresh(k)
+    else:
+        dq, dk = out
+        _, dq_stride = _beside("out[0]", dq, q.dtype, lead, d, dev, Hq)
+        _, dk_stride = _beside("out[1]", dk, q.dtype, lead, d, dev, Hkv)
     dq_weight = dk_weight = None
     if q_weight is not None:
         dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
@@ -945,19 +967,19 @@ def kv8_append_norm_rope(cache: Kv8Cache, q, k, v, slots, positions=None, rope: 
         return _there(kv8_append_norm_rope, dev, stream, cache, q, k, v, slots, positions, rope, q_weight=q_weight,
                       k_weight=k_weight, norm=norm, eps=eps, out=out)
     import torch
-    dtype = _dtype_code(q, k, v)
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d]")
-    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk_shape(q, k)
+    dtype, lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
     num_pages, heads, page, dk = _kv8_shape(cache, dev)
     if heads != Hkv or dk != d:
         raise ValueError(f"the cache has {heads} heads of {dk} channels, k {Hkv} of {d}")
-    heads, v_stride = _heads_of("v", v, lead, d, dev, q.dtype)
-    if heads != Hkv:
-        raise ValueError(f"v must have k's {Hkv} heads, got {heads}")
+    _, v_stride = _beside("v", v, q.dtype, lead, d, dev, Hkv)
     _int32("slots", slots, lead, dev)
     norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
-    out, out_stride = _like("out", out, q, dev)
+    if out is None:
+        out, out_stride = _fresh(q)
+    else:
+        _, out_stride = _beside("out", out, q.dtype, lead, d, dev, Hq)
     k8, k_scale, v8, v_scale = cache
     _check(load().fa_kv8_append_norm_rope(
         dtype, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, out.data_ptr(), out_stride,
