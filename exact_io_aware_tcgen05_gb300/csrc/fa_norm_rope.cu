@@ -1,6 +1,18 @@
 // fa_norm_rope.cu -- norms of queries and keys for each head with the rotation by position in
 // the same pass, and its gradient.  The formulas are those of fa_norm_rope and fa_norm_rope_bwd
 // in include/fa.h, the layout in registers that of fa_norm_rope.cuh.
+//
+// Both are bound by memory: the forward reads and writes each value once (4 bytes), the backward
+// reads two and writes one (6 bytes).  What it takes to come near: enough rows on their way (an SM
+// needs some 50 KB), few instructions a row (some 200 for the 4 or 8 rows of a warp, half of them the
+// arithmetic), and angles worked out once for many heads.
+//
+// Measured (one GB300, bf16, the shares of the measured copy rate): forward 32768 tokens, Hq 32, Hkv 8,
+// d = 128, three axes, slices of a projection 107.6 us, 92 % (a plain copy of such rows runs at 97 %);
+// 16384 tokens of 16 and 16 heads 47.5 us, 83 %, where the last CTAs leave SMs idle; one token 2.6 us, a
+// launch and the loads that wait for one another.  A warp on four heads of one token, its angles
+// shared, waited longer at every token's start (121 to 131 us); passes of rows through rings in shared
+// memory, by bulk or by asynchronous copies, took 118 to 126 us, bound by their instructions.
 #include "fa_kv8_work.cuh"
 #include "fa_norm_rope.cuh"
 
@@ -106,10 +118,19 @@ __device__ __forceinline__ void norm_back(float (&g)[16], float (&x)[16], float 
 // A CTA keeps to one side and goes through many units; it adds its rows' parts of dw up in
 // registers, then over its groups of lanes in shared memory, and norm_rope_weights_kernel adds the
 // CTAs' sums up in their order, so the result has one order of additions for given sizes.
+//
+// The rows come by asynchronous copies, kBwdAhead - 1 rows ahead and over the ends of units, into places
+// in shared memory that each thread reads back itself: no thread waits for another, and what is on its
+// way takes none of the registers, which dw, the weights and the angles fill.  With the rows loaded into
+// registers, two at a time, 16384 tokens of 16 and 16 heads (d = 128) took 79.6 us in place of 69.4
+// (5.8 TB/s, 85 % of the measured copy rate); more rows ahead, or rows in 2 KB pieces by bulk copies
+// (72.5), were no faster.
+constexpr int kBwdAhead = 3;
+
 template <int D, int E, bool IL>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
-    constexpr int kAhead = 2, kLanes = RowLane<D, IL>::kLanes, kGroups = kNormThreads / kLanes;
-    __shared__ alignas(16) float sums[kGroups][D];
+    constexpr int kAhead = kBwdAhead, kLanes = RowLane<D, IL>::kLanes, kGroups = kNormThreads / kLanes;
+    extern __shared__ uint4 places[];   // [kAhead][4][threads]; at the end [kGroups][D] floats
     grid_launch_dependents();
     grid_dependency_wait();
     const int side = static_cast<int>(blockIdx.x) >= p.ctas[0] ? 1 : 0, run = p.run[side];
@@ -119,48 +140,76 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const __
     if (p.norm) load_weights<D, E, IL>(p.w[side], p.wide, at, w);
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+    const long long start = static_cast<long long>(blockIdx.x - (side ? p.ctas[0] : 0)) * kGroups;
+    const long long step = static_cast<long long>(p.ctas[side]) * kGroups;
+    long long next = start;   // the unit that copies are in, its row
+    int row = 0, put = 0;
+    const uint16_t *cx = nullptr, *cdy = nullptr;
+    auto seek = [&] {
+        const long long mine = next + threadIdx.x / kLanes;
+        cx = cdy = nullptr;
+        if (mine >= units) return;
+        const Unit un(p, side, mine);
+        cdy = static_cast<const uint16_t*>(p.dy[side]) + un.token * p.dy_stride[side] + un.head * D;
+        cx = static_cast<const uint16_t*>(p.x[side]) + un.token * p.x_stride[side] + un.head * D;
+    };
+    auto copy = [&] {
+        if (next < units) {
+            if (cdy) {
+                uint4* to = places + put * 4 * kNormThreads + threadIdx.x;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    cp_async16(smem_addr(to + j * kNormThreads), cdy + 8 * at.unit[j]);
+                    if (p.norm) cp_async16(smem_addr(to + (2 + j) * kNormThreads), cx + 8 * at.unit[j]);
+                }
+                cdy += D;
+                cx += D;
+            }
+            if (++row == run) {
+                row = 0;
+                next += step;
+                seek();
+            }
+        }
+        put = put + 1 == kAhead ? 0 : put + 1;
+        cp_async_commit();
+    };
+    seek();
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) copy();
+    int take = 0;
 #pragma unroll 1
-    for (long long first = static_cast<long long>(blockIdx.x - (side ? p.ctas[0] : 0)) * kGroups; first < units;
-         first += static_cast<long long>(p.ctas[side]) * kGroups) {
+    for (long long first = start; first < units; first += step) {
         const bool real = first + threadIdx.x / kLanes < units;   // (the others take part in the sums)
         const Unit un(p, side, real ? first + threadIdx.x / kLanes : units - 1);
-        const uint16_t* x = static_cast<const uint16_t*>(p.x[side]) + un.token * p.x_stride[side] + un.head * D;
-        const uint16_t* dy = static_cast<const uint16_t*>(p.dy[side]) + un.token * p.dy_stride[side] + un.head * D;
         uint16_t* y = static_cast<uint16_t*>(p.y[side]) + un.token * p.y_stride[side] + un.head * D;
         Rotation rot;
         lane_rotation<D, IL>(p.rope, at, un.token, rot);
 #pragma unroll 1
-        for (int h0 = 0; h0 < run; h0 += kAhead) {
-            uint4 gin[kAhead][2], in[kAhead][2];
+        for (int h = 0; h < run; ++h) {
+            cp_async_wait<kAhead - 2>();
+            const uint4* from = places + take * 4 * kNormThreads + threadIdx.x;
+            take = take + 1 == kAhead ? 0 : take + 1;
+            float g[16], v[16];
+            widen<E>(from[0], from[kNormThreads], g);
+            if (p.norm) widen<E>(from[2 * kNormThreads], from[3 * kNormThreads], v);
+            copy();
+            if (!real) {   // (no row adds nothing to dw)
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const bool row = real && h0 + u < run;
-                    const int o = (h0 + u) * D + 8 * at.unit[j];
-                    gin[u][j] = row ? *reinterpret_cast<const uint4*>(dy + o) : make_uint4(0, 0, 0, 0);
-                    in[u][j] = row && p.norm ? *reinterpret_cast<const uint4*>(x + o) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                float g[16];
-                widen<E>(gin[u][0], gin[u][1], g);
-                rotate<D, IL, true>(at, rot, g);
-                if (p.norm) {   // (a row that is not there is zeros, and adds nothing to dw)
-                    float v[16];
-                    widen<E>(in[u][0], in[u][1], v);
-                    norm_back<D>(g, v, inverse_norm<D>(v, p.eps), w, dw);
-                }
-                if (real && h0 + u < run && fa_index_ok(un.token, p.T, p.status)) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<uint4*>(y + (h0 + u) * D + 8 * at.unit[j]) = narrow<E>(g + 8 * j);
-                }
+                for (int i = 0; i < 16; ++i) g[i] = v[i] = 0.f;
             }
+            rotate<D, IL, true>(at, rot, g);
+            if (p.norm) norm_back<D>(g, v, inverse_norm<D>(v, p.eps), w, dw);
+            if (real && fa_index_ok(un.token, p.T, p.status)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(y + 8 * at.unit[j]) = narrow<E>(g + 8 * j);
+            }
+            y += D;
         }
     }
     if (!p.partial) return;
     __syncthreads();
+    float (*sums)[D] = reinterpret_cast<float (*)[D]>(places);
 #pragma unroll
     for (int i = 0; i < 16; ++i) sums[threadIdx.x / kLanes][8 * at.unit[i / 8] + i % 8] = dw[i];
     __syncthreads();
@@ -203,9 +252,12 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
 
 template <int D, int E>
 cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t stream) {
-    const cudaError_t e = kv8::launch_dependent(
-        p.rope.interleaved ? norm_rope_bwd_kernel<D, E, true> : norm_rope_bwd_kernel<D, E, false>, p.ctas[0] + p.ctas[1],
-        kNormThreads, 0, stream, p);
+    auto kern = p.rope.interleaved ? norm_rope_bwd_kernel<D, E, true> : norm_rope_bwd_kernel<D, E, false>;
+    constexpr int smem = kBwdAhead * 4 * 16 * kNormThreads;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    e = kv8::launch_dependent(
+        kern, p.ctas[0] + p.ctas[1], kNormThreads, smem, stream, p);
     if (e != cudaSuccess || !p.partial) return e;
     return kv8::launch_dependent(norm_rope_weights_kernel<D>, 2 * (D / 32), 1024, 0, stream, p);
 }
