@@ -1245,7 +1245,6 @@ fa_status take_kv8_fwd(const char* who, fa_dtype dtype, const Geometry& g, const
     p->o = o;
     p->lse = lse;
     p->o_f32 = 0;
-    p->behind = 0;
     p->width = width;
     p->num_pages = num_pages;
     p->scale_log2 = scale * kLog2e;
@@ -1496,15 +1495,6 @@ fa_status fa_fwd_kv8_prefix(fa_dtype dtype, const void* q, long long q_stride, c
         j.part[i] = static_cast<const float*>(x->o);
         j.lse[i] = x->lse;
         ++i;
-    }
-    p.behind = 1;
-    // Few key tiles for each CTA: one CTA per SM for each pass, so that both run at once and fewer parts
-    // are left to join.
-    const long long tiles = (static_cast<long long>(g.tokens) * g0.seq.group / p0.columns + groups) * Hkv *
-                            ((static_cast<long long>(prefix_width) * page + 127) / 128);
-    if (tiles < 16 * static_cast<long long>(p0.ctas)) {
-        p0.ctas /= 2;
-        p.ctas /= 2;
     }
     const cudaError_t e = launch_fwd_kv8_prefix(p0, p, j, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_kv8_prefix launch");

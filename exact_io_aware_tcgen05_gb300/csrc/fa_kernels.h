@@ -204,7 +204,6 @@ struct Kv8FwdParams {
     void* o;            // 16-bit, or fp32 with o_f32
     float* lse;
     int o_f32;          // a pass of attention with shared prefixes
-    int behind;         // the second of them
     int width, num_pages, page_log2;
     uint32_t group_inv; // ceil(2^32 / group)
     int columns;        // rows of an item (kv8_columns)

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     uint8_t* sP = sQ + 2 * K::kQBytes;                    // [2][blocks of 16 columns][keys][16]
     Kv8Smem<C>& sm = *reinterpret_cast<Kv8Smem<C>*>(sP + 2 * K::kPBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (!F32) grid_launch_dependents();
+    grid_launch_dependents();
 
     if (threadIdx.x == 0) {
         sm.abort = 0;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
         fence_proxy_async_smem();
     }
     // what the kernels before this one wrote is there from here on
-    wait_and_launch<F32>(p);
+    grid_dependency_wait();
     find_share<C>(p, sm);
     tc_fence_before();
     __syncthreads();
@@ -691,7 +691,6 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, K::kTmemCols);
-    if (F32 && p.behind) grid_dependency_wait();
 }
 
 // Joins the parts of the item that begins at the end of CTA c's share, c = blockIdx.x: a warp

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     RowsSmem& sm = *reinterpret_cast<RowsSmem*>(sV + K::kV16Bufs * K::kV16Bytes);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (!F32) grid_launch_dependents();
+    grid_launch_dependents();
 
     if (threadIdx.x == 0) {
         sm.abort = 0;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
         tmem_relinquish();
     }
     // what the kernels before this one wrote is there from here on
-    wait_and_launch<F32>(p);
+    grid_dependency_wait();
     find_share<kRows>(p, sm);
     tc_fence_before();
     __syncthreads();
@@ -638,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, 2) fa_fwd_kv8_rows_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 256);
-    if (F32 && p.behind) grid_dependency_wait();
 }
 
 template <int D, int E, bool F32>

@@ -660,16 +660,6 @@ __device__ __forceinline__ void produce(const Kv8FwdParams& p, Smem& sm, uint8_t
         drain_on(smem_addr(&sm.scales_full[i % kScaleSlots]), (i / kScaleSlots) & 1);
 }
 
-// The start of a pass: what the kernels before it leave is there behind this.  Of two passes that are
-// parts of one call (F32) the first lets the second begin, while it runs itself, once it has waited
-// for them, so that the second (p.behind) need not wait: it waits for the first at its own end, and
-// with it what waits for the second waits for both.
-template <bool F32>
-__device__ __forceinline__ void wait_and_launch(const Kv8FwdParams& p) {
-    if (!F32 || !p.behind) grid_dependency_wait();
-    if (F32) grid_launch_dependents();
-}
-
 // A launch that may begin while the kernel before it on the stream is ending (it waits for
 // that one's results itself).
 template <class... Params>

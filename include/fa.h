@@ -493,7 +493,7 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
  * tokens each.  O and LSE of both parts are held in fp32 in the workspace of
  * fa_fwd_kv8_prefix_workspace_size(...) bytes (8 Hq d bytes a token and 2 of fa_fwd_kv8's) and joined
  * there: O = sum_i exp(LSE_i - LSE) O_i.  Limits: as fa_fwd_kv8's, for the prefixes with `groups`
- * and prefix_width in place of B and width.  Enqueues five kernels; takes no launch events.
+ * and prefix_width in place of B and width.  Enqueues four kernels; takes no launch events.
  *
  * The size does not depend on lens.  The result does not depend on anything but the
  * inputs, the geometry and the device's SM count.  Enqueues two kernels (L = 2 for
