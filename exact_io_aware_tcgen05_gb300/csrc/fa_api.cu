@@ -924,6 +924,19 @@ fa_status fa_debug_check_selftest(cudaStream_t stream) {
 namespace fa {
 namespace {
 
+// The status word for kernels without waits: only the checking build's use it (a look-up takes as long
+// on the host as a small kernel on the GPU).
+fa_status take_checks_status(const char* who, NormRopeParams* p) {
+#ifdef FA_DEBUG_CHECKS
+    p->status = status_word_ptr();
+    if (!p->status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
+#else
+    (void)who;
+    p->status = nullptr;
+#endif
+    return FA_OK;
+}
+
 bool tokens_ok(const void* x, long long stride, int heads, int d) {
     return aligned16(x) && stride % 8 == 0 && stride >= static_cast<long long>(heads) * d;
 }
@@ -989,7 +1002,7 @@ fa_status fa_norm_rope(fa_dtype dtype, const void* q, long long q_stride, const 
     using namespace fa;
     t_last_error[0] = '\0';
     NormRopeParams p;
-    const fa_status st = take_norm_rope("fa_norm_rope", dtype, T, Hq, Hkv, d, norm, q_weight, k_weight, weights_f32,
+    fa_status st = take_norm_rope("fa_norm_rope", dtype, T, Hq, Hkv, d, norm, q_weight, k_weight, weights_f32,
                                         eps, positions, axes, num_axes, turns, rot, interleaved, &p);
     if (st != FA_OK) return st;
     if (T == 0) return FA_OK;
@@ -1007,8 +1020,7 @@ fa_status fa_norm_rope(fa_dtype dtype, const void* q, long long q_stride, const 
     p.x_stride[1] = k_stride;
     p.y_stride[0] = q_out_stride;
     p.y_stride[1] = k_out_stride;
-    p.status = status_word_ptr();
-    if (!p.status) return fail(FA_ERR_CUDA, "fa_norm_rope: cannot resolve the device status word");
+    if ((st = take_checks_status("fa_norm_rope", &p)) != FA_OK) return st;
     if (norm_rope_plan(p, d, sm_count(), false) == 0)
         return fail(FA_ERR_UNSUPPORTED, "fa_norm_rope: problem too large for one launch");
     const cudaError_t e = launch_norm_rope(p, d, stream);
@@ -1037,7 +1049,7 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
     using namespace fa;
     t_last_error[0] = '\0';
     NormRopeParams p;
-    const fa_status st = take_norm_rope("fa_norm_rope_bwd", dtype, T, Hq, Hkv, d, norm, q_weight, k_weight,
+    fa_status st = take_norm_rope("fa_norm_rope_bwd", dtype, T, Hq, Hkv, d, norm, q_weight, k_weight,
                                         weights_f32, eps, positions, axes, num_axes, turns, rot, interleaved, &p);
     if (st != FA_OK) return st;
     if (!norm && (dq_weight || dk_weight))
@@ -1084,8 +1096,7 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
     p.y_stride[1] = dk_stride;
     p.dw[0] = dq_weight;
     p.dw[1] = dk_weight;
-    p.status = status_word_ptr();
-    if (!p.status) return fail(FA_ERR_CUDA, "fa_norm_rope_bwd: cannot resolve the device status word");
+    if ((st = take_checks_status("fa_norm_rope_bwd", &p)) != FA_OK) return st;
     if (norm_rope_plan(p, d, sm_count(), true) == 0)
         return fail(FA_ERR_UNSUPPORTED, "fa_norm_rope_bwd: problem too large for one launch");
     const cudaError_t e = launch_norm_rope_bwd(p, d, stream);
@@ -1390,8 +1401,7 @@ fa_status fa_kv8_append_norm_rope(fa_dtype dtype, const void* q, long long q_str
     n.x_stride[0] = q_stride;
     n.x_stride[1] = k_stride;
     n.y_stride[0] = q_out_stride;
-    n.status = status_word_ptr();
-    if (!n.status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
+    if ((st = take_checks_status(who, &n)) != FA_OK) return st;
     // a chunk is a block's tokens where that leaves two CTAs or more for every SM, and then a CTA has two
     p.chunk = static_cast<int>(std::min(std::max(T / (2LL * sm_count()), 1LL), static_cast<long long>(kKv8Block)));
     p.chunks = p.chunk == kKv8Block ? 2 : 1;
