@@ -4,7 +4,7 @@
 //
 // Both are bound by memory: the forward reads and writes each value once (4 bytes), the backward
 // reads two and writes one (6 bytes).  What it takes to come near: enough rows on their way (an SM
-// needs some 50 KB), few instructions a row (some 200 for the 4 or 8 rows of a warp, half of them the
+// needs some 50 KB), few instructions a row (some 180 for the 4 or 8 rows of a warp, half of them the
 // arithmetic), and angles worked out once for many heads.
 //
 // Measured (one GB300, bf16, the shares of the measured copy rate): forward 32768 tokens, Hq 32, Hkv 8,
@@ -256,17 +256,16 @@ cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t stream) {
     constexpr int smem = kBwdAhead * 4 * 16 * kNormThreads;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = kv8::launch_dependent(
-        kern, p.ctas[0] + p.ctas[1], kNormThreads, smem, stream, p);
+    e = kv8::launch_dependent(kern, p.ctas[0] + p.ctas[1], kNormThreads, smem, stream, p);
     if (e != cudaSuccess || !p.partial) return e;
     return kv8::launch_dependent(norm_rope_weights_kernel<D>, 2 * (D / 32), 1024, 0, stream, p);
 }
 
-// The heads of a unit: the largest divisor of `heads` that leaves `want` units or more (1 where even
-// single heads do not).
+// The heads of a unit: the largest divisor of `heads` (128 at most, by when angles cost nothing) that
+// leaves `want` units or more, 1 where even single heads do not.
 int heads_of_unit(long long T, int heads, long long want) {
     int best = 1;
-    for (int r = 2; r <= heads; ++r)
+    for (int r = 2; r <= std::min(heads, 128); ++r)
         if (heads % r == 0 && T * (heads / r) >= want) best = r;
     return best;
 }
