@@ -545,8 +545,12 @@ def _dtype_code(*tensors) -> int:
     """fa_dtype of torch tensors that must all be bf16, or all fp16."""
     import torch
     first = tensors[0].dtype
-    if first in (torch.bfloat16, torch.float16) and all([t.dtype == first for t in tensors]):
-        return FA_DTYPE_BF16 if first == torch.bfloat16 else FA_DTYPE_F16
+    if first == torch.bfloat16 or first == torch.float16:
+        for t in tensors:
+            if t.dtype != first:
+                break
+        else:
+            return FA_DTYPE_BF16 if first == torch.bfloat16 else FA_DTYPE_F16
     kinds = {t.dtype for t in tensors}
     raise TypeError(f"q, k, v (and o, dout) must all be bfloat16 or all float16, got {kinds}")
 
@@ -827,17 +831,19 @@ def _norm_rope(dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, e
 
 def _weight(name, w, dtype, d, dev, norm):
     """Whether a norm's weights are float32 (or else of q's type)."""
-    import torch
     kind = w.dtype
+    wide = kind != dtype
     if not norm:
         raise ValueError(f"{name} without a norm")
-    if kind != dtype and kind != torch.float32:
-        raise TypeError(f"{name} must be float32 or of q's type, got {kind}")
+    if wide:
+        import torch
+        if kind != torch.float32:
+            raise TypeError(f"{name} must be float32 or of q's type, got {kind}")
     if w.shape != (d,) or not w.is_contiguous():
         raise ValueError(f"{name} must be contiguous and have the shape ({d},), got {tuple(w.shape)}")
     if w.get_device() != dev:
         raise ValueError(_ONE_DEVICE)
-    return kind == torch.float32
+    return wide
 
 
 @functools.lru_cache(maxsize=4096)
@@ -866,20 +872,29 @@ def _beside(name, x, dtype, lead, d, dev, heads=0):
     return heads_x, stride
 
 
+@functools.lru_cache(maxsize=4096)
+def _pair(q_shape, q_strides, k_shape, k_strides):
+    """Leading dimensions, tokens, head dimension, and heads and strides of q and k."""
+    lead, T, Hq, d, q_stride = _tokens("q", q_shape, q_strides)
+    lead_k, _, Hkv, d_k, k_stride = _tokens("k", k_shape, k_strides)
+    if lead_k != lead or d_k != d:
+        raise ValueError(f"k must have the shape {tuple(lead)} + (heads, {d}), got {tuple(k_shape)}")
+    return lead, T, d, Hq, q_stride, Hkv, k_stride
+
+
 def _qk(q, k, dev):
-    """fa_dtype, leading dimensions, tokens, head dimension, and heads and strides of q and k."""
-    dtype = _dtype_code(q, k)
-    if dev < 0:
+    """_pair of q and k, on CUDA device number `dev`."""
+    if dev < 0 or k.get_device() != dev:
         raise ValueError(_ONE_DEVICE)
-    lead, T, Hq, d, q_stride = _tokens("q", q.shape, q.stride())
-    return (dtype, lead, T, d, Hq, q_stride, *_beside("k", k, q.dtype, lead, d, dev))
+    return _pair(q.shape, q.stride(), k.shape, k.stride())
 
 
 def _fresh(like):
-    """A new tensor of `like`'s shape and type, contiguous, and its tokens' distance."""
+    """A new tensor of `like`'s shape and type, contiguous."""
     import torch
-    shape = like.shape
-    return torch.empty_like(like, memory_format=torch.contiguous_format), shape[-2] * shape[-1]
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def norm_rope_forward(q, k, positions=None, rope: RopePlan | None = None, *, q_weight=None, k_weight=None, norm=True,
@@ -894,11 +909,12 @@ def norm_rope_forward(q, k, positions=None, rope: RopePlan | None = None, *, q_w
         return _there(norm_rope_forward, dev, stream, q, k, positions, rope, q_weight=q_weight, k_weight=k_weight,
                       norm=norm, eps=eps, out=out)
     import torch
-    dtype, lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
+    dtype = _dtype_code(q, k)
+    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
     norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
     if out is None:
-        q_out, q_out_stride = _fresh(q)
-        k_out, k_out_stride = _fresh(k)
+        q_out, q_out_stride = _fresh(q), Hq * d
+        k_out, k_out_stride = _fresh(k), Hkv * d
     else:
         q_out, k_out = out
         _, q_out_stride = _beside("out[0]", q_out, q.dtype, lead, d, dev, Hq)
@@ -927,13 +943,14 @@ def norm_rope_backward(q, k, dq_out, dk_out, positions=None, rope: RopePlan | No
         return _there(norm_rope_backward, dev, stream, q, k, dq_out, dk_out, positions, rope, q_weight=q_weight,
                       k_weight=k_weight, norm=norm, eps=eps, out=out, workspace=workspace)
     import torch
-    dtype, lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
+    dtype = _dtype_code(q, k, dq_out, dk_out)
+    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
     norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
     _, dq_out_stride = _beside("dq_out", dq_out, q.dtype, lead, d, dev, Hq)
     _, dk_out_stride = _beside("dk_out", dk_out, q.dtype, lead, d, dev, Hkv)
     if out is None:
-        dq, dq_stride = _fresh(q)
-        dk, dk_stride = _fresh(k)
+        dq, dq_stride = _fresh(q), Hq * d
+        dk, dk_stride = _fresh(k), Hkv * d
     else:
         dq, dk = out
         _, dq_stride = _beside("out[0]", dq, q.dtype, lead, d, dev, Hq)
@@ -969,7 +986,8 @@ def kv8_append_norm_rope(cache: Kv8Cache, q, k, v, slots, positions=None, rope: 
     import torch
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d]")
-    dtype, lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
+    dtype = _dtype_code(q, k, v)
+    lead, T, d, Hq, q_stride, Hkv, k_stride = _qk(q, k, dev)
     num_pages, heads, page, dk = _kv8_shape(cache, dev)
     if heads != Hkv or dk != d:
         raise ValueError(f"the cache has {heads} heads of {dk} channels, k {Hkv} of {d}")
@@ -977,7 +995,7 @@ def kv8_append_norm_rope(cache: Kv8Cache, q, k, v, slots, positions=None, rope: 
     _int32("slots", slots, lead, dev)
     norms, turned = _norm_rope(q.dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, eps)
     if out is None:
-        out, out_stride = _fresh(q)
+        out, out_stride = _fresh(q), Hq * d
     else:
         _, out_stride = _beside("out", out, q.dtype, lead, d, dev, Hq)
     k8, k_scale, v8, v_scale = cache
