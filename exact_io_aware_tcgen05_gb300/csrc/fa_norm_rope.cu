@@ -27,7 +27,7 @@ struct Unit {
     long long token;
     int head;
     __device__ __forceinline__ Unit(const NormRopeParams& p, int side, long long unit) {
-        const long long part = unit / p.T;
+        const long long part = kv8::divide(unit, static_cast<long long>(p.T));
         token = unit - part * p.T;
         head = static_cast<int>(part) * p.run[side];
     }
