@@ -386,22 +386,24 @@ __device__ __forceinline__ void key_row(const NormRopeParams& q, const RowLane<D
 template <int D, int E, bool IL, bool PAIR, bool RARE>
 __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const NormRopeParams& q, const RowLane<D, IL>& at,
                                               const float (&w)[16], int h, long long c0, int t, int c1,
-                                              const float* cosines, const float* sines, uint32_t (*tops)[2], int& turn) {
+                                              const float* cosines, const float* sines, uint2 (*tops)[2], int& turn) {
     constexpr int kLanes = D / 16;               // lanes of one token
     constexpr int kRows = 32 / kLanes;           // tokens the warp loads at a time
     constexpr int kMine = kKv8Block / 2, kSteps = kMine / kRows;
     const int lane = threadIdx.x & 31, pair = threadIdx.x / 64, second = PAIR ? threadIdx.x / 32 & 1 : 0;
     const int mine = second * kMine + lane / kLanes;   // the lane's first token in a run
-    // the larger of both warps' numbers (the buffers take turns: a warp that writes one again has met
-    // the other since that one read it)
-    auto both = [&](uint32_t top) {
+    // The larger of both warps' numbers, and the first one's `old`: where a block comes in several runs,
+    // the second may have read its scale before the first wrote it, and both must go the same way (the
+    // buffers take turns: a warp that writes one again has met the other since that one read it).
+    auto both = [&](uint32_t top, float& old) {
         top = __reduce_max_sync(0xffffffffu, top);
         if (!PAIR) return top;
-        uint32_t* x = tops[turn & 1];
+        uint2* x = tops[turn & 1];
         ++turn;
-        if (lane == 0) x[second] = top;
+        if (lane == 0) x[second] = make_uint2(top, __float_as_uint(old));
         named_bar_sync(1 + pair, 64);
-        return max(x[0], x[1]);
+        old = __uint_as_float(x[0].y);
+        return max(x[0].x, x[1].x);
     };
     while (t < c1) {
         const BlockRun run = next_run(p, t, c0);
@@ -426,7 +428,7 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
         const long long row0 = (static_cast<long long>(page) * p.Hkv + h) << p.page_log2;
         float* scale_at = p.scales[0] + (row0 + in_page) / kKv8Block;
         uint8_t* row = p.codes[0] + (row0 + in_page) * D;
-        const float old = off > 0 ? *scale_at : 0.f;
+        float old = off > 0 ? *scale_at : 0.f;
         float v[kSteps][16], r[kSteps];
         float most = 0.f;   // the largest magnitude (NaN does not count)
 #pragma unroll
@@ -438,7 +440,7 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
             for (int j = 0; j < 16; j += 2) m = fmax3(m, fabsf(v[i][j]), fabsf(v[i][j + 1]));
             if (i * kRows + mine < n) most = fmaxf(most, m * r[i]);
         }
-        uint32_t top = both(__float_as_uint(most));
+        uint32_t top = both(__float_as_uint(most), old);
         if (RARE && top >= 0x7f800000u) {
             top = 0;
             for (int i = 0; i < kSteps; ++i)
@@ -446,7 +448,7 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
                     const uint32_t a = __float_as_uint(v[i][j] * r[i]) & 0x7fffffffu;
                     if (i * kRows + mine < n && a < 0x7f800000u) top = max(top, a);
                 }
-            top = both(top);
+            top = both(top, old);
         }
         const float scale = fmaxf(pow2f(scale_exponent(top)), old);
         if (!RARE && (top >= 0x7f800000u || (__float_as_uint(scale) & 0x7fffffu) != 0)) return t;
@@ -482,7 +484,7 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
 template <int D, int E, bool IL, bool PAIR>
 __device__ __noinline__ int append_rotated_rare(const Kv8AppendParams& p, const NormRopeParams& q, int h, long long c0,
                                                 int t, int c1, const float* cosines, const float* sines,
-                                                uint32_t (*tops)[2], int turn) {
+                                                uint2 (*tops)[2], int turn) {
     const RowLane<D, IL> at(threadIdx.x % (D / 16), q.rope.rot);
     float w[16];
     if (q.norm) load_weights<D, E, IL>(q.w[1], q.wide, at, w);
@@ -494,7 +496,7 @@ __device__ __noinline__ int append_rotated_rare(const Kv8AppendParams& p, const 
 template <int D, int E, bool IL, bool PAIR>
 __device__ __forceinline__ void append_keys(const Kv8AppendParams& p, const NormRopeParams& q, long long c0, int tokens,
                                             const float (*cosines)[D / 2], const float (*sines)[D / 2],
-                                            uint32_t (*tops)[2][2]) {
+                                            uint2 (*tops)[2][2]) {
     constexpr int kTeams = kNormThreads / (PAIR ? 64 : 32);
     const int team = threadIdx.x / (PAIR ? 64 : 32);
     const RowLane<D, IL> at(threadIdx.x % (D / 16), q.rope.rot);
@@ -504,7 +506,7 @@ __device__ __forceinline__ void append_keys(const Kv8AppendParams& p, const Norm
     for (int i = team; i < p.Hkv * p.chunks; i += kTeams) {
         const int first = i / p.Hkv * p.chunk, h = i % p.Hkv;
         const int t0 = static_cast<int>(c0) + first, t1 = static_cast<int>(c0) + min(first + p.chunk, tokens);
-        uint32_t (*mine)[2] = tops[PAIR ? team : 0];
+        uint2 (*mine)[2] = tops[PAIR ? team : 0];
         const int t = append_rotated<D, E, IL, PAIR, false>(p, q, at, w, h, t0, t0, t1, cosines[first], sines[first], mine, turn);
         if (t < t1) turn = append_rotated_rare<D, E, IL, PAIR>(p, q, h, t0, t, t1, cosines[first], sines[first], mine, turn);
     }
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
     const __grid_constant__ Kv8AppendParams p, const __grid_constant__ NormRopeParams q) {
     constexpr int kTokens = 3 * kKv8Block - 1, kWarps = kNormThreads / 32;
     __shared__ alignas(16) float cosines[kTokens][D / 2], sines[kTokens][D / 2];
-    __shared__ uint32_t tops[kWarps / 2][2][2];
+    __shared__ uint2 tops[kWarps / 2][2][2];
     grid_launch_dependents();
     grid_dependency_wait();
     const int role = blockIdx.y, warp = threadIdx.x / 32;

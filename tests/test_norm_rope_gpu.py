@@ -240,6 +240,39 @@ def test_append_to_blocks_that_others_began(fa, case, bad):
     check_keys(torch, before, (cache.k8, cache.k_scale), y, bound.nan_to_num(0.0, 0.0), slots)
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "f16")])
+def test_blocks_whose_tokens_come_in_several_runs(fa, d, dtype):
+    """Two blocks' tokens in turn leave what these blocks hold undefined, and nothing else: the call
+    ends, whatever the blocks' scales were, and the other blocks and the queries are as ever."""
+    import torch
+    Hkv, page, T = 3, 16, 5120          # 16 tokens in turn from two blocks, then 16 of one block, and so on
+    rng = np.random.default_rng(d)
+    pages = T // 32 * 3
+    ids = rng.permutation(pages).reshape(-1, 3)
+    slots = []
+    for a, b, c in ids:
+        slots += [int(x) * page + 1 + i for i in range(8) for x in (a, b)] + [int(c) * page + i for i in range(16)]
+    for step in range(4):
+        codes = [torch.from_numpy(rng.integers(0, 256, (pages, Hkv, page, d)).astype(np.uint8)).cuda().view(torch.float8_e4m3fn)
+                 for _ in range(2)]
+        scales = [torch.from_numpy(2.0 ** rng.uniform(-9, 1, (pages, Hkv, 1)).astype(np.float32)).cuda() for _ in range(2)]
+        cache = fa.Kv8Cache((codes[0], scales[0], codes[1], scales[1]))
+        q, k, w, pos, axis = make(torch, step, (T,), 4, Hkv, d, dtype, d, 1, False, False, False)
+        k *= (2.0 ** -torch.arange(T, device="cuda").remainder(32).div(2, rounding_mode="floor"))[:, None, None] * 2.0 ** step
+        s = torch.tensor(slots, dtype=torch.int32, device="cuda")
+        before = cache.k8.clone(), cache.k_scale.clone()
+        p = plan(fa, d, axis, False)
+        got = fa.kv8_append_norm_rope(cache, q, k, torch.randn_like(k), s, pos, p, norm=False)
+        torch.cuda.synchronize()
+        assert torch.equal(got, fa.norm_rope_forward(q, k, pos, p, norm=False)[0])
+        y, bound = ref.forward(k, None, angle(pos, d, axis), False, False, EPS)
+        open_ = torch.from_numpy(ids[:, :2].copy()).cuda().flatten()
+        for x, old in zip((cache.k8.view(torch.uint8), cache.k_scale), (before[0].view(torch.uint8), before[1])):
+            x[open_] = old[open_]
+        sure = [x if t % 32 >= 16 else -1 for t, x in enumerate(slots)]
+        check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, sure)
+
+
 @pytest.mark.parametrize("norm,rot,il", [(False, 64, False), (False, 64, True), (False, 32, False), (True, 64, False), (False, 0, True)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_infinities_and_nan_stay_in_their_pairs(fa, norm, rot, il, dtype):
