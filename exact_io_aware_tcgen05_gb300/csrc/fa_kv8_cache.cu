@@ -377,7 +377,8 @@ __device__ __forceinline__ void key_row(const NormRopeParams& q, const RowLane<D
 // block's scale and codes come, so that a key is rounded once.  With PAIR two warps have a block, the
 // first and the last 8 of its new tokens, and both walk the chunk's runs (one warp's 64 numbers a lane
 // did not fit its registers beside the rest: 322 us in place of 301 for 8 prompts of 8192 tokens, Hq 32,
-// Hkv 8, d = 128); `tops` is theirs, for two runs in turn.  Without, runs have 8 tokens at most.
+// Hkv 8, d = 128); `tops` is theirs, for two runs in turn.  Without, runs have 512 / D tokens at most,
+// what a warp loads at a time.
 // `cosines` and `sines`: rows of D / 2 for the tokens from c0 on; w: the lane's weights.
 //
 // Returns the first token that is not done: c1, or, without RARE, where a run needs RARE: there are
@@ -389,7 +390,7 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
                                               const float* cosines, const float* sines, uint2 (*tops)[2], int& turn) {
     constexpr int kLanes = D / 16;               // lanes of one token
     constexpr int kRows = 32 / kLanes;           // tokens the warp loads at a time
-    constexpr int kMine = kKv8Block / 2, kSteps = kMine / kRows;
+    constexpr int kMine = kKv8Block / 2, kSteps = PAIR ? kMine / kRows : 1;
     const int lane = threadIdx.x & 31, pair = threadIdx.x / 64, second = PAIR ? threadIdx.x / 32 & 1 : 0;
     const int mine = second * kMine + lane / kLanes;   // the lane's first token in a run
     // The larger of both warps' numbers, and the first one's `old`: where a block comes in several runs,
@@ -520,9 +521,9 @@ __device__ __forceinline__ void append_keys(const Kv8AppendParams& p, const Norm
 //
 // In long batches the queries have norm_rope_kernel, which keeps more warps on an SM (queries here, all
 // kinds of CTAs side by side: 315 us and more for the prompts below).  Measured (one GB300, bf16, Hq 32,
-// Hkv 8, d = 128): 8 prompts of 8192 tokens 298 us, 73 % of the measured copy rate: the queries 169 us, 93 %,
-// then keys and values 130 us, where the keys' instructions bound (some 320 for the 4 rows of a warp's
-// pass) at 16 warps an SM; 64 single tokens 4.3 us, a launch and the slots, positions and rows that wait
+// Hkv 8, d = 128): 8 prompts of 8192 tokens 297 us, 73 % of the measured copy rate: the queries 169 us, 93 %,
+// then keys and values 130 us, where the keys wait for their loads and for the other warp of a block (issue
+// slots 45 % used, DRAM 36 %; four warps to a block, with 24 warps an SM: 300); 64 single tokens 3.9 us, a launch and the slots, positions and rows that wait
 // for one another.
 constexpr int kAppendValues = 0, kAppendKeys = 1, kAppendQueries = 2;
 
@@ -553,13 +554,16 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
             if (row >= tokens && p.slots[c0 + row] != last + row - tokens + 1) continue;
 #pragma unroll
             for (int f = lane; f < D / 2; f += 32)
-                if (f < half) cos_sin(q.rope, f, c0 + row, cosines[row][f], sines[row][f]);
+                if (f < half) {
+                    const int place = place_of<D, IL>(f);
+                    cos_sin(q.rope, f, c0 + row, cosines[row][place], sines[row][place]);
+                }
         }
     }
     __syncthreads();
     if (role == kAppendKeys) {
         // (a decoding step's single tokens need no pairs of warps)
-        if (tokens == 1 && next_run(p, static_cast<int>(c0), c0).n <= kKv8Block / 2)
+        if (tokens == 1 && next_run(p, static_cast<int>(c0), c0).n <= 512 / D)
             append_keys<D, E, IL, false>(p, q, c0, tokens, cosines, sines, tops);
         else
             append_keys<D, E, IL, true>(p, q, c0, tokens, cosines, sines, tops);

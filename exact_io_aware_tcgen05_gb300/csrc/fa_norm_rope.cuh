@@ -84,15 +84,21 @@ __device__ __forceinline__ void lane_rotation(const RopeParams& p, const RowLane
     }
 }
 
-// From rows of cosines and of sines in shared memory.
+// From rows of cosines and of sines in shared memory, where frequency f is at place_of(f): the lanes of
+// a row read neighbouring 16 bytes.
+template <int D, bool IL>
+__device__ __forceinline__ int place_of(int f) {
+    return IL ? f : (f & 4 ? D / 4 : 0) + f / 8 * 4 + f % 4;
+}
 template <int D, bool IL>
 __device__ __forceinline__ void rotation_from(const float* cos_row, const float* sin_row, const RowLane<D, IL>& at,
                                               Rotation& r) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (!at.turned[j]) continue;
-        *reinterpret_cast<float4*>(&r.c[4 * j]) = *reinterpret_cast<const float4*>(cos_row + at.freq[j]);
-        *reinterpret_cast<float4*>(&r.s[4 * j]) = *reinterpret_cast<const float4*>(sin_row + at.freq[j]);
+        const int place = place_of<D, IL>(at.freq[j]);
+        *reinterpret_cast<float4*>(&r.c[4 * j]) = *reinterpret_cast<const float4*>(cos_row + place);
+        *reinterpret_cast<float4*>(&r.s[4 * j]) = *reinterpret_cast<const float4*>(sin_row + place);
     }
 }
 
