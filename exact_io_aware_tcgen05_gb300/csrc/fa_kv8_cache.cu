@@ -523,8 +523,8 @@ __device__ __forceinline__ void append_keys(const Kv8AppendParams& p, const Norm
 // kinds of CTAs side by side: 315 us and more for the prompts below).  Measured (one GB300, bf16, Hq 32,
 // Hkv 8, d = 128): 8 prompts of 8192 tokens 297 us, 73 % of the measured copy rate: the queries 169 us, 93 %,
 // then keys and values 130 us, where the keys wait for their loads and for the other warp of a block (issue
-// slots 45 % used, DRAM 36 %; four warps to a block, with 24 warps an SM: 300); 64 single tokens 3.9 us, a launch and the slots, positions and rows that wait
-// for one another.
+// slots 45 % used, DRAM 36 %; four warps to a block, with 24 warps an SM: 300); 64 single tokens 3.9 us, a
+// launch and the slots, positions and rows that wait for one another.
 constexpr int kAppendValues = 0, kAppendKeys = 1, kAppendQueries = 2;
 
 template <int D, int E, bool IL>
