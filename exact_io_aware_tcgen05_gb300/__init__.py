@@ -755,15 +755,42 @@ def _there(call, device, stream, *args, **kwargs):
 class RopePlan(tuple):
     """(turns, axes, num_axes, interleaved), the frequencies of a rotation by position as the
     kernels take them (:func:`rope_plan`): int64 CUDA tensor [rot / 2] and, with several axes,
-    int32 CUDA tensor [rot / 2]."""
+    int32 CUDA tensor [rot / 2] on the same device.  Checked once, here: the kernels read the
+    tensors by rot."""
     __slots__ = ()
     _fields = ("turns", "axes", "num_axes", "interleaved")
+
+    def __new__(cls, parts):
+        import torch
+        self = super().__new__(cls, parts)
+        if len(self) != 4:
+            raise ValueError(f"a rope plan has {len(cls._fields)} parts, got {len(self)}")
+        turns, axes, num_axes, _ = self
+        if not isinstance(turns, torch.Tensor) or turns.dtype != torch.int64 or not turns.is_contiguous():
+            raise TypeError("turns must be a contiguous int64 tensor")
+        if turns.dim() != 1 or not _frequencies_ok(turns.shape[0]):
+            raise ValueError(f"turns must be [rot / 2], a multiple of 8 from 8 to 64, got {tuple(turns.shape)}")
+        if not isinstance(num_axes, int) or not 1 <= num_axes <= 4:
+            raise ValueError(f"num_axes must be a whole number from 1 to 4, got {num_axes}")
+        if axes is None:
+            if num_axes > 1:
+                raise ValueError("a plan of several axes needs axes")
+            return self
+        if not isinstance(axes, torch.Tensor) or axes.dtype != torch.int32 or not axes.is_contiguous():
+            raise TypeError("axes must be a contiguous int32 tensor")
+        if axes.shape != turns.shape or axes.device != turns.device:
+            raise ValueError("axes must have the shape of turns and be on their device")
+        return self
 
     def __getattr__(self, name):
         try:
             return self[self._fields.index(name)]
         except ValueError:
             raise AttributeError(name) from None
+
+
+def _frequencies_ok(n):
+    return 8 <= n <= 64 and n % 8 == 0
 
 
 # 2^64 / (2 pi) as a fraction
@@ -777,7 +804,7 @@ def rope_plan(frequencies, *, axes=None, interleaved=False, device="cuda") -> Ro
     ``axes``: for positions on several axes (up to 4), the axis that each frequency goes by."""
     import torch
     f = [float(x) for x in (frequencies.tolist() if isinstance(frequencies, torch.Tensor) else frequencies)]
-    if not f or len(f) % 8 or len(f) > 64:
+    if not _frequencies_ok(len(f)):
         raise ValueError(f"the number of frequencies must be a multiple of 8 from 8 to 64, got {len(f)}")
     if not all(math.isfinite(x) for x in f):
         raise ValueError("frequencies must be finite")
@@ -816,7 +843,7 @@ def _norm_rope(dtype, lead, d, dev, positions, rope, q_weight, k_weight, norm, e
         if positions is not None:
             raise ValueError("positions without a rope plan")
         return (norm, q_ptr, k_ptr, wide, eps), (None, None, 1, None, 0, 0)
-    turns, axes, num_axes, interleaved = rope
+    turns, axes, num_axes, interleaved = rope if isinstance(rope, RopePlan) else RopePlan(rope)
     if positions is None:
         raise ValueError("a rope plan needs positions")
     _int32("positions", positions, lead if num_axes == 1 else (num_axes, *lead), dev)
