@@ -393,12 +393,16 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
     constexpr int kMine = kKv8Block / 2, kSteps = PAIR ? kMine / kRows : 1;
     const int lane = threadIdx.x & 31, pair = threadIdx.x / 64, second = PAIR ? threadIdx.x / 32 & 1 : 0;
     const int mine = second * kMine + lane / kLanes;   // the lane's first token in a run
-    // The larger of both warps' numbers, and the first one's `old`: where a block comes in several runs,
-    // the second may have read its scale before the first wrote it, and both must go the same way (the
-    // buffers take turns: a warp that writes one again has met the other since that one read it).
+    // The larger of both warps' numbers, and the first one's first lane's `old`: where a block comes in
+    // several runs, another warp (of the pair or of any CTA) may write its scale while this one reads it,
+    // and all lanes of a pair must go the same way (the buffers take turns: a warp that writes one again
+    // has met the other since that one read it).
     auto both = [&](uint32_t top, float& old) {
         top = __reduce_max_sync(0xffffffffu, top);
-        if (!PAIR) return top;
+        if (!PAIR) {
+            old = __shfl_sync(0xffffffffu, old, 0);
+            return top;
+        }
         uint2* x = tops[turn & 1];
         ++turn;
         if (lane == 0) x[second] = make_uint2(top, __float_as_uint(old));

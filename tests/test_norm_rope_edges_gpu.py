@@ -27,3 +27,36 @@ def test_plans_as_plain_tuples(fa):
             fa.norm_rope_forward(q, k, pos, parts, norm=False)
         with pytest.raises(error):
             fa.norm_rope_backward(q, k, q, k, pos, parts, norm=False)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "f16")])
+def test_single_tokens_of_one_block_at_once(fa, d, dtype):
+    """Few tokens, each a run of its own, some blocks' by several warps at once, the blocks begun with scales
+    that are no powers of two: those blocks' contents are undefined, and nothing else; the call ends."""
+    import torch
+    Hkv, page, pages = 3, 16, 40
+    rng = np.random.default_rng(d)
+    for step in range(20):
+        ids = rng.permutation(pages)
+        # four tokens each of one block in turn with another's, then single tokens of blocks of their own
+        slots = [int(ids[2 * i + j]) * page + 1 + 2 * n for i in range(6) for n in range(4) for j in range(2)]
+        alone = [int(b) * page + int(rng.integers(1, 16)) for b in ids[12:30]]
+        slots += alone
+        cache = fa.Kv8Cache(tuple(
+            torch.from_numpy(x).cuda().view(t) for x, t in (
+                (rng.integers(0, 256, (pages, Hkv, page, d)).astype(np.uint8), torch.float8_e4m3fn),
+                (2.0 ** rng.uniform(-9, 1, (pages, Hkv, 1)).astype(np.float32), torch.float32)) * 2))
+        q, k, w, pos, axis = base.make(torch, step, (len(slots),), 4, Hkv, d, dtype, d, norm=False)
+        k *= 2.0 ** (step % 4)
+        s = torch.tensor(slots, dtype=torch.int32, device="cuda")
+        before = cache.k8.clone(), cache.k_scale.clone()
+        p = base.plan(fa, d, axis, False)
+        got = fa.kv8_append_norm_rope(cache, q, k, torch.randn_like(k), s, pos, p, norm=False)
+        torch.cuda.synchronize()
+        assert torch.equal(got, fa.norm_rope_forward(q, k, pos, p, norm=False)[0])
+        y, bound = ref.forward(k, None, base.angle(pos, d, axis), False, False, EPS)
+        open_ = torch.from_numpy(ids[:12].copy()).cuda()
+        for x, old in zip((cache.k8.view(torch.uint8), cache.k_scale), (before[0].view(torch.uint8), before[1])):
+            x[open_] = old[open_]
+        sure = [x if t >= len(slots) - len(alone) else -1 for t, x in enumerate(slots)]
+        base.check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, sure)
