@@ -356,18 +356,14 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendParams p
                        item / p.Hkv / 2 * p.chunk);
 }
 
-// The lane's part of a key, rotated but for its factor r (its inverse norm; rotation keeps factors).
+// The lane's part of a key, normed and rotated.  (The norm's factor could be put off to the product with the
+// block's 1 / scale, rotation keeping factors, which made the prompts below 0.5 % faster; but that product
+// is infinite for a row of zeros with a small eps, and x w may be where x r w is not.)
 template <int D, int E, bool IL>
 __device__ __forceinline__ void key_row(const NormRopeParams& q, const RowLane<D, IL>& at, const float* cosines,
-                                        const float* sines, uint4 a, uint4 b, const float (&w)[16], float (&v)[16],
-                                        float& r) {
+                                        const float* sines, uint4 a, uint4 b, const float (&w)[16], float (&v)[16]) {
     widen<E>(a, b, v);
-    r = 1.f;
-    if (q.norm) {
-        r = inverse_norm<D>(v, q.eps);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] *= w[j];
-    }
+    if (q.norm) scale_row(v, inverse_norm<D>(v, q.eps), w);
     Rotation rot;
     rotation_from<D, IL>(cosines, sines, at, rot);
     rotate<D, IL, false>(at, rot, v);
@@ -434,23 +430,23 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
         float* scale_at = p.scales[0] + (row0 + in_page) / kKv8Block;
         uint8_t* row = p.codes[0] + (row0 + in_page) * D;
         float old = off > 0 ? *scale_at : 0.f;
-        float v[kSteps][16], r[kSteps];
+        float v[kSteps][16];
         float most = 0.f;   // the largest magnitude (NaN does not count)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int place = static_cast<int>(t - c0) + min(i * kRows + mine, n - 1);
-            key_row<D, E, IL>(q, at, cosines + place * (D / 2), sines + place * (D / 2), in[i][0], in[i][1], w, v[i], r[i]);
+            key_row<D, E, IL>(q, at, cosines + place * (D / 2), sines + place * (D / 2), in[i][0], in[i][1], w, v[i]);
             float m = 0.f;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) m = fmax3(m, fabsf(v[i][j]), fabsf(v[i][j + 1]));
-            if (i * kRows + mine < n) most = fmaxf(most, m * r[i]);
+            if (i * kRows + mine < n) most = fmaxf(most, m);
         }
         uint32_t top = both(__float_as_uint(most), old);
         if (RARE && top >= 0x7f800000u) {
             top = 0;
             for (int i = 0; i < kSteps; ++i)
                 for (int j = 0; j < 16; ++j) {
-                    const uint32_t a = __float_as_uint(v[i][j] * r[i]) & 0x7fffffffu;
+                    const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
                     if (i * kRows + mine < n && a < 0x7f800000u) top = max(top, a);
                 }
             top = both(top, old);
@@ -466,12 +462,11 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
         uint8_t* to = row + mine * D;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const float f = r[i] * unscale;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 // (inf * 0 is NaN: infinities become NaN codes)
-                if (RARE) v[i][j] = div_odd(v[i][j] * r[i], scale) + v[i][j] * r[i] * 0.f;
-                else v[i][j] *= f;
+                if (RARE) v[i][j] = div_odd(v[i][j], scale) + v[i][j] * 0.f;
+                else v[i][j] *= unscale;
             }
             if (i * kRows + mine < n) {
 #pragma unroll

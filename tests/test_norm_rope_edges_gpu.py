@@ -60,3 +60,41 @@ def test_single_tokens_of_one_block_at_once(fa, d, dtype):
             x[open_] = old[open_]
         sure = [x if t >= len(slots) - len(alone) else -1 for t, x in enumerate(slots)]
         base.check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, sure)
+
+
+@pytest.mark.parametrize("eps", [1e-6, 2.0 ** -100, 2.0 ** -126, 2.0 ** -128, 2.0 ** -149])
+@pytest.mark.parametrize("T", [1, 3, 40, 6000])
+def test_keys_of_zeros_and_the_least_eps(fa, T, eps):
+    """Rows of zeros, whose inverse norm is eps ** -0.5, into blocks whose scale is the least there is, beside
+    rows that are not zero."""
+    import torch
+    Hkv, d, page = 2, 128, 64
+    q, k, w, pos, axis = base.make(torch, T, (T,), 4, Hkv, d, "bf16", d)
+    k[:, 0] = 0.0
+    q[T // 2:, 1] = 0.0
+    pages = -(-T // page) + 1
+    cache = fa.kv8_cache(pages, Hkv, d, page=page)
+    before = cache.k8.clone(), cache.k_scale.clone()
+    slots = list(range(T))
+    kw = dict(q_weight=w[0], k_weight=w[1], eps=eps)
+    p = base.plan(fa, d, axis, False)
+    got = fa.kv8_append_norm_rope(cache, q, k, k, torch.tensor(slots, dtype=torch.int32, device="cuda"), pos, p, **kw)
+    assert (cache.k8.view(torch.uint8)[:, 0] & 127 == 0).all()
+    assert (got[T // 2:, 1] == 0).all() and torch.equal(got, fa.norm_rope_forward(q, k, pos, p, **kw)[0])
+    y, bound = ref.forward(k, w[1], base.angle(pos, d, axis), False, True, eps)
+    base.check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, slots)
+
+
+def test_keys_with_large_weights(fa):
+    """x r w where x w goes beyond fp32."""
+    import torch
+    T, Hkv, d, page = 50, 2, 64, 16
+    q, k, _, pos, axis = base.make(torch, 5, (T,), 4, Hkv, d, "bf16", 0)
+    w = torch.full((d,), 2.0 ** 80, device="cuda")
+    k = (k.float() * 2.0 ** 55).to(k.dtype)
+    cache = fa.kv8_cache(4, Hkv, d, page=page)
+    before = cache.k8.clone(), cache.k_scale.clone()
+    slots = list(range(T))
+    fa.kv8_append_norm_rope(cache, q, k, k, torch.tensor(slots, dtype=torch.int32, device="cuda"), k_weight=w, eps=EPS)
+    y, bound = ref.forward(k, w, None, False, True, EPS)
+    base.check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, slots)
