@@ -886,9 +886,16 @@ namespace fa {
 namespace {
 
 // One thread tests an index one past a three-element range: a build with the bounds
-// checks records kDevBadIndex; no memory is touched either way.
+// checks records kDevBadIndex; no memory is touched either way.  Before that, addresses
+// on, before, behind and between a tensor's rows, and across a row's end (`other` takes
+// what these record): unless each is judged rightly, the status stays clear.
 __global__ void debug_check_selftest_kernel(int* status) {
-    (void)fa_index_ok(3, 3, status);
+    __shared__ char rows[3 * 48];   // three rows of 32 bytes, 48 apart
+    __shared__ int other;
+    auto ok = [&](int at) { return fa_row_ok(rows, rows + at, 16, 3, 32, 48, &other); };
+    const bool inside = ok(0) && ok(16) && ok(48) && ok(2 * 48 + 16);
+    const bool outside = !ok(-16) && !ok(20) && !ok(32) && !ok(47) && !ok(3 * 48);
+    if (inside && outside) (void)fa_index_ok(3, 3, status);
 }
 
 }  // namespace
@@ -926,15 +933,20 @@ namespace {
 
 // The status word for kernels without waits: only the checking build's use it (a look-up takes as long
 // on the host as a small kernel on the GPU).
-fa_status take_checks_status(const char* who, NormRopeParams* p) {
+fa_status take_checks_status(const char* who, int** status) {
 #ifdef FA_DEBUG_CHECKS
-    p->status = status_word_ptr();
-    if (!p->status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
+    *status = status_word_ptr();
+    if (!*status) return fail(FA_ERR_CUDA, "%s: cannot resolve the device status word", who);
 #else
     (void)who;
-    p->status = nullptr;
+    *status = nullptr;
 #endif
     return FA_OK;
+}
+fa_status take_checks_status(const char* who, NormRopeParams* p) {
+    const fa_status st = take_checks_status(who, &p->status);
+    p->rope.status = p->status;
+    return st;
 }
 
 bool tokens_ok(const void* x, long long stride, int heads, int d) {
@@ -1365,6 +1377,7 @@ fa_status fa_kv8_append(fa_dtype dtype, const void* k, const void* v, long long 
     if (T == 0) return FA_OK;
     p.stride = stride;
     p.elem = static_cast<int>(dtype);
+    if ((st = take_checks_status("fa_kv8_append", &p.status)) != FA_OK) return st;
     const cudaError_t e = launch_kv8_append(p, d, stream);
     return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_kv8_append launch");
 }
@@ -1402,6 +1415,7 @@ fa_status fa_kv8_append_norm_rope(fa_dtype dtype, const void* q, long long q_str
     n.x_stride[1] = k_stride;
     n.y_stride[0] = q_out_stride;
     if ((st = take_checks_status(who, &n)) != FA_OK) return st;
+    p.status = n.status;
     // a chunk is a block's tokens where that leaves two CTAs or more for every SM, and then a CTA has two
     p.chunk = static_cast<int>(std::min(std::max(T / (2LL * sm_count()), 1LL), static_cast<long long>(kKv8Block)));
     p.chunks = p.chunk == kKv8Block ? 2 : 1;
@@ -1497,6 +1511,7 @@ fa_status fa_fwd_kv8_prefix(fa_dtype dtype, const void* q, long long q_stride, c
     j.o = o;
     j.out_lse = lse;
     j.elem = p.elem;
+    j.status = p.status;
     int i = 0;
     for (Kv8FwdParams* x : {&p0, &p}) {
         x->o_f32 = 1;

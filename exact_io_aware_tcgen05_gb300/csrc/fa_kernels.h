@@ -144,6 +144,7 @@ struct Kv8AppendParams {
     int chunk;          // tokens of one warp: the blocks that start among them are its own
     int chunks;         // with norm and rotation: of a CTA
     int elem;
+    int* status;        // (the checking build's)
 };
 
 // Rotation by position (fa_norm_rope in fa.h).
@@ -155,6 +156,7 @@ struct RopeParams {
     int num_axes;
     int rot;                // channels rotated (0: none)
     int interleaved;        // pairs (2 f, 2 f + 1), else (f, f + rot / 2)
+    int* status;            // (the checking build's)
 };
 
 // Norms and rotation of queries (side 0) and keys (side 1), forward and backward.
@@ -174,7 +176,7 @@ struct NormRopeParams {
     int norm, wide;         // whether there is a norm; whether the weights are fp32
     float eps;
     int elem;
-    int* status;
+    int* status;            // (the checking build's)
 };
 
 // What the attention kernel's CTA c leaves for the joining kernel where its range ends
@@ -229,6 +231,7 @@ struct Kv8PrefixJoinParams {
     void* o;
     float* out_lse;
     int elem;
+    int* status;
 };
 
 // Launchers (defined in the kernel translation units).  They only enqueue on

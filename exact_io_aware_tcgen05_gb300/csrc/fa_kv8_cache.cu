@@ -7,7 +7,6 @@
 #include <algorithm>
 #include <climits>
 
-
 namespace fa {
 namespace {
 
@@ -189,12 +188,29 @@ __device__ __forceinline__ float div_odd(float a, float b) {
     return to_odd(x, __fmaf_rn(-x, b, a) == 0.f);
 }
 
+// Whether the addresses formed lie in their tensors (checking build): 8 codes and a scale of one side of
+// the cache, 8 channels of a new token's values (side 1; keys without norm and rotation: 0).
+template <int D>
+__device__ __forceinline__ bool codes_ok(const Kv8AppendParams& p, int side, const void* at) {
+    return fa_row_ok(p.codes[side], at, 8, static_cast<long long>(p.num_slots) * p.Hkv, D, D, p.status);
+}
+__device__ __forceinline__ bool scale_ok(const Kv8AppendParams& p, int side, const float* at) {
+    return fa_index_ok(at - p.scales[side], static_cast<long long>(p.num_slots) / kKv8Block * p.Hkv, p.status);
+}
+template <int D>
+__device__ __forceinline__ bool values_ok(const Kv8AppendParams& p, int side, const void* at) {
+    return fa_row_ok(p.x[side], at, 16, p.T, 2LL * D * p.Hkv, 2 * p.stride, p.status);
+}
+
 // The codes of n new tokens of a block whose scale is not a power of two, by a warp: a block that
 // another writer began (this one's scales are powers of two).  `x` and `row` are the lane's 8
 // values of the first token.
 template <int D, int E>
-__device__ __noinline__ void append_by_division(const uint16_t* x, long long stride, uint8_t* row, int n, float scale) {
+__device__ __noinline__ void append_by_division(const Kv8AppendParams& p, int side, const uint16_t* x, uint8_t* row, int n,
+                                                float scale) {
+    const long long stride = p.stride;
     for (int r = (threadIdx.x & 31) / (D / 8); r < n; r += 32 / (D / 8)) {
+        if (!values_ok<D>(p, side, x + r * stride) || !codes_ok<D>(p, side, row + static_cast<long long>(r) * D)) continue;
         const uint4 w = *reinterpret_cast<const uint4*>(x + r * stride);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         float f[8];
@@ -216,7 +232,7 @@ struct BlockRun {
 __device__ __forceinline__ BlockRun next_run(const Kv8AppendParams& p, int t, long long c0) {
     const int lane = threadIdx.x & 31;
     BlockRun r;
-    r.slot = p.slots[t];
+    r.slot = fa_index_ok(t, p.T, p.status) ? p.slots[t] : -1;
     r.off = r.slot & (kKv8Block - 1);
     const bool real = r.slot >= 0 && r.slot < p.num_slots;
     const int mine = lane < kKv8Block && t + lane < p.T ? p.slots[t + lane] : -1;
@@ -231,9 +247,10 @@ __device__ __forceinline__ BlockRun next_run(const Kv8AppendParams& p, int t, lo
 // lane's 8 codes of the block's first token, `ratio` the old scale by the new one (exact, the new
 // scale being a power of two, or too small for any code).
 template <int D>
-__device__ __forceinline__ void round_again(uint8_t* row, int off, float ratio) {
+__device__ __forceinline__ void round_again(const Kv8AppendParams& p, int side, uint8_t* row, int off, float ratio) {
     for (int r = (threadIdx.x & 31) / (D / 8); r < off; r += 32 / (D / 8)) {
         uint2* at = reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D);
+        if (!codes_ok<D>(p, side, at)) continue;
         uint2 c = *at;
         float f[4];
         unpack4_e4m3(c.x, f);
@@ -277,7 +294,8 @@ __device__ __forceinline__ void append_chunk(const Kv8AppendParams& p, int side,
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = i * kRows + lane / kLanes;
-            w[i] = r < n ? *reinterpret_cast<const uint4*>(x + (t + r) * p.stride) : make_uint4(0, 0, 0, 0);
+            w[i] = r < n && values_ok<D>(p, side, x + (t + r) * p.stride) ? *reinterpret_cast<const uint4*>(x + (t + r) * p.stride)
+                                                                        : make_uint4(0, 0, 0, 0);
         }
         // amax of the finite values, as integers (the order of magnitudes): of pairs of 16-bit
         // ones, or one by one where there is an infinity or NaN to leave out
@@ -312,13 +330,14 @@ __device__ __forceinline__ void append_chunk(const Kv8AppendParams& p, int side,
         float* scale_at = p.scales[side] + (row0 + in_page) / kKv8Block;
         uint8_t* row = p.codes[side] + (row0 + in_page) * D + (lane % kLanes) * 8;
         float scale = pow2f(need);
-        if (off > 0) {
+        const bool known = scale_ok(p, side, scale_at);
+        if (off > 0 && known) {
             const float old = *scale_at;
             scale = fmaxf(old, scale);
-            if (scale > old) round_again<D>(row - static_cast<long long>(off) * D, off, old / scale);
+            if (scale > old) round_again<D>(p, side, row - static_cast<long long>(off) * D, off, old / scale);
         }
         if ((__float_as_uint(scale) & 0x7fffffu) != 0) {
-            append_by_division<D, E>(x + t * p.stride, p.stride, row, n, scale);
+            append_by_division<D, E>(p, side, x + t * p.stride, row, n, scale);
         } else {
             const float inv = 1.f / scale;   // exact for a power of two
 #pragma unroll
@@ -336,13 +355,13 @@ __device__ __forceinline__ void append_chunk(const Kv8AppendParams& p, int side,
                         f[2 * j + 1] += g.y * 0.f;
                     }
                 }
-                if (r < n)
+                if (r < n && codes_ok<D>(p, side, row + static_cast<long long>(r) * D))
                     *reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) =
                         make_uint2(pack4_e4m3(f[0], f[1], f[2], f[3]), pack4_e4m3(f[4], f[5], f[6], f[7]));
             }
         }
         __syncwarp();   // every lane has read the old scale
-        if (lane == 0) *scale_at = scale;
+        if (lane == 0 && known) *scale_at = scale;
         t += n;
     }
 }
@@ -412,11 +431,14 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
         }
         const int off = run.off, n = run.n;
         const uint16_t* x = static_cast<const uint16_t*>(q.x[1]) + (t + mine) * q.x_stride[1] + static_cast<long long>(h) * D;
+        auto ok = [&](const uint16_t* from) {   // (q.heads[1] is 0 where the queries have a kernel of their own)
+            return fa_row_ok(q.x[1], from, 16, p.T, 2LL * D * p.Hkv, 2 * q.x_stride[1], p.status);
+        };
         uint4 in[kSteps][2];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
-            if (i * kRows + mine < n) {
+            if (i * kRows + mine < n && ok(x + 8 * at.unit[0]) && ok(x + 8 * at.unit[1])) {
                 in[i][0] = *reinterpret_cast<const uint4*>(x + 8 * at.unit[0]);
                 in[i][1] = *reinterpret_cast<const uint4*>(x + 8 * at.unit[1]);
             }
@@ -427,7 +449,8 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
         const long long row0 = (static_cast<long long>(page) * p.Hkv + h) << p.page_log2;
         float* scale_at = p.scales[0] + (row0 + in_page) / kKv8Block;
         uint8_t* row = p.codes[0] + (row0 + in_page) * D;
-        float old = off > 0 ? *scale_at : 0.f;
+        const bool known = scale_ok(p, 0, scale_at);
+        float old = off > 0 && known ? *scale_at : 0.f;
         float v[kSteps][16];
         float most = 0.f;   // the largest magnitude (NaN does not count)
 #pragma unroll
@@ -454,8 +477,8 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
         if (!RARE && (PAIR ? rare : __any_sync(0xffffffffu, rare))) return t;
         if (second == 0) {   // (both warps have read the old scale)
             if (off > 0 && scale > old)
-                round_again<D>(row - static_cast<long long>(off) * D + lane % (D / 8) * 8, off, old / scale);
-            if (lane == 0) *scale_at = scale;
+                round_again<D>(p, 0, row - static_cast<long long>(off) * D + lane % (D / 8) * 8, off, old / scale);
+            if (lane == 0 && known) *scale_at = scale;
         }
         const float unscale = 1.f / scale;   // exact for a power of two
         uint8_t* to = row + mine * D;
@@ -470,9 +493,10 @@ __device__ __forceinline__ int append_rotated(const Kv8AppendParams& p, const No
             if (i * kRows + mine < n) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<uint2*>(to + i * kRows * D + 8 * at.unit[j]) =
-                        make_uint2(pack4_e4m3(v[i][8 * j], v[i][8 * j + 1], v[i][8 * j + 2], v[i][8 * j + 3]),
-                                   pack4_e4m3(v[i][8 * j + 4], v[i][8 * j + 5], v[i][8 * j + 6], v[i][8 * j + 7]));
+                    if (codes_ok<D>(p, 0, to + i * kRows * D + 8 * at.unit[j]))
+                        *reinterpret_cast<uint2*>(to + i * kRows * D + 8 * at.unit[j]) =
+                            make_uint2(pack4_e4m3(v[i][8 * j], v[i][8 * j + 1], v[i][8 * j + 2], v[i][8 * j + 3]),
+                                       pack4_e4m3(v[i][8 * j + 4], v[i][8 * j + 5], v[i][8 * j + 6], v[i][8 * j + 7]));
             }
         }
         t += n;
@@ -545,10 +569,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
     if (half > 0) {
         int all = tokens, last = 0;
         if (role == kAppendKeys) {
-            last = p.slots[c0 + tokens - 1];
+            last = fa_index_ok(c0 + tokens - 1, p.T, p.status) ? p.slots[c0 + tokens - 1] : -1;
             all = min(tokens + kKv8Block - 1 - (last & (kKv8Block - 1)), static_cast<int>(min(p.T - c0, 64LL)));
         }
-        for (int row = warp; row < all; row += kWarps) {
+        for (int row = warp; row < all && fa_index_ok(row, kTokens, p.status); row += kWarps) {
             if (row >= tokens && p.slots[c0 + row] != last + row - tokens + 1) continue;
 #pragma unroll
             for (int f = lane; f < D / 2; f += 32)
@@ -587,8 +611,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int h = h0 + u * per + first;
-                in[u][j] = real && h < q.heads[0] ? *reinterpret_cast<const uint4*>(x + h * D + 8 * at.unit[j])
-                                                  : make_uint4(0, 0, 0, 0);
+                const uint16_t* from = x + h * D + 8 * at.unit[j];
+                in[u][j] = real && h < q.heads[0] && channels_ok<D>(q, 0, q.x[0], from, q.x_stride[0])
+                               ? *reinterpret_cast<const uint4*>(from)
+                               : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -597,10 +623,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) kv8_append_norm_rope_kernel(
             widen<E>(in[u][0], in[u][1], v);
             if (q.norm) scale_row(v, inverse_norm<D>(v, q.eps), w);
             rotate<D, IL, false>(at, rot, v);
-            if (real && h < q.heads[0] && fa_index_ok(token, p.T, q.status)) {
+            if (real && h < q.heads[0]) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<uint4*>(y + h * D + 8 * at.unit[j]) = narrow<E>(v + 8 * j);
+                    if (channels_ok<D>(q, 0, q.y[0], y + h * D + 8 * at.unit[j], q.y_stride[0]))
+                        *reinterpret_cast<uint4*>(y + h * D + 8 * at.unit[j]) = narrow<E>(v + 8 * j);
             }
         }
     }

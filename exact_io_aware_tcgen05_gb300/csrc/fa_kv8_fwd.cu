@@ -840,6 +840,7 @@ __global__ void __launch_bounds__(256) fa_kv8_prefix_join_kernel(const Kv8Prefix
     } else {
         at = (static_cast<long long>(token / p.seq.N) * p.seq.Hq + h) * p.seq.N + token % p.seq.N;
     }
+    if (!fa_index_ok(at, static_cast<long long>(p.seq.total_tokens) * p.seq.Hq, p.status)) return;
     const bool grouped = token >= p.prefix_cu[0] && token < p.prefix_cu[p.groups];
     const float l0 = grouped ? p.lse[0][static_cast<long long>(h) * p.seq.total_tokens + token] : kNegInf;
     const float l1 = p.lse[1][at];

@@ -43,6 +43,9 @@ struct LaneRows {
         unit[0] = first + 16 * at.unit[0];
         unit[1] = first + 16 * at.unit[1];
     }
+    __device__ __forceinline__ bool ok(const NormRopeParams& p, int side, const void* x, long long stride, int row) const {
+        return channels_ok<D>(p, side, x, unit[0] + row * kStep, stride) && channels_ok<D>(p, side, x, unit[1] + row * kStep, stride);
+    }
     __device__ __forceinline__ void load(int row, uint4 (&v)[2]) const {
         v[0] = *reinterpret_cast<const uint4*>(unit[0] + row * kStep);
         v[1] = *reinterpret_cast<const uint4*>(unit[1] + row * kStep);
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const __grid
         uint4 in[kAhead][2];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (whole || u < left) from.load(u, in[u]);
+            if ((whole || u < left) && from.ok(p, side, p.x[side], p.x_stride[side], u)) from.load(u, in[u]);
         if (fresh) lane_rotation<D, IL>(p.rope, at, un.token, rot);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const __grid
             widen<E>(in[u][0], in[u][1], v);
             if (p.norm) scale_row(v, inverse_norm<D>(v, p.eps), w);
             rotate<D, IL, false>(at, rot, v);
-            if (real && fa_index_ok(un.token, p.T, p.status)) to.template store<E>(u, v);
+            if (real && to.ok(p, side, p.y[side], p.y_stride[side], u)) to.template store<E>(u, v);
         }
         from.advance(kAhead);
         to.advance(kAhead);
@@ -159,8 +162,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const __
                 uint4* to = places + put * 4 * kNormThreads + threadIdx.x;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    cp_async16(smem_addr(to + j * kNormThreads), cdy + 8 * at.unit[j]);
-                    if (p.norm) cp_async16(smem_addr(to + (2 + j) * kNormThreads), cx + 8 * at.unit[j]);
+                    if (channels_ok<D>(p, side, p.dy[side], cdy + 8 * at.unit[j], p.dy_stride[side]))
+                        cp_async16(smem_addr(to + j * kNormThreads), cdy + 8 * at.unit[j]);
+                    if (p.norm && channels_ok<D>(p, side, p.x[side], cx + 8 * at.unit[j], p.x_stride[side]))
+                        cp_async16(smem_addr(to + (2 + j) * kNormThreads), cx + 8 * at.unit[j]);
                 }
                 cdy += D;
                 cx += D;
@@ -200,9 +205,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const __
             }
             rotate<D, IL, true>(at, rot, g);
             if (p.norm) norm_back<D>(g, v, inverse_norm<D>(v, p.eps), w, dw);
-            if (real && fa_index_ok(un.token, p.T, p.status)) {
+            if (real) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(y + 8 * at.unit[j]) = narrow<E>(g + 8 * j);
+                for (int j = 0; j < 2; ++j)
+                    if (channels_ok<D>(p, side, p.y[side], y + 8 * at.unit[j], p.y_stride[side]))
+                        *reinterpret_cast<uint4*>(y + 8 * at.unit[j]) = narrow<E>(g + 8 * j);
             }
             y += D;
         }
@@ -217,7 +224,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const __
         float v = 0.f;
 #pragma unroll 8
         for (int i = 0; i < kGroups; ++i) v += sums[i][threadIdx.x];
-        p.partial[static_cast<long long>(blockIdx.x) * D + threadIdx.x] = v;
+        const long long sum = static_cast<long long>(blockIdx.x) * D + threadIdx.x;
+        if (fa_index_ok(sum, (static_cast<long long>(p.ctas[0]) + p.ctas[1]) * D, p.status)) p.partial[sum] = v;
     }
 }
 
@@ -232,15 +240,17 @@ __global__ void __launch_bounds__(1024) norm_rope_weights_kernel(const __grid_co
     if (!p.dw[side]) return;
     double v = 0.0;
 #pragma unroll 8
-    for (int i = row; i < p.ctas[side]; i += 32)
-        v += p.partial[static_cast<long long>(i + (side ? p.ctas[0] : 0)) * D + ch];
+    for (int i = row; i < p.ctas[side]; i += 32) {
+        const long long sum = static_cast<long long>(i + (side ? p.ctas[0] : 0)) * D + ch;
+        if (fa_index_ok(sum, (static_cast<long long>(p.ctas[0]) + p.ctas[1]) * D, p.status)) v += p.partial[sum];
+    }
     sums[row][threadIdx.x % 32] = v;
     __syncthreads();
     if (row == 0) {
         v = 0.0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v += sums[i][threadIdx.x];
-        p.dw[side][ch] = static_cast<float>(v);
+        if (fa_index_ok(ch, D, p.status)) p.dw[side][ch] = static_cast<float>(v);
     }
 }
 

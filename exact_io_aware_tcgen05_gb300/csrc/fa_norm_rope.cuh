@@ -57,6 +57,10 @@ __device__ __forceinline__ int axis_of(const RopeParams& r, int f) {
 // integer first: what is left, an eighth of a turn at most, is an fp32 number to 2^-28 of a turn, where
 // a whole turn would be one to 2^-26.
 __device__ __forceinline__ void cos_sin(const RopeParams& r, int f, long long token, float& c, float& s) {
+    if (!fa_index_ok(f, r.rot / 2, r.status) || !fa_index_ok(token, r.axis_stride, r.status)) {
+        c = s = 0.f;
+        return;
+    }
     const long long pos = r.positions[axis_of(r, f) * r.axis_stride + token];
     const uint32_t turn = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * r.turns[f]) >> 32);
     const uint32_t quarter = (turn + 0x20000000u) >> 30;
@@ -133,6 +137,12 @@ __device__ __forceinline__ void widen(uint4 a, uint4 b, float (&x)[16]) {
 template <int E>
 __device__ __forceinline__ uint4 narrow(const float* x) {
     return make_uint4(pack2<E>(x[0], x[1]), pack2<E>(x[2], x[3]), pack2<E>(x[4], x[5]), pack2<E>(x[6], x[7]));
+}
+
+// Whether 8 channels at `at` lie in a token's heads of one side of the tensor at `base` (checking build).
+template <int D>
+__device__ __forceinline__ bool channels_ok(const NormRopeParams& p, int side, const void* base, const void* at, long long stride) {
+    return fa_row_ok(base, at, 16, p.T, 2LL * D * p.heads[side], 2 * stride, p.status);
 }
 
 // Sum over the D / 16 lanes of a row, in all of them.

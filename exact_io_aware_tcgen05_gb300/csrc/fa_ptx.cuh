@@ -39,6 +39,29 @@ __device__ __forceinline__ bool fa_index_ok(long long idx, long long size, int* 
 __device__ __forceinline__ bool fa_index_ok(long long, long long, int*) { return true; }
 #endif
 
+// Whether `n` bytes from byte `first` on lie in one row of a tensor of `rows` rows of `width` bytes, `stride`
+// bytes apart.
+__host__ __device__ constexpr bool row_holds(long long first, int n, long long rows, long long width, long long stride) {
+    return first >= 0 && first / stride < rows && first % stride + n <= width;
+}
+static_assert(row_holds(0, 16, 1, 16, 16) && row_holds(2 * 48 + 16, 16, 3, 32, 48), "the first and the last bytes");
+static_assert(!row_holds(-1, 1, 3, 32, 48) && !row_holds(-16, 16, 3, 32, 48), "before the tensor");
+static_assert(!row_holds(3 * 48, 16, 3, 32, 48) && !row_holds(1LL << 40, 1, 3, 32, 48), "behind its last row");
+static_assert(!row_holds(32, 1, 3, 32, 48) && !row_holds(48 + 17, 16, 3, 32, 48), "between two rows, across a row's end");
+
+// Whether the address formed, `n` bytes at `at`, lies so in the tensor at `base`.
+#ifdef FA_DEBUG_CHECKS
+__device__ __forceinline__ bool fa_row_ok(const void* base, const void* at, int n, long long rows, long long width,
+                                          long long stride, int* status) {
+    const long long first = static_cast<const char*>(at) - static_cast<const char*>(base);
+    return fa_index_ok(row_holds(first, n, rows, width, stride) ? 0 : -1, 1, status);
+}
+#else
+__device__ __forceinline__ bool fa_row_ok(const void*, const void*, int, long long, long long, long long, int*) {
+    return true;
+}
+#endif
+
 // A TMA store box of `rows` token rows from `row` and one head: it must lie inside
 // [0, tokens) x [0, heads) (stores may not start at negative coordinates).
 __device__ __forceinline__ bool fa_box_ok(long long row, int rows, long long tokens, int head,

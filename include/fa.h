@@ -631,15 +631,16 @@ void fa_set_launch_events(const cudaEvent_t* events, int count);
  * Bounds-checking build.  The library built with FA_DEBUG_CHECKS defined
  * (exact_io_aware_tcgen05_gb300.build.build(debug=True), libfa_gb300_debug.so)
  * checks, inside every kernel, each computed global index and TMA store box
- * against its tensor (in the paged cache's kernels, the rows of O and LSE only);
- * a failing check skips the access and records device
+ * against its tensor (in the paged cache's attention and plan kernels, the rows of O
+ * and LSE only); a failing check skips the access and records device
  * status 7, which fa_device_status() reports as FA_ERR_CUDA with a message.
  * Nothing traps.  (A stand-in for a memory checker; the kernels are otherwise
  * identical.)
  *   fa_debug_checks_enabled: 1 in that build, 0 in the normal one.
  *   fa_debug_check_selftest: enqueues one thread that tests an index one past
- *     its range without touching memory, so that fa_device_status() must then
- *     report the failed check; FA_ERR_UNSUPPORTED in the normal build.
+ *     its range, and addresses on and off a tensor's rows, without touching memory,
+ *     so that fa_device_status() must then report the failed check;
+ *     FA_ERR_UNSUPPORTED in the normal build.
  */
 int fa_debug_checks_enabled(void);
 fa_status fa_debug_check_selftest(cudaStream_t stream);

@@ -98,3 +98,21 @@ def test_keys_with_large_weights(fa):
     fa.kv8_append_norm_rope(cache, q, k, k, torch.tensor(slots, dtype=torch.int32, device="cuda"), k_weight=w, eps=EPS)
     y, bound = ref.forward(k, w, None, False, True, EPS)
     base.check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, slots)
+
+
+@pytest.mark.parametrize("name", ["test_norm_rope_edges_gpu.py", "test_kv8_gpu.py"])
+def test_suites_under_the_bounds_checking_build(fa, name):
+    """These tests, and those of the cache's writer without norms, with the library that checks the addresses it
+    forms; the status word has to be clear after each."""
+    import os
+    import subprocess
+    import sys
+    if fa.fa_debug_checks_enabled():
+        pytest.skip("this is the checking build")
+    from exact_io_aware_tcgen05_gb300 import build as b
+    env = dict(os.environ, FA_GB300_LIBRARY=b.build(debug=True), FA_GB300_CHECK_STATUS="1")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", "-p", "no:cacheprovider",
+                        os.path.join("tests", name), "-k", "not bounds_checking"], cwd=root, env=env,
+                       capture_output=True, text=True, timeout=1200)
+    assert r.returncode == 0 and " passed" in r.stdout, (r.stdout[-4000:], r.stderr[-2000:])
