@@ -356,9 +356,12 @@ fa_status fa_fwd_fp8(const void* q8, const float* q_scale, const void* k8, const
  *                   read if num_axes > 1 (up to 4)
  *   turns           device, uint64 [rot / 2]; null if rot is 0
  *   rot             a multiple of 16 from 0 to d
- * All arithmetic is in fp32 (squares of values beyond 2^63 overflow), the cosines and sines are
- * those of sincospif, and each output is rounded once.  Infinities and NaN go where the formula
- * takes them: into their own row only.  d in {64, 128}.  Enqueues one kernel.
+ * All arithmetic is in fp32, the cosines and sines are those of sincospif, and each output is
+ * rounded once.  A row's squares are summed before they are divided by d: a row whose squares sum
+ * to 2^128 or more counts as infinitely long, r = 0, and its finite values come out as 0, as do
+ * their gradients (values up to 2^60 are safe for both d; fp16 does not come near).  Infinities and
+ * NaN go where the formula takes them: into their own row only.  d in {64, 128}.  Enqueues one
+ * kernel.
  *
  * fa_norm_rope_bwd: the gradients dq, dk of q and k, and dq_weight, dk_weight (fp32 [d], each
  * may be null) of the weights, from the outputs' gradients dq_out, dk_out.  With dn the output's

@@ -100,6 +100,60 @@ def test_keys_with_large_weights(fa):
     base.check_keys(torch, before, (cache.k8, cache.k_scale), y, bound, slots)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_as_long_as_fp32_holds(fa, d):
+    """Rows whose squares sum to just below 2^128 are rows as others; from there on r is 0."""
+    import torch
+    T, Hkv, page = 40, 2, 64
+    q, k, w, pos, axis = base.make(torch, 7, (T,), 3, Hkv, d, "bf16", d)
+    sign = lambda x: torch.where(x < 0, -1.0, 1.0).to(x.dtype)
+    most = 2.0 ** 60 if d == 128 else 1.4140625 * 2.0 ** 60     # d x^2 = 2^127 and just below it
+    q[::2], k[::2] = sign(q[::2]) * most, sign(k[::2]) * most   # (the others: as they come)
+    q[1, 1], k[1, 1] = sign(q[1, 1]) * 2.0 ** 61, sign(k[1, 1]) * 2.0 ** 61   # squares of 2^122 each: 2^128 at d = 64
+    q[3, 0], k[3, 0, 5] = sign(q[3, 0]) * 2.0 ** 100, 2.0 ** 64
+    dy = [torch.randn_like(q), torch.randn_like(k)]
+    p, kw = base.plan(fa, d, axis, False), dict(q_weight=w[0], k_weight=w[1])
+    a = base.angle(pos, d, axis)
+    got, grads = fa.norm_rope_forward(q, k, pos, p, **kw), fa.norm_rope_backward(q, k, *dy, pos, p, **kw)
+    cache = fa.kv8_cache(1, Hkv, d, page=page)
+    before = cache.k8.clone(), cache.k_scale.clone()
+    slots = list(range(T))
+    s = torch.tensor(slots, dtype=torch.int32, device="cuda")
+    assert torch.equal(fa.kv8_append_norm_rope(cache, q, k, k, s, pos, p, **kw), got[0])
+    for i, x in enumerate((q, k)):
+        long_ = x.double().square().sum(-1) >= 2.0 ** 128
+        assert int(long_.sum()) == 2
+        x = torch.where(long_[..., None], 0.0, x)               # (a row of zeros: outputs 0)
+        want, bound = ref.forward(x, w[i], a, False, True, EPS)
+        ref.check("y", got[i], want, bound, "bf16")
+        if i:
+            base.check_keys(torch, before, (cache.k8, cache.k_scale), want, bound, slots)
+        assert (grads[i][long_] == 0).all()
+        dx, dx_bound, dw, dw_bound = ref.backward(x, torch.where(long_[..., None], 0.0, dy[i]), w[i], a, False, True, EPS)
+        ref.check("dx", grads[i], dx, dx_bound, "bf16")
+        ref.check("dw", grads[2 + i], dw, dw_bound, None)
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_one_sides_weight_alone(fa, side):
+    """A norm with weights for queries or for keys only, its gradient too."""
+    import torch
+    q, k, w, pos, axis = base.make(torch, 8 + side, (333,), 6, 2, 128, "bf16", 64, wide=True)
+    w[1 - side] = None
+    dy = [torch.randn_like(q), torch.randn_like(k)]
+    p, kw = base.plan(fa, 64, axis, False), dict(q_weight=w[0], k_weight=w[1])
+    a = base.angle(pos, 64, axis)
+    got, grads = fa.norm_rope_forward(q, k, pos, p, **kw), fa.norm_rope_backward(q, k, *dy, pos, p, **kw)
+    for i, x in enumerate((q, k)):
+        ref.check("y", got[i], *ref.forward(x, w[i], a, False, True, EPS), "bf16")
+        dx, bound, dw, dw_bound = ref.backward(x, dy[i], w[i], a, False, True, EPS)
+        ref.check("dx", grads[i], dx, bound, "bf16")
+        if i == side:
+            ref.check("dw", grads[2 + i], dw, dw_bound, None)
+        else:
+            assert grads[2 + i] is None
+
+
 @pytest.mark.parametrize("name", ["test_norm_rope_edges_gpu.py", "test_kv8_gpu.py"])
 def test_suites_under_the_bounds_checking_build(fa, name):
     """These tests, and those of the cache's writer without norms, with the library that checks the addresses it
