@@ -480,7 +480,7 @@ def fa_norm_rope_bwd(dtype, q, q_stride, k, k_stride, dq_out, dq_out_stride, dk_
 def fa_kv8_append_norm_rope(dtype, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, k8, k_scale, v8, v_scale,
                             num_pages, page, Hq, Hkv, d, slots, T, norm, q_weight, k_weight, weights_f32, eps,
                             positions, axes, num_axes, turns, rot, interleaved, stream=None, check: bool = True) -> int:
-    """fa_norm_rope and fa_kv8_append in one kernel (see include/fa.h)."""
+    """fa_norm_rope and fa_kv8_append in one call (see include/fa.h)."""
     st = load().fa_kv8_append_norm_rope(int(dtype), _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v),
                                         int(v_stride), _ptr(q_out), int(q_out_stride), _ptr(k8), _ptr(k_scale),
                                         _ptr(v8), _ptr(v_scale), num_pages, page, Hq, Hkv, d, _ptr(slots), T,

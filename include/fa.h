@@ -450,11 +450,12 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
  * a block begun by another writer may have any positive scale.)  Infinities and NaN become NaN
  * codes.
  *
- * fa_kv8_append_norm_rope: fa_norm_rope and fa_kv8_append in one kernel.  q goes to q_out as
+ * fa_kv8_append_norm_rope: fa_norm_rope and fa_kv8_append in one call.  q goes to q_out as
  * in fa_norm_rope; k is normed and rotated in fp32, and the block's scale and codes come from
  * those numbers as above (rounded once, where the two calls would round them to 16 bits in
  * between); v goes to the cache as it is.  T tokens of each, with strides of their own; the
- * tokens without a slot get their q_out too.  Arguments otherwise as there.
+ * tokens without a slot get their q_out too.  Arguments otherwise as there.  Enqueues one kernel,
+ * or two (the queries have one of their own) from 32 tokens for each of the device's SMs on.
  *
  * fa_fwd_kv8: O and LSE of the new tokens' attention over the cache.
  *   q            device, read: bf16 or fp16; dense [B, N, Hq, d] or packed [T, Hq, d],
@@ -482,6 +483,11 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
  *                contents ignored; not to be shared by calls in flight together
  *                (calls captured into graphs that replay at the same time among them)
  *
+ * The workspace's size does not depend on lens.  The result does not depend on anything but
+ * the inputs, the geometry and the device's SM count.  Enqueues two kernels (L = 2 for
+ * fa_set_launch_events).  A wait inside them gives up after fa_set_wait_limit_cycles' budget
+ * or 6e9 cycles, whichever is less.
+ *
  * fa_fwd_kv8_prefix: the same for a batch whose requests share prefixes, each read once for
  * all of its group.  Group p = 0 .. groups - 1 is the new tokens prefix_cu[p] .. prefix_cu[p + 1] - 1
  * (dense: token b N + i), whole requests one behind the other, and its prefix the first
@@ -496,12 +502,8 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
  * tokens each.  O and LSE of both parts are held in fp32 in the workspace of
  * fa_fwd_kv8_prefix_workspace_size(...) bytes (8 Hq d bytes a token and 2 of fa_fwd_kv8's) and joined
  * there: O = sum_i exp(LSE_i - LSE) O_i.  Limits: as fa_fwd_kv8's, for the prefixes with `groups`
- * and prefix_width in place of B and width.  Enqueues four kernels; takes no launch events.
- *
- * The size does not depend on lens.  The result does not depend on anything but the
- * inputs, the geometry and the device's SM count.  Enqueues two kernels (L = 2 for
- * fa_set_launch_events).  A wait inside them gives up after fa_set_wait_limit_cycles' budget
- * or 6e9 cycles, whichever is less.
+ * and prefix_width in place of B and width.  Enqueues four kernels; takes no launch events (armed
+ * ones stay armed).
  */
 #define FA_KV8_BLOCK 16
 fa_status fa_kv8_plan(const int* lens, const int* grow, int B, int* table, int width, int* ring,
