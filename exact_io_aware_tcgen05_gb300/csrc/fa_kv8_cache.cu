@@ -543,10 +543,11 @@ __device__ __forceinline__ void append_keys(const Kv8AppendParams& p, const Norm
 //
 // In long batches the queries have norm_rope_kernel, which keeps more warps on an SM (queries here, all
 // kinds of CTAs side by side: 315 us and more for the prompts below).  Measured (one GB300, bf16, Hq 32,
-// Hkv 8, d = 128): 8 prompts of 8192 tokens 297 us, 73 % of the measured copy rate: the queries 169 us, 93 %,
-// then keys and values 130 us, where the keys wait for their loads and for the other warp of a block (issue
-// slots 45 % used, DRAM 36 %; four warps to a block, with 24 warps an SM: 300); 64 single tokens 3.9 us, a
-// launch and the slots, positions and rows that wait for one another.
+// Hkv 8, d = 128): 8 prompts of 8192 tokens 298 us, 73 % of the measured copy rate: the queries 168 us, 94 %,
+// then keys and values 132 us, where the keys wait for their loads and for the other warp of a block (issue
+// slots 46 % used, DRAM 36 %; four warps to a block, with 24 warps an SM: 300); 64 single tokens 3.8 us, a
+// launch and the slots, positions and rows that wait for one another.  At d = 128 this kernel's 128 registers
+// do not hold everything: 100 bytes a thread are spilled (44 with neighbouring pairs).
 constexpr int kAppendValues = 0, kAppendKeys = 1, kAppendQueries = 2;
 
 template <int D, int E, bool IL>

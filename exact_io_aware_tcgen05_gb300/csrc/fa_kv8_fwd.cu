@@ -823,8 +823,10 @@ cudaError_t launch_both(const Kv8FwdParams& p, const cudaEvent_t* ev, cudaStream
 //   LSE = log sum_i exp(LSE_i),  O = sum_i exp(LSE_i - LSE) O_i.
 // A warp has a row.  A row behind the last request is left as it was, one outside all groups has no first
 // part.  Measured (one GB300, bf16, Hq 32, Hkv 8, d = 128, all four kernels): 64 single tokens behind 8192
-// shared ones 55 us, some 10 of them until the first products over the prefix, 12 in the joins of
-// split items, 4 here (bound by latency: 3 MB).  Both passes on the GPU at once, a CTA per SM each, took as long.
+// shared ones 59 us from call to call, 55 in a graph, some 10 of them until the first products over the prefix,
+// 12 in the joins of split items, 4 here (bound by latency: 3 MB).  Both passes on the GPU at once, a CTA per SM
+// each, took as long.  With few requests to a group or short prefixes that is slower than reading the prefix
+// once for each request (fa.h says from where on sharing pays).
 template <int D, int E>
 __global__ void __launch_bounds__(256) fa_kv8_prefix_join_kernel(const Kv8PrefixJoinParams p) {
     grid_launch_dependents();

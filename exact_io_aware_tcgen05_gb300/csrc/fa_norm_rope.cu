@@ -7,9 +7,9 @@
 // needs some 50 KB), few instructions a row (some 180 for the 4 or 8 rows of a warp, half of them the
 // arithmetic), and angles worked out once for many heads.
 //
-// Measured (one GB300, bf16, the shares of the measured copy rate): forward 32768 tokens, Hq 32, Hkv 8,
-// d = 128, three axes, slices of a projection 107.6 us, 92 % (a plain copy of such rows runs at 97 %);
-// 16384 tokens of 16 and 16 heads 47.5 us, 83 %, where the last CTAs leave SMs idle; one token 2.6 us, a
+// Measured (one GB300, bf16, in a graph, the shares of the measured copy rate): forward 32768 tokens, Hq 32,
+// Hkv 8, d = 128, three axes, slices of a projection 107.6 us, 92 % (a plain copy of such rows runs at 97 %);
+// 16384 tokens of 16 and 16 heads 47.8 us, 83 %, where the last CTAs leave SMs idle; one token 2.6 us, a
 // launch and the loads that wait for one another.  A warp on four heads of one token, its angles
 // shared, waited longer at every token's start (121 to 131 us); passes of rows through rings in shared
 // memory, by bulk or by asynchronous copies, took 118 to 126 us, bound by their instructions.
@@ -125,7 +125,7 @@ __device__ __forceinline__ void norm_back(float (&g)[16], float (&x)[16], float 
 // The rows come by asynchronous copies, kBwdAhead - 1 rows ahead and over the ends of units, into places
 // in shared memory that each thread reads back itself: no thread waits for another, and what is on its
 // way takes none of the registers, which dw, the weights and the angles fill.  With the rows loaded into
-// registers, two at a time, 16384 tokens of 16 and 16 heads (d = 128) took 79.6 us in place of 69.4
+// registers, two at a time, 16384 tokens of 16 and 16 heads (d = 128) took 79.6 us in place of 69.8
 // (5.8 TB/s, 85 % of the measured copy rate); more rows ahead, or rows in 2 KB pieces by bulk copies
 // (72.5), were no faster.
 constexpr int kBwdAhead = 3;

@@ -504,6 +504,14 @@ fa_status fa_norm_rope_bwd(fa_dtype dtype, const void* q, long long q_stride, co
  * there: O = sum_i exp(LSE_i - LSE) O_i.  Limits: as fa_fwd_kv8's, for the prefixes with `groups`
  * and prefix_width in place of B and width.  Enqueues four kernels; takes no launch events (armed
  * ones stay armed).
+ * Sharing pays for long prefixes of many requests.  fa_fwd_kv8 over rows that name the prefix's
+ * pages for every request (prefixes of whole pages) gives the same attention, and for single new
+ * tokens is the faster call until about 0.5 GB of keys and values need not be read again: the sum
+ * over the groups of (requests - 1) * prefix tokens * 2 Hkv d bytes.  (One GB300, bf16, Hq 32,
+ * Hkv 8, d = 128, 512 own tokens, shared / by fa_fwd_kv8: 64 requests behind 8192 tokens 62 / 116
+ * us, behind 2048 54 / 44; 8 behind 32768 48 / 60, behind 8192 37 / 23; 32 groups of 2 behind 8192
+ * each 177 / 176, of 3 184 / 257.  Chunks of 200 new tokens gain little: 24 requests behind 16384,
+ * d = 64, 560 / 632.)
  */
 #define FA_KV8_BLOCK 16
 fa_status fa_kv8_plan(const int* lens, const int* grow, int B, int* table, int width, int* ring,
