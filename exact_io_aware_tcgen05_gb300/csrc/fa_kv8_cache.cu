@@ -188,8 +188,8 @@ __device__ __forceinline__ float div_odd(float a, float b) {
     return to_odd(x, __fmaf_rn(-x, b, a) == 0.f);
 }
 
-// Whether the addresses formed lie in their tensors (checking build): 8 codes and a scale of one side of
-// the cache, 8 channels of a new token's values (side 1; keys without norm and rotation: 0).
+// Whether the addresses formed lie in their tensors (checking build): 8 codes, or a scale, of one side of the
+// cache (keys 0, values 1), and 8 channels of a new token, as it is written without norm and rotation.
 template <int D>
 __device__ __forceinline__ bool codes_ok(const Kv8AppendParams& p, int side, const void* at) {
     return fa_row_ok(p.codes[side], at, 8, static_cast<long long>(p.num_slots) * p.Hkv, D, D, p.status);

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(1024) norm_rope_weights_kernel(const __grid_co
         v = 0.0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v += sums[i][threadIdx.x];
-        if (fa_index_ok(ch, D, p.status)) p.dw[side][ch] = static_cast<float>(v);
+        p.dw[side][ch] = static_cast<float>(v);
     }
 }
 
